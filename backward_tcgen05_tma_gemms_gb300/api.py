@@ -86,6 +86,10 @@ def library():
     lib.tps_ce_workspace_bytes.restype = sz
     lib.tps_ce_workspace_bytes_ex.argtypes = [i64, i64, i32, i32]
     lib.tps_ce_workspace_bytes_ex.restype = sz
+    lib.tps_linear_ce_fwd.argtypes = [P, P, P, i32, ctypes.POINTER(TpsCeOptions), P, P, P, vp, sz, vp]
+    lib.tps_linear_ce_bwd.argtypes = [P, P, P, P, P, i32, ctypes.POINTER(TpsCeOptions), P, P, vp, sz, vp]
+    lib.tps_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i64]
+    lib.tps_linear_ce_workspace_bytes.restype = sz
     lib.tps_last_device_error.argtypes = [vp]
     lib.tps_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.tps_strerror.argtypes = [ctypes.c_int]
@@ -421,6 +425,88 @@ def vocab_ce_fwd_bwd_ex(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tens
         _ref(red_t), *[_ref(a) for a in tail], ctypes.c_void_p(ws.data_ptr()), ws.numel() * ws.element_size(),
         _stream(dev)), T, V, tp, h.dtype, workspace, dev)
     return loss, red, dlog, dh, dw, owner
+
+
+def linear_ce_workspace_bytes(T: int, d: int, V: int, dtype: torch.dtype, backward: bool, piece: int = 0) -> int:
+    """Workspace bytes of linear_ce_fwd / linear_ce_bwd for pieces of `piece`
+    vocabulary columns (0: the library's choice)."""
+    return int(library().tps_linear_ce_workspace_bytes(T, d, V, _DTYPES[dtype], 1 if backward else 0, piece))
+
+
+def _linear_ce_call(fn, T, d, V, dtype, backward, workspace, device):
+    """Run fn(workspace pointer, bytes) with the given workspace, or with one
+    for the tensor-core path; operands that do not qualify for it are refused
+    before any launch and run again with the other path's size."""
+    if workspace is not None:
+        _check(fn(ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()))
+        return
+    for dt in (dtype, torch.float32):
+        n = max(linear_ce_workspace_bytes(T, d, V, dt, backward), 1)
+        ws = torch.empty(n, dtype=torch.uint8, device=device)
+        rc = fn(ctypes.c_void_p(ws.data_ptr()), n)
+        if rc != ERR_WORKSPACE:
+            break
+    _check(rc)
+
+
+def _linear_ce_args(h, Whead, weight_layout, ignore_index, vocab_size, reduction, denominator):
+    if weight_layout not in LAYOUTS or reduction not in REDUCTIONS:
+        raise ValueError("argument")
+    if Whead.dim() != 2:
+        raise ValueError("shape")
+    d = h.shape[-1]
+    V = Whead.shape[1] if weight_layout == "in_out" else Whead.shape[0]
+    opts = TpsCeOptions(NO_IGNORE if ignore_index is None else int(ignore_index), int(vocab_size),
+                        REDUCTIONS[reduction], 0, float(denominator))
+    return (h.numel() // d if d else 0), d, V, opts
+
+
+def linear_ce_fwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, weight_layout: str = "in_out",
+                  ignore_index: Optional[int] = None, vocab_size: int = 0, reduction: str = "none",
+                  denominator: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                  out: Optional[Sequence] = None):
+    """Cross entropy of the head in pieces of the vocabulary, without the
+    logits.  Returns (loss [T], loss_reduced (0-d) or None, lse [T]), all
+    fp32; lse is what linear_ce_bwd needs.  Options as vocab_ce_fwd_bwd_ex."""
+    T, d, V, opts = _linear_ce_args(h, Whead, weight_layout, ignore_index, vocab_size, reduction, denominator)
+    if out is not None:
+        loss, red, lse = out
+    else:
+        loss = torch.empty(T, device=h.device, dtype=torch.float32)
+        lse = torch.empty(T, device=h.device, dtype=torch.float32)
+        red = torch.empty((), device=h.device, dtype=torch.float32) if reduction != "none" else None
+    a = [_tt(t) for t in (h, Whead, labels, loss, red.reshape(1) if red is not None else None, lse)]
+    stream = _stream(h.device)
+    _linear_ce_call(lambda ws, n: library().tps_linear_ce_fwd(
+        _ref(a[0]), _ref(a[1]), _ref(a[2]), LAYOUTS[weight_layout], ctypes.byref(opts), _ref(a[3]), _ref(a[4]),
+        _ref(a[5]), ws, n, stream), T, d, V, h.dtype, False, workspace, h.device)
+    return loss, red, lse
+
+
+def linear_ce_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
+                  grad_loss: Optional[torch.Tensor] = None, weight_layout: str = "in_out",
+                  ignore_index: Optional[int] = None, vocab_size: int = 0, reduction: str = "none",
+                  denominator: float = 0.0, want_dhidden: bool = True, want_dwhead: bool = True,
+                  grad_dtype: torch.dtype = torch.float32, workspace: Optional[torch.Tensor] = None,
+                  out: Optional[Sequence] = None):
+    """Backward of linear_ce_fwd from its lse: (dHidden like h, dWhead like
+    Whead) in `grad_dtype` (fp32 or bf16), None for one that is not wanted.
+    grad_loss: the upstream gradient (T values for reduction "none", else
+    one; default ones)."""
+    T, d, V, opts = _linear_ce_args(h, Whead, weight_layout, ignore_index, vocab_size, reduction, denominator)
+    if out is not None:
+        dh, dw = out
+    else:
+        dh = torch.empty(h.shape, device=h.device, dtype=grad_dtype) if want_dhidden else None
+        dw = torch.empty(Whead.shape, device=h.device, dtype=grad_dtype) if want_dwhead else None
+    if grad_loss is not None and grad_loss.dim() == 0:
+        grad_loss = grad_loss.reshape(1)
+    a = [_tt(t) for t in (h, Whead, labels, lse, grad_loss, dh, dw)]
+    stream = _stream(h.device)
+    _linear_ce_call(lambda ws, n: library().tps_linear_ce_bwd(
+        _ref(a[0]), _ref(a[1]), _ref(a[2]), _ref(a[3]), _ref(a[4]), LAYOUTS[weight_layout], ctypes.byref(opts),
+        _ref(a[5]), _ref(a[6]), ws, n, stream), T, d, V, h.dtype, True, workspace, h.device)
+    return dh, dw
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

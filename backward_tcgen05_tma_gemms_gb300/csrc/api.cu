@@ -15,6 +15,7 @@
 #include <string>
 #include <vector>
 
+#include "api_common.cuh"
 #include "internal.cuh"
 #include "tps.h"
 
@@ -23,7 +24,7 @@ namespace tps {
 // ------------------------------------------------------------ error detail
 static thread_local std::string t_detail;
 
-static int fail(int code, const char* fmt, ...) {
+int fail(int code, const char* fmt, ...) {
   char buf[512];
   va_list ap;
   va_start(ap, fmt);
@@ -34,6 +35,7 @@ static int fail(int code, const char* fmt, ...) {
 }
 
 void set_error_detail(const char* msg) { t_detail = msg; }
+void clear_detail() { t_detail.clear(); }
 
 // ------------------------------------------------------------ device error word
 // One word per device; kernels OR TPS_DEVERR_* bits into it.
@@ -101,13 +103,7 @@ void note_launch() {
 }
 
 // ------------------------------------------------------------ tensor views
-struct Mat {  // 2-D strided view
-  void* data = nullptr;
-  int dtype = 0;
-  int64_t rows = 0, cols = 0, sr = 0, sc = 0;
-};
-
-static const char* dtname(int d) {
+const char* dtname(int d) {
   switch (d) {
     case TPS_F32: return "f32";
     case TPS_BF16: return "bf16";
@@ -121,7 +117,7 @@ static const char* dtname(int d) {
 // merged into rows, which requires them to be mutually contiguous.
 // The view must have unit stride in one dimension (either one when a
 // dimension has extent <= 1).
-static int as_mat(const tps_tensor* t, const char* name, bool flatten, Mat* m) {
+int as_mat(const tps_tensor* t, const char* name, bool flatten, Mat* m) {
   if (t == nullptr) return fail(TPS_ERR_ARG, "%s: missing tensor", name);
   if (t->ndim < 1 || t->ndim > 4) return fail(TPS_ERR_SHAPE, "%s: ndim %d", name, t->ndim);
   int64_t numel = 1;
@@ -158,7 +154,7 @@ static int as_mat(const tps_tensor* t, const char* name, bool flatten, Mat* m) {
   return TPS_OK;
 }
 
-static int expect(const Mat& m, const char* name, int64_t rows, int64_t cols) {
+int expect(const Mat& m, const char* name, int64_t rows, int64_t cols) {
   if (m.rows != rows || m.cols != cols)
     return fail(TPS_ERR_SHAPE, "%s: shape (%lld, %lld), expected (%lld, %lld)", name, (long long)m.rows,
                 (long long)m.cols, (long long)rows, (long long)cols);
@@ -177,8 +173,7 @@ __global__ void fill_kernel(void* base, int dtype, int64_t rows, int64_t cols, i
   }
 }
 
-static int launch_fill(void* base, int dtype, int64_t rows, int64_t cols, int64_t sr, int64_t sc,
-                       cudaStream_t stream) {
+int launch_fill(void* base, int dtype, int64_t rows, int64_t cols, int64_t sr, int64_t sc, cudaStream_t stream) {
   if (rows <= 0 || cols <= 0 || base == nullptr) return TPS_OK;
   const int64_t n = rows * cols;
   const int blocks = static_cast<int>(n / 256 + 1 < 4096 ? n / 256 + 1 : 4096);
@@ -193,7 +188,7 @@ static int launch_fill(void* base, int dtype, int64_t rows, int64_t cols, int64_
 // (unit stride along M) is produced as D^T = B^T A^T with the roles of the
 // operands swapped.  Epilogues other than a plain store only ever target the
 // library's own row-major workspace.
-static int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream) {
+int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream) {
   if (g.M == 0 || g.N == 0) return TPS_OK;
   uint32_t* err = dev_err_ptr();
   if (err == nullptr) return fail(TPS_ERR_CUDA, "cannot resolve the device error word");
@@ -244,6 +239,7 @@ static int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream)
     if (rc == TPS_ERR_CUDA) return fail(rc, "%s: launch failed: %s", g.name, cudaGetErrorString(cudaGetLastError()));
     return rc;
   }
+  if (g.K == 0 && g.epi.accumulate) return TPS_OK;  // adds nothing
   if (g.K == 0) {
     // An empty contraction is the zero matrix; phi(0) = 0 and 0 * phi' = 0
     // for every supported activation, and every gated output is a product
@@ -300,7 +296,30 @@ static int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream)
   return rc;
 }
 
-static size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+int expect_vector(const tps_tensor* t, const char* name, int dtype, int64_t n) {
+  if (t == nullptr || (t->data == nullptr && n > 0)) return fail(TPS_ERR_ARG, "%s: missing tensor", name);
+  if (t->ndim < 1 || t->ndim > 4) return fail(TPS_ERR_SHAPE, "%s: ndim %d", name, t->ndim);
+  if (t->dtype != dtype) return fail(TPS_ERR_DTYPE, "%s must be %s", name, dtname(dtype));
+  int64_t have = 1;
+  for (int i = 0; i < t->ndim; ++i) have *= t->shape[i];
+  if (have != n) return fail(TPS_ERR_SHAPE, "%s holds %lld entries, expected %lld", name, (long long)have, (long long)n);
+  int64_t run = 1;
+  for (int i = t->ndim - 1; i >= 0; --i) {
+    if (t->shape[i] > 1 && t->stride[i] != run) return fail(TPS_ERR_LAYOUT, "%s must be contiguous", name);
+    run *= t->shape[i];
+  }
+  return TPS_OK;
+}
+
+void weight_strides(const Mat& w, int layout, int64_t* s_in, int64_t* s_out) {
+  if (layout == TPS_W_IN_OUT) {
+    *s_in = w.sr;
+    *s_out = w.sc;
+  } else {
+    *s_in = w.sc;
+    *s_out = w.sr;
+  }
+}
 
 }  // namespace tps
 
@@ -388,16 +407,6 @@ extern "C" size_t tps_mlp_workspace_bytes(int64_t T, int64_t d, int64_t F, int32
 }
 
 // A weight's logical (in, out) strides for either layout.
-static void weight_strides(const Mat& w, int layout, int64_t* s_in, int64_t* s_out) {
-  if (layout == TPS_W_IN_OUT) {
-    *s_in = w.sr;
-    *s_out = w.sc;
-  } else {
-    *s_in = w.sc;
-    *s_out = w.sr;
-  }
-}
-
 extern "C" int tps_mlp_fwd_bwd(const tps_tensor* X, const tps_tensor* W1, const tps_tensor* W2,
                                const tps_tensor* GY, int32_t tp, int32_t act, int32_t weight_layout,
                                const tps_tensor* Y, const tps_tensor* dX, const tps_tensor* dW1,

@@ -179,6 +179,7 @@ __device__ __forceinline__ void epilogue_glu_run32(const Epilogue& e, int64_t ro
 __device__ __forceinline__ void epilogue_elem(const Epilogue& e, int64_t row, int64_t col, float v) {
   if (!dbg_store_ok(e, row, col, 1)) return;
   if (e.mode == EPI_STORE || e.mode == EPI_CE_STATS) {
+    if (e.accumulate) v += static_cast<const float*>(e.d)[row * e.ldd + col];
     store_elem(e.d, e.d_dtype, row * e.ldd + col, v);
   } else if (e.mode == EPI_ACT_FWD) {
     if (e.d != nullptr) store_elem(e.d, e.d_dtype, row * e.ldd + col, v);

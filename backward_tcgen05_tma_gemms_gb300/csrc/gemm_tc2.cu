@@ -112,7 +112,8 @@ struct T2Params {
 //   T2_GLU_FWD  EPI_GLU_FWD
 //   T2_GLU_BWD  EPI_GLU_BWD
 //   T2_SEG      EPI_STORE with contraction or column segments
-enum T2Family : int { T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5 };
+//   T2_CE       EPI_CE_LSE, EPI_CE_GRAD
+enum T2Family : int { T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6 };
 
 // Shared-memory layout per family: five operand stages of 32 KB and the
 // epilogue's staging.  With four stages the mainloop measured latency-bound
@@ -127,7 +128,7 @@ enum T2Family : int { T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, 
 //                     (6 KB), single-buffered                -> 5 stages
 template <int FAM>
 struct T2Layout {
-  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG;
+  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG || FAM == T2_CE;
   static constexpr int kStages = 5;
   static constexpr bool kTwoBf16 = FAM == T2_GLU_BWD || FAM == T2_ACT16;  // two bf16 boxes per buffer
   static constexpr int kBufBytes = kStoreOnly ? TC_STG_F32_BYTES : (kTwoBf16 ? 2 * TC_STG_BF16_BYTES : T2_STG_BUF);
@@ -341,6 +342,17 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
       }
       const int row0 = m0 + q * 32;
       const int64_t row = row0 + lane;
+      // What the head cross entropy knows of this row, also before the wait.
+      float4 ce_row = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
+      int64_t ce_y = -1;
+      if constexpr (FAM == T2_CE) {
+        if (row < p.M) {
+          if (e.mode == EPI_CE_GRAD)
+            ce_row = __ldg(e.ce_rows + row);
+          else
+            ce_y = ce_row_label(e, row) - e.ce_col0;
+        }
+      }
       // The first chunk's AUX input does not depend on the accumulator: it
       // is loaded before waiting for it.
       float a_next[32];
@@ -398,6 +410,12 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             });
             if (have) e.ce_zy[row] = zy;
           }
+        }
+      }
+      if constexpr (FAM == T2_CE) {
+        if (e.mode == EPI_CE_LSE) {
+          ce_done = true;
+          if (nh0 < p.N) ce_lse_tile(e, t_row, nh0, p.N, row < p.M, row, ce_y);
         }
       }
       for (int c = 0; !ce_done && c < warp_cols / 32; ++c) {
@@ -460,14 +478,15 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
         const int n = min(32, p.N - col0);
-        if (!p.tma_store) {
+        if (FAM != T2_CE && !p.tma_store) {
           if (row < p.M) epilogue_run32(e, row, col0, n, v);
           continue;
         }
         // the fp32 and bf16 slots (store-only: one shared box), single- or double-buffered
         uint8_t* buf = stg + (L::kBufs == 2 ? (chunk & 1u) * L::kBufBytes : 0u);
+        if constexpr (FAM == T2_CE) ce_grad32(ce_row, e.ce_col0 + col0, v);
         if constexpr (FAM == T2_PLAIN) {
-          if (run > 0) {  // K split: add this run's partial tile to the output
+          if (run > 0 || e.accumulate) {  // K split (or a sum over pieces): add this partial tile to the output
             tc_store_chunk<L::kBufs - 1, true, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, a);
             ++chunk;
             continue;
@@ -565,6 +584,8 @@ static int launch_pair_family(const GemmDesc& g, const T2Maps& m, const T2Params
     if (g.epi.mode != EPI_STORE) return TPS_ERR_ARG;
     return launch_pair_majors<T2_SEG>(g, m, p, pairs, a_mn, b_mn, stream);
   }
+  if (g.epi.mode == EPI_CE_LSE || g.epi.mode == EPI_CE_GRAD)
+    return launch_pair_majors<T2_CE>(g, m, p, pairs, a_mn, b_mn, stream);
   const bool pre16 = (g.epi.mode == EPI_ACT_FWD && (g.epi.d == nullptr || g.epi.d_dtype == TPS_BF16)) ||
                      (g.epi.mode == EPI_ACT_BWD && g.epi.aux_bf16 != nullptr && g.epi.d_dtype == TPS_BF16);
   if (pre16) return launch_pair_majors<T2_ACT16>(g, m, p, pairs, a_mn, b_mn, stream);
@@ -657,7 +678,14 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   if (p.group > p.m_tiles) p.group = p.m_tiles;
   p.epi = g.epi;
   p.err = dev_err;
-  p.tma_store = tc_make_output_maps(g, &m.d[0], &m.d[1], &m.d[2]) ? 1 : 0;
+  if (g.epi.mode == EPI_CE_LSE) {  // only the statistics leave the kernel
+    p.tma_store = 0;
+  } else {
+    p.tma_store = tc_make_output_maps(g, &m.d[0], &m.d[1], &m.d[2]) ? 1 : 0;
+    if (g.epi.mode == EPI_CE_GRAD && !p.tma_store) return TPS_ERR_LAYOUT;
+    if (g.epi.accumulate && (!p.tma_store || g.epi.mode != EPI_STORE || g.epi.d_dtype != TPS_F32 || n_segs || k_segs))
+      return TPS_ERR_LAYOUT;
+  }
   if (n_segs && !p.tma_store) return TPS_ERR_LAYOUT;  // column segments leave through TMA stores only
   // K split: plain fp32 stores through TMA, at least one K tile per run
   if (g.ksplit > 1 && g.kflags != nullptr && g.epi.mode == EPI_STORE && g.epi.d_dtype == TPS_F32 && p.tma_store &&

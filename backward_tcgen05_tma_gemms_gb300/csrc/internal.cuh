@@ -39,6 +39,11 @@ constexpr uint32_t TPS_DEVERR_BOUNDS = 4u;  // debug builds: a store outside its
 //              AUX = Hg (the two-GEMM form of EPI_GLU_FWD)
 // EPI_GLU_BWD  acc = dA: D = dHg = acc * AUX2 * phi'(AUX), D2 = dU =
 //              acc * phi(AUX), with AUX = Hg and AUX2 = U (fp32)
+// Head cross entropy in pieces of the vocabulary (CTA-pair kernel only; acc
+// = logits, nothing of them is stored):
+// EPI_CE_LSE   per (row, 128-column tile) the max and the sum of
+//              e^{acc - max}, and per row the logit at its label column
+// EPI_CE_GRAD  D = bf16(g_row (e^{acc - lse_row} - [column = label_row]))
 enum EpiMode : int {
   EPI_STORE = 0,
   EPI_ACT_FWD = 1,
@@ -46,7 +51,9 @@ enum EpiMode : int {
   EPI_CE_STATS = 3,
   EPI_GLU_FWD = 4,
   EPI_GLU_UP = 5,
-  EPI_GLU_BWD = 6
+  EPI_GLU_BWD = 6,
+  EPI_CE_LSE = 7,
+  EPI_CE_GRAD = 8
 };
 
 // Width of the column tiles the CE statistics are kept for (the GEMM
@@ -92,11 +99,24 @@ struct Epilogue {
   const void* ce_labels = nullptr;  // the label of each row, int32 or int64
   int ce_label_i64 = 0;
   float* ce_zy = nullptr;           // zy[row]: the logit at the label (labels in [0, N))
+  // EPI_CE_LSE: stats[(tile * stats_ld + row) * 2 + {0, 1}], with ce_labels and
+  // ce_zy as above; column 0 of this GEMM is vocabulary entry ce_col0.
+  int64_t stats_ld = 0;
+  int64_t ce_col0 = 0;
+  const float4* ce_rows = nullptr;  // EPI_CE_GRAD: CeRow of each row
+  // EPI_STORE to fp32: add to D instead of storing (CTA-pair kernels with
+  // TMA stores, and the SIMT kernel).
+  int accumulate = 0;
   // Debug builds: the output's extent (rows, columns) and the error word the
   // bounds checks report to.
   int64_t dbg_rows = 0, dbg_cols = 0;
   uint32_t* dbg_err = nullptr;
 };
+
+// What EPI_CE_GRAD knows of a row (a float4): lse * log2(e), the upstream
+// gradient g (0: the whole row is 0, whatever the logits hold), the bits of
+// the int32 label (-1: no one-hot term) and lse itself.
+constexpr float kCeLog2e = 1.4426950408889634f;
 
 // The vocabulary CE's gradient as the A operand of the dHidden GEMM, formed
 // from the logits GEMM's shifted bf16 logits as their tiles arrive in

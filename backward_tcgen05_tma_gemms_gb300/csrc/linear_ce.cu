@@ -1,0 +1,600 @@
+// linear_ce.cu -- softmax cross entropy of a vocabulary head without keeping
+// its logits, in pieces of the vocabulary.
+//
+//   z = h W,  lse_t = log sum_j e^{z_tj},  loss_t = lse_t - z_{t,y_t}
+//   dz_tj = g_t (e^{z_tj - lse_t} - 1[j = y_t]),  dh = dz W^T,  dW = h^T dz
+//
+// ("多卡张量：拆开计算，再合回同一结果", 04 / VOCABULARY SHARDS gives the loss
+// and dz over shards of the vocabulary: the maxima and sums of the pieces are
+// what has to be combined, never the logits.)
+//
+// Forward, bf16: one tensor-core GEMM whose epilogue reduces each row's 128
+// columns to (max, sum of e^{z - max}) while they are in tensor memory
+// (EPI_CE_LSE), so T x V logits become T x V / 128 pairs, and one kernel that
+// joins the pairs of a row.  2 T d V operations; the pairs are 1/32 of what
+// bf16 logits would be.
+//
+// Backward, bf16: nothing but lse is kept, so each piece of the vocabulary
+// has its logits formed again, and the epilogue turns them into dz at once
+// (EPI_CE_GRAD: one exponential and one product an element; dz leaves as
+// bf16, the type in which the tensor cores take it).  The piece is then the
+// K-major operand of dh += dz W_piece^T, summed over the pieces in fp32 by
+// TMA reductions in piece order, and the MN-major operand of dW_piece.
+// 8 T d V operations against the 6 T d V of a backward pass that is given
+// the logits: the quarter more is what not keeping them costs.
+//
+// Other operands (fp32, or bf16 that TMA cannot describe) run the same
+// pieces through the fp32-FMA GEMM, with the logits of one piece in fp32.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdlib>
+
+#include "api_common.cuh"
+#include "ptx.cuh"
+
+namespace tps {
+
+namespace {
+
+constexpr int64_t kRowBlock = 65536;       // rows of one forward GEMM: bounds the pairs' workspace
+constexpr int64_t kPieceStep = 256;        // pieces start on whole pair tiles
+constexpr int64_t kPieceBytes = 512ll << 20;  // one piece of dz by default
+
+struct Labels {
+  const void* p;
+  int i64;
+  int64_t ignore;
+  int64_t vreal;
+  __device__ int64_t at(int64_t t) const {
+    return i64 ? static_cast<const int64_t*>(p)[t] : static_cast<int64_t>(static_cast<const int32_t*>(p)[t]);
+  }
+  // 0: a supervised label in [0, vreal); 1: ignore_index; 2: invalid.
+  __device__ int kind(int64_t y) const {
+    if (ignore != TPS_NO_IGNORE && y == ignore) return 1;
+    return y >= 0 && y < vreal ? 0 : 2;
+  }
+};
+
+// (m, s) += (m2, s2); (-inf, 0) is empty, a NaN in either s stays.
+__device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
+  const float M = fmaxf(m, m2);
+  if (M == -INFINITY) {
+    s += s2;
+    return;
+  }
+  s = (m == -INFINITY ? s : s * ex2_approx((m - M) * kCeLog2e)) +
+      (m2 == -INFINITY ? s2 : s2 * ex2_approx((m2 - M) * kCeLog2e));
+  m = M;
+}
+
+// lse and loss of 32 rows from their pairs, pairs[tile * ld + row]: lane =
+// row, each warp a run of tiles (consecutive rows are consecutive in memory,
+// so every load of a warp is one 256-byte line pair), then the 32 partial
+// pairs of a row in warp order.  At T = 8192 this reads 66 MB.
+constexpr int kJoinWarps = 32;
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    ce_join_kernel(const float2* pairs, int64_t ld, int64_t tiles, int64_t rows, int64_t row0, const float* zy,
+                   Labels lab, float* loss, float* lse, uint32_t* err) {
+  __shared__ float2 part[kJoinWarps][33];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
+  float m = -INFINITY, s = 0.0f;
+  if (r < rows) {
+#pragma unroll 4
+    for (int64_t i = w; i < tiles; i += kJoinWarps) {
+      const float2 e = __ldg(pairs + i * ld + r);
+      join(m, s, e.x, e.y);
+    }
+  }
+  part[w][lane] = make_float2(m, s);
+  __syncthreads();
+  if (w != 0 || r >= rows) return;
+  m = -INFINITY;
+  s = 0.0f;
+  for (int i = 0; i < kJoinWarps; ++i) join(m, s, part[i][lane].x, part[i][lane].y);
+  const int64_t t = row0 + r;
+  const float l = m + logf(s);
+  lse[t] = l;
+  const int kind = lab.kind(lab.at(t));
+  loss[t] = kind == 1 ? 0.0f : (kind == 0 ? l - zy[r] : __int_as_float(0x7fc00000));
+  if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
+}
+
+// Sum over a block of 1024 threads, to thread 0.
+template <class V>
+__device__ __forceinline__ V block_sum(V x, V* red) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = x;
+  __syncthreads();
+  V total = 0;
+  if (threadIdx.x == 0)
+    for (int i = 0; i < 32; ++i) total += red[i];
+  return total;
+}
+
+// One block: the reduced loss, sum or mean, summed in fp64 in a fixed order.
+__global__ void __launch_bounds__(1024) ce_total_kernel(const float* loss, int64_t T, Labels lab, int reduction,
+                                                        double denominator, float* out) {
+  __shared__ double red[32];
+  __shared__ int64_t redi[32];
+  double acc = 0.0;
+  int64_t n = 0;
+  for (int64_t t = threadIdx.x; t < T; t += 1024) {
+    acc += loss[t];
+    if (reduction == TPS_REDUCE_MEAN && denominator == 0.0) n += lab.kind(lab.at(t)) == 0;
+  }
+  acc = block_sum(acc, red);
+  n = block_sum(n, redi);
+  if (threadIdx.x == 0) {
+    double D = 1.0;
+    if (reduction == TPS_REDUCE_MEAN) D = denominator > 0.0 ? denominator : (n > 0 ? double(n) : 1.0);
+    *out = static_cast<float>(acc / D);
+  }
+}
+
+// What the gradient epilogue knows of each row (Epilogue::ce_rows).  A mean
+// over this call's labels needs their count first: one block then does both,
+// else the rows are spread over blocks.
+__global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, const float* lse, const float* g,
+                                                       int64_t g_step, int reduction, double denominator,
+                                                       float4* rows, uint32_t* err) {
+  __shared__ int64_t redi[32];
+  __shared__ float share;
+  if (reduction == TPS_REDUCE_MEAN && denominator == 0.0) {  // one block
+    int64_t n = 0;
+    for (int64_t t = threadIdx.x; t < T; t += 1024) n += lab.kind(lab.at(t)) == 0;
+    n = block_sum(n, redi);
+    if (threadIdx.x == 0) share = static_cast<float>(1.0 / (n > 0 ? double(n) : 1.0));
+  } else if (threadIdx.x == 0) {
+    share = reduction == TPS_REDUCE_MEAN ? static_cast<float>(1.0 / denominator) : 1.0f;
+  }
+  __syncthreads();
+  for (int64_t t = blockIdx.x * int64_t(1024) + threadIdx.x; t < T; t += int64_t(gridDim.x) * 1024) {
+    const int64_t y = lab.at(t);
+    const int kind = lab.kind(y);
+    if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
+    const float up = g == nullptr ? 1.0f : g[t * g_step];
+    const float l = lse[t];
+    rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : up * share,
+                          __int_as_float(kind == 0 ? static_cast<int>(y) : -1), l);
+  }
+}
+
+// fp32 logits of a piece: the pair of each row (one block a row).
+__global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* z, int64_t ld, int64_t n, int64_t col0,
+                                                             Labels lab, float2* pairs, float* zy) {
+  __shared__ float2 part[8];
+  const int64_t t = blockIdx.x;
+  const float* row = z + t * ld;
+  float m = -INFINITY, s = 0.0f;
+  for (int64_t j = threadIdx.x; j < n; j += 256) m = fmaxf(m, row[j]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  for (int64_t j = threadIdx.x; j < n; j += 256) s += m == -INFINITY && row[j] == m ? 0.0f : expf(row[j] - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  float M = -INFINITY, S = 0.0f;
+  for (int i = 0; i < 8; ++i) {  // accurate exponentials here: this path serves fp32
+    const float2 e = part[i];
+    const float N = fmaxf(M, e.x);
+    S = N == -INFINITY ? S + e.y : (M == -INFINITY ? S : S * expf(M - N)) + (e.x == -INFINITY ? e.y : e.y * expf(e.x - N));
+    M = N;
+  }
+  pairs[t] = make_float2(M, S);
+  const int64_t y = lab.at(t);
+  if (lab.kind(y) == 0 && y >= col0 && y < col0 + n) zy[t] = row[y - col0];
+}
+
+// fp32 logits of a piece to dz, in place or as bf16.
+template <class Out>
+__global__ void __launch_bounds__(256) ce_piece_grad_kernel(const float* z, int64_t ld, int64_t n, int64_t col0,
+                                                            const float4* rows, Out* dz, int64_t ldd) {
+  const int64_t t = blockIdx.x;
+  const float4 r = rows[t];
+  const int64_t y = static_cast<int64_t>(__float_as_int(r.z)) - col0;
+  for (int64_t j = threadIdx.x; j < n; j += 256) {
+    const float p = r.y == 0.0f ? 0.0f : r.y * (expf(z[t * ld + j] - r.w) - (j == y ? 1.0f : 0.0f));
+    if constexpr (sizeof(Out) == 4)
+      dz[t * ldd + j] = p;
+    else
+      dz[t * ldd + j] = __float2bfloat16_rn(p);
+  }
+}
+
+// The fp32 sum over pieces to the caller's dHidden.
+__global__ void __launch_bounds__(256) ce_convert_kernel(const float* a, int64_t lda, void* out, int dtype, int64_t rows,
+                                                         int64_t cols, int64_t sr, int64_t sc, int vec) {
+  if (vec) {  // 8 columns a thread, rows of whole 16-byte runs
+    const int64_t per = cols / 8;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+      const int64_t r = i / per, c = (i % per) * 8;
+      const float4 x = *reinterpret_cast<const float4*>(a + r * lda + c);
+      const float4 y = *reinterpret_cast<const float4*>(a + r * lda + c + 4);
+      __nv_bfloat162 b[4] = {__floats2bfloat162_rn(x.x, x.y), __floats2bfloat162_rn(x.z, x.w),
+                             __floats2bfloat162_rn(y.x, y.y), __floats2bfloat162_rn(y.z, y.w)};
+      *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + r * sr + c) = *reinterpret_cast<uint4*>(b);
+    }
+    return;
+  }
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < rows * cols; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / cols, c = i % cols;
+    const float x = a[r * lda + c];
+    if (dtype == TPS_F32)
+      static_cast<float*>(out)[r * sr + c * sc] = x;
+    else
+      static_cast<__nv_bfloat16*>(out)[r * sr + c * sc] = __float2bfloat16_rn(x);
+  }
+}
+
+// ------------------------------------------------------------------ host
+
+struct Call {  // what both directions check alike
+  Mat h, w;
+  int64_t T = 0, d = 0, V = 0, vreal = 0, w_in = 0, w_out = 0;
+  int dt = 0;
+  Labels lab = {};
+  int reduction = TPS_REDUCE_NONE;
+  double denominator = 0.0;
+};
+
+int check_call(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels, int32_t layout,
+               const tps_ce_options* o, Call* c) {
+  int rc;
+  if ((rc = as_mat(h, "h", true, &c->h)) || (rc = as_mat(Whead, "Whead", false, &c->w))) return rc;
+  if (layout != TPS_W_IN_OUT && layout != TPS_W_OUT_IN) return fail(TPS_ERR_ARG, "unknown weight layout %d", layout);
+  const bool io = layout == TPS_W_IN_OUT;
+  c->T = c->h.rows;
+  c->d = c->h.cols;
+  c->V = io ? c->w.cols : c->w.rows;
+  if ((io ? c->w.rows : c->w.cols) != c->d)
+    return fail(TPS_ERR_SHAPE, "Whead does not match h's width %lld", (long long)c->d);
+  if (c->V < 1 || c->d < 1) return fail(TPS_ERR_SHAPE, "empty vocabulary or width");
+  if (c->V >= (1ll << 31) || c->T >= (1ll << 31) || c->d >= (1ll << 31))
+    return fail(TPS_ERR_SHAPE, "an extent of 2^31 or more");
+  c->dt = c->h.dtype;
+  if ((c->dt != TPS_F32 && c->dt != TPS_BF16) || c->w.dtype != c->dt)
+    return fail(TPS_ERR_DTYPE, "h and Whead must share f32 or bf16");
+  if (labels == nullptr) return fail(TPS_ERR_ARG, "labels missing");
+  if (labels->dtype != TPS_I64 && labels->dtype != TPS_I32) return fail(TPS_ERR_DTYPE, "labels must be i32 or i64");
+  if ((rc = expect_vector(labels, "labels", labels->dtype, c->T))) return rc;
+  weight_strides(c->w, layout, &c->w_in, &c->w_out);
+  c->vreal = c->V;
+  int64_t ignore = TPS_NO_IGNORE;
+  if (o != nullptr) {
+    if (o->vocab_size < 0 || o->vocab_size > c->V)
+      return fail(TPS_ERR_SHAPE, "vocab_size %lld outside [0, %lld]", (long long)o->vocab_size, (long long)c->V);
+    if (o->vocab_size > 0) c->vreal = o->vocab_size;
+    if (o->reduction != TPS_REDUCE_NONE && o->reduction != TPS_REDUCE_SUM && o->reduction != TPS_REDUCE_MEAN)
+      return fail(TPS_ERR_ARG, "unknown reduction %d", o->reduction);
+    if (!(o->denominator >= 0.0) || !std::isfinite(o->denominator))
+      return fail(TPS_ERR_ARG, "denominator must be finite and >= 0");
+    if (o->reserved != 0) return fail(TPS_ERR_ARG, "reserved must be 0");
+    ignore = o->ignore_index;
+    c->reduction = o->reduction;
+    c->denominator = o->denominator;
+  }
+  c->lab = Labels{labels->data, labels->dtype == TPS_I64 ? 1 : 0, ignore, c->vreal};
+  return TPS_OK;
+}
+
+// The logits GEMM of rows [r0, r0 + rows) and vocabulary columns [v0, v0 + n).
+GemmDesc logits_gemm(const Call& c, int64_t r0, int64_t rows, int64_t v0, int64_t n) {
+  const int64_t es = c.dt == TPS_F32 ? 4 : 2;
+  GemmDesc g;
+  g.M = rows; g.N = n; g.K = c.d; g.in_dtype = c.dt;
+  g.a = static_cast<const char*>(c.h.data) + r0 * c.h.sr * es; g.a_sm = c.h.sr; g.a_sk = c.h.sc;
+  g.b = static_cast<const char*>(c.w.data) + v0 * c.w_out * es; g.b_sk = c.w_in; g.b_sn = c.w_out;
+  return g;
+}
+
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// Columns of one piece that fit into `room` bytes at `row_bytes` per column.
+int64_t piece_columns(int64_t V, int64_t room, int64_t column_bytes) {
+  const int64_t most = round_up(V, kPieceStep);
+  const int64_t fit = column_bytes > 0 ? room / column_bytes / kPieceStep * kPieceStep : most;
+  return fit < most ? fit : most;
+}
+
+// Bytes of a piece's buffers per vocabulary column: bf16 dz on the tensor
+// cores; else fp32 logits, and beside them bf16 dz for bf16 operands.
+int64_t column_bytes(int64_t T, int dtype, bool tc, bool backward) {
+  if (tc) return backward ? 2 * T : 0;
+  return 4 * T + (backward && dtype == TPS_BF16 ? 2 * T : 0);
+}
+
+struct Fixed {  // workspace before the pieces
+  size_t pairs, zy, rows, flags, acc, pieces;
+};
+Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool tc, bool backward) {
+  Fixed f = {};
+  size_t at = 0;
+  auto take = [&at](int64_t bytes) {
+    const size_t p = at;
+    at += align256(static_cast<size_t>(bytes));
+    return p;
+  };
+  if (!backward) {
+    const int64_t rows = T < kRowBlock ? T : kRowBlock;
+    const int64_t per_row = tc ? (V + kStatsTileN - 1) / kStatsTileN : (V + kPieceStep - 1) / kPieceStep;
+    f.pairs = take(8 * per_row * (tc ? rows : T));
+    f.zy = take(4 * T);
+  } else {
+    f.rows = take(16 * T);
+    f.flags = take(4 * (pair_tile_count(T, d) + 1));
+    f.acc = take(4 * T * round_up(d, 4));
+  }
+  f.pieces = at;
+  return f;
+}
+
+// K split of the dh GEMM over a piece: as many runs as bring the (tile, run)
+// units nearest to whole waves of the CTA pairs, each run at least 32 K tiles.
+int split_runs(int64_t tiles, int64_t k_tiles) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 1;
+  const int64_t pairs = sms / 2;
+  if (pairs < 1 || tiles < 1) return 1;
+  int best = 1;
+  double best_fill = 0.0;
+  for (int runs = 1; runs <= 16 && (runs == 1 || k_tiles / runs >= 32); ++runs) {
+    const int64_t units = tiles * runs, waves = (units + pairs - 1) / pairs;
+    const double fill = double(units) / double(waves * pairs);
+    if (fill > best_fill * 1.05) {  // another run costs one more read and write of the output
+      best = runs;
+      best_fill = fill;
+    }
+  }
+  return best;
+}
+
+int launched(const char* what) {
+  note_launch();
+  const cudaError_t e = cudaPeekAtLastError();
+  return e == cudaSuccess ? TPS_OK : fail(TPS_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(cudaGetLastError()));
+}
+
+}  // namespace
+
+}  // namespace tps
+
+using namespace tps;
+
+extern "C" size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dtype, int32_t backward,
+                                                int64_t piece) {
+  if (T < 0 || d < 1 || V < 1 || piece < 0 || (dtype != TPS_F32 && dtype != TPS_BF16)) return 0;
+  const bool tc = dtype == TPS_BF16;
+  // The bytes for fp32 also serve bf16 operands outside the tensor cores' reach.
+  const int64_t per = column_bytes(T, TPS_BF16, tc, backward != 0);
+  int64_t cols = piece > 0 ? round_up(piece < V ? piece : V, kPieceStep)
+                           : piece_columns(V, kPieceBytes > kPieceStep * per ? kPieceBytes : kPieceStep * per, per);
+  return fixed_layout(T, d, V, tc, backward != 0).pieces + align256(static_cast<size_t>(per) * cols) + 512;
+}
+
+extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels,
+                                 int32_t weight_layout, const tps_ce_options* options, const tps_tensor* loss,
+                                 const tps_tensor* loss_reduced, const tps_tensor* lse, void* workspace,
+                                 size_t workspace_bytes, void* cuda_stream) {
+  clear_detail();
+  Call c;
+  int rc;
+  if ((rc = check_call(h, Whead, labels, weight_layout, options, &c))) return rc;
+  if ((rc = expect_vector(loss, "loss", TPS_F32, c.T)) || (rc = expect_vector(lse, "lse", TPS_F32, c.T))) return rc;
+  float* total = nullptr;
+  if (loss_reduced != nullptr && loss_reduced->data != nullptr) {
+    if ((rc = expect_vector(loss_reduced, "loss_reduced", TPS_F32, 1))) return rc;
+    total = static_cast<float*>(loss_reduced->data);
+  }
+  if (c.reduction == TPS_REDUCE_NONE) total = nullptr;
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  if (c.T == 0) {
+    if (total != nullptr && cudaMemsetAsync(total, 0, sizeof(float), s) != cudaSuccess)
+      return fail(TPS_ERR_CUDA, "memset failed");
+    return TPS_OK;
+  }
+  GemmDesc g = logits_gemm(c, 0, c.T, 0, c.vreal);
+  const bool tc = gemm_tc_supported(g);
+  const Fixed f = fixed_layout(c.T, c.d, c.V, tc, false);
+  const int64_t per = column_bytes(c.T, c.dt, tc, false);
+  const size_t least = f.pieces + static_cast<size_t>(kPieceStep * per) + 256;
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < least)
+    return fail(TPS_ERR_WORKSPACE, "workspace needs at least %zu bytes, 256-byte aligned", least);
+  uint32_t* err = device_error_word();
+  if (err == nullptr) return fail(TPS_ERR_CUDA, "cannot resolve the device error word");
+  char* ws = static_cast<char*>(workspace);
+  float2* pairs = reinterpret_cast<float2*>(ws + f.pairs);
+  float* zy = reinterpret_cast<float*>(ws + f.zy);
+  float* loss_p = static_cast<float*>(loss->data);
+  float* lse_p = static_cast<float*>(lse->data);
+  if (tc) {
+    const int64_t tiles = (c.vreal + kStatsTileN - 1) / kStatsTileN;
+    const int64_t es = c.lab.i64 ? 8 : 4;
+    for (int64_t r0 = 0; r0 < c.T; r0 += kRowBlock) {
+      const int64_t rows = c.T - r0 < kRowBlock ? c.T - r0 : kRowBlock;
+      g = logits_gemm(c, r0, rows, 0, c.vreal);
+      g.name = "lce_logits";
+      g.epi.mode = EPI_CE_LSE;
+      g.epi.stats = reinterpret_cast<float*>(pairs);
+      g.epi.stats_ld = rows;
+      g.epi.ce_labels = static_cast<const char*>(c.lab.p) + r0 * es;
+      g.epi.ce_label_i64 = c.lab.i64;
+      g.epi.ce_zy = zy + r0;
+      if ((rc = run_gemm(g, c.vreal, 1, s))) return rc;
+      ProfScope prof("ce_join", "lce", 0.0, 8.0 * double(rows) * double(tiles), s);
+      ce_join_kernel<<<static_cast<unsigned>((rows + 31) / 32), 32 * kJoinWarps, 0, s>>>(
+          pairs, rows, tiles, rows, r0, zy + r0, c.lab, loss_p, lse_p, err);
+      if ((rc = launched("ce_join"))) return rc;
+    }
+  } else {
+    float* z = reinterpret_cast<float*>(ws + f.pieces);
+    const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
+    int64_t n_pieces = 0;
+    for (int64_t v0 = 0; v0 < c.vreal; v0 += cols, ++n_pieces) {
+      const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
+      g = logits_gemm(c, 0, c.T, v0, n);
+      g.name = "lce_logits";
+      g.epi.d = z;
+      if ((rc = run_gemm(g, cols, 1, s))) return rc;
+      ProfScope prof("ce_piece_stats", "lce", 0.0, 4.0 * double(c.T) * double(n), s);
+      ce_piece_stats_kernel<<<static_cast<unsigned>(c.T), 256, 0, s>>>(z, cols, n, v0, c.lab, pairs + n_pieces * c.T, zy);
+      if ((rc = launched("ce_piece_stats"))) return rc;
+    }
+    ce_join_kernel<<<static_cast<unsigned>((c.T + 31) / 32), 32 * kJoinWarps, 0, s>>>(
+        pairs, c.T, n_pieces, c.T, 0, zy, c.lab, loss_p, lse_p, err);
+    if ((rc = launched("ce_join"))) return rc;
+  }
+  if (total != nullptr) {
+    ce_total_kernel<<<1, 1024, 0, s>>>(loss_p, c.T, c.lab, c.reduction, c.denominator, total);
+    if ((rc = launched("ce_total"))) return rc;
+  }
+  return TPS_OK;
+}
+
+extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels,
+                                 const tps_tensor* lse, const tps_tensor* grad_loss, int32_t weight_layout,
+                                 const tps_ce_options* options, const tps_tensor* dHidden, const tps_tensor* dWhead,
+                                 void* workspace, size_t workspace_bytes, void* cuda_stream) {
+  clear_detail();
+  Call c;
+  int rc;
+  if ((rc = check_call(h, Whead, labels, weight_layout, options, &c))) return rc;
+  if ((rc = expect_vector(lse, "lse", TPS_F32, c.T))) return rc;
+  const float* up = nullptr;
+  int64_t up_step = 0;
+  if (grad_loss != nullptr && grad_loss->data != nullptr) {
+    const bool per_token = c.reduction == TPS_REDUCE_NONE;
+    if ((rc = expect_vector(grad_loss, "grad_loss", TPS_F32, per_token ? c.T : 1))) return rc;
+    up = static_cast<const float*>(grad_loss->data);
+    up_step = per_token ? 1 : 0;
+  }
+  Mat dh, dw;
+  const bool want_dh = dHidden != nullptr, want_dw = dWhead != nullptr;
+  if (want_dh) {
+    if ((rc = as_mat(dHidden, "dHidden", true, &dh)) || (rc = expect(dh, "dHidden", c.T, c.d))) return rc;
+    if (dh.dtype != TPS_F32 && dh.dtype != TPS_BF16) return fail(TPS_ERR_DTYPE, "dHidden must be f32 or bf16");
+  }
+  int64_t dw_in = 0, dw_out = 0;
+  if (want_dw) {
+    if ((rc = as_mat(dWhead, "dWhead", false, &dw)) || (rc = expect(dw, "dWhead", c.w.rows, c.w.cols))) return rc;
+    if (dw.dtype != TPS_F32 && dw.dtype != TPS_BF16) return fail(TPS_ERR_DTYPE, "dWhead must be f32 or bf16");
+    weight_strides(dw, weight_layout, &dw_in, &dw_out);
+  }
+  if (!want_dh && !want_dw) return fail(TPS_ERR_ARG, "neither dHidden nor dWhead is wanted");
+  cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
+  const int64_t dw_es = dw.dtype == TPS_F32 ? 4 : 2;
+  if (want_dw && (c.T == 0 || c.vreal < c.V)) {  // columns that no token reaches
+    const int64_t v0 = c.T == 0 ? 0 : c.vreal;
+    if ((rc = launch_fill(static_cast<char*>(dw.data) + v0 * dw_out * dw_es, dw.dtype, c.d, c.V - v0, dw_in, dw_out, s)))
+      return rc;
+  }
+  if (c.T == 0) return TPS_OK;
+
+  // Both the logits and the two products with dz have to be within reach of
+  // the tensor cores: their operands are h, Whead and this call's own dz.
+  GemmDesc probe = logits_gemm(c, 0, c.T, 0, c.vreal);
+  bool tc = gemm_tc_supported(probe);
+  const Fixed f = fixed_layout(c.T, c.d, c.V, tc, true);
+  const int64_t per = column_bytes(c.T, c.dt, tc, true);
+  const size_t least = f.pieces + static_cast<size_t>(kPieceStep * per) + 256;  // 256: between the two buffers of a piece
+  if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < least)
+    return fail(TPS_ERR_WORKSPACE, "workspace needs at least %zu bytes, 256-byte aligned", least);
+  uint32_t* err = device_error_word();
+  if (err == nullptr) return fail(TPS_ERR_CUDA, "cannot resolve the device error word");
+  char* ws = static_cast<char*>(workspace);
+  float4* rows = reinterpret_cast<float4*>(ws + f.rows);
+  uint32_t* flags = reinterpret_cast<uint32_t*>(ws + f.flags);
+  const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
+
+  {
+    const bool count = c.reduction == TPS_REDUCE_MEAN && c.denominator == 0.0;
+    const int64_t blocks = count ? 1 : (c.T + 1023) / 1024;
+    ce_rows_kernel<<<static_cast<unsigned>(blocks < 1024 ? blocks : 1024), 1024, 0, s>>>(
+        c.T, c.lab, static_cast<const float*>(lse->data), up, up_step, c.reduction, c.denominator, rows, err);
+    if ((rc = launched("ce_rows"))) return rc;
+  }
+  // dh is summed over the pieces in fp32: in the caller's buffer where that
+  // is fp32 rows that TMA can add to, else in the workspace.
+  float* acc = reinterpret_cast<float*>(ws + f.acc);
+  int64_t ld_acc = round_up(c.d, 4);
+  const bool direct = want_dh && dh.dtype == TPS_F32 && dh.sc == 1 &&
+                      (reinterpret_cast<uintptr_t>(dh.data) & 15u) == 0 && dh.sr % 4 == 0 && dh.sr >= c.d;
+  if (direct) {
+    acc = static_cast<float*>(dh.data);
+    ld_acc = dh.sr;
+  }
+  char* piece = ws + f.pieces;
+  const int64_t es = c.dt == TPS_F32 ? 4 : 2;
+  float* z = reinterpret_cast<float*>(piece);                                   // other operands: fp32 logits
+  char* dz = tc || c.dt == TPS_F32 ? piece : piece + align256(4 * c.T * cols);  // dz, operand dtype
+  for (int64_t v0 = 0; v0 < c.vreal; v0 += cols) {
+    const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
+    GemmDesc g = logits_gemm(c, 0, c.T, v0, n);
+    g.name = "lce_dlogits";
+    if (tc) {
+      g.epi.mode = EPI_CE_GRAD;
+      g.epi.d = dz; g.epi.d_dtype = TPS_BF16;
+      g.epi.ce_rows = rows;
+      g.epi.ce_col0 = v0;
+      if ((rc = run_gemm(g, cols, 1, s))) return rc;
+    } else {
+      g.epi.d = z;
+      if ((rc = run_gemm(g, cols, 1, s))) return rc;
+      ProfScope prof("ce_piece_grad", "lce", 0.0, 8.0 * double(c.T) * double(n), s);
+      if (c.dt == TPS_F32)
+        ce_piece_grad_kernel<float><<<static_cast<unsigned>(c.T), 256, 0, s>>>(z, cols, n, v0, rows, z, cols);
+      else
+        ce_piece_grad_kernel<__nv_bfloat16><<<static_cast<unsigned>(c.T), 256, 0, s>>>(
+            z, cols, n, v0, rows, reinterpret_cast<__nv_bfloat16*>(dz), cols);
+      if ((rc = launched("ce_piece_grad"))) return rc;
+    }
+    if (want_dh) {  // dh += dz W_piece^T
+      GemmDesc q;
+      q.name = "lce_dhidden";
+      q.M = c.T; q.N = c.d; q.K = n; q.in_dtype = c.dt;
+      q.a = dz; q.a_sm = cols; q.a_sk = 1;
+      q.b = static_cast<const char*>(c.w.data) + v0 * c.w_out * es; q.b_sk = c.w_out; q.b_sn = c.w_in;
+      q.epi.d = acc; q.epi.ldd = ld_acc;
+      q.epi.accumulate = v0 > 0;
+      q.wide = true;
+      q.wide = gemm_wide_supported(q);
+      if (tc) {
+        const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
+        if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles + 1) * sizeof(uint32_t), s) != cudaSuccess)
+          return fail(TPS_ERR_CUDA, "memset failed");
+        q.ksplit = split_runs(tiles, (n + 63) / 64);
+        q.kflags = flags;
+        q.unit_counter = flags + tiles;
+      }
+      if ((rc = run_gemm(q, ld_acc, 1, s))) return rc;
+    }
+    if (want_dw) {  // dW_piece = h^T dz
+      GemmDesc q;
+      q.name = "lce_dwhead";
+      q.M = c.d; q.N = n; q.K = c.T; q.in_dtype = c.dt;
+      q.a = c.h.data; q.a_sm = c.h.sc; q.a_sk = c.h.sr;
+      q.b = dz; q.b_sk = cols; q.b_sn = 1;
+      q.epi.d = static_cast<char*>(dw.data) + v0 * dw_out * dw_es; q.epi.d_dtype = dw.dtype;
+      if ((rc = run_gemm(q, dw_in, dw_out, s))) return rc;
+    }
+  }
+  if (want_dh && !direct) {
+    const bool vec = dh.dtype == TPS_BF16 && dh.sc == 1 && c.d % 8 == 0 && dh.sr % 8 == 0 &&
+                     (reinterpret_cast<uintptr_t>(dh.data) & 15u) == 0;
+    const int64_t items = vec ? c.T * c.d / 8 : c.T * c.d;
+    const int64_t blocks = (items + 255) / 256;
+    ProfScope prof("ce_convert", "lce", 0.0, 6.0 * double(c.T) * double(c.d), s);
+    ce_convert_kernel<<<static_cast<unsigned>(blocks < 4096 ? blocks : 4096), 256, 0, s>>>(
+        acc, ld_acc, dh.data, dh.dtype, c.T, c.d, dh.sr, dh.sc, vec ? 1 : 0);
+    if ((rc = launched("ce_convert"))) return rc;
+  }
+  return TPS_OK;
+}

@@ -349,6 +349,69 @@ __device__ __forceinline__ void ce_stats_tile(const Epilogue& e, uint32_t t_col,
   if (row_ok) st.flush(e, row, tc0 / kStatsTileN);
 }
 
+// EPI_CE_LSE over the statistics tile that starts at column tc0 (TMEM address
+// t_col), for the row this thread owns (label y relative to column 0, or
+// negative): one read of the accumulator, 32 columns at a time, with the
+// running maximum m and the sum s of e^{z - m}, which is rescaled whenever m
+// grows.  Nothing is stored but (m, s) and, where the label lies here, its
+// logit.  A tile of -inf leaves (-inf, 0); a NaN makes s NaN.
+__device__ __forceinline__ void ce_lse_tile(const Epilogue& e, uint32_t t_col, int64_t tc0, int64_t N, bool row_ok,
+                                            int64_t row, int64_t y) {
+  constexpr int kChunks = kStatsTileN / 32;
+  const int chunks = static_cast<int>((N - tc0) / 32 < kChunks ? (N - tc0 + 31) / 32 : kChunks);
+  float m = -INFINITY, s = 0.0f, zy = 0.0f;
+  bool have = false;
+  for (int c = 0; c < chunks; ++c) {
+    uint32_t r[32];
+    tmem_ld_32x32b_x32(t_col + c * 32, r);
+    tmem_ld_wait();
+    float v[32];
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+    const int64_t col0 = tc0 + 32 * c;
+    const int n = static_cast<int>(N - col0 < 32 ? N - col0 : 32);
+    if (n < 32) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i >= n) v[i] = -INFINITY;
+    }
+    const int64_t dy = y - col0;
+    if (dy >= 0 && dy < n) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i == dy) zy = v[i];
+      have = true;
+    }
+    const float cm = ce_max32(v);
+    if (!(cm <= m)) {
+      s = m == -INFINITY ? s : s * ex2_approx((m - cm) * kTcLog2e);
+      m = cm;
+    }
+    if (m != -INFINITY) s += ce_sum32(v, m);
+  }
+  if (!row_ok) return;
+  const int64_t tile = tc0 / kStatsTileN;
+  if (dbg_store_ok(e, row, tc0, 1)) reinterpret_cast<float2*>(e.stats)[tile * e.stats_ld + row] = make_float2(m, s);
+  if (have) e.ce_zy[row] = zy;
+}
+
+// EPI_CE_GRAD of 32 columns from col0: v becomes g (e^{v - lse} - [column = label]).
+__device__ __forceinline__ void ce_grad32(float4 row, int64_t col0, float (&v)[32]) {
+  const float g = row.y;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(v[i], kTcLog2e, -row.x)) * g;
+  const int64_t dy = static_cast<int64_t>(__float_as_int(row.z)) - col0;
+  if (dy >= 0 && dy < 32) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i == dy) v[i] -= g;
+  }
+  if (g == 0.0f) {  // an unsupervised token: 0 even where the logits are not finite
+#pragma unroll
+    for (int i = 0; i < 32; ++i) v[i] = 0.0f;
+  }
+}
+
 // ---- work units of a CTA pair ---------------------------------------------
 // The units one role of a CTA pair processes, in order.  Static: pair p
 // takes units p, p + pairs, p + 2 pairs, ...  Dynamic (a zeroed global

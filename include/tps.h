@@ -361,6 +361,50 @@ int tps_vocab_ce_fwd_bwd_ex(const tps_tensor* h, const tps_tensor* Whead, const 
                             size_t workspace_bytes, void* cuda_stream);
 
 /* ------------------------------------------------------------------------
+ * tps_linear_ce_fwd / tps_linear_ce_bwd -- the vocabulary cross-entropy
+ * without the logits: z = h Whead is formed in pieces of the vocabulary and
+ * only the log-sum-exp of each token is kept from the forward to the
+ * backward call (tps_vocab_ce_fwd_bwd keeps T x V logits and returns
+ * T x V dlogits).  [MC] "04 / VOCABULARY SHARDS" gives the combination of
+ * the pieces' maxima and sums and the gradient of the logits.
+ *   lse_t = log sum_{j < vocab} e^{z_tj},  loss_t = lse_t - z_{t, y_t};
+ *   dz_tj = g_t (e^{z_tj - lse_t} - 1[j = y_t]) (formed again from h and
+ *   Whead, piece by piece; bf16 for bf16 operands),
+ *   dHidden = dz Whead^T (summed over the pieces in fp32),
+ *   dWhead = h^T dz.
+ * h (..., d) and Whead (d x V, or V x d for TPS_W_OUT_IN): both F32 or both
+ * BF16.  labels (T): I64 or I32.  loss, lse: T contiguous floats;
+ * loss_reduced: one f32 or NULL.  options (NULL: defaults) as
+ * tps_vocab_ce_fwd_bwd_ex: vocabulary padding (columns at or beyond
+ * vocab_size are not read, their dWhead is 0), ignore_index (loss 0 and
+ * dz 0), reduction and denominator.
+ * Backward: lse from the forward call with the same arguments.  grad_loss
+ * (NULL: ones): the upstream gradient, T floats for TPS_REDUCE_NONE (one for
+ * each token's loss), one float for a sum or a mean (which also divides by
+ * its denominator, or by the number of supervised labels).  dHidden and
+ * dWhead: F32 or BF16; either may be NULL.
+ * A label that is neither in [0, vocab) nor ignore_index makes its loss NaN,
+ * has no one-hot term in dz, and sets TPS_ERR_LABEL in the device error word.
+ * `workspace`: 256-byte aligned.  tps_linear_ce_workspace_bytes gives what a
+ * call needs for pieces of `piece` columns (rounded up to 256; 0: pieces of
+ * about 512 MB); a call takes pieces as large as its workspace holds and
+ * refuses one that does not hold 256 columns (TPS_ERR_WORKSPACE).  bf16
+ * operands that TMA cannot describe (a base or a row pitch that is not a
+ * multiple of 16 bytes, no unit stride along rows) run through the fp32-FMA
+ * GEMM and need the bytes given for TPS_F32.  Results do not depend on the
+ * piece beyond the order in which dHidden is summed.  0 for bad arguments.
+ * Both calls may be captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels, int32_t weight_layout,
+                      const tps_ce_options* options, const tps_tensor* loss, const tps_tensor* loss_reduced,
+                      const tps_tensor* lse, void* workspace, size_t workspace_bytes, void* cuda_stream);
+int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels, const tps_tensor* lse,
+                      const tps_tensor* grad_loss, int32_t weight_layout, const tps_ce_options* options,
+                      const tps_tensor* dHidden, const tps_tensor* dWhead, void* workspace, size_t workspace_bytes,
+                      void* cuda_stream);
+size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dtype, int32_t backward, int64_t piece);
+
+/* ------------------------------------------------------------------------
  * tps_last_device_error -- synchronizes `cuda_stream`, then reads and clears
  * the current device's error word.  Returns TPS_OK, TPS_ERR_TIMEOUT (a
  * kernel gave up waiting and exited early; its outputs are invalid),
