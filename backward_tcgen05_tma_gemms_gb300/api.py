@@ -12,6 +12,7 @@ import ctypes
 import os
 from typing import Optional, Sequence
 
+import numpy as np
 import torch
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -19,7 +20,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 # libtps_debug.so, whose kernels bounds-check every store).
 LIB_PATH = os.environ.get("TPS_LIBRARY") or os.path.join(_PKG, "libtps.so")
 
-F32, BF16, I32, I64 = 0, 1, 2, 3
+F32, BF16, I32, I64, E4M3 = 0, 1, 2, 3, 4
 (OK, ERR_SHAPE, ERR_PARTITION, ERR_DTYPE, ERR_LAYOUT, ERR_LABEL, ERR_WORKSPACE, ERR_CUDA, ERR_TIMEOUT, ERR_ARG,
  ERR_BOUNDS) = range(11)
 BUILD_DEBUG = 1  # bit of tps_build_flags()
@@ -28,6 +29,7 @@ ACTS = {"gelu": 0, "gelu_erf": 0, "gelu_tanh": 1, "tanh": 2, "silu": 3}
 LAYOUTS = {"in_out": 0, "out_in": 1}
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32, torch.int64: I64}
+_STATE_DTYPES = {torch.float32: F32, torch.float8_e4m3fn: E4M3}
 
 
 class TpsTensor(ctypes.Structure):
@@ -40,6 +42,41 @@ class TpsCeOptions(ctypes.Structure):
     _fields_ = [("ignore_index", ctypes.c_int64), ("vocab_size", ctypes.c_int64), ("reduction", ctypes.c_int32),
                 ("reserved", ctypes.c_int32), ("denominator", ctypes.c_double)]
 
+
+ROPE_MAX_PAIRS = 256
+ROPE_SCALINGS = {"none": 0, "linear": 1, "ntk": 2, "yarn": 3}
+ADAMW_BLOCK = 256  # elements that share a scale of the e4m3 moments
+
+
+class TpsRopeOptions(ctypes.Structure):
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("scaling", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("base", ctypes.c_double), ("factor", ctypes.c_double),
+                ("original_context", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("attention_factor", ctypes.c_double)]
+
+
+class RopePlan(ctypes.Structure):
+    """tps_rope_plan: what rope_fwd and rope_bwd need of the frequencies."""
+    _fields_ = [("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("amplitude", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * ROPE_MAX_PAIRS)]
+
+
+class TpsAdamwHyper(ctypes.Structure):
+    _fields_ = [("lr", ctypes.c_double), ("beta1", ctypes.c_double), ("beta2", ctypes.c_double),
+                ("eps", ctypes.c_double), ("weight_decay", ctypes.c_double), ("step", ctypes.c_int64),
+                ("seed", ctypes.c_uint32), ("stochastic", ctypes.c_int32)]
+
+
+class TpsAdamwScalars(ctypes.Structure):
+    _fields_ = [("step_size", ctypes.c_float), ("root_scale", ctypes.c_float), ("decay", ctypes.c_float),
+                ("seed", ctypes.c_uint32)]
+
+
+# tps_adamw_tensor and tps_span as rows of a table
+_ADAMW_ROW = np.dtype([(n, np.uint64) for n in ("param", "grad", "master", "m", "v", "m_scale", "v_scale")] +
+                      [("numel", np.int64), ("place", np.int64), ("param_dtype", np.int32), ("grad_dtype", np.int32),
+                       ("state_dtype", np.int32), ("reserved", np.int32)])
+_SPAN_ROW = np.dtype([("data", np.uint64), ("numel", np.int64), ("dtype", np.int32), ("reserved", np.int32)])
 
 NO_IGNORE = -(2 ** 63)
 REDUCTIONS = {"none": 0, "sum": 1, "mean": 2}
@@ -90,6 +127,14 @@ def library():
     lib.tps_linear_ce_bwd.argtypes = [P, P, P, P, P, i32, ctypes.POINTER(TpsCeOptions), P, P, vp, sz, vp]
     lib.tps_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i64]
     lib.tps_linear_ce_workspace_bytes.restype = sz
+    lib.tps_rope_plan_init.argtypes = [ctypes.POINTER(TpsRopeOptions), ctypes.POINTER(RopePlan)]
+    lib.tps_rope_fwd.argtypes = [ctypes.POINTER(RopePlan), P, P, P, P, P, vp]
+    lib.tps_rope_bwd.argtypes = [ctypes.POINTER(RopePlan), P, P, P, P, P, vp]
+    lib.tps_adamw_prepare.argtypes = [ctypes.POINTER(TpsAdamwHyper), ctypes.POINTER(TpsAdamwScalars)]
+    lib.tps_adamw_step.argtypes = [vp, i32, ctypes.POINTER(TpsAdamwHyper), vp, vp, vp]
+    lib.tps_grad_norm.argtypes = [vp, i32, ctypes.c_double, vp, vp, sz, vp]
+    lib.tps_grad_norm_workspace_bytes.argtypes = [i32]
+    lib.tps_grad_norm_workspace_bytes.restype = sz
     lib.tps_last_device_error.argtypes = [vp]
     lib.tps_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.tps_strerror.argtypes = [ctypes.c_int]
@@ -507,6 +552,206 @@ def linear_ce_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, ls
         _ref(a[0]), _ref(a[1]), _ref(a[2]), _ref(a[3]), _ref(a[4]), LAYOUTS[weight_layout], ctypes.byref(opts),
         _ref(a[5]), _ref(a[6]), ws, n, stream), T, d, V, h.dtype, True, workspace, h.device)
     return dh, dw
+
+
+# --------------------------------------------------------------------- rotary positions
+
+def rope_plan(rotary_dim: int, base: float = 10000.0, interleaved: bool = False, scaling: str = "none",
+              factor: float = 1.0, original_context: float = 0.0, beta_fast: float = 32.0, beta_slow: float = 1.0,
+              attention_factor: float = 0.0) -> RopePlan:
+    """Plan of a rotary embedding of the first `rotary_dim` elements of each
+    head: halves (default) or interleaved pairs, scaled for long contexts by
+    "linear", "ntk" or "yarn" (host only)."""
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError("argument")
+    plan = RopePlan()
+    opts = TpsRopeOptions(int(rotary_dim), 1 if interleaved else 0, ROPE_SCALINGS[scaling], 0, float(base),
+                          float(factor), float(original_context), float(beta_fast), float(beta_slow),
+                          float(attention_factor))
+    _check(library().tps_rope_plan_init(ctypes.byref(opts), ctypes.byref(plan)))
+    return plan
+
+
+def _rope(fn, plan, q, k, positions, head_dim, out):
+    def heads(t):
+        if t is None or t.dim() != 2:
+            return t
+        if head_dim is None or head_dim < 1 or t.shape[1] % head_dim:
+            raise ValueError("shape")
+        return t.unflatten(1, (t.shape[1] // head_dim, head_dim))
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
+    a = [_tt(heads(t)) for t in (q, k)] + [_tt(positions)] + [_tt(heads(t)) for t in out]
+    _check(fn(ctypes.byref(plan), *[_ref(x) for x in a], _stream(q.device)))
+    return tuple(out)
+
+
+def rope_fwd(plan: RopePlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
+             head_dim: Optional[int] = None, out: Optional[Sequence[torch.Tensor]] = None):
+    """(q', k'): the heads turned by their positions.  q and k are (T, H, D)
+    or (B, S, H, D), or T x H*D as attn_qkv_fwd leaves them (with head_dim);
+    out=(q, k) works in place; k may be None."""
+    return _rope(library().tps_rope_fwd, plan, q, k, positions, head_dim, out)
+
+
+def rope_bwd(plan: RopePlan, dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
+             head_dim: Optional[int] = None, out: Optional[Sequence[torch.Tensor]] = None):
+    """Gradients of q and k from those of rope_fwd's results."""
+    return _rope(library().tps_rope_bwd, plan, dq, dk, positions, head_dim, out)
+
+
+# --------------------------------------------------------------------- optimizer step
+
+class AdamWPlan:
+    """The tensors an optimizer updates and their moments (adamw_plan)."""
+
+    def __init__(self, params, master, m, v, m_scale, v_scale):
+        self.params, self.master, self.m, self.v, self.m_scale, self.v_scale = params, master, m, v, m_scale, v_scale
+        n = len(params)
+        self.numels = [p.numel() for p in params]
+        self.device = params[0].get_device() if n else 0
+        t = np.zeros(n, _ADAMW_ROW)
+        for name, ts in (("param", params), ("master", master), ("m", m), ("v", v), ("m_scale", m_scale),
+                         ("v_scale", v_scale)):
+            if ts is not None:
+                t[name] = [x.data_ptr() for x in ts]
+        t["numel"] = self.numels
+        blocks = [-(-x // ADAMW_BLOCK) for x in self.numels]
+        t["place"] = ADAMW_BLOCK * np.concatenate(([0], np.cumsum(blocks)[:-1])) if n else []
+        t["param_dtype"] = [_DTYPES[p.dtype] for p in params]
+        t["state_dtype"] = [_STATE_DTYPES[x.dtype] for x in m]
+        self._table = t
+
+
+def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.float32, master=None,
+               m: Optional[Sequence[torch.Tensor]] = None, v: Optional[Sequence[torch.Tensor]] = None,
+               m_scale: Optional[Sequence[torch.Tensor]] = None,
+               v_scale: Optional[Sequence[torch.Tensor]] = None) -> AdamWPlan:
+    """What adamw_step updates: contiguous fp32 or bf16 weights on one GPU
+    and their moments, fp32 or (state_dtype=torch.float8_e4m3fn) e4m3 numbers
+    with a scale for every 256 elements, where v holds sqrt(v).  Moments are
+    made here (zeros) unless given, as from a checkpoint.  master: True keeps
+    fp32 copies of bf16 weights (or the copies themselves, one each)."""
+    params = list(params)
+    for p in params:
+        if not isinstance(p, torch.Tensor) or not p.is_cuda:
+            raise ValueError("tensors must live on the GPU (no CPU path)")
+        if p.get_device() != params[0].get_device():
+            raise ValueError("weights on different GPUs")
+        if not p.is_contiguous():
+            raise TpsError(ERR_LAYOUT, "weights must be contiguous")
+        if p.dtype not in (torch.float32, torch.bfloat16):
+            raise TypeError(f"unsupported dtype {p.dtype}")
+    if m is not None:
+        m, v = list(m), list(v)
+        state_dtype = m[0].dtype if m else state_dtype
+    if state_dtype not in _STATE_DTYPES:
+        raise TypeError(f"unsupported dtype {state_dtype}")
+    scaled = state_dtype == torch.float8_e4m3fn
+
+    def zeros(dtype, per=1):  # byte by byte: e4m3 zeros are zero bytes
+        return [torch.zeros(-(-p.numel() // per) * dtype.itemsize, dtype=torch.uint8, device=p.device).view(dtype)
+                for p in params]
+    if m is None:
+        m, v = zeros(state_dtype), zeros(state_dtype)
+        m_scale = zeros(torch.float32, ADAMW_BLOCK) if scaled else None
+        v_scale = zeros(torch.float32, ADAMW_BLOCK) if scaled else None
+    if master is True:
+        master = [p.detach().to(torch.float32).contiguous() for p in params]
+    master = list(master) if master else None
+    m_scale, v_scale = (list(x) if x is not None else None for x in (m_scale, v_scale))
+    if scaled != (m_scale is not None) or scaled != (v_scale is not None):
+        raise ValueError("argument")
+    for ts, dtype, per in ((m, state_dtype, 1), (v, state_dtype, 1), (master, torch.float32, 1),
+                           (m_scale, torch.float32, ADAMW_BLOCK), (v_scale, torch.float32, ADAMW_BLOCK)):
+        if ts is None:
+            continue
+        if len(ts) != len(params):
+            raise ValueError("shape")
+        for t, p in zip(ts, params):
+            if t.numel() != -(-p.numel() // per):
+                raise ValueError("shape")
+            if t.dtype != dtype:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            if not t.is_contiguous() or t.device != p.device:
+                raise TpsError(ERR_LAYOUT, "state must be contiguous, on the weights' GPU")
+    return AdamWPlan(params, master, m, v, m_scale, v_scale)
+
+
+def _grad_list(grads):
+    """Pointers, sizes and dtype codes of contiguous gradients on one GPU."""
+    cls = torch.Tensor
+    if not all(map(cls.is_contiguous, grads)):
+        raise TpsError(ERR_LAYOUT, "gradients must be contiguous")
+    devices = set(map(cls.get_device, grads))
+    if len(devices) > 1 or -1 in devices:
+        raise ValueError("tensors must live on the GPU (no CPU path)" if -1 in devices else "gradients on different GPUs")
+    dtypes = [g.dtype for g in grads]
+    if not set(dtypes) <= {torch.float32, torch.bfloat16}:
+        raise TypeError("gradients must be fp32 or bf16")
+    return list(map(cls.data_ptr, grads)), list(map(cls.numel, grads)), [_DTYPES[d] for d in dtypes], devices
+
+
+def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: Optional[torch.Tensor] = None,
+              out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """fp32 tensor (norm, coefficient): the 2-norm of all gradients together
+    and what brings it to max_norm (1 if it is below, or max_norm is 0; NaN
+    for a norm that is not finite), both on the device."""
+    ptrs, numels, dtypes, devices = _grad_list(grads)
+    dev = torch.device("cuda", next(iter(devices)) if devices else torch.cuda.current_device())
+    t = np.zeros(len(ptrs), _SPAN_ROW)
+    t["data"], t["numel"], t["dtype"] = ptrs, numels, dtypes
+    lib = library()
+    need = int(lib.tps_grad_norm_workspace_bytes(len(ptrs)))
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    if out is None:
+        out = torch.empty(2, dtype=torch.float32, device=dev)
+    elif out.numel() != 2 or out.dtype != torch.float32 or not out.is_contiguous() or not out.is_cuda:
+        raise ValueError("shape")
+    _check(lib.tps_grad_norm(t.ctypes.data, len(ptrs), float(max_norm), out.data_ptr(), workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(dev)))
+    return out
+
+
+def adamw_scalars(lr: float, step: int, beta1: float = 0.9, beta2: float = 0.999, weight_decay: float = 0.0,
+                  seed: int = 0) -> torch.Tensor:
+    """The numbers of an adamw_step that change from step to step, as four
+    int32 words on the host: copied into a device tensor that was given as
+    `scalars` when a CUDA graph was captured, they are what its replay uses."""
+    h, s = TpsAdamwHyper(lr, beta1, beta2, 0.0, weight_decay, step, seed & 0xffffffff, 0), TpsAdamwScalars()
+    _check(library().tps_adamw_prepare(ctypes.byref(h), ctypes.byref(s)))
+    return torch.from_numpy(np.frombuffer(bytes(s), dtype=np.int32).copy())
+
+
+def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: int, beta1: float = 0.9,
+               beta2: float = 0.999, eps: float = 1e-8, weight_decay: float = 0.0,
+               grad_scale: Optional[torch.Tensor] = None, seed: Optional[int] = None,
+               scalars: Optional[torch.Tensor] = None) -> None:
+    """One AdamW step of every tensor of `plan`, in place.  step counts from
+    1.  grad_scale: a device float that multiplies the gradients (grad_norm's
+    coefficient); nothing changes if it is not finite.  seed: rounds e4m3
+    moments, and bf16 weights without a master copy, at random (another seed
+    each step); None rounds to nearest.  scalars: see adamw_scalars."""
+    ptrs, numels, dtypes, devices = _grad_list(grads)
+    if numels != plan.numels:
+        raise ValueError("shape")
+    if not ptrs:
+        return
+    if devices != {plan.device}:
+        raise ValueError("gradients on another GPU than the weights")
+    for t, n, dtype in ((grad_scale, 1, torch.float32), (scalars, 4, torch.int32)):
+        if t is not None and (not t.is_cuda or t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
+            raise ValueError("shape")
+    t = plan._table.copy()
+    t["grad"], t["grad_dtype"] = ptrs, dtypes
+    h = TpsAdamwHyper(lr, beta1, beta2, eps, weight_decay, step, 0 if seed is None else seed & 0xffffffff,
+                      0 if seed is None else 1)
+    _check(library().tps_adamw_step(t.ctypes.data, len(ptrs), ctypes.byref(h),
+                                    None if grad_scale is None else grad_scale.data_ptr(),
+                                    None if scalars is None else scalars.data_ptr(),
+                                    _stream(torch.device("cuda", plan.device))))
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -58,7 +58,7 @@ extern "C" {
 #endif
 
 /* Element types. */
-enum { TPS_F32 = 0, TPS_BF16 = 1, TPS_I32 = 2, TPS_I64 = 3 };
+enum { TPS_F32 = 0, TPS_BF16 = 1, TPS_I32 = 2, TPS_I64 = 3, TPS_E4M3 = 4 };
 
 /* A strided tensor view.  `data` is a device pointer (host pointer only
  * where an entry point says so); shape/stride entries past `ndim` are
@@ -403,6 +403,131 @@ int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, const tps_te
                       const tps_tensor* dHidden, const tps_tensor* dWhead, void* workspace, size_t workspace_bytes,
                       void* cuda_stream);
 size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dtype, int32_t backward, int64_t piece);
+
+/* ------------------------------------------------------------------------
+ * Rotary positions of the query and key heads, between tps_attn_qkv_fwd and
+ * the attention core ([TP] core concept 2.B leaves the core to the caller;
+ * no counterpart on the source pages).  Pair i of the first rotary_dim
+ * elements of a head turns by position * f_i, f_i = base^(-2 i / rotary_dim);
+ * the remaining elements are copied.
+ *   interleaved 0: pair i is elements i and i + rotary_dim / 2;
+ *   interleaved 1: elements 2 i and 2 i + 1.
+ * Scaling for longer contexts than a model was trained on:
+ *   LINEAR f_i / factor;  NTK base * factor^(r / (r - 2));
+ *   YARN   f_i below, f_i / factor above, and a linear ramp between the pair
+ *          indices whose pairs make beta_fast and beta_slow turns within
+ *          original_context positions (0: 32 and 1); cosines and sines are
+ *          multiplied by 0.1 ln(factor) + 1.
+ * attention_factor > 0 replaces that multiplier (1 for the other scalings).
+ *
+ * tps_rope_plan_init fills a plan on the host (no device work): the turns a
+ * position of each pair as 64-bit fractions, so that angles are exact to
+ * 2^-24 of a turn at any position (int32 or int64, negative ones too).
+ * Errors: TPS_ERR_SHAPE (rotary_dim odd, below 2 or above 512), TPS_ERR_ARG.
+ *
+ * tps_rope_fwd: Q (T, H, D) or (B, S, H, D), K (T, Hkv, D) or (B, S, Hkv, D)
+ * or NULL; any strides but the last, which is 1; F32 or BF16, all alike.
+ * Arithmetic is fp32, rounded once.  positions: T or B S entries, or S shared
+ * by all batch entries; contiguous.  Qo and Ko may be Q and K themselves (in
+ * place), and otherwise must not overlap them.
+ * tps_rope_bwd: the transposed rotation, from the gradients of Qo and Ko to
+ * those of Q and K.  Both may be captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+#define TPS_ROPE_MAX_PAIRS 256
+enum { TPS_ROPE_NONE = 0, TPS_ROPE_LINEAR = 1, TPS_ROPE_NTK = 2, TPS_ROPE_YARN = 3 };
+typedef struct tps_rope_options {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  int32_t scaling;
+  int32_t reserved; /* must be 0 */
+  double base;
+  double factor;
+  double original_context;
+  double beta_fast, beta_slow;
+  double attention_factor;
+} tps_rope_options;
+typedef struct tps_rope_plan {
+  int32_t rotary_dim;
+  int32_t interleaved;
+  float amplitude;
+  int32_t reserved;
+  uint64_t turns[TPS_ROPE_MAX_PAIRS];
+} tps_rope_plan;
+int tps_rope_plan_init(const tps_rope_options* options, tps_rope_plan* plan);
+int tps_rope_fwd(const tps_rope_plan* plan, const tps_tensor* Q, const tps_tensor* K, const tps_tensor* positions,
+                 const tps_tensor* Qo, const tps_tensor* Ko, void* cuda_stream);
+int tps_rope_bwd(const tps_rope_plan* plan, const tps_tensor* dQo, const tps_tensor* dKo, const tps_tensor* positions,
+                 const tps_tensor* dQ, const tps_tensor* dK, void* cuda_stream);
+
+/* ------------------------------------------------------------------------
+ * The optimizer step that consumes this library's gradients ([MC] "02 /
+ * BACKWARD" names an optimizer step as part of training parity; the update
+ * is the usual AdamW).  For every tensor, with g = grad * grad_scale:
+ *   m = beta1 m + (1 - beta1) g,   v = beta2 v + (1 - beta2) g^2,
+ *   w = w (1 - lr wd) - lr / (1 - beta1^step) m
+ *       / (sqrt(v) / sqrt(1 - beta2^step) + eps).
+ * param: F32 or BF16, grad: F32 or BF16, each contiguous with numel
+ * elements.  master (F32, or NULL): the weights in fp32; param is then its
+ * bf16 copy.  Moments: state_dtype F32 (m and v), or TPS_E4M3: m and sqrt(v)
+ * as e4m3 bytes with m_scale and v_scale, one float for each run of
+ * TPS_ADAMW_BLOCK elements (value = number * scale; zeros are zero moments).
+ * grad_scale (device float, NULL: 1): multiplies the gradients, e.g. the
+ * coefficient of tps_grad_norm; if it is not finite, nothing is changed.
+ * stochastic != 0: e4m3 moments, and bf16 weights without a master copy, are
+ * rounded up or down at random so that they keep their expectation; the
+ * random bits are a function of `seed` (another one each step) and of each
+ * element's place = tensor.place + its index.  Otherwise they are rounded to
+ * nearest, which leaves e4m3 moments where they are once they change by less
+ * than half a step.
+ * device_scalars (device, 16-byte aligned, NULL: computed from `hyper`): the
+ * four numbers that change from step to step, as tps_adamw_prepare gives
+ * them on the host; a captured CUDA graph then replays with whatever the
+ * caller has copied there.
+ * Tensors of up to 320 that agree in types take one launch.  Nothing is
+ * launched when an argument is refused.
+ *
+ * tps_grad_norm: out[0] = the 2-norm of all gradients together (sums in
+ * fp32 and fp64, in a fixed order), out[1] = min(1, max_norm / (norm + 1e-6))
+ * (1 for max_norm <= 0; NaN for a norm that is not finite).
+ * ---------------------------------------------------------------------- */
+#define TPS_ADAMW_BLOCK 256
+typedef struct tps_adamw_tensor {
+  void* param;
+  const void* grad;
+  float* master;
+  void* m;
+  void* v;
+  float* m_scale;
+  float* v_scale;
+  int64_t numel;
+  int64_t place;
+  int32_t param_dtype, grad_dtype, state_dtype;
+  int32_t reserved;
+} tps_adamw_tensor;
+typedef struct tps_adamw_hyper {
+  double lr, beta1, beta2, eps, weight_decay;
+  int64_t step;
+  uint32_t seed;
+  int32_t stochastic;
+} tps_adamw_hyper;
+typedef struct tps_adamw_scalars {
+  float step_size;  /* lr / (1 - beta1^step) */
+  float root_scale; /* 1 / sqrt(1 - beta2^step) */
+  float decay;      /* 1 - lr weight_decay */
+  uint32_t seed;
+} tps_adamw_scalars;
+typedef struct tps_span {
+  const void* data;
+  int64_t numel;
+  int32_t dtype;
+  int32_t reserved;
+} tps_span;
+int tps_adamw_prepare(const tps_adamw_hyper* hyper, tps_adamw_scalars* out);
+int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const tps_adamw_hyper* hyper, const float* grad_scale,
+                   const tps_adamw_scalars* device_scalars, void* cuda_stream);
+int tps_grad_norm(const tps_span* grads, int32_t n, double max_norm, float* out, void* workspace,
+                  size_t workspace_bytes, void* cuda_stream);
+size_t tps_grad_norm_workspace_bytes(int32_t n);
 
 /* ------------------------------------------------------------------------
  * tps_last_device_error -- synchronizes `cuda_stream`, then reads and clears
