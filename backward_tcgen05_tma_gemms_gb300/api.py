@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence
 
 import numpy as np
@@ -123,13 +124,14 @@ def library():
     lib.tps_ce_workspace_bytes.restype = sz
     lib.tps_ce_workspace_bytes_ex.argtypes = [i64, i64, i32, i32]
     lib.tps_ce_workspace_bytes_ex.restype = sz
-    lib.tps_linear_ce_fwd.argtypes = [P, P, P, i32, ctypes.POINTER(TpsCeOptions), P, P, P, vp, sz, vp]
-    lib.tps_linear_ce_bwd.argtypes = [P, P, P, P, P, i32, ctypes.POINTER(TpsCeOptions), P, P, vp, sz, vp]
+    V = ctypes.c_char_p  # a tps_tensor packed by _view
+    lib.tps_linear_ce_fwd.argtypes = [V, V, V, i32, ctypes.POINTER(TpsCeOptions), V, V, V, vp, sz, vp]
+    lib.tps_linear_ce_bwd.argtypes = [V, V, V, V, V, i32, ctypes.POINTER(TpsCeOptions), V, V, vp, sz, vp]
     lib.tps_linear_ce_workspace_bytes.argtypes = [i64, i64, i64, i32, i32, i64]
     lib.tps_linear_ce_workspace_bytes.restype = sz
     lib.tps_rope_plan_init.argtypes = [ctypes.POINTER(TpsRopeOptions), ctypes.POINTER(RopePlan)]
-    lib.tps_rope_fwd.argtypes = [ctypes.POINTER(RopePlan), P, P, P, P, P, vp]
-    lib.tps_rope_bwd.argtypes = [ctypes.POINTER(RopePlan), P, P, P, P, P, vp]
+    lib.tps_rope_fwd.argtypes = [ctypes.POINTER(RopePlan), V, V, V, V, V, vp]
+    lib.tps_rope_bwd.argtypes = [ctypes.POINTER(RopePlan), V, V, V, V, V, vp]
     lib.tps_adamw_prepare.argtypes = [ctypes.POINTER(TpsAdamwHyper), ctypes.POINTER(TpsAdamwScalars)]
     lib.tps_adamw_step.argtypes = [vp, i32, ctypes.POINTER(TpsAdamwHyper), vp, vp, vp]
     lib.tps_grad_norm.argtypes = [vp, i32, ctypes.c_double, vp, vp, sz, vp]
@@ -177,6 +179,28 @@ def _ref(x):
     return None if x is None else x[0]
 
 
+_VIEW = struct.Struct("=Qii8q")  # tps_tensor
+_PAD = (0, 0, 0, 0)
+
+
+def _view(t: Optional[torch.Tensor]):
+    """tps_tensor view of a CUDA tensor as bytes (None -> NULL): the same
+    checks as _tt, packed in one step for the short calls."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError("tensors must live on the GPU (no CPU path)")
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported dtype {t.dtype}")
+    n = t.dim()
+    if n > 4 or n < 1:
+        raise ValueError("shape")
+    return _VIEW.pack(t.data_ptr(), code, n, *t.shape, *_PAD[n:], *t.stride(), *_PAD[n:])
+
+
 def _check(rc: int):
     if rc == OK:
         return
@@ -191,6 +215,11 @@ def _check(rc: int):
 
 def _stream(device) -> ctypes.c_void_p:
     return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    """The current stream of t's GPU, without building a Stream object."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _parts(v, name="parts") -> int:
@@ -483,12 +512,12 @@ def _linear_ce_call(fn, T, d, V, dtype, backward, workspace, device):
     for the tensor-core path; operands that do not qualify for it are refused
     before any launch and run again with the other path's size."""
     if workspace is not None:
-        _check(fn(ctypes.c_void_p(workspace.data_ptr()), workspace.numel() * workspace.element_size()))
+        _check(fn(workspace.data_ptr(), workspace.numel() * workspace.element_size()))
         return
     for dt in (dtype, torch.float32):
         n = max(linear_ce_workspace_bytes(T, d, V, dt, backward), 1)
         ws = torch.empty(n, dtype=torch.uint8, device=device)
-        rc = fn(ctypes.c_void_p(ws.data_ptr()), n)
+        rc = fn(ws.data_ptr(), n)
         if rc != ERR_WORKSPACE:
             break
     _check(rc)
@@ -520,11 +549,11 @@ def linear_ce_fwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, we
         loss = torch.empty(T, device=h.device, dtype=torch.float32)
         lse = torch.empty(T, device=h.device, dtype=torch.float32)
         red = torch.empty((), device=h.device, dtype=torch.float32) if reduction != "none" else None
-    a = [_tt(t) for t in (h, Whead, labels, loss, red.reshape(1) if red is not None else None, lse)]
-    stream = _stream(h.device)
+    a = [_view(t) for t in (h, Whead, labels, loss, red.reshape(1) if red is not None else None, lse)]
+    stream = _raw_stream(h)
     _linear_ce_call(lambda ws, n: library().tps_linear_ce_fwd(
-        _ref(a[0]), _ref(a[1]), _ref(a[2]), LAYOUTS[weight_layout], ctypes.byref(opts), _ref(a[3]), _ref(a[4]),
-        _ref(a[5]), ws, n, stream), T, d, V, h.dtype, False, workspace, h.device)
+        a[0], a[1], a[2], LAYOUTS[weight_layout], ctypes.byref(opts), a[3], a[4], a[5], ws, n, stream),
+        T, d, V, h.dtype, False, workspace, h.device)
     return loss, red, lse
 
 
@@ -546,11 +575,11 @@ def linear_ce_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, ls
         dw = torch.empty(Whead.shape, device=h.device, dtype=grad_dtype) if want_dwhead else None
     if grad_loss is not None and grad_loss.dim() == 0:
         grad_loss = grad_loss.reshape(1)
-    a = [_tt(t) for t in (h, Whead, labels, lse, grad_loss, dh, dw)]
-    stream = _stream(h.device)
+    a = [_view(t) for t in (h, Whead, labels, lse, grad_loss, dh, dw)]
+    stream = _raw_stream(h)
     _linear_ce_call(lambda ws, n: library().tps_linear_ce_bwd(
-        _ref(a[0]), _ref(a[1]), _ref(a[2]), _ref(a[3]), _ref(a[4]), LAYOUTS[weight_layout], ctypes.byref(opts),
-        _ref(a[5]), _ref(a[6]), ws, n, stream), T, d, V, h.dtype, True, workspace, h.device)
+        *a[:5], LAYOUTS[weight_layout], ctypes.byref(opts), a[5], a[6], ws, n, stream),
+        T, d, V, h.dtype, True, workspace, h.device)
     return dh, dw
 
 
@@ -580,10 +609,9 @@ def _rope(fn, plan, q, k, positions, head_dim, out):
             raise ValueError("shape")
         return t.unflatten(1, (t.shape[1] // head_dim, head_dim))
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=k.dtype, device=k.device))
-    a = [_tt(heads(t)) for t in (q, k)] + [_tt(positions)] + [_tt(heads(t)) for t in out]
-    _check(fn(ctypes.byref(plan), *[_ref(x) for x in a], _stream(q.device)))
+        out = (q.new_empty(q.shape), None if k is None else k.new_empty(k.shape))
+    _check(fn(plan, _view(heads(q)), _view(heads(k)), _view(positions), _view(heads(out[0])), _view(heads(out[1])),
+              _raw_stream(q)))
     return tuple(out)
 
 
@@ -680,7 +708,8 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
 
 
 def _grad_list(grads):
-    """Pointers, sizes and dtype codes of contiguous gradients on one GPU."""
+    """Pointers, sizes and dtype codes of contiguous gradients, and the GPUs
+    they are on."""
     cls = torch.Tensor
     if not all(map(cls.is_contiguous, grads)):
         raise TpsError(ERR_LAYOUT, "gradients must be contiguous")
@@ -688,9 +717,11 @@ def _grad_list(grads):
     if len(devices) > 1 or -1 in devices:
         raise ValueError("tensors must live on the GPU (no CPU path)" if -1 in devices else "gradients on different GPUs")
     dtypes = [g.dtype for g in grads]
-    if not set(dtypes) <= {torch.float32, torch.bfloat16}:
+    kinds = set(dtypes)
+    if not kinds <= {torch.float32, torch.bfloat16}:
         raise TypeError("gradients must be fp32 or bf16")
-    return list(map(cls.data_ptr, grads)), list(map(cls.numel, grads)), [_DTYPES[d] for d in dtypes], devices
+    codes = _DTYPES[dtypes[0]] if len(kinds) == 1 else [_DTYPES[d] for d in dtypes]
+    return list(map(cls.data_ptr, grads)), list(map(cls.numel, grads)), codes, devices
 
 
 def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: Optional[torch.Tensor] = None,
@@ -698,20 +729,20 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: O
     """fp32 tensor (norm, coefficient): the 2-norm of all gradients together
     and what brings it to max_norm (1 if it is below, or max_norm is 0; NaN
     for a norm that is not finite), both on the device."""
-    ptrs, numels, dtypes, devices = _grad_list(grads)
-    dev = torch.device("cuda", next(iter(devices)) if devices else torch.cuda.current_device())
+    ptrs, numels, codes, devices = _grad_list(grads)
+    index = next(iter(devices)) if devices else torch.cuda.current_device()
     t = np.zeros(len(ptrs), _SPAN_ROW)
-    t["data"], t["numel"], t["dtype"] = ptrs, numels, dtypes
+    t["data"], t["numel"], t["dtype"] = ptrs, numels, codes
     lib = library()
     need = int(lib.tps_grad_norm_workspace_bytes(len(ptrs)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=dev)
+        out = torch.empty(2, dtype=torch.float32, device=torch.device("cuda", index))
     elif out.numel() != 2 or out.dtype != torch.float32 or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("shape")
     _check(lib.tps_grad_norm(t.ctypes.data, len(ptrs), float(max_norm), out.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream(dev)))
+                             workspace.numel() * workspace.element_size(), _raw_stream(out)))
     return out
 
 
@@ -734,7 +765,7 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
     coefficient); nothing changes if it is not finite.  seed: rounds e4m3
     moments, and bf16 weights without a master copy, at random (another seed
     each step); None rounds to nearest.  scalars: see adamw_scalars."""
-    ptrs, numels, dtypes, devices = _grad_list(grads)
+    ptrs, numels, codes, devices = _grad_list(grads)
     if numels != plan.numels:
         raise ValueError("shape")
     if not ptrs:
@@ -745,13 +776,12 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
         if t is not None and (not t.is_cuda or t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
             raise ValueError("shape")
     t = plan._table.copy()
-    t["grad"], t["grad_dtype"] = ptrs, dtypes
+    t["grad"], t["grad_dtype"] = ptrs, codes
     h = TpsAdamwHyper(lr, beta1, beta2, eps, weight_decay, step, 0 if seed is None else seed & 0xffffffff,
                       0 if seed is None else 1)
     _check(library().tps_adamw_step(t.ctypes.data, len(ptrs), ctypes.byref(h),
                                     None if grad_scale is None else grad_scale.data_ptr(),
-                                    None if scalars is None else scalars.data_ptr(),
-                                    _stream(torch.device("cuda", plan.device))))
+                                    None if scalars is None else scalars.data_ptr(), _raw_stream(grads[0])))
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -27,6 +27,7 @@
 
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "api_common.cuh"
 
@@ -52,141 +53,171 @@ struct Entry {
 template <int N>
 struct Table {
   int32_t count;
-  int32_t stochastic;
+  int32_t chunk;             // consecutive units of a warp
+  uint32_t random, nearest;  // of 32 random bits: those kept, and those set (two halves) to round to nearest
   int64_t units;
   const float* coef;
   const tps_adamw_scalars* dev;  // read instead of `s` when given
   tps_adamw_scalars s;
-  float b1, c1, b2, c2, eps;
+  float b1, c1, b2, c2, rb2, rc2, eps;  // beta, 1 - beta, and the roots of the second pair
   Entry e[N];
 };
 
-__device__ __forceinline__ uint32_t mix(uint64_t place, uint32_t seed) {
-  uint32_t x = (static_cast<uint32_t>(place) * 0x9e3779b1u + static_cast<uint32_t>(place >> 32) * 0x85ebca77u) ^ seed;
-  x = (x ^ (x >> 16)) * 0x2c1b3c6du;
+constexpr uint32_t kPlaceMul = 0x9e3779b1u;
+// 32 random bits of a place: `x` is place * kPlaceMul plus its upper half's
+// share.  seed2 = seed ^ seed >> 16: what x ^= seed leaves after the first
+// shift, folded into one operation.
+__device__ __forceinline__ uint32_t mix(uint32_t x, uint32_t seed2) {
+  x = (x ^ (x >> 16) ^ seed2) * 0x2c1b3c6du;
   x = (x ^ (x >> 12)) * 0x297a2d39u;
   return x ^ (x >> 15);
 }
-// fp32 to the bf16 below or above by 16 random bits.
-__device__ __forceinline__ __nv_bfloat16 bf16_by(float x, uint32_t rnd) {
-  const uint32_t b = __float_as_uint(x);
-  // infinities and NaN have no neighbour to go to
-  const uint32_t r = (b & 0x7f800000u) == 0x7f800000u ? b : b + rnd;
-  return __ushort_as_bfloat16(static_cast<unsigned short>(r >> 16));
+// fp32 (not a NaN) to the bf16 below or above by 16 random bits, in the upper
+// half; infinity has no bits to carry from.
+__device__ __forceinline__ uint32_t bf16_by(float x, uint32_t rnd) { return __float_as_uint(x) + rnd; }
+// The e4m3 code below or above |x| 448 / a by 16 random bits, in the low
+// byte; s = 448 / a * 2^-120.  That product has the code's exponent in a
+// float's exponent field and its mantissa on top of the float's, and e4m3
+// subnormals are float subnormals there, so that one addition and one shift
+// do it for all of them.  (The product may pass 448 by its rounding; 16 units
+// of that stay below the last random bit.)
+__device__ __forceinline__ uint32_t e4m3_by(float x, float s, uint32_t rnd) {
+  return (rnd * 16u + __float_as_uint(fabsf(x) * s)) >> 20;
 }
-// y in [0, 448] to e4m3 by 16 random bits: numbers of at least 2^-6 have 3
-// mantissa bits, smaller ones lie on the grid of 2^-9.
-__device__ __forceinline__ uint32_t e4m3_by(float y, uint32_t rnd) {
-  const uint32_t big = ((__float_as_uint(y) + (rnd << 4)) >> 20) - 960u;
-  const uint32_t small = static_cast<uint32_t>(__fadd_rn(y * 512.0f, static_cast<float>(rnd) * 0x1p-16f));
-  return y >= 0x1p-6f ? big : small;
+// And back: the code's bits in place of a float's are the number times 2^-120;
+// s = scale * 2^120.
+__device__ __forceinline__ float e4m3_float(uint32_t bits, float s) { return __uint_as_float(bits) * s; }
+// Blocks whose scale times 2^120 would overflow, or whose 448 / a would lose
+// bits, are held 2^-40 smaller meanwhile; a whole warp agrees on it.
+constexpr float kSmaller = 0x1p-40f, kLarger = 0x1p40f, kLargeScale = 64.0f;
+// Bits of code i of four: exponent and mantissa from bit 26 down, and the sign
+// in bit 31.  (Shifts to the left are products here: they run beside the
+// logical operations, which this kernel has most of.)
+__device__ __forceinline__ uint32_t unsigned_code(uint32_t q, int i) {
+  return (i < 3 ? q * (1u << (20 - 8 * (i < 3 ? i : 0))) : q >> 4) & 0x07f00000u;
 }
-__device__ __forceinline__ float e4m3_value(uint32_t code) {  // sign, 4 exponent bits, 3 mantissa bits
-  const uint32_t mag = code & 0x7fu;
-  // a float whose exponent field is the code's times 2^120 is the number, subnormals included
-  const float x = __uint_as_float(mag << 20) * 0x1p120f;
-  return code & 0x80u ? -x : x;
-}
-
-// Four consecutive elements.
-__device__ __forceinline__ void load4(const float* p, float (&x)[4]) {
-  const float4 q = *reinterpret_cast<const float4*>(p);
-  x[0] = q.x; x[1] = q.y; x[2] = q.z; x[3] = q.w;
-}
-__device__ __forceinline__ void load4(const __nv_bfloat16* p, float (&x)[4]) {
-  const uint2 q = *reinterpret_cast<const uint2*>(p);
-  x[0] = __uint_as_float(q.x << 16); x[1] = __uint_as_float(q.x & 0xffff0000u);
-  x[2] = __uint_as_float(q.y << 16); x[3] = __uint_as_float(q.y & 0xffff0000u);
-}
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
-__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
-  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
-}
-__device__ __forceinline__ void store4(__nv_bfloat16* p, const __nv_bfloat16 (&x)[4]) {
-  uint2 q;
-  q.x = __bfloat16_as_ushort(x[0]) | static_cast<uint32_t>(__bfloat16_as_ushort(x[1])) << 16;
-  q.y = __bfloat16_as_ushort(x[2]) | static_cast<uint32_t>(__bfloat16_as_ushort(x[3])) << 16;
-  *reinterpret_cast<uint2*>(p) = q;
+__device__ __forceinline__ uint32_t signed_code(uint32_t q, int i) {
+  return ((q * (1u << (24 - 8 * i))) & 0x80000000u) | unsigned_code(q, i);
 }
 
-// The index of element i (0..3) of group j (0, 1) of a lane within a unit.
+// The index of a lane's first element of group j (0, 1) of four within a unit.
 __device__ __forceinline__ int in_unit(int lane, int j) { return j * 128 + lane * 4; }
 
-// The eight values of a lane, `n` of the unit's 256 being there.
-template <class T>
-__device__ __forceinline__ void read8(const T* p, int lane, bool full, int n, float (&x)[2][4]) {
+// Four consecutive elements as they come from memory.
+template <class T> struct Four { uint2 q; };
+template <> struct Four<float> { float4 q; };
+__device__ __forceinline__ void unpack(const Four<float>& f, float (&x)[4]) {
+  x[0] = f.q.x; x[1] = f.q.y; x[2] = f.q.z; x[3] = f.q.w;
+}
+__device__ __forceinline__ void unpack(const Four<__nv_bfloat16>& f, float (&x)[4]) {
+  x[0] = __uint_as_float(f.q.x << 16); x[1] = __uint_as_float(f.q.x & 0xffff0000u);
+  x[2] = __uint_as_float(f.q.y << 16); x[3] = __uint_as_float(f.q.y & 0xffff0000u);
+}
+// FULL, here and below: all 256 elements of the unit are there and every
+// pointer is aligned; else `n` of them are, and they go one by one.
+template <bool FULL, class T>
+__device__ __forceinline__ void fetch(const T* p, int lane, int n, Four<T> (&f)[2]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int at = in_unit(lane, j);
-    if (full) {
-      load4(p + at, x[j]);
+    if (FULL) {
+      f[j].q = *reinterpret_cast<const decltype(f[j].q)*>(p + at);
     } else {
+      T x[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) x[j][i] = at + i < n ? load1(p + at + i) : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        x[i] = T(0.0f);
+        if (at + i < n) x[i] = p[at + i];
+      }
+      memcpy(&f[j], x, sizeof(x));
     }
   }
 }
-template <class T>
-__device__ __forceinline__ void write8(T* p, int lane, bool full, int n, const T (&x)[2][4]) {
+template <bool FULL>
+__device__ __forceinline__ void fetch_codes(const uint8_t* p, int lane, int n, uint32_t (&q)[2]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int at = in_unit(lane, j);
-    if (full) {
+    q[j] = 0;
+    if (FULL) {
+      q[j] = *reinterpret_cast<const uint32_t*>(p + at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (at + i < n) q[j] |= static_cast<uint32_t>(p[at + i]) << (8 * i);
+    }
+  }
+}
+__device__ __forceinline__ void store4(float* p, const float (&x)[4]) {
+  *reinterpret_cast<float4*>(p) = make_float4(x[0], x[1], x[2], x[3]);
+}
+// bf16 values in the upper halves of words.
+__device__ __forceinline__ void store4(__nv_bfloat16* p, const uint32_t (&x)[4]) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(__byte_perm(x[0], x[1], 0x7632), __byte_perm(x[2], x[3], 0x7632));
+}
+__device__ __forceinline__ void store1(float* p, float x) { *p = x; }
+__device__ __forceinline__ void store1(__nv_bfloat16* p, uint32_t x) {
+  *p = __ushort_as_bfloat16(static_cast<unsigned short>(x >> 16));
+}
+template <bool FULL, class T, class V>
+__device__ __forceinline__ void write8(T* p, int lane, int n, const V (&x)[2][4]) {
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int at = in_unit(lane, j);
+    if (FULL) {
       store4(p + at, x[j]);
     } else {
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        if (at + i < n) p[at + i] = x[j][i];
+        if (at + i < n) store1(p + at + i, x[j][i]);
     }
   }
 }
-__device__ __forceinline__ void read8_codes(const uint8_t* p, int lane, bool full, int n, float scale, float (&x)[2][4]) {
-#pragma unroll
-  for (int j = 0; j < 2; ++j) {
-    const int at = in_unit(lane, j);
-    uint32_t q = 0;
-    if (full) {
-      q = *reinterpret_cast<const uint32_t*>(p + at);
-    } else {
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (at + i < n) q |= static_cast<uint32_t>(p[at + i]) << (8 * i);
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[j][i] = __fmul_rn(e4m3_value((q >> (8 * i)) & 0xffu), scale);
-  }
+// Largest of three that keeps a NaN (positive, as fabsf leaves it).
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
 }
 // x as e4m3 numbers with the block's scale.  SQRT: x >= 0 and nothing but 0 becomes 0.
-template <bool SQRT>
-__device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane, bool full, int n,
-                                             const float (&x)[2][4], const uint32_t (&rnd)[2][4]) {
-  uint32_t top = 0;  // as bits, so that a NaN is the largest
+template <bool FULL, bool SQRT>
+__device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane, int n, float (&x)[2][4],
+                                             const uint32_t (&rnd)[2][4]) {
+  float part = 0.0f;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, __float_as_uint(x[j][i]) & 0x7fffffffu);
-  top = __reduce_max_sync(0xffffffffu, top);
-  float a = __uint_as_float(top);
+    for (int i = 0; i < 4; i += 2) part = max_nan(part, fabsf(x[j][i]), fabsf(x[j][i + 1]));
+  float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(part)));  // a NaN has the largest bits
   if (a < 1e-30f) a = 0.0f;
-  const float inv = a > 0.0f ? __fdiv_rn(448.0f, a) : (a == 0.0f ? 0.0f : a);
   if (lane == 0) *scale = __fmul_rn(a, 1.0f / 448.0f);
+  if (a > kLargeScale * 256.0f) {
+    a *= kSmaller;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) x[j][i] *= kSmaller;
+  }
+  const float inv = (a > 0.0f ? __fdividef(448.0f, a) : a) * 0x1p-120f;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    uint32_t q = 0;
+    uint32_t c[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float y = fminf(__fmul_rn(fabsf(x[j][i]), inv), 448.0f);
-      uint32_t c = e4m3_by(y, rnd[j][i]);
-      if (SQRT) {
-        if (c == 0 && y > 0.0f) c = 1;
-      } else if (c != 0 && x[j][i] < 0.0f) {
-        c |= 0x80u;
+    for (int i = 0; i < 4; ++i) c[i] = e4m3_by(x[j][i], inv, rnd[j][i]);
+    uint32_t q = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+    if (SQRT) {
+      if ((q - 0x01010101u) & ~q & 0x80808080u) {  // a code is 0 (this test may name too many): is its element?
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if ((q >> (8 * i) & 0xffu) == 0 && x[j][i] > 0.0f) q |= 1u << (8 * i);
       }
-      q |= c << (8 * i);
+    } else {  // the signs; a zero may keep its own
+      const uint32_t s01 = __byte_perm(__float_as_uint(x[j][0]), __float_as_uint(x[j][1]), 0x0073);
+      const uint32_t s23 = __byte_perm(__float_as_uint(x[j][2]), __float_as_uint(x[j][3]), 0x0073);
+      q |= __byte_perm(s01, s23, 0x5410) & 0x80808080u;
     }
     const int at = in_unit(lane, j);
-    if (full) {
+    if (FULL) {
       *reinterpret_cast<uint32_t*>(p + at) = q;
     } else {
 #pragma unroll
@@ -196,77 +227,205 @@ __device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane,
   }
 }
 
-template <class PT, class GT, bool MASTER, bool E4M3, int N>
-__global__ void __launch_bounds__(32 * kWarps) adamw_kernel(const __grid_constant__ Table<N> t) {
-  const int lane = threadIdx.x & 31;
-  const float coef = t.coef != nullptr ? *t.coef : 1.0f;
-  if (!isfinite(coef)) return;  // the gradient is not finite: this step leaves everything as it is
-  const tps_adamw_scalars s = t.dev != nullptr ? *t.dev : t.s;
-  int k = 0;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5); u < t.units;
-       u += static_cast<int64_t>(gridDim.x) * kWarps) {
-    while (k + 1 < t.count && u >= t.e[k + 1].first) ++k;
-    const Entry& e = t.e[k];
-    const int64_t unit = u - e.first, at = unit * kUnit;
-    const int n = static_cast<int>(e.n - at < kUnit ? e.n - at : kUnit);
-    const bool full = e.wide && n == kUnit;
-    float g[2][4], w[2][4], m[2][4], v[2][4];
-    read8(static_cast<const GT*>(e.g) + at, lane, full, n, g);
-    if (MASTER)
-      read8(static_cast<const float*>(e.w) + at, lane, full, n, w);
-    else
-      read8(static_cast<const PT*>(e.p) + at, lane, full, n, w);
-    if (E4M3) {
-      read8_codes(static_cast<const uint8_t*>(e.m) + at, lane, full, n, e.ms[unit], m);
-      read8_codes(static_cast<const uint8_t*>(e.v) + at, lane, full, n, e.vs[unit], v);
-    } else {
-      read8(static_cast<const float*>(e.m) + at, lane, full, n, m);
-      read8(static_cast<const float*>(e.v) + at, lane, full, n, v);
+// Square root and quotient to two units each.  FAST also takes subnormals for
+// 0 (moments in 8 bits: their blocks end 2^-18 below the largest element).
+template <bool FAST>
+__device__ __forceinline__ float root_of(float x) {
+  float r;
+  if (FAST)
+    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  else
+    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+template <bool FAST>
+__device__ __forceinline__ float over(float a, float b) {
+  float r;
+  if (FAST)
+    asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  else
+    r = __fdividef(a, b);
+  return r;
+}
+
+// The entry of unit u: the last that starts at or before it.
+template <class E>
+__device__ __forceinline__ int entry_of(const E* e, int count, int64_t u) {
+  int lo = 0;
+  for (int hi = count; hi - lo > 1;) {
+    const int mid = (lo + hi) >> 1;
+    if (u >= e[mid].first) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// What a lane reads of a unit, so that the next unit's loads can be in
+// flight while this one is computed.
+template <class GT, class WT, bool E4M3>
+struct Raw {
+  Four<GT> g[2];
+  Four<WT> w[2];
+  Four<float> m[2], v[2];  // fp32 moments
+  uint32_t qm[2], qv[2];   // e4m3 moments and their scales
+  float ms, vs;
+};
+
+template <bool FULL, class WT, class GT, bool MASTER, bool E4M3>
+__device__ __forceinline__ void adamw_fetch(const Entry& e, int64_t unit, int n, int lane, Raw<GT, WT, E4M3>& r) {
+  const int64_t at = unit * kUnit;
+  fetch<FULL>(static_cast<const GT*>(e.g) + at, lane, n, r.g);
+  fetch<FULL>((MASTER ? reinterpret_cast<const WT*>(e.w) : static_cast<const WT*>(e.p)) + at, lane, n, r.w);
+  if (E4M3) {
+    fetch_codes<FULL>(static_cast<const uint8_t*>(e.m) + at, lane, n, r.qm);
+    fetch_codes<FULL>(static_cast<const uint8_t*>(e.v) + at, lane, n, r.qv);
+    r.ms = e.ms[unit];
+    r.vs = e.vs[unit];
+  } else {
+    fetch<FULL>(static_cast<const float*>(e.m) + at, lane, n, r.m);
+    fetch<FULL>(static_cast<const float*>(e.v) + at, lane, n, r.v);
+  }
+}
+
+template <bool FULL, class PT, class WT, class GT, bool MASTER, bool E4M3, int N>
+__device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, int64_t unit, int n, float coef,
+                                           const tps_adamw_scalars& s, int lane, const Raw<GT, WT, E4M3>& r) {
+  const int64_t at = unit * kUnit;
+  float g[2][4], w[2][4], m[2][4], v[2][4], root[2][4];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    unpack(r.g[j], g[j]);
+    unpack(r.w[j], w[j]);
+    if (!E4M3) {
+      unpack(r.m[j], m[j]);
+      unpack(r.v[j], v[j]);
     }
-    float root[2][4];
+  }
+  if (E4M3) {
+    // the constants go into the scales: b1 m, and sqrt(b2) sqrt(v)
+    const bool bm = r.ms > kLargeScale, bv = r.vs > kLargeScale;
+    const float sm = (bm ? r.ms * kSmaller : r.ms) * 0x1p120f * t.b1;
+    const float sv = (bv ? r.vs * kSmaller : r.vs) * 0x1p120f * t.rb2;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float gg = g[j][i] * coef;
-        if (E4M3) v[j][i] = __fmul_rn(v[j][i], v[j][i]);
-        m[j][i] = __fadd_rn(__fmul_rn(m[j][i], t.b1), __fmul_rn(gg, t.c1));
-        v[j][i] = __fadd_rn(__fmul_rn(v[j][i], t.b2), __fmul_rn(__fmul_rn(gg, gg), t.c2));
-        root[j][i] = __fsqrt_rn(v[j][i]);
-        const float step = __fdiv_rn(__fmul_rn(m[j][i], s.step_size), fmaf(root[j][i], s.root_scale, t.eps));
-        w[j][i] = __fsub_rn(__fmul_rn(w[j][i], s.decay), step);
+        m[j][i] = e4m3_float(signed_code(r.qm[j], i), sm);
+        root[j][i] = e4m3_float(unsigned_code(r.qv[j], i), sv);
       }
-    constexpr bool kRandom = E4M3 || (!MASTER && sizeof(PT) == 2);
-    uint32_t rm[2][4], rv[2][4], rp[2][4];
-    if (kRandom) {
+    if (bm || bv) {
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const uint32_t x = mix(static_cast<uint64_t>(e.place + at + in_unit(lane, j) + i), s.seed);
-          rm[j][i] = t.stochastic ? x & 0xffffu : 0x8000u;
-          rv[j][i] = t.stochastic ? x >> 16 : 0x8000u;
-          rp[j][i] = t.stochastic ? (x * 0x9e3779b1u) >> 16 : 0x8000u;
+          if (bm) m[j][i] *= kLarger;
+          if (bv) root[j][i] *= kLarger;
         }
     }
-    if (sizeof(PT) == 2) {
-      __nv_bfloat16 b[2][4];
+  }
+  const float gm = coef * t.c1, gv = coef * t.rc2;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+  for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          b[j][i] = MASTER || !t.stochastic ? __float2bfloat16_rn(w[j][i]) : bf16_by(w[j][i], rp[j][i]);
-      write8(static_cast<__nv_bfloat16*>(e.p) + at, lane, full, n, b);
-      if (MASTER) write8(e.w + at, lane, full, n, w);
-    } else {
-      write8(static_cast<float*>(e.p) + at, lane, full, n, w);
+    for (int i = 0; i < 4; ++i) {
+      if (E4M3) {
+        m[j][i] = fmaf(g[j][i], gm, m[j][i]);
+        const float h = g[j][i] * gv;
+        v[j][i] = fmaf(h, h, root[j][i] * root[j][i]);
+      } else {
+        const float gg = g[j][i] * coef;
+        m[j][i] = fmaf(m[j][i], t.b1, gg * t.c1);
+        v[j][i] = fmaf(v[j][i], t.b2, gg * gg * t.c2);
+      }
+      root[j][i] = root_of<E4M3>(v[j][i]);
+      const float step = over<E4M3>(m[j][i] * s.step_size, fmaf(root[j][i], s.root_scale, t.eps));
+      w[j][i] = fmaf(w[j][i], s.decay, -step);
     }
-    if (E4M3) {
-      write8_codes<false>(static_cast<uint8_t*>(e.m) + at, e.ms + unit, lane, full, n, m, rm);
-      write8_codes<true>(static_cast<uint8_t*>(e.v) + at, e.vs + unit, lane, full, n, root, rv);
-    } else {
-      write8(static_cast<float*>(e.m) + at, lane, full, n, m);
-      write8(static_cast<float*>(e.v) + at, lane, full, n, v);
+  constexpr bool kRandom = E4M3 || (!MASTER && sizeof(PT) == 2);
+  uint32_t rm[2][4], rv[2][4], rp[2][4];
+  if (kRandom) {
+    // places of a unit share their upper half: both they and units start on multiples of 256
+    const uint64_t place = static_cast<uint64_t>(e.place + at);
+    const uint32_t seed2 = s.seed ^ s.seed >> 16;
+    const uint32_t base = (static_cast<uint32_t>(place) + 4 * lane) * kPlaceMul + static_cast<uint32_t>(place >> 32) * 0x85ebca77u;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t x = mix(base + static_cast<uint32_t>(128 * j + i) * kPlaceMul, seed2);
+        rp[j][i] = (x * kPlaceMul) >> 16;
+        x = (x & t.random) | t.nearest;
+        rm[j][i] = x & 0xffffu;
+        rv[j][i] = x >> 16;
+      }
+  }
+  if (sizeof(PT) == 2) {
+    uint32_t b[2][4];
+    float probe = 0.0f;  // NaN if a weight is not finite
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) probe = fmaf(w[j][i], 0.0f, probe);
+    const bool nearest = MASTER || t.nearest || probe != 0.0f;
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        b[j][i] = nearest ? static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(w[j][i]))) << 16
+                          : bf16_by(w[j][i], rp[j][i]);
+    write8<FULL>(static_cast<__nv_bfloat16*>(e.p) + at, lane, n, b);
+    if (MASTER) write8<FULL>(e.w + at, lane, n, w);
+  } else {
+    write8<FULL>(static_cast<float*>(e.p) + at, lane, n, w);
+  }
+  if (E4M3) {
+    write8_codes<FULL, false>(static_cast<uint8_t*>(e.m) + at, e.ms + unit, lane, n, m, rm);
+    write8_codes<FULL, true>(static_cast<uint8_t*>(e.v) + at, e.vs + unit, lane, n, root, rv);
+  } else {
+    write8<FULL>(static_cast<float*>(e.m) + at, lane, n, m);
+    write8<FULL>(static_cast<float*>(e.v) + at, lane, n, v);
+  }
+}
+
+template <class PT, class GT, bool MASTER, bool E4M3, int N>
+__global__ void __launch_bounds__(32 * kWarps, E4M3 ? 3 : 4) adamw_kernel(const __grid_constant__ Table<N> t) {
+  using WT = typename std::conditional<MASTER, float, PT>::type;
+  const int lane = threadIdx.x & 31;
+  const float coef = t.coef != nullptr ? *t.coef : 1.0f;
+  if (!isfinite(coef)) return;  // the gradient is not finite: this step leaves everything as it is
+  const tps_adamw_scalars s = t.dev != nullptr ? *t.dev : t.s;
+  // Consecutive units of one tensor share its pointers: the table is read and
+  // the addresses are formed once for `chunk` of them.
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kWarps * t.chunk;
+  int64_t u = (static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5)) * t.chunk;
+  int k = entry_of(t.e, t.count, u);
+  for (; u < t.units; u += step) {
+    const int64_t end = u + t.chunk < t.units ? u + t.chunk : t.units;
+    for (int64_t at = u; at < end;) {
+      while (k + 1 < t.count && at >= t.e[k + 1].first) ++k;
+      const Entry& e = t.e[k];
+      int64_t unit = at - e.first;
+      const int64_t whole = e.wide ? e.n / kUnit : 0;
+      const int64_t stop = end - e.first < whole ? end - e.first : whole;
+      if (unit < stop) {
+        at += stop - unit;
+        Raw<GT, WT, E4M3> now, next;
+        if (E4M3) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
+        for (; unit < stop; ++unit) {
+          if (!E4M3)
+            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
+          else if (unit + 1 < stop)
+            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, next);
+          adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, now);
+          if (E4M3) now = next;
+        }
+      } else {
+        const int64_t left = e.n - unit * kUnit;
+        const int n = static_cast<int>(left < kUnit ? left : kUnit);
+        Raw<GT, WT, E4M3> now;
+        adamw_fetch<false, WT, GT, MASTER, E4M3>(e, unit, n, lane, now);
+        adamw_unit<false, PT, WT, GT, MASTER, E4M3>(t, e, unit, n, coef, s, lane, now);
+        ++at;
+      }
     }
   }
 }
@@ -284,6 +443,7 @@ struct Spans {
 };
 
 constexpr int kNormBlocks = 152 * 8;
+constexpr int kAhead = 8;  // units of a warp in flight
 
 // Partial sums of squares, one for each block, of a fixed assignment of units.
 template <int N>
@@ -291,20 +451,66 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
   __shared__ float red[kWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  int k = 0;
-  for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + w; u < t.units; u += static_cast<int64_t>(gridDim.x) * kWarps) {
-    while (k + 1 < t.count && u >= t.e[k + 1].first) ++k;
-    const Span& e = t.e[k];
-    const int64_t at = (u - e.first) * kUnit;
-    const int n = static_cast<int>(e.n - at < kUnit ? e.n - at : kUnit);
-    const bool full = e.wide && n == kUnit;
-    float x[2][4];
-    if (e.bf16)
-      read8(static_cast<const __nv_bfloat16*>(e.p) + at, lane, full, n, x);
-    else
-      read8(static_cast<const float*>(e.p) + at, lane, full, n, x);
+  // kAhead consecutive units of a warp at a time: inside one tensor, all
+  // their loads are in flight before the first sum
+  const int64_t runs = (t.units + kAhead - 1) / kAhead;
+  int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + w;
+  int k = entry_of(t.e, t.count, r * kAhead);
+  for (; r < runs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
+    const int64_t u0 = r * kAhead;
+    while (k + 1 < t.count && u0 >= t.e[k + 1].first) ++k;
+    const int64_t at0 = (u0 - t.e[k].first) * kUnit;
+    if (t.e[k].wide && t.e[k].n - at0 >= kAhead * kUnit) {
+      if (t.e[k].bf16) {  // 16 bytes a lane and load
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(t.e[k].p) + at0) + lane;
+        uint4 q[kAhead];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc[i] = fmaf(x[0][i], x[0][i], fmaf(x[1][i], x[1][i], acc[i]));
+        for (int i = 0; i < kAhead; ++i) q[i] = p[32 * i];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+          const uint32_t v[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float lo = __uint_as_float(v[j] << 16), hi = __uint_as_float(v[j] & 0xffff0000u);
+            acc[j] = fmaf(lo, lo, fmaf(hi, hi, acc[j]));
+          }
+        }
+      } else {
+        const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(t.e[k].p) + at0) + lane;
+        float4 q[2 * kAhead];
+#pragma unroll
+        for (int i = 0; i < 2 * kAhead; ++i) q[i] = p[32 * i];
+#pragma unroll
+        for (int i = 0; i < 2 * kAhead; ++i) {
+          acc[0] = fmaf(q[i].x, q[i].x, acc[0]);
+          acc[1] = fmaf(q[i].y, q[i].y, acc[1]);
+          acc[2] = fmaf(q[i].z, q[i].z, acc[2]);
+          acc[3] = fmaf(q[i].w, q[i].w, acc[3]);
+        }
+      }
+      continue;
+    }
+    int kk = k;
+    for (int64_t u = u0; u < u0 + kAhead && u < t.units; ++u) {
+      while (kk + 1 < t.count && u >= t.e[kk + 1].first) ++kk;
+      const Span& e = t.e[kk];
+      const int64_t at = (u - e.first) * kUnit, left = e.n - at;
+      const int n = static_cast<int>(left < kUnit ? left : kUnit);
+      float x[2][4];
+      if (e.bf16) {
+        Four<__nv_bfloat16> f[2];
+        fetch<false>(static_cast<const __nv_bfloat16*>(e.p) + at, lane, n, f);
+        unpack(f[0], x[0]);
+        unpack(f[1], x[1]);
+      } else {
+        Four<float> f[2];
+        fetch<false>(static_cast<const float*>(e.p) + at, lane, n, f);
+        unpack(f[0], x[0]);
+        unpack(f[1], x[1]);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], acc[j]));
+    }
   }
   float a = (acc[0] + acc[1]) + (acc[2] + acc[3]);
 #pragma unroll
@@ -358,6 +564,7 @@ int launch_adamw(const Table<kMany>& all, int64_t elements, int per_element, cud
   memcpy(&t, &all, offsetof(Table<kMany>, e));
   memcpy(t.e, all.e, sizeof(Entry) * all.count);
   const int64_t blocks = (t.units + kWarps - 1) / kWarps, most = int64_t(sms()) * 8;
+  t.chunk = t.units >= 32 * kWarps * most ? 8 : t.units >= 4 * kWarps * most ? 4 : 1;
   ProfScope prof("adamw", E4M3 ? "e4m3" : "f32", 0.0, double(elements) * per_element, s);
   adamw_kernel<PT, GT, MASTER, E4M3, N><<<static_cast<unsigned>(blocks < most ? blocks : most), 32 * kWarps, 0, s>>>(t);
   note_launch();
@@ -448,6 +655,8 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
   for (int32_t i = 0; i < n; ++i) {  // everything is checked before anything is launched
     const tps_adamw_tensor& t = tensors[i];
     if (t.numel < 0) return fail(TPS_ERR_SHAPE, "tensor %d: negative numel", i);
+    if (t.place < 0 || t.place % kUnit != 0)
+      return fail(TPS_ERR_ARG, "tensor %d: place must be a multiple of %d, at least 0", i, kUnit);
     const int pd = t.param_dtype, gd = t.grad_dtype, sd = t.state_dtype;
     if ((pd != TPS_F32 && pd != TPS_BF16) || (gd != TPS_F32 && gd != TPS_BF16) || (sd != TPS_F32 && sd != TPS_E4M3))
       return fail(TPS_ERR_DTYPE, "tensor %d: weights and gradients are f32 or bf16, moments f32 or e4m3", i);
@@ -467,8 +676,11 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   for (int kind = 0; kind < 12; ++kind) {
     if (!(kinds >> kind & 1u)) continue;
-    Table<kMany> tab = {};
-    tab.stochastic = h->stochastic != 0;
+    Table<kMany> tab;
+    tab.count = 0;
+    tab.units = 0;
+    tab.random = h->stochastic ? 0xffffffffu : 0u;
+    tab.nearest = h->stochastic ? 0u : 0x80008000u;
     tab.coef = grad_scale;
     tab.dev = device_scalars;
     tab.s = sc;
@@ -476,6 +688,8 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
     tab.c1 = static_cast<float>(1.0 - h->beta1);
     tab.b2 = static_cast<float>(h->beta2);
     tab.c2 = static_cast<float>(1.0 - h->beta2);
+    tab.rb2 = static_cast<float>(std::sqrt(h->beta2));
+    tab.rc2 = static_cast<float>(std::sqrt(1.0 - h->beta2));
     tab.eps = static_cast<float>(h->eps);
     int64_t elements = 0;
     for (int32_t i = 0; i <= n; ++i) {
@@ -522,14 +736,16 @@ extern "C" int tps_grad_norm(const tps_span* grads, int32_t n, double max_norm, 
   }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   float* part = static_cast<float*>(workspace);
-  Spans<kMany> t = {};
+  Spans<kMany> t;
+  t.count = 0;
+  t.units = 0;
   int parts = 0, rc;
   double bytes = 0.0;
   for (int32_t i = 0; i <= n; ++i) {
     const bool end = i == n;
     if (!end && grads[i].numel == 0) continue;
     if ((end || t.count == kMany) && t.count > 0) {
-      const int64_t want = (t.units + kWarps - 1) / kWarps;
+      const int64_t want = (t.units + kAhead * kWarps - 1) / (kAhead * kWarps);
       const int blocks = static_cast<int>(want < kNormBlocks ? want : kNormBlocks);
       {
         ProfScope prof("grad_norm", "partial", 0.0, bytes, s);

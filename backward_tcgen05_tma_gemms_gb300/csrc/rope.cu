@@ -13,9 +13,10 @@
 // signed number of half turns / 2^31, go through sincospif.  The error is
 // 2^-34 of a turn at p = 2^30 and the 2^-25 of the conversion.
 //
-// One thread takes 16 bytes of each half of a pair run (8 pairs of bf16) of
-// one token and forms its angles once for several heads, whose loads it
-// issues before it uses the first; a warp reads whole 128-byte lines.
+// A block takes a few tokens: each thread forms the cosine and sine of one
+// (token, pair), which all heads of the token share through shared memory,
+// and streams its items -- 16 bytes of either run of a head's pairs -- with
+// the loads of the first ones issued before the angles are formed.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -29,6 +30,8 @@ namespace tps {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kTokenPairs = 256;  // (token, pair)s of a block
+static_assert(kTokenPairs >= TPS_ROPE_MAX_PAIRS, "one token's pairs fit");
 
 struct View {
   char* p;
@@ -41,7 +44,7 @@ struct RopeParams {
   int64_t rows, S;         // tokens, tokens of one batch entry
   int D, rot;              // elements of a head, those that turn
   int units, rot_units;    // thread units of a head, those that turn
-  int heads_per_thread;
+  int tokens, block_heads; // of one block
   const void* pos;
   int pos_i64, pos_shared; // int64 positions; one row of positions for all batches
   float amp, sign;
@@ -63,81 +66,94 @@ struct __align__(sizeof(T) * N) Run {
   T v[N];
 };
 
+// A block's items are (token, head, unit), unit fastest; item i of a thread
+// is threadIdx.x + i * kThreads.
 template <class T, int N, bool INTER, bool VEC_TAIL>
 __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Turns turns, const RopeParams p) {
-  __shared__ uint64_t tab[TPS_ROPE_MAX_PAIRS];
-  for (int i = threadIdx.x; i < p.rot / 2; i += kThreads) tab[i] = turns.t[i];
-  __syncthreads();
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-  if (at >= p.rows * p.units) return;
-  const int64_t row = at / p.units;
-  const int u = static_cast<int>(at - row * p.units);
-  const int64_t b = row / p.S, s = row - b * p.S;
-  const bool turn = u < p.rot_units;
-  // the unit's two runs of N elements in a head
-  int e0, e1;
-  if (!turn) {
-    e0 = p.rot + (u - p.rot_units) * 2 * N;
-    e1 = e0 + N;
-  } else if (INTER) {
-    e0 = u * 2 * N;
-    e1 = e0 + N;
-  } else {
-    e0 = u * N;
-    e1 = p.rot / 2 + u * N;
-  }
-  float c[N], n[N];
-  if (turn) {
-    const int64_t at_pos = p.pos_shared ? s : row;
+  __shared__ __align__(16) float2 cs[kTokenPairs];  // (cosine, sine) of each (token, pair)
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+  const int tokens = static_cast<int>(p.rows - row0 < p.tokens ? p.rows - row0 : p.tokens);
+  const int h0 = blockIdx.y * p.block_heads, heads = min(p.block_heads, p.heads - h0);
+  const int per_token = heads * p.units, items = tokens * per_token, half = p.rot / 2;
+  using R = Run<T, N>;
+  struct Item {
+    const char* src;
+    char* dst;
+    int e1;    // second run, relative to the first, in elements
+    int at;    // (token, first pair) in `cs`, or -1 outside the turned part
+    bool two;  // the second run is there
+  };
+  auto item = [&](int i) {
+    Item it;
+    const int tok = i / per_token, in = i - tok * per_token, hh = in / p.units, u = in - hh * p.units, h = h0 + hh;
+    const int64_t row = row0 + tok, b = row / p.S, s = row - b * p.S;
+    int e0;
+    if (u >= p.rot_units) {
+      e0 = p.rot + (u - p.rot_units) * 2 * N;
+      it.e1 = N;
+      it.at = -1;
+    } else {
+      e0 = INTER ? u * 2 * N : u * N;
+      it.e1 = INTER ? N : half;
+      it.at = tok * half + u * N;
+    }
+    it.two = VEC_TAIL || e0 + it.e1 + N <= p.D;  // a tail may end with a single run
+    if (h < p.heads_q) {
+      it.src = p.qi.p + b * p.qi.sb + s * p.qi.ss + h * p.qi.sh + e0 * int(sizeof(T));
+      it.dst = p.qo.p + b * p.qo.sb + s * p.qo.ss + h * p.qo.sh + e0 * int(sizeof(T));
+    } else {
+      it.src = p.ki.p + b * p.ki.sb + s * p.ki.ss + (h - p.heads_q) * p.ki.sh + e0 * int(sizeof(T));
+      it.dst = p.ko.p + b * p.ko.sb + s * p.ko.ss + (h - p.heads_q) * p.ko.sh + e0 * int(sizeof(T));
+    }
+    return it;
+  };
+  constexpr int UNROLL = 2;
+  R x[UNROLL], y[UNROLL];
+  Item it[UNROLL];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < UNROLL; ++j) {
+      const int i = i0 + j * kThreads;
+      if (i < items) {
+        it[j] = item(i);
+        x[j] = *reinterpret_cast<const R*>(it[j].src);
+        if (it[j].two) y[j] = *reinterpret_cast<const R*>(it[j].src + it[j].e1 * int(sizeof(T)));
+      }
+    }
+  };
+  load(threadIdx.x);
+  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
+    const int tok = i / half;
+    const int64_t row = row0 + tok, at_pos = p.pos_shared ? row % p.S : row;
     const int64_t pos = p.pos_i64 ? static_cast<const int64_t*>(p.pos)[at_pos]
                                   : static_cast<int64_t>(static_cast<const int32_t*>(p.pos)[at_pos]);
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const uint64_t f = static_cast<uint64_t>(pos) * tab[u * N + i];
-      sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &n[i], &c[i]);
-      c[i] *= p.amp;
-      n[i] *= p.amp * p.sign;
-    }
+    const uint64_t f = static_cast<uint64_t>(pos) * turns.t[i - tok * half];
+    float c, n;
+    sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &n, &c);
+    cs[i] = make_float2(c * p.amp, n * p.amp * p.sign);
   }
-  const bool second = VEC_TAIL || e1 + N <= p.D;  // a tail may end with a single run
-  const int h0 = blockIdx.y * p.heads_per_thread;
-  const int h1 = min(p.heads, h0 + p.heads_per_thread);
-  constexpr int UNROLL = 4;
-  const int64_t in_q = b * p.qi.sb + s * p.qi.ss, in_k = b * p.ki.sb + s * p.ki.ss;
-  const int64_t out_q = b * p.qo.sb + s * p.qo.ss, out_k = b * p.ko.sb + s * p.ko.ss;
-  using R = Run<T, N>;
-  for (int hh = h0; hh < h1; hh += UNROLL) {
-    R x[UNROLL], y[UNROLL];
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < items; i0 += UNROLL * kThreads) {
+    if (i0 != static_cast<int>(threadIdx.x)) load(i0);
 #pragma unroll
     for (int j = 0; j < UNROLL; ++j) {
-      const int h = hh + j;
-      if (h < h1) {
-        const char* src = h < p.heads_q ? p.qi.p + in_q + h * p.qi.sh : p.ki.p + in_k + (h - p.heads_q) * p.ki.sh;
-        x[j] = *reinterpret_cast<const R*>(src + e0 * sizeof(T));
-        if (second) y[j] = *reinterpret_cast<const R*>(src + e1 * sizeof(T));
-      }
-    }
+      if (i0 + j * kThreads >= items) break;
+      if (it[j].at >= 0) {
+        const float2* t = cs + it[j].at;
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int h = hh + j;
-      if (h < h1) {
-        char* dst = h < p.heads_q ? p.qo.p + out_q + h * p.qo.sh : p.ko.p + out_k + (h - p.heads_q) * p.ko.sh;
-        if (turn) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            // the unit's 2 N elements: pair i is (x_i, y_i), or elements 2i and 2i+1 of x followed by y
-            T& ra = INTER ? (2 * i < N ? x[j].v[2 * i < N ? 2 * i : 0] : y[j].v[2 * i < N ? 0 : 2 * i - N]) : x[j].v[i];
-            T& rb = INTER ? (2 * i + 1 < N ? x[j].v[2 * i + 1 < N ? 2 * i + 1 : 0]
-                                           : y[j].v[2 * i + 1 < N ? 0 : 2 * i + 1 - N])
-                          : y[j].v[i];
-            const float a = to_f(ra), d = to_f(rb);
-            ra = from_f<T>(fmaf(a, c[i], -d * n[i]));
-            rb = from_f<T>(fmaf(d, c[i], a * n[i]));
-          }
+        for (int i = 0; i < N; ++i) {
+          // the unit's 2 N elements: pair i is (x_i, y_i), or elements 2i and 2i+1 of x followed by y
+          T& ra = INTER ? (2 * i < N ? x[j].v[2 * i < N ? 2 * i : 0] : y[j].v[2 * i < N ? 0 : 2 * i - N]) : x[j].v[i];
+          T& rb = INTER ? (2 * i + 1 < N ? x[j].v[2 * i + 1 < N ? 2 * i + 1 : 0]
+                                         : y[j].v[2 * i + 1 < N ? 0 : 2 * i + 1 - N])
+                        : y[j].v[i];
+          const float a = to_f(ra), d = to_f(rb);
+          ra = from_f<T>(fmaf(a, t[i].x, -d * t[i].y));
+          rb = from_f<T>(fmaf(d, t[i].x, a * t[i].y));
         }
-        *reinterpret_cast<R*>(dst + e0 * sizeof(T)) = x[j];
-        if (second) *reinterpret_cast<R*>(dst + e1 * sizeof(T)) = y[j];
       }
+      *reinterpret_cast<R*>(it[j].dst) = x[j];
+      if (it[j].two) *reinterpret_cast<R*>(it[j].dst + it[j].e1 * int(sizeof(T))) = y[j];
     }
   }
 }
@@ -238,15 +254,20 @@ int rope(const tps_rope_plan* plan, const tps_tensor* Q, const tps_tensor* K, co
   p.rot_units = p.rot / (2 * N);
   p.units = p.rot_units + (tail + 2 * N - 1) / (2 * N);
   const bool vec_tail = tail % (2 * N) == 0;
-  // Heads of one thread: as many as leave every SM 1024 threads, up to 8
-  // (the angles, some 200 instructions for 8 pairs, are formed once a thread).
-  const int64_t units = p.rows * p.units;
-  p.heads_per_thread = 8;
-  while (p.heads_per_thread > 1 && units * ((p.heads + p.heads_per_thread - 1) / p.heads_per_thread) < 152 * 1024)
-    p.heads_per_thread /= 2;
-  const int64_t blocks = (units + kThreads - 1) / kThreads;
-  const int64_t groups = (p.heads + p.heads_per_thread - 1) / p.heads_per_thread;
-  if (blocks > 0x7fffffff || groups > 65535) return fail(TPS_ERR_SHAPE, "too many tokens or heads for one launch");
+  // Tokens of one block: as many as leave every SM eight blocks, up to what
+  // `cs` holds; with few tokens, their heads are spread over blocks as well,
+  // down to one round of items each.
+  const int64_t sms = 152;
+  p.tokens = kTokenPairs / (p.rot / 2);
+  while (p.tokens > 1 && (p.rows + p.tokens - 1) / p.tokens < 8 * sms) p.tokens /= 2;
+  const int64_t blocks = (p.rows + p.tokens - 1) / p.tokens;
+  p.block_heads = p.heads;
+  while (p.block_heads > 1 && blocks * ((p.heads + p.block_heads - 1) / p.block_heads) < 2 * sms &&
+         int64_t(p.tokens) * p.block_heads * p.units > kThreads)
+    p.block_heads = (p.block_heads + 1) / 2;
+  const int64_t groups = (p.heads + p.block_heads - 1) / p.block_heads;
+  if (blocks > 0x7fffffff || groups > 65535 || int64_t(p.tokens) * p.block_heads * p.units > (1 << 30))
+    return fail(TPS_ERR_SHAPE, "too many tokens or heads for one launch");
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
   Turns t;
   memcpy(t.t, plan->turns, sizeof(t.t));

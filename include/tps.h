@@ -476,7 +476,8 @@ int tps_rope_bwd(const tps_rope_plan* plan, const tps_tensor* dQo, const tps_ten
  * stochastic != 0: e4m3 moments, and bf16 weights without a master copy, are
  * rounded up or down at random so that they keep their expectation; the
  * random bits are a function of `seed` (another one each step) and of each
- * element's place = tensor.place + its index.  Otherwise they are rounded to
+ * element's place = tensor.place (a multiple of TPS_ADAMW_BLOCK) + its index.
+ * Otherwise they are rounded to
  * nearest, which leaves e4m3 moments where they are once they change by less
  * than half a step.
  * device_scalars (device, 16-byte aligned, NULL: computed from `hyper`): the

@@ -15,18 +15,18 @@ def _opts(ignore=-100, vocab=0, red=0, reserved=0, den=0.0):
 
 
 def _r(t):
-    return ctypes.byref(t) if t is not None else None
+    return bytes(t) if t is not None else None
 
 
 def _fwd(lib, h=None, W=None, y=None, layout=0, o=None, loss=None, red=None, lse=None, ws=0x100000, n=1 << 40):
     return lib.tps_linear_ce_fwd(_r(h or _fake([8, 64], BF16)), _r(W or _fake([64, 512], BF16)),
-                                 _r(y or _fake([8], I64)), layout, _r(o), _r(loss or _fake([8])), _r(red),
+                                 _r(y or _fake([8], I64)), layout, ctypes.byref(o) if o else None, _r(loss or _fake([8])), _r(red),
                                  _r(lse or _fake([8])), ctypes.c_void_p(ws), n, None)
 
 
 def _bwd(lib, lse=None, g=None, o=None, dh=None, dW=None, ws=0x100000, n=1 << 40, none=False):
     return lib.tps_linear_ce_bwd(_r(_fake([8, 64], BF16)), _r(_fake([64, 512], BF16)), _r(_fake([8], I64)),
-                                 _r(lse or _fake([8])), _r(g), 0, _r(o),
+                                 _r(lse or _fake([8])), _r(g), 0, ctypes.byref(o) if o else None,
                                  None if none else _r(dh or _fake([8, 64])), None if none else _r(dW or _fake([64, 512])),
                                  ctypes.c_void_p(ws), n, None)
 

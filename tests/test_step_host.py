@@ -13,7 +13,7 @@ BF16, I32, I64, E4M3 = 1, 2, 3, 4
 
 
 def _r(t):
-    return ctypes.byref(t) if t is not None else None
+    return bytes(t) if t is not None else None
 
 
 def test_rope_plan_frequencies(lib):  # noqa: F811
@@ -57,7 +57,7 @@ def test_rope_refusals(lib):  # noqa: F811
     def call(q=None, k=None, pos=None, qo=None, ko=None, plan=plan, no_k=False):
         q, qo = q or _fake([6, 4, 64], BF16), qo or _fake([6, 4, 64], BF16)
         k, ko = (None, None) if no_k else (k or _fake([6, 2, 64], BF16), ko or _fake([6, 2, 64], BF16))
-        return lib.tps_rope_fwd(_r(plan), _r(q), _r(k), _r(pos or _fake([6], I64)), _r(qo), _r(ko), None)
+        return lib.tps_rope_fwd(ctypes.byref(plan), _r(q), _r(k), _r(pos or _fake([6], I64)), _r(qo), _r(ko), None)
     assert call(q=_fake([6, 256], BF16)) == 1                              # 2-D
     assert call(q=_fake([6, 4, 32], BF16), qo=_fake([6, 4, 32], BF16), no_k=True) == 1   # heads narrower than the plan
     assert call(qo=_fake([6, 4, 65], BF16)) == 1 and call(qo=_fake([6, 4, 64])) == 3
@@ -66,7 +66,7 @@ def test_rope_refusals(lib):  # noqa: F811
     assert call(q=_fake([6, 4, 64], BF16, [256, 1, 4])) == 4               # head not contiguous
     assert call(q=_fake([6, 4, 64], I32)) == 3
     assert call(pos=_fake([5], I64)) == 1 and call(pos=_fake([6])) == 3 and call(pos=_fake([6], I64, [2])) == 4
-    assert lib.tps_rope_fwd(_r(plan), _r(_fake([6, 4, 64])), _r(_fake([6, 2, 64])), _r(_fake([6], I64)),
+    assert lib.tps_rope_fwd(ctypes.byref(plan), _r(_fake([6, 4, 64])), _r(_fake([6, 2, 64])), _r(_fake([6], I64)),
                             _r(_fake([6, 4, 64])), None, None) == 9        # K without K out
     assert lib.tps_rope_fwd(None, _r(_fake([6, 4, 64])), None, _r(_fake([6], I64)), _r(_fake([6, 4, 64])), None, None) == 9
     assert call(plan=api.RopePlan()) == 9                                  # never initialised
@@ -91,7 +91,7 @@ def test_adamw_refusals(lib):  # noqa: F811
     for bad in (dict(lr=-1.0), dict(lr=math.nan), dict(beta1=1.0), dict(beta2=-0.1), dict(eps=-1e-9), dict(eps=math.inf),
                 dict(step=0), dict(weight_decay=math.inf), dict(beta2=math.nan)):
         assert _step(lib, _row(), **bad) == 9, bad
-    assert _step(lib, _row(numel=-1)) == 1
+    assert _step(lib, _row(numel=-1)) == 1 and _step(lib, _row(place=128)) == 9 and _step(lib, _row(place=-256)) == 9
     assert _step(lib, _row(param_dtype=I32)) == 3 and _step(lib, _row(grad_dtype=E4M3)) == 3
     assert _step(lib, _row(state_dtype=BF16)) == 3
     assert _step(lib, _row(master=0x5000)) == 3                            # master of fp32 weights
