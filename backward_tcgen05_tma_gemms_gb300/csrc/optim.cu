@@ -59,7 +59,7 @@ struct Table {
   const float* coef;
   const tps_adamw_scalars* dev;  // read instead of `s` when given
   tps_adamw_scalars s;
-  float b1, c1, b2, c2, rb2, rc2, eps;  // beta, 1 - beta, and the roots of the second pair
+  float b1, c1, b2, c2, eps;  // beta, 1 - beta
   Entry e[N];
 };
 
@@ -179,18 +179,18 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
   asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
-// x as e4m3 numbers with the block's scale.  SQRT: x >= 0 and nothing but 0 becomes 0.
-template <bool FULL, bool SQRT>
-__device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane, int n, float (&x)[2][4],
-                                             const uint32_t (&rnd)[2][4]) {
+// The largest magnitude of the warp's block, 0 where it is next to nothing.
+__device__ __forceinline__ float block_top(const float (&x)[2][4]) {
   float part = 0.0f;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int i = 0; i < 4; i += 2) part = max_nan(part, fabsf(x[j][i]), fabsf(x[j][i + 1]));
-  float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(part)));  // a NaN has the largest bits
-  if (a < 1e-30f) a = 0.0f;
-  if (lane == 0) *scale = __fmul_rn(a, 1.0f / 448.0f);
+  const float a = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(part)));  // a NaN has the largest bits
+  return a < 1e-30f ? 0.0f : a;
+}
+// x with its block's largest magnitude a brought to where 448 / a keeps all its bits.
+__device__ __forceinline__ float bring_down(float a, float (&x)[2][4]) {
   if (a > kLargeScale * 256.0f) {
     a *= kSmaller;
 #pragma unroll
@@ -198,7 +198,12 @@ __device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane,
 #pragma unroll
       for (int i = 0; i < 4; ++i) x[j][i] *= kSmaller;
   }
-  const float inv = (a > 0.0f ? __fdividef(448.0f, a) : a) * 0x1p-120f;
+  return a;
+}
+// x as e4m3 numbers, inv = 448 / a * 2^-120.  SQRT: x >= 0 and nothing but 0 becomes 0.
+template <bool FULL, bool SQRT>
+__device__ __forceinline__ void write8_codes(uint8_t* p, float inv, int lane, int n, const float (&x)[2][4],
+                                             const uint32_t (&rnd)[2][4]) {
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     uint32_t c[4];
@@ -227,17 +232,26 @@ __device__ __forceinline__ void write8_codes(uint8_t* p, float* scale, int lane,
   }
 }
 
-// Square root and quotient to two units each.  FAST also takes subnormals for
-// 0 (moments in 8 bits: their blocks end 2^-18 below the largest element).
-template <bool FAST>
+// Square root.  ROUNDED (it goes into the state: the codes then are those of
+// the correctly rounded root): Markstein's correction, P. Markstein,
+// "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990 -- with y near 1 / sqrt(x), r = x y is off by little and
+// r + (x - r^2) y / 2 by that squared before its one rounding.  Subnormals
+// count as 0 there.  Else to two units.
+template <bool ROUNDED>
 __device__ __forceinline__ float root_of(float x) {
+  if (ROUNDED) {
+    float y;
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    const float r = x * y;
+    const float c = fmaf(fmaf(-r, r, x), 0.5f * y, r);
+    return y < INFINITY ? c : x;  // 0 stays 0 (and infinity, whose y is 0, becomes a NaN)
+  }
   float r;
-  if (FAST)
-    asm("sqrt.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  else
-    asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
+// Quotient to two units; FAST takes subnormals for 0.
 template <bool FAST>
 __device__ __forceinline__ float over(float a, float b) {
   float r;
@@ -301,10 +315,9 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
     }
   }
   if (E4M3) {
-    // the constants go into the scales: b1 m, and sqrt(b2) sqrt(v)
     const bool bm = r.ms > kLargeScale, bv = r.vs > kLargeScale;
-    const float sm = (bm ? r.ms * kSmaller : r.ms) * 0x1p120f * t.b1;
-    const float sv = (bv ? r.vs * kSmaller : r.vs) * 0x1p120f * t.rb2;
+    const float sm = (bm ? r.ms * kSmaller : r.ms) * 0x1p120f;
+    const float sv = (bv ? r.vs * kSmaller : r.vs) * 0x1p120f;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
@@ -322,17 +335,17 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
         }
     }
   }
-  const float gm = coef * t.c1, gv = coef * t.rc2;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
+      const float gg = g[j][i] * coef;
       if (E4M3) {
-        m[j][i] = fmaf(g[j][i], gm, m[j][i]);
-        const float h = g[j][i] * gv;
-        v[j][i] = fmaf(h, h, root[j][i] * root[j][i]);
+        // One rounding an operation, as any elementary implementation has
+        // it: a last bit that differs here can move a code by a whole step.
+        m[j][i] = __fadd_rn(__fmul_rn(m[j][i], t.b1), __fmul_rn(gg, t.c1));
+        v[j][i] = __fadd_rn(__fmul_rn(__fmul_rn(root[j][i], root[j][i]), t.b2), __fmul_rn(__fmul_rn(gg, gg), t.c2));
       } else {
-        const float gg = g[j][i] * coef;
         m[j][i] = fmaf(m[j][i], t.b1, gg * t.c1);
         v[j][i] = fmaf(v[j][i], t.b2, gg * gg * t.c2);
       }
@@ -378,8 +391,15 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
     write8<FULL>(static_cast<float*>(e.p) + at, lane, n, w);
   }
   if (E4M3) {
-    write8_codes<FULL, false>(static_cast<uint8_t*>(e.m) + at, e.ms + unit, lane, n, m, rm);
-    write8_codes<FULL, true>(static_cast<uint8_t*>(e.v) + at, e.vs + unit, lane, n, root, rv);
+    // even lanes divide for m, odd ones for sqrt(v)
+    float am = block_top(m), av = block_top(root);
+    if (lane < 2) (lane ? e.vs : e.ms)[unit] = __fmul_rn(lane ? av : am, 1.0f / 448.0f);
+    am = bring_down(am, m);
+    av = bring_down(av, root);
+    const float a = (lane & 1) ? av : am;
+    const float inv = (a > 0.0f ? __fdiv_rn(448.0f, a) : a) * 0x1p-120f;
+    write8_codes<FULL, false>(static_cast<uint8_t*>(e.m) + at, __shfl_sync(0xffffffffu, inv, 0), lane, n, m, rm);
+    write8_codes<FULL, true>(static_cast<uint8_t*>(e.v) + at, __shfl_sync(0xffffffffu, inv, 1), lane, n, root, rv);
   } else {
     write8<FULL>(static_cast<float*>(e.m) + at, lane, n, m);
     write8<FULL>(static_cast<float*>(e.v) + at, lane, n, v);
@@ -447,8 +467,8 @@ constexpr int kAhead = 8;  // units of a warp in flight
 
 // Partial sums of squares, one for each block, of a fixed assignment of units.
 template <int N>
-__global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant__ Spans<N> t, float* part) {
-  __shared__ float red[kWarps];
+__global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant__ Spans<N> t, double* part) {
+  __shared__ double red[kWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
   // kAhead consecutive units of a warp at a time: inside one tensor, all
@@ -512,13 +532,13 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
       for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], acc[j]));
     }
   }
-  float a = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+  double a = (double(acc[0]) + acc[1]) + (double(acc[2]) + acc[3]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   if (lane == 0) red[w] = a;
   __syncthreads();
   if (threadIdx.x == 0) {
-    a = 0.0f;
+    a = 0.0;
     for (int i = 0; i < kWarps; ++i) a += red[i];
     part[blockIdx.x] = a;
   }
@@ -526,7 +546,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
 
 // norm = sqrt of the sum of the partial sums (fp64, fixed order) and the
 // coefficient that brings it to max_norm (max_norm <= 0: 1).
-__global__ void __launch_bounds__(1024) norm_finish_kernel(const float* part, int n, double max_norm, float* out) {
+__global__ void __launch_bounds__(1024) norm_finish_kernel(const double* part, int n, double max_norm, float* out) {
   __shared__ double red[32];
   double a = 0.0;
   for (int i = threadIdx.x; i < n; i += 1024) a += part[i];
@@ -543,7 +563,7 @@ __global__ void __launch_bounds__(1024) norm_finish_kernel(const float* part, in
   if (!isfinite(norm))
     c = __int_as_float(0x7fc00000);  // NaN: tps_adamw_step then changes nothing
   else if (max_norm > 0.0)
-    c = fminf(1.0f, static_cast<float>(max_norm / (static_cast<double>(norm) + 1e-6)));
+    c = fminf(1.0f, __fdiv_rn(static_cast<float>(max_norm), __fadd_rn(norm, 1e-6f)));
   out[1] = c;
 }
 
@@ -573,7 +593,7 @@ int launch_adamw(const Table<kMany>& all, int64_t elements, int per_element, cud
 }
 
 template <int N>
-int launch_norm(const Spans<kMany>& all, float* part, int blocks, cudaStream_t s) {
+int launch_norm(const Spans<kMany>& all, double* part, int blocks, cudaStream_t s) {
   Spans<N> t;
   t.count = all.count;
   t.units = all.units;
@@ -688,8 +708,6 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
     tab.c1 = static_cast<float>(1.0 - h->beta1);
     tab.b2 = static_cast<float>(h->beta2);
     tab.c2 = static_cast<float>(1.0 - h->beta2);
-    tab.rb2 = static_cast<float>(std::sqrt(h->beta2));
-    tab.rc2 = static_cast<float>(std::sqrt(1.0 - h->beta2));
     tab.eps = static_cast<float>(h->eps);
     int64_t elements = 0;
     for (int32_t i = 0; i <= n; ++i) {
@@ -714,7 +732,7 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
 }
 
 extern "C" size_t tps_grad_norm_workspace_bytes(int32_t n) {
-  return n < 0 ? 0 : align256(static_cast<size_t>(kNormBlocks) * ((n + kMany - 1) / kMany + 1) * sizeof(float));
+  return n < 0 ? 0 : align256(static_cast<size_t>(kNormBlocks) * ((n + kMany - 1) / kMany + 1) * sizeof(double));
 }
 
 extern "C" int tps_grad_norm(const tps_span* grads, int32_t n, double max_norm, float* out, void* workspace,
@@ -735,7 +753,7 @@ extern "C" int tps_grad_norm(const tps_span* grads, int32_t n, double max_norm, 
       return fail(TPS_ERR_LAYOUT, "gradient %d: misaligned data", i);
   }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  float* part = static_cast<float*>(workspace);
+  double* part = static_cast<double*>(workspace);
   Spans<kMany> t;
   t.count = 0;
   t.units = 0;

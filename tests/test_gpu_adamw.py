@@ -172,6 +172,52 @@ def test_moments_move_under_random_rounding():
     assert mean[None] > 0.99
 
 
+def dither(place, seed):
+    """The 32 random bits of each place, from the definition."""
+    x = ((place & 0xffffffff) * 0x9e3779b1 + (place >> 32) * 0x85ebca77) & 0xffffffff
+    x = x ^ seed
+    x = ((x ^ (x >> 16)) * 0x2c1b3c6d) & 0xffffffff
+    x = ((x ^ (x >> 12)) * 0x297a2d39) & 0xffffffff
+    return x ^ (x >> 15)
+
+
+@pytest.mark.parametrize("scale", [1e-6, 1.0, 1e7])
+def test_e4m3_codes_bit_for_bit(scale):
+    """Codes and scales are those of the update in fp32 with one rounding an
+    operation, two steps in a row: at ordinary sizes, and for blocks whose
+    scales pass what a float holds times 2^120."""
+    n, b1, b2 = 256 * 200, 0.9, 0.95
+    place = torch.arange(n, device="cuda")
+    p = torch.zeros(n, device="cuda")
+    plan = api.adamw_plan([p], E4M3)
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+
+    def coded(x, rnd, keep):
+        x, rnd = x.view(-1, 256), rnd.view(-1, 256)
+        top = x.abs().amax(1)
+        y = (x.abs() * (448.0 / top)[:, None]).clamp(max=448.0)
+        big = ((y.view(torch.int32).long() + (rnd << 4)) >> 20) - 960
+        code = torch.where(y >= 2.0 ** -6, big, (y * 512 + rnd.float() / 65536).floor().long())
+        if keep:
+            code = torch.where((y > 0) & (code == 0), 1, code)
+        value = code.to(torch.uint8).view(E4M3).float() * torch.where(x < 0, -1.0, 1.0)
+        s = top * (1.0 / 448)
+        return value.flatten(), s, (value * s[:, None]).flatten()
+    for step in (1, 2):
+        g = torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(step)) * scale
+        api.adamw_step(plan, [g], step=step, seed=step, lr=0.0, beta1=b1, beta2=b2)
+        m, v = m * b1 + g * (1 - b1), v * b2 + g * g * (1 - b2)
+        bits = dither(place, step)
+        cm, sm, m = coded(m, bits & 0xffff, False)
+        cv, sv, root = coded(v.sqrt(), bits >> 16, True)
+        v = root * root
+        assert torch.equal(plan.m_scale[0], sm) and torch.equal(plan.v_scale[0], sv)
+        # below 2^-6 the sum with the random bits is rounded elsewhere: a code in a million may differ there
+        for got, want in ((plan.m[0].float(), cm), (plan.v[0].float(), cv)):
+            assert torch.equal(got[want.abs() >= 2.0 ** -5], want[want.abs() >= 2.0 ** -5])
+            assert (got - want).abs().max() <= 2.0 ** -9
+
+
 def test_one_place_one_random_number():
     """Tensors of a plan draw from one stream: cut at block borders, they get the same bits."""
     n = 256 * 10
