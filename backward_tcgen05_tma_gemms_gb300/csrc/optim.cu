@@ -200,7 +200,7 @@ __device__ __forceinline__ float bring_down(float a, float (&x)[2][4]) {
   }
   return a;
 }
-// x as e4m3 numbers, inv = 448 / a * 2^-120.  SQRT: x >= 0 and nothing but 0 becomes 0.
+// x as e4m3 numbers, inv = 448 (1 / a) 2^-120.  SQRT: x >= 0 and nothing but 0 becomes 0.
 template <bool FULL, bool SQRT>
 __device__ __forceinline__ void write8_codes(uint8_t* p, float inv, int lane, int n, const float (&x)[2][4],
                                              const uint32_t (&rnd)[2][4]) {
@@ -391,13 +391,13 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
     write8<FULL>(static_cast<float*>(e.p) + at, lane, n, w);
   }
   if (E4M3) {
-    // even lanes divide for m, odd ones for sqrt(v)
+    // even lanes form the reciprocal for m, odd ones for sqrt(v)
     float am = block_top(m), av = block_top(root);
     if (lane < 2) (lane ? e.vs : e.ms)[unit] = __fmul_rn(lane ? av : am, 1.0f / 448.0f);
     am = bring_down(am, m);
     av = bring_down(av, root);
     const float a = (lane & 1) ? av : am;
-    const float inv = (a > 0.0f ? __fdiv_rn(448.0f, a) : a) * 0x1p-120f;
+    const float inv = (a > 0.0f ? __fmul_rn(__frcp_rn(a), 448.0f) : a) * 0x1p-120f;
     write8_codes<FULL, false>(static_cast<uint8_t*>(e.m) + at, __shfl_sync(0xffffffffu, inv, 0), lane, n, m, rm);
     write8_codes<FULL, true>(static_cast<uint8_t*>(e.v) + at, __shfl_sync(0xffffffffu, inv, 1), lane, n, root, rv);
   } else {
@@ -470,7 +470,7 @@ template <int N>
 __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant__ Spans<N> t, double* part) {
   __shared__ double red[kWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  double total = 0.0;
   // kAhead consecutive units of a warp at a time: inside one tensor, all
   // their loads are in flight before the first sum
   const int64_t runs = (t.units + kAhead - 1) / kAhead;
@@ -478,6 +478,9 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
   int k = entry_of(t.e, t.count, r * kAhead);
   for (; r < runs; r += static_cast<int64_t>(gridDim.x) * kWarps) {
     const int64_t u0 = r * kAhead;
+    // a run's 64 squares of a lane in fp32, runs in fp64: a long fp32 sum
+    // would lose the small terms, always downwards
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     while (k + 1 < t.count && u0 >= t.e[k + 1].first) ++k;
     const int64_t at0 = (u0 - t.e[k].first) * kUnit;
     if (t.e[k].wide && t.e[k].n - at0 >= kAhead * kUnit) {
@@ -508,6 +511,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
           acc[3] = fmaf(q[i].w, q[i].w, acc[3]);
         }
       }
+      total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
       continue;
     }
     int kk = k;
@@ -531,8 +535,9 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
 #pragma unroll
       for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], acc[j]));
     }
+    total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
   }
-  double a = (double(acc[0]) + acc[1]) + (double(acc[2]) + acc[3]);
+  double a = total;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
   if (lane == 0) red[w] = a;
