@@ -277,6 +277,10 @@ int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream) {
     t.b3_sn = g.a3_sm;
     t.epi.ldd = d_sn;
     t.wide = false;
+    t.a_plane = g.b_plane;
+    t.a_cols = g.b_cols;
+    t.b_plane = g.a_plane;
+    t.b_cols = g.a_cols;
     if (g.ce_grad.ms != nullptr) return fail(TPS_ERR_LAYOUT, "%s: the CE-gradient operand needs a row-major output", g.name);
     g = t;
   } else {
@@ -291,7 +295,9 @@ int run_gemm(GemmDesc g, int64_t d_sm, int64_t d_sn, cudaStream_t stream) {
   else if (g.ce_grad.ms != nullptr)
     return fail(TPS_ERR_ARG, "%s: the CE-gradient operand needs the wide-tile kernel", g.name);
   else
-    rc = gemm_tc_supported(g) ? launch_gemm_tc(g, err, stream) : launch_gemm_simt(g, err, stream);
+    rc = gemm_tc_supported(g) ? launch_gemm_tc(g, err, stream)
+         : g.planes > 1       ? fail(TPS_ERR_ARG, "%s: planes need the tensor-core kernel", g.name)
+                              : launch_gemm_simt(g, err, stream);
   if (rc == TPS_ERR_CUDA) return fail(rc, "%s: launch failed: %s", g.name, cudaGetErrorString(cudaGetLastError()));
   return rc;
 }

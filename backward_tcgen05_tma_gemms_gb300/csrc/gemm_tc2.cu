@@ -97,6 +97,8 @@ struct T2Params {
   int k_end[3];                              // cumulative K tiles of the contraction segments
   int n_segs, n_end[3];                      // column segments: cumulative column ends
   int glu;                                   // EPI_GLU_FWD: b[1] is the up weight
+  // planes (GemmDesc::planes): K tiles of one product of planes, else 0
+  int kt1, a_plane, b_plane, d_plane, n_store;
   int raster_n, group;
   int pol_a, pol_b;  // L2 policy kinds of the operand loads (0 none, 1 evict-first, 2 evict-last)
   int tma_store;
@@ -242,20 +244,29 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             while (ks < 2 && kt >= p.k_end[ks]) ++ks;
           const CUtensorMap* ma = &m.a[ks];
           const CUtensorMap* mb = ks > 0 ? &m.b[ks] : mb0;
-          const int k0 = (kt - (ks > 0 ? p.k_end[ks - 1] : 0)) * TC_BK;
+          int k0 = (kt - (ks > 0 ? p.k_end[ks - 1] : 0)) * TC_BK;
+          int xa = 0, xb = 0;  // the operands' planes along their contiguous dimensions
+          if constexpr (FAM == T2_PLAIN || FAM == T2_CE) {
+            if (p.kt1 > 0) {
+              const int prod = kt / p.kt1;  // planes of A: 2 1 0 1 0 0, of B: 0 1 2 0 1 0
+              k0 = (kt - prod * p.kt1) * TC_BK;
+              xa = ((0x046 >> (2 * prod)) & 3) * p.a_plane;
+              xb = ((0x124 >> (2 * prod)) & 3) * p.b_plane;
+            }
+          }
           if (!A_MN) {
-            pair_load(sa, ma, fb, k0, m0, p.pol_a, pa);
+            pair_load(sa, ma, fb, k0 + xa, m0, p.pol_a, pa);
           } else {
 #pragma unroll
             for (int j = 0; j < T2_BM / 64; ++j)
-              pair_load(sa + j * TC_MN_BOX_BYTES, ma, fb, m0 + 64 * j, k0, p.pol_a, pa);
+              pair_load(sa + j * TC_MN_BOX_BYTES, ma, fb, m0 + xa + 64 * j, k0, p.pol_a, pa);
           }
           if (!B_MN) {
-            pair_load(sb, mb, fb, k0, nb0, p.pol_b, pb);
+            pair_load(sb, mb, fb, k0 + xb, nb0, p.pol_b, pb);
           } else {
 #pragma unroll
             for (int j = 0; j < T2_BN_CTA / 64; ++j)
-              pair_load(sb + j * TC_MN_BOX_BYTES, mb, fb, nb0 + 64 * j, k0, p.pol_b, pb);
+              pair_load(sb + j * TC_MN_BOX_BYTES, mb, fb, nb0 + xb + 64 * j, k0, p.pol_b, pb);
           }
           ++issued;
           if (++stage == T2_STAGES) {
@@ -420,7 +431,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
       }
       for (int c = 0; !ce_done && c < warp_cols / 32; ++c) {
         const int col0 = nh0 + c * 32;
-        if (col0 >= p.N) break;  // warp-uniform
+        if (col0 >= (FAM == T2_CE ? p.n_store : p.N)) break;  // warp-uniform
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_row + c * 32, r);
         if constexpr (glu) {  // gate in r, the same hidden units' up projection 128 columns on
@@ -484,7 +495,22 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
         }
         // the fp32 and bf16 slots (store-only: one shared box), single- or double-buffered
         uint8_t* buf = stg + (L::kBufs == 2 ? (chunk & 1u) * L::kBufBytes : 0u);
-        if constexpr (FAM == T2_CE) ce_grad32(ce_row, e.ce_col0 + col0, v);
+        if constexpr (FAM == T2_CE) {
+          ce_grad32(ce_row, e.ce_col0 + col0, v);
+          if (p.d_plane > 0) {  // three bf16 planes whose sum is the fp32 gradient, zeros past column N
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i >= n) v[i] = 0.0f;
+            for (int pl = 0; pl < 3; ++pl) {
+              buf = stg + (chunk & 1u) * L::kBufBytes;
+              tc_store_chunk<L::kBufs - 1, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0 + pl * p.d_plane, v, a);
+              ++chunk;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+            }
+            continue;
+          }
+        }
         if constexpr (FAM == T2_PLAIN) {
           if (run > 0 || e.accumulate) {  // K split (or a sum over pieces): add this partial tile to the output
             tc_store_chunk<L::kBufs - 1, true, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, a);
@@ -559,7 +585,8 @@ static int launch_pair_typed(const GemmDesc& g, const T2Maps& m, const T2Params&
     if (max_clusters < 1) return TPS_ERR_CUDA;
     if (pairs > max_clusters) cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
   }
-  const double flops = 2.0 * double(g.M) * double(g.N) * double(g.K + g.K2 + g.K3) * (p.glu ? 2.0 : 1.0);
+  const double flops = 2.0 * double(g.M) * double(g.N) * double(g.K + g.K2 + g.K3) * (p.glu ? 2.0 : 1.0) *
+                       (g.planes > 1 ? 6.0 : 1.0);
   ProfScope prof("gemm_tc", g.name, flops, 0.0, stream);
   const cudaError_t e =
       cudaLaunchKernelEx(&cfg, gemm_tc2_kernel<A_MN, B_MN, FAM>, m, p);
@@ -594,10 +621,11 @@ static int launch_pair_family(const GemmDesc& g, const T2Maps& m, const T2Params
   return launch_pair_majors<T2_PLAIN>(g, m, p, pairs, a_mn, b_mn, stream);
 }
 
+// `cols` > 0: the extent of the contiguous dimension, where it is not the operand's own (planes).
 static bool pair_operand_map(CUtensorMap* map, const void* base, bool mn, int64_t K, int64_t MN, int64_t ld,
-                             int box_mn) {
-  return mn ? tc_make_map(map, base, K, MN, ld, 64, TC_BK)       // stored K x MN
-            : tc_make_map(map, base, MN, K, ld, TC_BK, box_mn);  // stored MN x K
+                             int box_mn, int64_t cols = 0) {
+  return mn ? tc_make_map(map, base, K, cols > 0 ? cols : MN, ld, 64, TC_BK)       // stored K x MN
+            : tc_make_map(map, base, MN, cols > 0 ? cols : K, ld, TC_BK, box_mn);  // stored MN x K
 }
 
 int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
@@ -622,8 +650,9 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   bool ok = true;
   for (int s = 0; s < 3; ++s) {
     if (s > 0 && ks[s] == 0) continue;
-    ok = ok && pair_operand_map(&m.a[s], as[s], a_mn, ks[s], g.M, a_mn ? a_sk[s] : a_sm[s], T2_BM);
-    if (!n_segs) ok = ok && pair_operand_map(&m.b[s], bs[s], b_mn, ks[s], g.N, b_mn ? b_sk[s] : b_sn[s], T2_BN_CTA);
+    ok = ok && pair_operand_map(&m.a[s], as[s], a_mn, ks[s], g.M, a_mn ? a_sk[s] : a_sm[s], T2_BM, g.a_cols);
+    if (!n_segs)
+      ok = ok && pair_operand_map(&m.b[s], bs[s], b_mn, ks[s], g.N, b_mn ? b_sk[s] : b_sn[s], T2_BN_CTA, g.b_cols);
   }
   if (glu) ok = ok && pair_operand_map(&m.b[1], g.b_up, b_mn, g.K, g.N, b_mn ? g.b_sk : g.b_sn, T2_BN_CTA);
   if (n_segs)
@@ -643,6 +672,20 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   for (int s = 0; s < 3; ++s) {
     kt += static_cast<int>((ks[s] + TC_BK - 1) / TC_BK);
     p.k_end[s] = kt;
+  }
+  p.kt1 = p.a_plane = p.b_plane = p.d_plane = 0;
+  p.n_store = p.N;
+  if (g.planes > 1) {
+    if (g.planes != 3 || k_segs || n_segs || glu) return TPS_ERR_ARG;
+    p.kt1 = kt;
+    kt *= 6;
+    p.k_end[0] = p.k_end[1] = p.k_end[2] = kt;
+    p.a_plane = static_cast<int>(g.a_plane);
+    p.b_plane = static_cast<int>(g.b_plane);
+    if (g.epi.mode == EPI_CE_GRAD) {
+      p.d_plane = static_cast<int>(g.d_plane);
+      p.n_store = static_cast<int>(g.n_store);
+    }
   }
   p.k_tiles = kt;
   p.n_segs = g.n_segs;
@@ -681,7 +724,10 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   if (g.epi.mode == EPI_CE_LSE) {  // only the statistics leave the kernel
     p.tma_store = 0;
   } else {
-    p.tma_store = tc_make_output_maps(g, &m.d[0], &m.d[1], &m.d[2]) ? 1 : 0;
+    if (p.d_plane > 0)
+      p.tma_store = tc_make_out_map(&m.d[0], g.epi.d, g.M, 3 * g.d_plane, g.epi.ldd, TPS_BF16) ? 1 : 0;
+    else
+      p.tma_store = tc_make_output_maps(g, &m.d[0], &m.d[1], &m.d[2]) ? 1 : 0;
     if (g.epi.mode == EPI_CE_GRAD && !p.tma_store) return TPS_ERR_LAYOUT;
     if (g.epi.accumulate && (!p.tma_store || g.epi.mode != EPI_STORE || g.epi.d_dtype != TPS_F32 || n_segs || k_segs))
       return TPS_ERR_LAYOUT;

@@ -455,7 +455,7 @@ __global__ void __launch_bounds__(W_THREADS, 1) gemm_wide_kernel(const __grid_co
 bool gemm_wide_supported(const GemmDesc& g) {
   if (!gemm_tc_supported(g)) return false;
   if (g.epi.mode != EPI_STORE || g.epi.d_dtype != TPS_F32) return false;
-  if (g.a_sk != 1 || g.n_segs > 1 || g.K2 > 0 || g.K3 > 0) return false;
+  if (g.a_sk != 1 || g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.planes > 1) return false;
   if (g.epi.d == nullptr || (reinterpret_cast<uintptr_t>(g.epi.d) & 15u) != 0 || (g.epi.ldd * 4) % 16 != 0 ||
       g.epi.ldd < g.N)
     return false;

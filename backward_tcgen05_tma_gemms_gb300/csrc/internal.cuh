@@ -200,6 +200,18 @@ struct GemmDesc {
   // counter as they start on them, instead of the static round-robin (pair
   // p: units p, p + pairs, ...).  Results are the same bits either way.
   uint32_t* unit_counter = nullptr;
+  // Operands held as three bf16 planes whose sum is an fp32 value (CTA-pair
+  // kernel, EPI_STORE, EPI_CE_LSE and EPI_CE_GRAD): planes = 3, plane i of A
+  // lying a_plane elements further along A's contiguous dimension (which
+  // holds a_cols elements in all, zeros between K and a whole K tile), B
+  // likewise.  The contraction runs over the six products of planes that
+  // matter at fp32's 2^-24, smallest first: (2,0) (1,1) (0,2) (1,0) (0,1) (0,0).
+  // EPI_CE_GRAD then writes D as planes too, d_plane columns apart, with
+  // zeros from column N up to n_store.  planes = 1 with a_cols / b_cols set:
+  // only the extents.
+  int planes = 1;
+  int64_t a_plane = 0, b_plane = 0, a_cols = 0, b_cols = 0;
+  int64_t d_plane = 0, n_store = 0;
   const char* name = "gemm";  // label used by the launch profiler
 };
 // Pair tiles of a GEMM on the CTA-pair kernel (the size of GemmDesc::kflags).

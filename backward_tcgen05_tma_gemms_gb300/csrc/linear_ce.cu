@@ -23,8 +23,13 @@
 // 8 T d V operations against the 6 T d V of a backward pass that is given
 // the logits: the quarter more is what not keeping them costs.
 //
-// Other operands (fp32, or bf16 that TMA cannot describe) run the same
-// pieces through the fp32-FMA GEMM, with the logits of one piece in fp32.
+// fp32 operands take the tensor cores too: each value is the sum of three
+// bf16 values exactly (8 + 8 + 8 bits), and of the nine products of such
+// planes the six that reach fp32's 2^-24 are summed into one fp32
+// accumulator, smallest first (GemmDesc::planes); dz is split the same way in
+// the epilogue.  Six times the tensor-core work of bf16 is still a fraction of
+// the fp32 pipes' time.  These planes, and bf16 operands that TMA cannot
+// describe, are laid out in the workspace, Whead one piece at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -164,47 +169,42 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, co
   }
 }
 
-// fp32 logits of a piece: the pair of each row (one block a row).
-__global__ void __launch_bounds__(256) ce_piece_stats_kernel(const float* z, int64_t ld, int64_t n, int64_t col0,
-                                                             Labels lab, float2* pairs, float* zy) {
-  __shared__ float2 part[8];
-  const int64_t t = blockIdx.x;
-  const float* row = z + t * ld;
-  float m = -INFINITY, s = 0.0f;
-  for (int64_t j = threadIdx.x; j < n; j += 256) m = fmaxf(m, row[j]);
+// Lays an operand out for TMA: rows x cols of bf16, or three planes of an
+// fp32 one side by side, each `plane` columns with zeros from `cols` on.
+// Plane 1 holds what plane 0's rounding left, plane 2 what both left: exactly
+// the value, unless its last bits are below bf16's smallest number.
+template <class T>
+__global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows, int64_t cols, int64_t ld,
+                                                     __nv_bfloat16* dst, int64_t plane) {
+  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
+  const int64_t per = plane / 8;
+  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
+    const int64_t r = i / per, c = (i - r * per) * 8;
+    const T* p = src + r * ld + c;
+    T x[8];
+    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  for (int64_t j = threadIdx.x; j < n; j += 256) s += m == -INFINITY && row[j] == m ? 0.0f : expf(row[j] - m);
+      for (int q = 0; q < static_cast<int>(sizeof(x)) / 16; ++q) reinterpret_cast<uint4*>(x)[q] = reinterpret_cast<const uint4*>(p)[q];
+    } else {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(m, s);
-  __syncthreads();
-  if (threadIdx.x != 0) return;
-  float M = -INFINITY, S = 0.0f;
-  for (int i = 0; i < 8; ++i) {  // accurate exponentials here: this path serves fp32
-    const float2 e = part[i];
-    const float N = fmaxf(M, e.x);
-    S = N == -INFINITY ? S + e.y : (M == -INFINITY ? S : S * expf(M - N)) + (e.x == -INFINITY ? e.y : e.y * expf(e.x - N));
-    M = N;
-  }
-  pairs[t] = make_float2(M, S);
-  const int64_t y = lab.at(t);
-  if (lab.kind(y) == 0 && y >= col0 && y < col0 + n) zy[t] = row[y - col0];
-}
-
-// fp32 logits of a piece to dz, in place or as bf16.
-template <class Out>
-__global__ void __launch_bounds__(256) ce_piece_grad_kernel(const float* z, int64_t ld, int64_t n, int64_t col0,
-                                                            const float4* rows, Out* dz, int64_t ldd) {
-  const int64_t t = blockIdx.x;
-  const float4 r = rows[t];
-  const int64_t y = static_cast<int64_t>(__float_as_int(r.z)) - col0;
-  for (int64_t j = threadIdx.x; j < n; j += 256) {
-    const float p = r.y == 0.0f ? 0.0f : r.y * (expf(z[t * ld + j] - r.w) - (j == y ? 1.0f : 0.0f));
-    if constexpr (sizeof(Out) == 4)
-      dz[t * ldd + j] = p;
-    else
-      dz[t * ldd + j] = __float2bfloat16_rn(p);
+      for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? p[j] : T(0.0f);
+    }
+    __nv_bfloat16* out = dst + r * kPlanes * plane + c;
+    if constexpr (kPlanes == 1) {
+      *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(x);
+    } else {
+#pragma unroll
+      for (int pl = 0; pl < 3; ++pl) {
+        __align__(16) __nv_bfloat16 b[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          b[j] = __float2bfloat16_rn(x[j]);
+          if (__hisinf(b[j]) && isfinite(x[j])) b[j] = __float2bfloat16_rz(x[j]);
+          x[j] = isfinite(x[j]) ? x[j] - __bfloat162float(b[j]) : 0.0f;  // infinities and NaN stay in plane 0
+        }
+        *reinterpret_cast<uint4*>(out + pl * plane) = *reinterpret_cast<const uint4*>(b);
+      }
+    }
   }
 }
 
@@ -259,6 +259,8 @@ int check_call(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* l
   if (c->V >= (1ll << 31) || c->T >= (1ll << 31) || c->d >= (1ll << 31))
     return fail(TPS_ERR_SHAPE, "an extent of 2^31 or more");
   c->dt = c->h.dtype;
+  if (c->dt == TPS_F32 && (c->T >= (1 << 29) || c->d >= (1 << 29) || c->V >= (1 << 29)))
+    return fail(TPS_ERR_SHAPE, "an fp32 extent of 2^29 or more");  // three planes side by side stay below 2^31
   if ((c->dt != TPS_F32 && c->dt != TPS_BF16) || c->w.dtype != c->dt)
     return fail(TPS_ERR_DTYPE, "h and Whead must share f32 or bf16");
   if (labels == nullptr) return fail(TPS_ERR_ARG, "labels missing");
@@ -284,36 +286,110 @@ int check_call(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* l
   return TPS_OK;
 }
 
-// The logits GEMM of rows [r0, r0 + rows) and vocabulary columns [v0, v0 + n).
-GemmDesc logits_gemm(const Call& c, int64_t r0, int64_t rows, int64_t v0, int64_t n) {
+int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
+
+// An operand X(i, j) as the GEMMs take it: the caller's, or laid out anew.
+struct Operand {
+  const char* p = nullptr;
+  int64_t si = 0, sj = 0;         // strides of i and j, one of them 1
+  int64_t plane = 0, cols = 0;    // GemmDesc::a_plane, a_cols when laid out
+};
+struct Layout {  // of all operands of a call
+  bool direct = true;  // bf16 as TMA takes it
+  int planes = 1;
+};
+
+bool tma_can(const void* p, int64_t si, int64_t sj) {
+  const int64_t outer = sj == 1 ? si : sj;
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (si == 1 || sj == 1) && outer % 8 == 0;
+}
+Layout layout_of(const Call& c) {
+  Layout l;
+  l.planes = c.dt == TPS_F32 ? 3 : 1;
+  GemmDesc g;  // the logits GEMM as it would be
+  g.M = c.T; g.N = c.vreal; g.K = c.d; g.in_dtype = c.dt;
+  g.a = c.h.data; g.a_sm = c.h.sr; g.a_sk = c.h.sc;
+  g.b = c.w.data; g.b_sk = c.w_in; g.b_sn = c.w_out;
+  l.direct = c.dt == TPS_BF16 && tma_can(g.a, g.a_sm, g.a_sk) && tma_can(g.b, g.b_sk, g.b_sn) && gemm_tc_supported(g);
+  return l;
+}
+// Bytes of X (ni x nj) laid out, in either orientation.
+int64_t laid_bytes(int64_t ni, int64_t nj, int planes) {
+  const int64_t a = ni * round_up(nj, 64), b = nj * round_up(ni, 64);
+  return 2 * planes * (a > b ? a : b);
+}
+
+int launched(const char* what) {
+  note_launch();
+  const cudaError_t e = cudaPeekAtLastError();
+  return e == cudaSuccess ? TPS_OK : fail(TPS_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(cudaGetLastError()));
+}
+
+// X (ni x nj, strides si, sj, of the call's dtype) laid out at `dst`.
+int lay_out(const Call& c, const char* src, int64_t ni, int64_t nj, int64_t si, int64_t sj, char* dst, cudaStream_t s,
+            Operand* o) {
+  const bool j_inner = sj == 1;
+  const int64_t rows = j_inner ? ni : nj, cols = j_inner ? nj : ni, ld = j_inner ? si : sj;
+  const int64_t plane = round_up(cols, 64), blocks = (rows * plane / 8 + 255) / 256;
+  const int planes = c.dt == TPS_F32 ? 3 : 1;
+  const unsigned grid = static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16);
+  ProfScope prof("ce_lay", "lce", 0.0, double(rows) * (double(cols) * (c.dt == TPS_F32 ? 4 : 2) + 2.0 * planes * double(plane)), s);
+  if (planes == 3)
+    ce_lay_kernel<float><<<grid, 256, 0, s>>>(reinterpret_cast<const float*>(src), rows, cols, ld,
+                                              reinterpret_cast<__nv_bfloat16*>(dst), plane);
+  else
+    ce_lay_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(src), rows, cols, ld,
+                                                      reinterpret_cast<__nv_bfloat16*>(dst), plane);
+  o->p = dst;
+  o->si = j_inner ? planes * plane : 1;
+  o->sj = j_inner ? 1 : planes * plane;
+  o->plane = plane;
+  o->cols = planes * plane;
+  return launched("ce_lay");
+}
+// The piece [v0, v0 + n) of Whead as Operand(d, v).
+int head_piece(const Call& c, const Layout& l, int64_t v0, int64_t n, char* room, cudaStream_t s, Operand* o) {
   const int64_t es = c.dt == TPS_F32 ? 4 : 2;
+  const char* src = static_cast<const char*>(c.w.data) + v0 * c.w_out * es;
+  if (!l.direct) return lay_out(c, src, c.d, n, c.w_in, c.w_out, room, s, o);
+  *o = Operand{src, c.w_in, c.w_out, 0, 0};
+  return TPS_OK;
+}
+int hidden(const Call& c, const Layout& l, char* room, cudaStream_t s, Operand* o) {
+  if (!l.direct) return lay_out(c, static_cast<const char*>(c.h.data), c.T, c.d, c.h.sr, c.h.sc, room, s, o);
+  *o = Operand{static_cast<const char*>(c.h.data), c.h.sr, c.h.sc, 0, 0};
+  return TPS_OK;
+}
+// A(m, k) = X(i, j) or, transposed, X(j, i); B(k, n) alike.
+void set_a(GemmDesc* g, const Operand& x, bool t) {
+  g->a = x.p; g->a_sm = t ? x.sj : x.si; g->a_sk = t ? x.si : x.sj; g->a_plane = x.plane; g->a_cols = x.cols;
+}
+void set_b(GemmDesc* g, const Operand& x, bool t) {
+  g->b = x.p; g->b_sk = t ? x.sj : x.si; g->b_sn = t ? x.si : x.sj; g->b_plane = x.plane; g->b_cols = x.cols;
+}
+GemmDesc gemm_of(const char* name, const Layout& l, int64_t M, int64_t N, int64_t K) {
   GemmDesc g;
-  g.M = rows; g.N = n; g.K = c.d; g.in_dtype = c.dt;
-  g.a = static_cast<const char*>(c.h.data) + r0 * c.h.sr * es; g.a_sm = c.h.sr; g.a_sk = c.h.sc;
-  g.b = static_cast<const char*>(c.w.data) + v0 * c.w_out * es; g.b_sk = c.w_in; g.b_sn = c.w_out;
+  g.name = name;
+  g.M = M; g.N = N; g.K = K; g.in_dtype = TPS_BF16;
+  g.planes = l.planes;
   return g;
 }
 
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-// Columns of one piece that fit into `room` bytes at `row_bytes` per column.
+// Columns of one piece that fit into `room` bytes at `column_bytes` per column.
 int64_t piece_columns(int64_t V, int64_t room, int64_t column_bytes) {
   const int64_t most = round_up(V, kPieceStep);
   const int64_t fit = column_bytes > 0 ? room / column_bytes / kPieceStep * kPieceStep : most;
   return fit < most ? fit : most;
 }
-
-// Bytes of a piece's buffers per vocabulary column: bf16 dz on the tensor
-// cores; else fp32 logits, and beside them bf16 dz for bf16 operands.
-int64_t column_bytes(int64_t T, int dtype, bool tc, bool backward) {
-  if (tc) return backward ? 2 * T : 0;
-  return 4 * T + (backward && dtype == TPS_BF16 ? 2 * T : 0);
+// Bytes of a piece's buffers per vocabulary column: dz, and Whead laid out.
+int64_t column_bytes(int64_t T, int64_t d, bool direct, int planes, bool backward) {
+  return (backward ? 2 * planes * T : 0) + (direct ? 0 : 2 * planes * round_up(d, 64));
 }
 
 struct Fixed {  // workspace before the pieces
-  size_t pairs, zy, rows, flags, acc, pieces;
+  size_t pairs, zy, rows, flags, acc, h, pieces;
 };
-Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool tc, bool backward) {
+Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool direct, int planes, bool backward) {
   Fixed f = {};
   size_t at = 0;
   auto take = [&at](int64_t bytes) {
@@ -322,17 +398,20 @@ Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool tc, bool backward) {
     return p;
   };
   if (!backward) {
-    const int64_t rows = T < kRowBlock ? T : kRowBlock;
-    const int64_t per_row = tc ? (V + kStatsTileN - 1) / kStatsTileN : (V + kPieceStep - 1) / kPieceStep;
-    f.pairs = take(8 * per_row * (tc ? rows : T));
+    f.pairs = take(8 * ((V + kStatsTileN - 1) / kStatsTileN) * (T < kRowBlock ? T : kRowBlock));
     f.zy = take(4 * T);
   } else {
     f.rows = take(16 * T);
     f.flags = take(4 * (pair_tile_count(T, d) + 1));
     f.acc = take(4 * T * round_up(d, 4));
   }
+  if (!direct) f.h = take(laid_bytes(T, d, planes));
   f.pieces = at;
   return f;
+}
+// Where a piece's columns are laid out: behind its dz.
+size_t head_room(const Fixed& f, int64_t T, int planes, bool backward, int64_t cols) {
+  return f.pieces + (backward ? align256(static_cast<size_t>(2 * planes * T * cols)) : 0);
 }
 
 // K split of the dh GEMM over a piece: as many runs as bring the (tile, run)
@@ -357,12 +436,6 @@ int split_runs(int64_t tiles, int64_t k_tiles) {
   return best;
 }
 
-int launched(const char* what) {
-  note_launch();
-  const cudaError_t e = cudaPeekAtLastError();
-  return e == cudaSuccess ? TPS_OK : fail(TPS_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(cudaGetLastError()));
-}
-
 }  // namespace
 
 }  // namespace tps
@@ -372,12 +445,13 @@ using namespace tps;
 extern "C" size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dtype, int32_t backward,
                                                 int64_t piece) {
   if (T < 0 || d < 1 || V < 1 || piece < 0 || (dtype != TPS_F32 && dtype != TPS_BF16)) return 0;
-  const bool tc = dtype == TPS_BF16;
-  // The bytes for fp32 also serve bf16 operands outside the tensor cores' reach.
-  const int64_t per = column_bytes(T, TPS_BF16, tc, backward != 0);
-  int64_t cols = piece > 0 ? round_up(piece < V ? piece : V, kPieceStep)
-                           : piece_columns(V, kPieceBytes > kPieceStep * per ? kPieceBytes : kPieceStep * per, per);
-  return fixed_layout(T, d, V, tc, backward != 0).pieces + align256(static_cast<size_t>(per) * cols) + 512;
+  // The bytes for fp32 also serve bf16 operands that have to be laid out.
+  const bool direct = dtype == TPS_BF16;
+  const int planes = direct ? 1 : 3;
+  const int64_t per = column_bytes(T, d, direct, planes, backward != 0);
+  const int64_t cols = piece > 0 ? round_up(piece < V ? piece : V, kPieceStep)
+                                 : piece_columns(V, kPieceBytes > kPieceStep * per ? kPieceBytes : kPieceStep * per, per);
+  return fixed_layout(T, d, V, direct, planes, backward != 0).pieces + align256(static_cast<size_t>(per) * cols) + 512;
 }
 
 extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* labels,
@@ -401,10 +475,9 @@ extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, c
       return fail(TPS_ERR_CUDA, "memset failed");
     return TPS_OK;
   }
-  GemmDesc g = logits_gemm(c, 0, c.T, 0, c.vreal);
-  const bool tc = gemm_tc_supported(g);
-  const Fixed f = fixed_layout(c.T, c.d, c.V, tc, false);
-  const int64_t per = column_bytes(c.T, c.dt, tc, false);
+  const Layout l = layout_of(c);
+  const Fixed f = fixed_layout(c.T, c.d, c.V, l.direct, l.planes, false);
+  const int64_t per = column_bytes(c.T, c.d, l.direct, l.planes, false);
   const size_t least = f.pieces + static_cast<size_t>(kPieceStep * per) + 256;
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < least)
     return fail(TPS_ERR_WORKSPACE, "workspace needs at least %zu bytes, 256-byte aligned", least);
@@ -415,41 +488,32 @@ extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, c
   float* zy = reinterpret_cast<float*>(ws + f.zy);
   float* loss_p = static_cast<float*>(loss->data);
   float* lse_p = static_cast<float*>(lse->data);
-  if (tc) {
-    const int64_t tiles = (c.vreal + kStatsTileN - 1) / kStatsTileN;
-    const int64_t es = c.lab.i64 ? 8 : 4;
-    for (int64_t r0 = 0; r0 < c.T; r0 += kRowBlock) {
-      const int64_t rows = c.T - r0 < kRowBlock ? c.T - r0 : kRowBlock;
-      g = logits_gemm(c, r0, rows, 0, c.vreal);
-      g.name = "lce_logits";
+  const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
+  const int64_t tiles = (c.vreal + kStatsTileN - 1) / kStatsTileN, label_bytes = c.lab.i64 ? 8 : 4;
+  Operand x, w;
+  if ((rc = hidden(c, l, ws + f.h, s, &x))) return rc;
+  for (int64_t r0 = 0; r0 < c.T; r0 += kRowBlock) {
+    const int64_t rows = c.T - r0 < kRowBlock ? c.T - r0 : kRowBlock;
+    for (int64_t v0 = 0; v0 < c.vreal; v0 += cols) {
+      const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
+      if ((rc = head_piece(c, l, v0, n, ws + f.pieces, s, &w))) return rc;
+      GemmDesc g = gemm_of("lce_logits", l, rows, n, c.d);
+      set_a(&g, x, false);
+      g.a = x.p + r0 * x.si * 2;
+      if (g.a_cols > 0 && x.si == 1) g.a_cols -= r0;
+      set_b(&g, w, false);
       g.epi.mode = EPI_CE_LSE;
-      g.epi.stats = reinterpret_cast<float*>(pairs);
+      g.epi.stats = reinterpret_cast<float*>(pairs + v0 / kStatsTileN * rows);
       g.epi.stats_ld = rows;
-      g.epi.ce_labels = static_cast<const char*>(c.lab.p) + r0 * es;
+      g.epi.ce_col0 = v0;
+      g.epi.ce_labels = static_cast<const char*>(c.lab.p) + r0 * label_bytes;
       g.epi.ce_label_i64 = c.lab.i64;
       g.epi.ce_zy = zy + r0;
-      if ((rc = run_gemm(g, c.vreal, 1, s))) return rc;
-      ProfScope prof("ce_join", "lce", 0.0, 8.0 * double(rows) * double(tiles), s);
-      ce_join_kernel<<<static_cast<unsigned>((rows + 31) / 32), 32 * kJoinWarps, 0, s>>>(
-          pairs, rows, tiles, rows, r0, zy + r0, c.lab, loss_p, lse_p, err);
-      if ((rc = launched("ce_join"))) return rc;
+      if ((rc = run_gemm(g, n, 1, s))) return rc;
     }
-  } else {
-    float* z = reinterpret_cast<float*>(ws + f.pieces);
-    const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
-    int64_t n_pieces = 0;
-    for (int64_t v0 = 0; v0 < c.vreal; v0 += cols, ++n_pieces) {
-      const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
-      g = logits_gemm(c, 0, c.T, v0, n);
-      g.name = "lce_logits";
-      g.epi.d = z;
-      if ((rc = run_gemm(g, cols, 1, s))) return rc;
-      ProfScope prof("ce_piece_stats", "lce", 0.0, 4.0 * double(c.T) * double(n), s);
-      ce_piece_stats_kernel<<<static_cast<unsigned>(c.T), 256, 0, s>>>(z, cols, n, v0, c.lab, pairs + n_pieces * c.T, zy);
-      if ((rc = launched("ce_piece_stats"))) return rc;
-    }
-    ce_join_kernel<<<static_cast<unsigned>((c.T + 31) / 32), 32 * kJoinWarps, 0, s>>>(
-        pairs, c.T, n_pieces, c.T, 0, zy, c.lab, loss_p, lse_p, err);
+    ProfScope prof("ce_join", "lce", 0.0, 8.0 * double(rows) * double(tiles), s);
+    ce_join_kernel<<<static_cast<unsigned>((rows + 31) / 32), 32 * kJoinWarps, 0, s>>>(pairs, rows, tiles, rows, r0,
+                                                                                     zy + r0, c.lab, loss_p, lse_p, err);
     if ((rc = launched("ce_join"))) return rc;
   }
   if (total != nullptr) {
@@ -498,13 +562,10 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
   }
   if (c.T == 0) return TPS_OK;
 
-  // Both the logits and the two products with dz have to be within reach of
-  // the tensor cores: their operands are h, Whead and this call's own dz.
-  GemmDesc probe = logits_gemm(c, 0, c.T, 0, c.vreal);
-  bool tc = gemm_tc_supported(probe);
-  const Fixed f = fixed_layout(c.T, c.d, c.V, tc, true);
-  const int64_t per = column_bytes(c.T, c.dt, tc, true);
-  const size_t least = f.pieces + static_cast<size_t>(kPieceStep * per) + 256;  // 256: between the two buffers of a piece
+  const Layout l = layout_of(c);
+  const Fixed f = fixed_layout(c.T, c.d, c.V, l.direct, l.planes, true);
+  const int64_t per = column_bytes(c.T, c.d, l.direct, l.planes, true);
+  const size_t least = f.pieces + static_cast<size_t>(kPieceStep * per) + 256;  // 256: between a piece's two buffers
   if (workspace == nullptr || (reinterpret_cast<uintptr_t>(workspace) & 255) || workspace_bytes < least)
     return fail(TPS_ERR_WORKSPACE, "workspace needs at least %zu bytes, 256-byte aligned", least);
   uint32_t* err = device_error_word();
@@ -531,57 +592,44 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
     acc = static_cast<float*>(dh.data);
     ld_acc = dh.sr;
   }
-  char* piece = ws + f.pieces;
-  const int64_t es = c.dt == TPS_F32 ? 4 : 2;
-  float* z = reinterpret_cast<float*>(piece);                                   // other operands: fp32 logits
-  char* dz = tc || c.dt == TPS_F32 ? piece : piece + align256(4 * c.T * cols);  // dz, operand dtype
+  char* dz_p = ws + f.pieces;  // T x cols, or its planes side by side
+  const Operand dz = {dz_p, l.planes * cols, 1, l.planes > 1 ? cols : 0, l.planes > 1 ? l.planes * cols : 0};
+  char* w_room = ws + head_room(f, c.T, l.planes, true, cols);
+  Operand x, w;
+  if ((rc = hidden(c, l, ws + f.h, s, &x))) return rc;
   for (int64_t v0 = 0; v0 < c.vreal; v0 += cols) {
     const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
-    GemmDesc g = logits_gemm(c, 0, c.T, v0, n);
-    g.name = "lce_dlogits";
-    if (tc) {
-      g.epi.mode = EPI_CE_GRAD;
-      g.epi.d = dz; g.epi.d_dtype = TPS_BF16;
-      g.epi.ce_rows = rows;
-      g.epi.ce_col0 = v0;
-      if ((rc = run_gemm(g, cols, 1, s))) return rc;
-    } else {
-      g.epi.d = z;
-      if ((rc = run_gemm(g, cols, 1, s))) return rc;
-      ProfScope prof("ce_piece_grad", "lce", 0.0, 8.0 * double(c.T) * double(n), s);
-      if (c.dt == TPS_F32)
-        ce_piece_grad_kernel<float><<<static_cast<unsigned>(c.T), 256, 0, s>>>(z, cols, n, v0, rows, z, cols);
-      else
-        ce_piece_grad_kernel<__nv_bfloat16><<<static_cast<unsigned>(c.T), 256, 0, s>>>(
-            z, cols, n, v0, rows, reinterpret_cast<__nv_bfloat16*>(dz), cols);
-      if ((rc = launched("ce_piece_grad"))) return rc;
-    }
+    if ((rc = head_piece(c, l, v0, n, w_room, s, &w))) return rc;
+    GemmDesc g = gemm_of("lce_dlogits", l, c.T, n, c.d);
+    set_a(&g, x, false);
+    set_b(&g, w, false);
+    g.epi.mode = EPI_CE_GRAD;
+    g.epi.d = dz_p; g.epi.d_dtype = TPS_BF16;
+    g.epi.ce_rows = rows;
+    g.epi.ce_col0 = v0;
+    g.d_plane = dz.plane;
+    g.n_store = round_up(n, 64);
+    if ((rc = run_gemm(g, dz.si, 1, s))) return rc;
     if (want_dh) {  // dh += dz W_piece^T
-      GemmDesc q;
-      q.name = "lce_dhidden";
-      q.M = c.T; q.N = c.d; q.K = n; q.in_dtype = c.dt;
-      q.a = dz; q.a_sm = cols; q.a_sk = 1;
-      q.b = static_cast<const char*>(c.w.data) + v0 * c.w_out * es; q.b_sk = c.w_out; q.b_sn = c.w_in;
+      GemmDesc q = gemm_of("lce_dhidden", l, c.T, c.d, n);
+      set_a(&q, dz, false);
+      set_b(&q, w, true);
       q.epi.d = acc; q.epi.ldd = ld_acc;
       q.epi.accumulate = v0 > 0;
       q.wide = true;
       q.wide = gemm_wide_supported(q);
-      if (tc) {
-        const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
-        if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles + 1) * sizeof(uint32_t), s) != cudaSuccess)
-          return fail(TPS_ERR_CUDA, "memset failed");
-        q.ksplit = split_runs(tiles, (n + 63) / 64);
-        q.kflags = flags;
-        q.unit_counter = flags + tiles;
-      }
+      const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
+      if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles + 1) * sizeof(uint32_t), s) != cudaSuccess)
+        return fail(TPS_ERR_CUDA, "memset failed");
+      q.ksplit = split_runs(tiles, (n + 63) / 64 * (l.planes > 1 ? 6 : 1));
+      q.kflags = flags;
+      q.unit_counter = flags + tiles;
       if ((rc = run_gemm(q, ld_acc, 1, s))) return rc;
     }
     if (want_dw) {  // dW_piece = h^T dz
-      GemmDesc q;
-      q.name = "lce_dwhead";
-      q.M = c.d; q.N = n; q.K = c.T; q.in_dtype = c.dt;
-      q.a = c.h.data; q.a_sm = c.h.sc; q.a_sk = c.h.sr;
-      q.b = dz; q.b_sk = cols; q.b_sn = 1;
+      GemmDesc q = gemm_of("lce_dwhead", l, c.d, n, c.T);
+      set_a(&q, x, true);
+      set_b(&q, dz, false);
       q.epi.d = static_cast<char*>(dw.data) + v0 * dw_out * dw_es; q.epi.d_dtype = dw.dtype;
       if ((rc = run_gemm(q, dw_in, dw_out, s))) return rc;
     }

@@ -388,10 +388,12 @@ int tps_vocab_ce_fwd_bwd_ex(const tps_tensor* h, const tps_tensor* Whead, const 
  * `workspace`: 256-byte aligned.  tps_linear_ce_workspace_bytes gives what a
  * call needs for pieces of `piece` columns (rounded up to 256; 0: pieces of
  * about 512 MB); a call takes pieces as large as its workspace holds and
- * refuses one that does not hold 256 columns (TPS_ERR_WORKSPACE).  bf16
- * operands that TMA cannot describe (a base or a row pitch that is not a
- * multiple of 16 bytes, no unit stride along rows) run through the fp32-FMA
- * GEMM and need the bytes given for TPS_F32.  Results do not depend on the
+ * refuses one that does not hold 256 columns (TPS_ERR_WORKSPACE).  fp32
+ * operands are taken as sums of three bf16 values each, exactly, and their
+ * products to fp32's precision on the tensor cores; they, and bf16 operands
+ * that TMA cannot describe (a base or a row pitch that is not a multiple of
+ * 16 bytes), are laid out in the workspace piece by piece, and such bf16
+ * operands need the bytes given for TPS_F32.  Results do not depend on the
  * piece beyond the order in which dHidden is summed.  0 for bad arguments.
  * Both calls may be captured into a CUDA graph.
  * ---------------------------------------------------------------------- */
