@@ -35,6 +35,7 @@
 
 #include <cmath>
 #include <cstdlib>
+#include <mutex>
 
 #include "api_common.cuh"
 #include "ptx.cuh"
@@ -79,6 +80,14 @@ __device__ __forceinline__ void join(float& m, float& s, float m2, float s2) {
 // so every load of a warp is one 256-byte line pair), then the 32 partial
 // pairs of a row in warp order.  At T = 8192 this reads 66 MB.
 constexpr int kJoinWarps = 32;
+__device__ __forceinline__ void ce_finish(int64_t t, float m, float s, float zy, const Labels& lab, float* loss,
+                                          float* lse, uint32_t* err) {
+  const float l = m + logf(s);
+  lse[t] = l;
+  const int kind = lab.kind(lab.at(t));
+  loss[t] = kind == 1 ? 0.0f : (kind == 0 ? l - zy : __int_as_float(0x7fc00000));
+  if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
+}
 __global__ void __launch_bounds__(32 * kJoinWarps)
     ce_join_kernel(const float2* pairs, int64_t ld, int64_t tiles, int64_t rows, int64_t row0, const float* zy,
                    Labels lab, float* loss, float* lse, uint32_t* err) {
@@ -87,10 +96,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   const int64_t r = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float m = -INFINITY, s = 0.0f;
   if (r < rows) {
-#pragma unroll 4
-    for (int64_t i = w; i < tiles; i += kJoinWarps) {
-      const float2 e = __ldg(pairs + i * ld + r);
-      join(m, s, e.x, e.y);
+    constexpr int U = 8;  // loads in flight
+    for (int64_t i = w; i < tiles; i += U * kJoinWarps) {
+      float2 e[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        e[u] = i + u * kJoinWarps < tiles ? __ldg(pairs + (i + u * kJoinWarps) * ld + r) : make_float2(-INFINITY, 0.0f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) join(m, s, e[u].x, e[u].y);
     }
   }
   part[w][lane] = make_float2(m, s);
@@ -99,12 +112,29 @@ __global__ void __launch_bounds__(32 * kJoinWarps)
   m = -INFINITY;
   s = 0.0f;
   for (int i = 0; i < kJoinWarps; ++i) join(m, s, part[i][lane].x, part[i][lane].y);
-  const int64_t t = row0 + r;
-  const float l = m + logf(s);
-  lse[t] = l;
-  const int kind = lab.kind(lab.at(t));
-  loss[t] = kind == 1 ? 0.0f : (kind == 0 ? l - zy[r] : __int_as_float(0x7fc00000));
-  if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
+  ce_finish(row0 + r, m, s, zy[r], lab, loss, lse, err);
+}
+// The same for a few rows: one block a row, threads along the tiles.
+__global__ void __launch_bounds__(32 * kJoinWarps)
+    ce_join_row_kernel(const float2* pairs, int64_t ld, int64_t tiles, const float* zy, Labels lab, float* loss,
+                       float* lse, uint32_t* err) {
+  __shared__ float2 part[kJoinWarps];
+  const int64_t r = blockIdx.x;
+  float m = -INFINITY, s = 0.0f;
+  for (int64_t i = threadIdx.x; i < tiles; i += 32 * kJoinWarps) {
+    const float2 e = __ldg(pairs + i * ld + r);
+    join(m, s, e.x, e.y);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1)
+    join(m, s, __shfl_xor_sync(0xffffffffu, m, o), __shfl_xor_sync(0xffffffffu, s, o));
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = make_float2(m, s);
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  m = -INFINITY;
+  s = 0.0f;
+  for (int i = 0; i < kJoinWarps; ++i) join(m, s, part[i].x, part[i].y);
+  ce_finish(r, m, s, zy[r], lab, loss, lse, err);
 }
 
 // Sum over a block of 1024 threads, to thread 0.
@@ -206,6 +236,186 @@ __global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows,
       }
     }
   }
+}
+
+// ---- a few tokens -----------------------------------------------------------
+// With up to kFewTokens tokens the forward pass is one reading of Whead, and
+// the 256-row tiles of the GEMM do it at half of the memory's rate (T = 1,
+// d = 4096, V = 128256: 291 us, 3.6 TB/s: five stages of 16 KB of Whead an SM
+// are not enough bytes in flight).  Here a block takes 128 columns, 16 bytes
+// a thread and load with eight loads in flight, fp32 sums on the fp32 pipes,
+// and leaves the pair of its columns for each token.
+constexpr int kFewTokens = 8;
+constexpr int kFewWarps = 8;
+constexpr int kFewChunk = 1024;       // rows of Whead whose h is in shared memory
+constexpr int kFewShared = 96 << 10;  // h of an OUT_IN call, whole
+
+struct FewParams {
+  const void* h;
+  int64_t h_t, h_k;  // strides of token and k
+  const void* w;
+  int64_t ld;        // Whead's pitch
+  int64_t T, d, V, vreal;
+  Labels lab;
+  float2* pairs;     // pairs[tile * T + t]
+  float* zy;
+};
+
+template <class E> __device__ __forceinline__ float few_f(E x);
+template <> __device__ __forceinline__ float few_f(float x) { return x; }
+template <> __device__ __forceinline__ float few_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+
+// 16 bytes from p, of which `left` elements exist.
+template <class E, int N>
+__device__ __forceinline__ void few_load(const E* p, int64_t left, E (&x)[N]) {
+  if (left >= N) {
+    *reinterpret_cast<uint4*>(x) = __ldg(reinterpret_cast<const uint4*>(p));
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; ++i) x[i] = i < left ? p[i] : E(0.0f);
+  }
+}
+
+// The pair of 128 logits of each token, z[t * 128 + column], and the label's logit.
+template <int TT>
+__device__ __forceinline__ void few_pairs(const FewParams& p, const float* z, int64_t tile) {
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (w >= TT || w >= p.T) return;
+  const int64_t col0 = tile * 128 + lane * 4;
+  float4 q = reinterpret_cast<const float4*>(z + w * 128)[lane];
+  float v[4] = {q.x, q.y, q.z, q.w}, m = -INFINITY, s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (col0 + i >= p.vreal) v[i] = -INFINITY;
+    m = fmaxf(m, v[i]);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+#pragma unroll
+  for (int i = 0; i < 4; ++i) s += v[i] == -INFINITY ? 0.0f : expf(v[i] - m);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) p.pairs[tile * p.T + w] = make_float2(m, s);
+  const int64_t y = p.lab.at(w) - col0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (y == i && col0 + i < p.vreal) p.zy[w] = v[i];
+}
+
+// Whead with unit stride along the vocabulary: lanes along columns, warps
+// (and halves of a warp) along k.
+template <class E, int TT>
+__global__ void __launch_bounds__(32 * kFewWarps) ce_few_in_out_kernel(const FewParams p) {
+  constexpr int N = 16 / sizeof(E), kLanes = 128 / N, kRows = 32 / kLanes * kFewWarps, U = 8;
+  __shared__ __align__(16) float sh[TT * 1024];  // h of a chunk [k][t], then the warps' sums [warp][t][128]
+  static_assert(kFewWarps * 128 <= 1024 && kFewChunk <= 1024, "both uses fit");
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane % kLanes * N, r0 = w * (32 / kLanes) + lane / kLanes;
+  const int64_t tile = blockIdx.x, col = tile * 128 + c;
+  float acc[TT][N];
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int i = 0; i < N; ++i) acc[t][i] = 0.0f;
+  for (int64_t k0 = 0; k0 < p.d; k0 += kFewChunk) {
+    const int kn = static_cast<int>(p.d - k0 < kFewChunk ? p.d - k0 : kFewChunk);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kn * TT; i += 32 * kFewWarps) {
+      const int k = i / TT, t = i % TT;
+      sh[i] = t < p.T ? few_f(static_cast<const E*>(p.h)[t * p.h_t + (k0 + k) * p.h_k]) : 0.0f;
+    }
+    __syncthreads();
+    if (col < p.vreal) {
+      const E* src = static_cast<const E*>(p.w) + k0 * p.ld + col;
+      for (int k = r0; k < kn; k += kRows * U) {
+        E x[U][N];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (k + u * kRows < kn) few_load<E, N>(src + (k + u * kRows) * p.ld, p.V - col, x[u]);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          if (k + u * kRows < kn) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) {
+              const float hv = sh[(k + u * kRows) * TT + t];
+#pragma unroll
+              for (int i = 0; i < N; ++i) acc[t][i] = fmaf(few_f(x[u][i]), hv, acc[t][i]);
+            }
+          }
+        }
+      }
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int t = 0; t < TT; ++t)
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float a = acc[t][i];
+      if (kLanes == 16) a += __shfl_xor_sync(0xffffffffu, a, 16);
+      if (lane < kLanes) sh[(w * TT + t) * 128 + c + i] = a;
+    }
+  __syncthreads();
+  for (int i = threadIdx.x; i < TT * 128; i += 32 * kFewWarps) {
+    float a = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kFewWarps; ++q) a += sh[q * TT * 128 + i];
+    sh[i] = a;  // read and written by this thread alone: warp 0's part
+  }
+  __syncthreads();
+  few_pairs<TT>(p, sh, tile);
+}
+
+// Whead with unit stride along k: a warp takes four vocabulary rows at a
+// time, lanes along k.
+template <class E, int TT>
+__global__ void __launch_bounds__(32 * kFewWarps) ce_few_out_in_kernel(const FewParams p) {
+  constexpr int N = 16 / sizeof(E), R = 4, kWarpRows = 128 / kFewWarps;
+  extern __shared__ __align__(16) uint8_t raw[];
+  __shared__ __align__(16) float z[TT * 128];
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t tile = blockIdx.x, dp = (p.d + N - 1) / N * N;
+  E* hs = reinterpret_cast<E*>(raw);  // [t][dp], zeros past d
+  for (int64_t i = threadIdx.x; i < TT * dp; i += 32 * kFewWarps) {
+    const int64_t t = i / dp, k = i - t * dp;
+    hs[i] = t < p.T && k < p.d ? static_cast<const E*>(p.h)[t * p.h_t + k * p.h_k] : E(0.0f);
+  }
+  __syncthreads();
+  for (int g = 0; g < kWarpRows; g += R) {
+    const int row = w * kWarpRows + g;
+    const int64_t v = tile * 128 + row;
+    float acc[R][TT];
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) acc[r][t] = 0.0f;
+#pragma unroll 2
+    for (int64_t k = lane * N; k < p.d; k += 32 * N) {
+      E x[R][N];
+#pragma unroll
+      for (int r = 0; r < R; ++r)
+        few_load<E, N>(static_cast<const E*>(p.w) + (v + r) * p.ld + k, v + r < p.V ? p.d - k : 0, x[r]);
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        E y[N];
+        *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(hs + t * dp + k);
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+#pragma unroll
+          for (int i = 0; i < N; ++i) acc[r][t] = fmaf(few_f(x[r][i]), few_f(y[i]), acc[r][t]);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < R; ++r)
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        float a = acc[r][t];
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);
+        if (lane == 0) z[t * 128 + row + r] = a;
+      }
+  }
+  __syncthreads();
+  few_pairs<TT>(p, z, tile);
 }
 
 // The fp32 sum over pieces to the caller's dHidden.
@@ -375,6 +585,40 @@ GemmDesc gemm_of(const char* name, const Layout& l, int64_t M, int64_t N, int64_
   return g;
 }
 
+// Whether the few-token kernels take a forward call.
+bool few_tokens(const Call& c) {
+  if (c.T < 1 || c.T > kFewTokens) return false;
+  const int64_t es = c.dt == TPS_F32 ? 4 : 2, pitch = c.w_out == 1 ? c.w_in : c.w_out;
+  if ((reinterpret_cast<uintptr_t>(c.w.data) & 15u) != 0 || pitch * es % 16 != 0) return false;
+  const int64_t tt = c.T <= 1 ? 1 : c.T <= 2 ? 2 : c.T <= 4 ? 4 : 8;
+  return c.w_out == 1 || (c.w_in == 1 && tt * (c.d + 16) * es <= kFewShared);
+}
+template <class E, int TT>
+int launch_few(const Call& c, const FewParams& p, cudaStream_t s) {
+  const unsigned blocks = static_cast<unsigned>((c.vreal + 127) / 128);
+  ProfScope prof("ce_few", "lce", 2.0 * double(c.T) * double(c.d) * double(c.vreal), double(c.d) * double(c.vreal) * sizeof(E), s);
+  if (c.w_out == 1) {
+    ce_few_in_out_kernel<E, TT><<<blocks, 32 * kFewWarps, 0, s>>>(p);
+  } else {
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [] {
+      attr = cudaFuncSetAttribute(ce_few_out_in_kernel<E, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewShared);
+    });
+    if (attr != cudaSuccess) return fail(TPS_ERR_CUDA, "ce_few: %s", cudaGetErrorString(attr));
+    const size_t n = 16 / sizeof(E);
+    ce_few_out_in_kernel<E, TT><<<blocks, 32 * kFewWarps, TT * ((c.d + n - 1) / n * n) * sizeof(E), s>>>(p);
+  }
+  return launched("ce_few");
+}
+template <class E>
+int few_of(const Call& c, const FewParams& p, cudaStream_t s) {
+  if (c.T <= 1) return launch_few<E, 1>(c, p, s);
+  if (c.T <= 2) return launch_few<E, 2>(c, p, s);
+  if (c.T <= 4) return launch_few<E, 4>(c, p, s);
+  return launch_few<E, 8>(c, p, s);
+}
+
 // Columns of one piece that fit into `room` bytes at `column_bytes` per column.
 int64_t piece_columns(int64_t V, int64_t room, int64_t column_bytes) {
   const int64_t most = round_up(V, kPieceStep);
@@ -491,10 +735,18 @@ extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, c
   const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
   const int64_t tiles = (c.vreal + kStatsTileN - 1) / kStatsTileN, label_bytes = c.lab.i64 ? 8 : 4;
   Operand x, w;
-  if ((rc = hidden(c, l, ws + f.h, s, &x))) return rc;
+  const bool few = few_tokens(c);
+  if (few) {
+    const FewParams p = {c.h.data, c.h.sr, c.h.sc, c.w.data, c.w_out == 1 ? c.w_in : c.w_out, c.T, c.d, c.V, c.vreal,
+                         c.lab, pairs, zy};
+    rc = c.dt == TPS_F32 ? few_of<float>(c, p, s) : few_of<__nv_bfloat16>(c, p, s);
+  } else {
+    rc = hidden(c, l, ws + f.h, s, &x);
+  }
+  if (rc) return rc;
   for (int64_t r0 = 0; r0 < c.T; r0 += kRowBlock) {
     const int64_t rows = c.T - r0 < kRowBlock ? c.T - r0 : kRowBlock;
-    for (int64_t v0 = 0; v0 < c.vreal; v0 += cols) {
+    for (int64_t v0 = 0; !few && v0 < c.vreal; v0 += cols) {
       const int64_t n = c.vreal - v0 < cols ? c.vreal - v0 : cols;
       if ((rc = head_piece(c, l, v0, n, ws + f.pieces, s, &w))) return rc;
       GemmDesc g = gemm_of("lce_logits", l, rows, n, c.d);
@@ -512,8 +764,12 @@ extern "C" int tps_linear_ce_fwd(const tps_tensor* h, const tps_tensor* Whead, c
       if ((rc = run_gemm(g, n, 1, s))) return rc;
     }
     ProfScope prof("ce_join", "lce", 0.0, 8.0 * double(rows) * double(tiles), s);
-    ce_join_kernel<<<static_cast<unsigned>((rows + 31) / 32), 32 * kJoinWarps, 0, s>>>(pairs, rows, tiles, rows, r0,
-                                                                                     zy + r0, c.lab, loss_p, lse_p, err);
+    if (c.T < 152)  // fewer rows than would keep every SM busy 32 at a time
+      ce_join_row_kernel<<<static_cast<unsigned>(rows), 32 * kJoinWarps, 0, s>>>(pairs, rows, tiles, zy, c.lab, loss_p,
+                                                                                lse_p, err);
+    else
+      ce_join_kernel<<<static_cast<unsigned>((rows + 31) / 32), 32 * kJoinWarps, 0, s>>>(
+          pairs, rows, tiles, rows, r0, zy + r0, c.lab, loss_p, lse_p, err);
     if ((rc = launched("ce_join"))) return rc;
   }
   if (total != nullptr) {

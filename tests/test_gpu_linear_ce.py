@@ -118,6 +118,34 @@ def test_fp32(T, d, V, layout):
     check(*case(T, T, d, V, layout, torch.float32, ignored=T // 8), layout, "mean", piece=512)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+@pytest.mark.parametrize("d,V,vocab", [(8, 16, 0), (72, 136, 129), (1000, 1288, 0), (2056, 520, 513)])
+def test_few_tokens(T, d, V, vocab, layout, dtype):
+    """One to eight tokens read the head once, a block for 128 columns."""
+    h, W, y = case(T + d, T, d, V, layout, dtype, vocab=vocab)
+    loss, total, lse = api.linear_ce_fwd(h, W, y, weight_layout=layout, vocab_size=vocab, reduction="sum")
+    ref = reference(h, W, y, layout, "sum", vocab)
+    near(lse, ref["lse"], "lse")
+    near(loss, ref["loss"], "loss")
+    near(total, ref["total"], "total")
+
+
+def test_few_tokens_with_masked_and_infinite_logits():
+    h, W, y = case(2, 4, 64, 300, "out_in", torch.float32)
+    W[:256] = 0
+    W[:256, 0] = -float("inf")  # two whole blocks of columns, and all but 44 logits, are -inf for positive h
+    h = h.abs() + 0.1
+    y[:] = 290
+    loss, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
+    want = torch.logsumexp(h.double() @ W[256:].double().t(), 1)
+    assert (lse.double() - want).abs().max() <= 64 * 2.0 ** -23 * (h.double() @ W[256:].double().abs().t()).max() + 2.0 ** -17
+    h[1, 3] = float("nan")
+    loss, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
+    assert torch.isnan(lse[1]) and torch.isfinite(lse[[0, 2, 3]]).all()
+
+
 @pytest.mark.parametrize("reduction", ["none", "sum", "mean"])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_padding_reductions_and_upstream(reduction, dtype):
