@@ -245,7 +245,11 @@ __global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows,
 // are not enough bytes in flight).  Here a block takes 128 columns, 16 bytes
 // a thread and load with eight loads in flight, fp32 sums on the fp32 pipes,
 // and leaves the pair of its columns for each token.
-constexpr int kFewTokens = 8;
+// Measured (us, d = 4096; bf16 V = 128256, fp32 V = 65536, the GEMM's time
+// after the stroke): bf16 1 token 185 / 250, 2 tokens 245 / 274, from 4 on the
+// GEMM is ahead; fp32 1 token 179 / 1600, 4 tokens 267 / 1600, 8 tokens
+// 276 / 1500 (the GEMM has 256 rows of six products to do for them).
+constexpr int kFewTokens = 8, kFewTokensBf16 = 2;
 constexpr int kFewWarps = 8;
 constexpr int kFewChunk = 1024;       // rows of Whead whose h is in shared memory
 constexpr int kFewShared = 96 << 10;  // h of an OUT_IN call, whole
@@ -324,24 +328,26 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_in_out_kernel(const Few
       sh[i] = t < p.T ? few_f(static_cast<const E*>(p.h)[t * p.h_t + (k0 + k) * p.h_k]) : 0.0f;
     }
     __syncthreads();
+    const E* src = static_cast<const E*>(p.w) + k0 * p.ld + col;
+    auto add = [&](const E(&x)[N], int k) {
+#pragma unroll
+      for (int t = 0; t < TT; ++t) {
+        const float hv = sh[k * TT + t];
+#pragma unroll
+        for (int i = 0; i < N; ++i) acc[t][i] = fmaf(few_f(x[i]), hv, acc[t][i]);
+      }
+    };
+    // U loads in flight, each behind its own test: written without the tests
+    // the compiler took the loads one by one (T = 1: 215 us against 185).
     if (col < p.vreal) {
-      const E* src = static_cast<const E*>(p.w) + k0 * p.ld + col;
       for (int k = r0; k < kn; k += kRows * U) {
-        E x[U][N];
+        __align__(16) E x[U][N];
 #pragma unroll
         for (int u = 0; u < U; ++u)
           if (k + u * kRows < kn) few_load<E, N>(src + (k + u * kRows) * p.ld, p.V - col, x[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-          if (k + u * kRows < kn) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) {
-              const float hv = sh[(k + u * kRows) * TT + t];
-#pragma unroll
-              for (int i = 0; i < N; ++i) acc[t][i] = fmaf(few_f(x[u][i]), hv, acc[t][i]);
-            }
-          }
-        }
+        for (int u = 0; u < U; ++u)
+          if (k + u * kRows < kn) add(x[u], k + u * kRows);
       }
     }
   }
@@ -388,21 +394,37 @@ __global__ void __launch_bounds__(32 * kFewWarps) ce_few_out_in_kernel(const Few
     for (int r = 0; r < R; ++r)
 #pragma unroll
       for (int t = 0; t < TT; ++t) acc[r][t] = 0.0f;
-#pragma unroll 2
-    for (int64_t k = lane * N; k < p.d; k += 32 * N) {
-      E x[R][N];
+    const E* src[R];  // rows past the vocabulary read the last one; their sums are masked
 #pragma unroll
-      for (int r = 0; r < R; ++r)
-        few_load<E, N>(static_cast<const E*>(p.w) + (v + r) * p.ld + k, v + r < p.V ? p.d - k : 0, x[r]);
+    for (int r = 0; r < R; ++r)
+      src[r] = static_cast<const E*>(p.w) + (v + r < p.V ? v + r : p.V - 1) * p.ld;
+    auto add = [&](const E(&x)[R][N], int64_t k) {
 #pragma unroll
       for (int t = 0; t < TT; ++t) {
-        E y[N];
+        __align__(16) E y[N];
         *reinterpret_cast<uint4*>(y) = *reinterpret_cast<const uint4*>(hs + t * dp + k);
 #pragma unroll
         for (int r = 0; r < R; ++r)
 #pragma unroll
           for (int i = 0; i < N; ++i) acc[r][t] = fmaf(few_f(x[r][i]), few_f(y[i]), acc[r][t]);
       }
+    };
+    int64_t k = lane * N;
+    for (; k + 32 * N + N <= p.d; k += 64 * N) {  // straight-line: 2 R loads in flight
+      __align__(16) E x[2][R][N];
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int r = 0; r < R; ++r)
+          *reinterpret_cast<uint4*>(x[u][r]) = __ldg(reinterpret_cast<const uint4*>(src[r] + k + u * 32 * N));
+#pragma unroll
+      for (int u = 0; u < 2; ++u) add(x[u], k + u * 32 * N);
+    }
+    for (; k < p.d; k += 32 * N) {
+      __align__(16) E x[R][N];
+#pragma unroll
+      for (int r = 0; r < R; ++r) few_load<E, N>(src[r] + k, p.d - k, x[r]);
+      add(x, k);
     }
 #pragma unroll
     for (int r = 0; r < R; ++r)
@@ -587,7 +609,8 @@ GemmDesc gemm_of(const char* name, const Layout& l, int64_t M, int64_t N, int64_
 
 // Whether the few-token kernels take a forward call.
 bool few_tokens(const Call& c) {
-  if (c.T < 1 || c.T > kFewTokens) return false;
+  const char* most = getenv("TPS_LCE_FEW");
+  if (c.T < 1 || c.T > (c.dt == TPS_F32 ? kFewTokens : kFewTokensBf16) || (most != nullptr && c.T > atoi(most))) return false;
   const int64_t es = c.dt == TPS_F32 ? 4 : 2, pitch = c.w_out == 1 ? c.w_in : c.w_out;
   if ((reinterpret_cast<uintptr_t>(c.w.data) & 15u) != 0 || pitch * es % 16 != 0) return false;
   const int64_t tt = c.T <= 1 ? 1 : c.T <= 2 ? 2 : c.T <= 4 ? 4 : 8;
@@ -615,8 +638,11 @@ template <class E>
 int few_of(const Call& c, const FewParams& p, cudaStream_t s) {
   if (c.T <= 1) return launch_few<E, 1>(c, p, s);
   if (c.T <= 2) return launch_few<E, 2>(c, p, s);
-  if (c.T <= 4) return launch_few<E, 4>(c, p, s);
-  return launch_few<E, 8>(c, p, s);
+  if constexpr (sizeof(E) == 4) {
+    if (c.T <= 4) return launch_few<E, 4>(c, p, s);
+    return launch_few<E, 8>(c, p, s);
+  }
+  return fail(TPS_ERR_ARG, "ce_few: too many tokens");
 }
 
 // Columns of one piece that fit into `room` bytes at `column_bytes` per column.
