@@ -242,10 +242,9 @@ template <bool ROUNDED>
 __device__ __forceinline__ float root_of(float x) {
   if (ROUNDED) {
     float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x + 1e-36f));  // finite for 0, whose root stays 0
     const float r = x * y;
-    const float c = fmaf(fmaf(-r, r, x), 0.5f * y, r);
-    return y < INFINITY ? c : x;  // 0 stays 0 (and infinity, whose y is 0, becomes a NaN)
+    return fmaf(fmaf(-r, r, x), 0.5f * y, r);
   }
   float r;
   asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -378,13 +377,20 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int i = 0; i < 4; ++i) probe = fmaf(w[j][i], 0.0f, probe);
-    const bool nearest = MASTER || t.nearest || probe != 0.0f;
+    if (MASTER || __any_sync(0xffffffffu, t.nearest || probe != 0.0f)) {
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        b[j][i] = nearest ? static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(w[j][i]))) << 16
-                          : bf16_by(w[j][i], rp[j][i]);
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t rn = static_cast<uint32_t>(__bfloat16_as_ushort(__float2bfloat16_rn(w[j][i]))) << 16;
+          b[j][i] = MASTER || t.nearest || probe != 0.0f ? rn : bf16_by(w[j][i], rp[j][i]);
+        }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[j][i] = bf16_by(w[j][i], rp[j][i]);
+    }
     write8<FULL>(static_cast<__nv_bfloat16*>(e.p) + at, lane, n, b);
     if (MASTER) write8<FULL>(e.w + at, lane, n, w);
   } else {
@@ -428,15 +434,22 @@ __global__ void __launch_bounds__(32 * kWarps, E4M3 ? 3 : 4) adamw_kernel(const 
       const int64_t stop = end - e.first < whole ? end - e.first : whole;
       if (unit < stop) {
         at += stop - unit;
-        Raw<GT, WT, E4M3> now, next;
-        if (E4M3) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
-        for (; unit < stop; ++unit) {
-          if (!E4M3)
-            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
-          else if (unit + 1 < stop)
-            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, next);
-          adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, now);
-          if (E4M3) now = next;
+        Raw<GT, WT, E4M3> r[2];
+        if (E4M3) {  // two units at a time, the next one's loads always in flight
+          adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, r[0]);
+          while (true) {
+            if (unit + 1 < stop) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, r[1]);
+            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[0]);
+            if (++unit >= stop) break;
+            if (unit + 1 < stop) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, r[0]);
+            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[1]);
+            if (++unit >= stop) break;
+          }
+        } else {
+          for (; unit < stop; ++unit) {
+            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, r[0]);
+            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[0]);
+          }
         }
       } else {
         const int64_t left = e.n - unit * kUnit;

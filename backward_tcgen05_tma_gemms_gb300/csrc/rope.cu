@@ -45,6 +45,7 @@ struct RopeParams {
   int D, rot;              // elements of a head, those that turn
   int units, rot_units;    // thread units of a head, those that turn
   int tokens, block_heads; // of one block
+  uint32_t inv_units, inv_units_heads[2];  // 2^32 / units, and / (units heads) of a block and of the last one
   const void* pos;
   int pos_i64, pos_shared; // int64 positions; one row of positions for all batches
   float amp, sign;
@@ -69,24 +70,40 @@ struct __align__(sizeof(T) * N) Run {
 // A block's items are (token, head, unit), unit fastest; item i of a thread
 // is threadIdx.x + i * kThreads.
 template <class T, int N, bool INTER, bool VEC_TAIL>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ Turns turns, const RopeParams p) {
+__global__ void __launch_bounds__(kThreads, 6) rope_kernel(const __grid_constant__ Turns turns, const RopeParams p) {
   __shared__ __align__(16) float2 cs[kTokenPairs];  // (cosine, sine) of each (token, pair)
+  __shared__ int64_t base[4][kTokenPairs];           // byte offsets of each token in q, k and the outputs
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
   const int tokens = static_cast<int>(p.rows - row0 < p.tokens ? p.rows - row0 : p.tokens);
   const int h0 = blockIdx.y * p.block_heads, heads = min(p.block_heads, p.heads - h0);
   const int per_token = heads * p.units, items = tokens * per_token, half = p.rot / 2;
   using R = Run<T, N>;
+  for (int i = threadIdx.x; i < tokens; i += kThreads) {
+    const int64_t b = (row0 + i) / p.S, t = row0 + i - b * p.S;
+    base[0][i] = b * p.qi.sb + t * p.qi.ss;
+    base[1][i] = b * p.qo.sb + t * p.qo.ss;
+    base[2][i] = b * p.ki.sb + t * p.ki.ss;
+    base[3][i] = b * p.ko.sb + t * p.ko.ss;
+  }
+  __syncthreads();
   struct Item {
     const char* src;
     char* dst;
     int e1;    // second run, relative to the first, in elements
-    int at;    // (token, first pair) in `cs`, or -1 outside the turned part
+    int at;    // token and unit in `cs` (slot), or -1 outside the turned part
     bool two;  // the second run is there
   };
+  // Where pair i of unit u of a token lies in `cs`: two pairs (16 bytes) of
+  // neighbouring units side by side, so that a warp reads without conflicts.
+  constexpr int kPairRun = N > 1 ? 2 : 1;
+  auto slot = [&](int tok, int u, int i) { return tok * half + (i / kPairRun * p.rot_units + u) * kPairRun + i % kPairRun; };
+  // Quotients by 32-bit reciprocals: exact while i times the divisor is below 2^32.
+  const uint32_t by_token = p.inv_units_heads[blockIdx.y + 1 == gridDim.y], by_units = p.inv_units;
+  auto quotient = [](int i, int d, uint32_t inv) { return d == 1 ? i : static_cast<int>(__umulhi(i, inv)); };
   auto item = [&](int i) {
     Item it;
-    const int tok = i / per_token, in = i - tok * per_token, hh = in / p.units, u = in - hh * p.units, h = h0 + hh;
-    const int64_t row = row0 + tok, b = row / p.S, s = row - b * p.S;
+    const int tok = quotient(i, per_token, by_token), in = i - tok * per_token;
+    const int hh = quotient(in, p.units, by_units), u = in - hh * p.units, h = h0 + hh;
     int e0;
     if (u >= p.rot_units) {
       e0 = p.rot + (u - p.rot_units) * 2 * N;
@@ -95,33 +112,26 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     } else {
       e0 = INTER ? u * 2 * N : u * N;
       it.e1 = INTER ? N : half;
-      it.at = tok * half + u * N;
+      it.at = slot(tok, u, 0);
     }
     it.two = VEC_TAIL || e0 + it.e1 + N <= p.D;  // a tail may end with a single run
-    if (h < p.heads_q) {
-      it.src = p.qi.p + b * p.qi.sb + s * p.qi.ss + h * p.qi.sh + e0 * int(sizeof(T));
-      it.dst = p.qo.p + b * p.qo.sb + s * p.qo.ss + h * p.qo.sh + e0 * int(sizeof(T));
-    } else {
-      it.src = p.ki.p + b * p.ki.sb + s * p.ki.ss + (h - p.heads_q) * p.ki.sh + e0 * int(sizeof(T));
-      it.dst = p.ko.p + b * p.ko.sb + s * p.ko.ss + (h - p.heads_q) * p.ko.sh + e0 * int(sizeof(T));
-    }
+    const bool q = h < p.heads_q;
+    const int hr = q ? h : h - p.heads_q, bytes = e0 * static_cast<int>(sizeof(T));
+    it.src = (q ? p.qi.p : p.ki.p) + base[q ? 0 : 2][tok] + hr * (q ? p.qi.sh : p.ki.sh) + bytes;
+    it.dst = (q ? p.qo.p : p.ko.p) + base[q ? 1 : 3][tok] + hr * (q ? p.qo.sh : p.ko.sh) + bytes;
     return it;
   };
-  constexpr int UNROLL = 2;
-  R x[UNROLL], y[UNROLL];
-  Item it[UNROLL];
-  auto load = [&](int i0) {
-#pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      const int i = i0 + j * kThreads;
-      if (i < items) {
-        it[j] = item(i);
-        x[j] = *reinterpret_cast<const R*>(it[j].src);
-        if (it[j].two) y[j] = *reinterpret_cast<const R*>(it[j].src + it[j].e1 * int(sizeof(T)));
-      }
-    }
+  // One item in flight a thread and six blocks an SM: 8192 tokens of 40 heads
+  // of 128 in 32.8 us (5.1 TB/s); two to five items in flight at the registers
+  // they take, 37 to 51 us.
+  R x, y;
+  Item it;
+  auto load = [&](int i) {
+    it = item(i);
+    x = *reinterpret_cast<const R*>(it.src);
+    if (it.two) y = *reinterpret_cast<const R*>(it.src + it.e1 * int(sizeof(T)));
   };
-  load(threadIdx.x);
+  if (static_cast<int>(threadIdx.x) < items) load(threadIdx.x);
   for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
     const int tok = i / half;
     const int64_t row = row0 + tok, at_pos = p.pos_shared ? row % p.S : row;
@@ -130,31 +140,27 @@ __global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ 
     const uint64_t f = static_cast<uint64_t>(pos) * turns.t[i - tok * half];
     float c, n;
     sincospif(static_cast<float>(static_cast<int32_t>(f >> 32)) * 0x1p-31f, &n, &c);
-    cs[i] = make_float2(c * p.amp, n * p.amp * p.sign);
+    const int pair = i - tok * half;
+    cs[slot(tok, pair / N, pair % N)] = make_float2(c * p.amp, n * p.amp * p.sign);
   }
   __syncthreads();
-  for (int i0 = threadIdx.x; i0 < items; i0 += UNROLL * kThreads) {
+  for (int i0 = threadIdx.x; i0 < items; i0 += kThreads) {
     if (i0 != static_cast<int>(threadIdx.x)) load(i0);
+    if (it.at >= 0) {
 #pragma unroll
-    for (int j = 0; j < UNROLL; ++j) {
-      if (i0 + j * kThreads >= items) break;
-      if (it[j].at >= 0) {
-        const float2* t = cs + it[j].at;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-          // the unit's 2 N elements: pair i is (x_i, y_i), or elements 2i and 2i+1 of x followed by y
-          T& ra = INTER ? (2 * i < N ? x[j].v[2 * i < N ? 2 * i : 0] : y[j].v[2 * i < N ? 0 : 2 * i - N]) : x[j].v[i];
-          T& rb = INTER ? (2 * i + 1 < N ? x[j].v[2 * i + 1 < N ? 2 * i + 1 : 0]
-                                         : y[j].v[2 * i + 1 < N ? 0 : 2 * i + 1 - N])
-                        : y[j].v[i];
-          const float a = to_f(ra), d = to_f(rb);
-          ra = from_f<T>(fmaf(a, t[i].x, -d * t[i].y));
-          rb = from_f<T>(fmaf(d, t[i].x, a * t[i].y));
-        }
+      for (int i = 0; i < N; ++i) {
+        const float2 t = cs[it.at + i / kPairRun * p.rot_units * kPairRun + i % kPairRun];
+        // the unit's 2 N elements: pair i is (x_i, y_i), or elements 2i and 2i+1 of x followed by y
+        T& ra = INTER ? (2 * i < N ? x.v[2 * i < N ? 2 * i : 0] : y.v[2 * i < N ? 0 : 2 * i - N]) : x.v[i];
+        T& rb = INTER ? (2 * i + 1 < N ? x.v[2 * i + 1 < N ? 2 * i + 1 : 0] : y.v[2 * i + 1 < N ? 0 : 2 * i + 1 - N])
+                      : y.v[i];
+        const float a = to_f(ra), d = to_f(rb);
+        ra = from_f<T>(fmaf(a, t.x, -d * t.y));
+        rb = from_f<T>(fmaf(d, t.x, a * t.y));
       }
-      *reinterpret_cast<R*>(it[j].dst) = x[j];
-      if (it[j].two) *reinterpret_cast<R*>(it[j].dst + it[j].e1 * int(sizeof(T))) = y[j];
     }
+    *reinterpret_cast<R*>(it.dst) = x;
+    if (it.two) *reinterpret_cast<R*>(it.dst + it.e1 * int(sizeof(T))) = y;
   }
 }
 
@@ -265,8 +271,14 @@ int rope(const tps_rope_plan* plan, const tps_tensor* Q, const tps_tensor* K, co
   while (p.block_heads > 1 && blocks * ((p.heads + p.block_heads - 1) / p.block_heads) < 2 * sms &&
          int64_t(p.tokens) * p.block_heads * p.units > kThreads)
     p.block_heads = (p.block_heads + 1) / 2;
+  while (p.block_heads > 1 && int64_t(p.tokens) * p.block_heads * p.units > 32768) p.block_heads = (p.block_heads + 1) / 2;
   const int64_t groups = (p.heads + p.block_heads - 1) / p.block_heads;
-  if (blocks > 0x7fffffff || groups > 65535 || int64_t(p.tokens) * p.block_heads * p.units > (1 << 30))
+  const int64_t items = int64_t(p.tokens) * p.block_heads * p.units, last_heads = p.heads - (groups - 1) * p.block_heads;
+  auto inverse = [](int64_t d) { return static_cast<uint32_t>(((int64_t(1) << 32) + d - 1) / d); };
+  p.inv_units = inverse(p.units);
+  p.inv_units_heads[0] = inverse(int64_t(p.units) * p.block_heads);
+  p.inv_units_heads[1] = inverse(int64_t(p.units) * last_heads);
+  if (blocks > 0x7fffffff || groups > 65535 || items * p.units * p.block_heads >= (int64_t(1) << 32))
     return fail(TPS_ERR_SHAPE, "too many tokens or heads for one launch");
   const dim3 grid(static_cast<unsigned>(blocks), static_cast<unsigned>(groups));
   Turns t;
