@@ -60,6 +60,7 @@ struct Table {
   const tps_adamw_scalars* dev;  // read instead of `s` when given
   tps_adamw_scalars s;
   float b1, c1, b2, c2, eps;  // beta, 1 - beta
+  float minus_zero;
   Entry e[N];
 };
 
@@ -232,32 +233,51 @@ __device__ __forceinline__ void write8_codes(uint8_t* p, float inv, int lane, in
   }
 }
 
-// Square root.  ROUNDED (it goes into the state: the codes then are those of
-// the correctly rounded root): Markstein's correction, P. Markstein,
+// Pairs of fp32 operations as one instruction, each rounded on its own.
+__device__ __forceinline__ uint64_t two(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void both(uint64_t x, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+// Square roots of a pair that go into the state, correctly rounded (so the
+// codes are those of the rounded root): Markstein's correction, P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990 -- with y near 1 / sqrt(x), r = x y is off by little and
 // r + (x - r^2) y / 2 by that squared before its one rounding.  Subnormals
-// count as 0 there.  Else to two units.
-template <bool ROUNDED>
-__device__ __forceinline__ float root_of(float x) {
-  if (ROUNDED) {
-    float y;
-    asm("rsqrt.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x + 1e-36f));  // finite for 0, whose root stays 0
-    const float r = x * y;
-    return fmaf(fmaf(-r, r, x), 0.5f * y, r);
-  }
+// count as 0.
+__device__ __forceinline__ uint64_t root2(uint64_t x) {
+  float a, b;
+  both(add2(x, two(1e-36f, 1e-36f)), a, b);  // finite reciprocals for 0, whose root stays 0
+  asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(a));
+  asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(b));
+  const uint64_t y = two(a, b), r = mul2(x, y);
+  return fma2(fma2(mul2(r, two(-1.0f, -1.0f)), r, x), mul2(y, two(0.5f, 0.5f)), r);
+}
+__device__ __forceinline__ float rcp_of(float x) {  // to one unit; subnormals count as 0
   float r;
-  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
-// Quotient to two units; FAST takes subnormals for 0.
-template <bool FAST>
-__device__ __forceinline__ float over(float a, float b) {
+// Square root to two units, for a step only.
+__device__ __forceinline__ float root_of(float x) {
   float r;
-  if (FAST)
-    asm("div.approx.ftz.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  else
-    r = __fdividef(a, b);
+  asm("sqrt.approx.f32 %0, %1;" : "=f"(r) : "f"(x));
   return r;
 }
 
@@ -334,24 +354,41 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
         }
     }
   }
+  if (E4M3) {
+    // One rounding an operation, as any elementary implementation has it: a
+    // last bit that differs here can move a code by a whole step.
+    const uint64_t b1 = two(t.b1, t.b1), c1 = two(t.c1, t.c1), b2 = two(t.b2, t.b2), c2 = two(t.c2, t.c2);
+    const uint64_t cc = two(coef, coef), ss = two(s.step_size, s.step_size), rs = two(s.root_scale, s.root_scale);
+    // products that go into a sum are fma's with a -0 the compiler cannot see:
+    // it would fuse a packed product and sum into one rounding
+    const uint64_t zero = two(t.minus_zero, t.minus_zero);
+    const uint64_t eps = two(t.eps, t.eps), dc = two(s.decay, s.decay), minus = two(-1.0f, -1.0f);
 #pragma unroll
-  for (int j = 0; j < 2; ++j)
+    for (int j = 0; j < 2; ++j)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float gg = g[j][i] * coef;
-      if (E4M3) {
-        // One rounding an operation, as any elementary implementation has
-        // it: a last bit that differs here can move a code by a whole step.
-        m[j][i] = __fadd_rn(__fmul_rn(m[j][i], t.b1), __fmul_rn(gg, t.c1));
-        v[j][i] = __fadd_rn(__fmul_rn(__fmul_rn(root[j][i], root[j][i]), t.b2), __fmul_rn(__fmul_rn(gg, gg), t.c2));
-      } else {
+      for (int i = 0; i < 4; i += 2) {
+        const uint64_t gg = mul2(two(g[j][i], g[j][i + 1]), cc), r0 = two(root[j][i], root[j][i + 1]);
+        const uint64_t mm = add2(fma2(two(m[j][i], m[j][i + 1]), b1, zero), fma2(gg, c1, zero));
+        const uint64_t rr = root2(add2(fma2(mul2(r0, r0), b2, zero), fma2(mul2(gg, gg), c2, zero)));
+        float d0, d1;
+        both(fma2(rr, rs, eps), d0, d1);
+        const uint64_t step = mul2(mul2(mm, ss), two(rcp_of(d0), rcp_of(d1)));
+        both(fma2(step, minus, mul2(two(w[j][i], w[j][i + 1]), dc)), w[j][i], w[j][i + 1]);
+        both(mm, m[j][i], m[j][i + 1]);
+        both(rr, root[j][i], root[j][i + 1]);
+      }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float gg = g[j][i] * coef;
         m[j][i] = fmaf(m[j][i], t.b1, gg * t.c1);
         v[j][i] = fmaf(v[j][i], t.b2, gg * gg * t.c2);
+        const float step = __fdividef(m[j][i] * s.step_size, fmaf(root_of(v[j][i]), s.root_scale, t.eps));
+        w[j][i] = fmaf(w[j][i], s.decay, -step);
       }
-      root[j][i] = root_of<E4M3>(v[j][i]);
-      const float step = over<E4M3>(m[j][i] * s.step_size, fmaf(root[j][i], s.root_scale, t.eps));
-      w[j][i] = fmaf(w[j][i], s.decay, -step);
-    }
+  }
   constexpr bool kRandom = E4M3 || (!MASTER && sizeof(PT) == 2);
   uint32_t rm[2][4], rv[2][4], rp[2][4];
   if (kRandom) {
@@ -434,22 +471,15 @@ __global__ void __launch_bounds__(32 * kWarps, E4M3 ? 3 : 4) adamw_kernel(const 
       const int64_t stop = end - e.first < whole ? end - e.first : whole;
       if (unit < stop) {
         at += stop - unit;
-        Raw<GT, WT, E4M3> r[2];
-        if (E4M3) {  // two units at a time, the next one's loads always in flight
-          adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, r[0]);
-          while (true) {
-            if (unit + 1 < stop) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, r[1]);
-            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[0]);
-            if (++unit >= stop) break;
-            if (unit + 1 < stop) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, r[0]);
-            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[1]);
-            if (++unit >= stop) break;
-          }
-        } else {
-          for (; unit < stop; ++unit) {
-            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, r[0]);
-            adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, r[0]);
-          }
+        Raw<GT, WT, E4M3> now, next;
+        if (E4M3) adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
+        for (; unit < stop; ++unit) {
+          if (!E4M3)
+            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit, kUnit, lane, now);
+          else if (unit + 1 < stop)
+            adamw_fetch<true, WT, GT, MASTER, E4M3>(e, unit + 1, kUnit, lane, next);
+          adamw_unit<true, PT, WT, GT, MASTER, E4M3>(t, e, unit, kUnit, coef, s, lane, now);
+          if (E4M3) now = next;
         }
       } else {
         const int64_t left = e.n - unit * kUnit;
@@ -727,6 +757,7 @@ extern "C" int tps_adamw_step(const tps_adamw_tensor* tensors, int32_t n, const 
     tab.b2 = static_cast<float>(h->beta2);
     tab.c2 = static_cast<float>(1.0 - h->beta2);
     tab.eps = static_cast<float>(h->eps);
+    tab.minus_zero = -0.0f;
     int64_t elements = 0;
     for (int32_t i = 0; i <= n; ++i) {
       const bool end = i == n;
