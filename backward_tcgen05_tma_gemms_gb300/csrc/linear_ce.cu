@@ -684,23 +684,36 @@ size_t head_room(const Fixed& f, int64_t T, int planes, bool backward, int64_t c
   return f.pieces + (backward ? align256(static_cast<size_t>(2 * planes * T * cols)) : 0);
 }
 
-// K split of the dh GEMM over a piece: as many runs as bring the (tile, run)
-// units nearest to whole waves of the CTA pairs, each run at least 32 K tiles.
-int split_runs(int64_t tiles, int64_t k_tiles) {
+// Tiles and K split of the dh GEMM over a piece of k_tiles K tiles: 256 x 512
+// (wide) or 256 x 256 pair tiles, and the runs whose partial sums are added in
+// order.  Its time follows waves of (tile, run) units, a K tile costing 0.555
+// or 0.31 us, and some 8 us for each run's addition, which waits for the run
+// before it.  Measured (us): T = 1000, d = 2048, 501 K tiles: wide with 1, 2,
+// 4, 5, 9 runs 278, 156, 107, 159, 133, narrow with 1, 2, 4, 9 runs 156, 94,
+// 100, 106; T = 8192, d = 4096, 512 K tiles: wide with 1, 2, 3, 4 runs 1286,
+// 1190, 1251, 1243.
+struct Split {
+  bool wide = false;
+  int runs = 1;
+};
+Split choose_split(int64_t T, int64_t d, int64_t k_tiles, bool may_wide) {
+  Split best;
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return 1;
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2)
+    return best;
   const int64_t pairs = sms / 2;
-  if (pairs < 1 || tiles < 1) return 1;
-  int best = 1;
-  double best_fill = 0.0;
-  for (int runs = 1; runs <= 16 && (runs == 1 || k_tiles / runs >= 32); ++runs) {
-    const int64_t units = tiles * runs, waves = (units + pairs - 1) / pairs;
-    const double fill = double(units) / double(waves * pairs);
-    if (fill > best_fill * 1.05) {  // another run costs one more read and write of the output
-      best = runs;
-      best_fill = fill;
+  double least = 0.0;
+  for (int wide = 0; wide <= (may_wide ? 1 : 0); ++wide) {
+    const int64_t tiles = wide ? wide_tile_count(T, d) : pair_tile_count(T, d);
+    for (int runs = 1; runs <= 16 && (runs == 1 || k_tiles / runs >= 16); ++runs) {
+      const int64_t waves = (tiles * runs + pairs - 1) / pairs, steps = (k_tiles + runs - 1) / runs;
+      const double us = double(waves) * double(steps) * (wide ? 0.555 : 0.31) + (runs > 1 ? 8.0 * runs : 0.0);
+      if (least == 0.0 || us < least) {
+        least = us;
+        best.wide = wide != 0;
+        best.runs = runs;
+      }
     }
   }
   return best;
@@ -899,11 +912,12 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
       q.epi.d = acc; q.epi.ldd = ld_acc;
       q.epi.accumulate = v0 > 0;
       q.wide = true;
-      q.wide = gemm_wide_supported(q);
+      const Split split = choose_split(c.T, c.d, (n + 63) / 64 * (l.planes > 1 ? 6 : 1), gemm_wide_supported(q));
+      q.wide = split.wide;
+      q.ksplit = split.runs;
       const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
       if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles + 1) * sizeof(uint32_t), s) != cudaSuccess)
         return fail(TPS_ERR_CUDA, "memset failed");
-      q.ksplit = split_runs(tiles, (n + 63) / 64 * (l.planes > 1 ? 6 : 1));
       q.kflags = flags;
       q.unit_counter = flags + tiles;
       if ((rc = run_gemm(q, ld_acc, 1, s))) return rc;
