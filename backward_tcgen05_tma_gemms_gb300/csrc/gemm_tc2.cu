@@ -115,7 +115,17 @@ struct T2Params {
 //   T2_GLU_BWD  EPI_GLU_BWD
 //   T2_SEG      EPI_STORE with contraction or column segments
 //   T2_CE       EPI_CE_LSE, EPI_CE_GRAD
-enum T2Family : int { T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6 };
+//   T2_PLANES   EPI_STORE, EPI_CE_LSE, EPI_CE_GRAD of operands in bf16 planes
+//               (GemmDesc::planes).  The tensor cores cut each partial sum
+//               where fp32 would round it, always towards zero: after 300
+//               steps a sum was 9e-6 off.  So the accumulator is drained every
+//               T2_SUB K tiles (32 steps) and added up, rounded, in the
+//               registers of the epilogue threads, 128 columns each, while the
+//               other accumulator fills.
+enum T2Family : int {
+  T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6, T2_PLANES = 7
+};
+constexpr int T2_SUB = 8;
 
 // Shared-memory layout per family: five operand stages of 32 KB and the
 // epilogue's staging.  With four stages the mainloop measured latency-bound
@@ -130,7 +140,7 @@ enum T2Family : int { T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, 
 //                     (6 KB), single-buffered                -> 5 stages
 template <int FAM>
 struct T2Layout {
-  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG || FAM == T2_CE;
+  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG || FAM == T2_CE || FAM == T2_PLANES;
   static constexpr int kStages = 5;
   static constexpr bool kTwoBf16 = FAM == T2_GLU_BWD || FAM == T2_ACT16;  // two bf16 boxes per buffer
   static constexpr int kBufBytes = kStoreOnly ? TC_STG_F32_BYTES : (kTwoBf16 ? 2 * TC_STG_BF16_BYTES : T2_STG_BUF);
@@ -246,13 +256,11 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
           const CUtensorMap* mb = ks > 0 ? &m.b[ks] : mb0;
           int k0 = (kt - (ks > 0 ? p.k_end[ks - 1] : 0)) * TC_BK;
           int xa = 0, xb = 0;  // the operands' planes along their contiguous dimensions
-          if constexpr (FAM == T2_PLAIN || FAM == T2_CE) {
-            if (p.kt1 > 0) {
-              const int prod = kt / p.kt1;  // planes of A: 2 1 0 1 0 0, of B: 0 1 2 0 1 0
-              k0 = (kt - prod * p.kt1) * TC_BK;
-              xa = ((0x046 >> (2 * prod)) & 3) * p.a_plane;
-              xb = ((0x124 >> (2 * prod)) & 3) * p.b_plane;
-            }
+          if constexpr (FAM == T2_PLANES) {
+            const int prod = kt / p.kt1;  // planes of A: 2 1 0 1 0 0, of B: 0 1 2 0 1 0
+            k0 = (kt - prod * p.kt1) * TC_BK;
+            xa = ((0x046 >> (2 * prod)) & 3) * p.a_plane;
+            xb = ((0x124 >> (2 * prod)) & 3) * p.b_plane;
           }
           if (!A_MN) {
             pair_load(sa, ma, fb, k0 + xa, m0, p.pol_a, pa);
@@ -291,10 +299,20 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
       for (int u = units.take(); ok && u >= 0; u = units.take()) {
         const int run = u / p.num_tiles;
         const int kt_begin = run * p.kt_run, kt_end = min(p.k_tiles, kt_begin + p.kt_run);
-        if (!mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
+        if (FAM != T2_PLANES && !mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
         tc_fence_after();
-        const uint32_t d_tmem = tmem_base + acc * T2_BN;
+        uint32_t d_tmem = tmem_base + acc * T2_BN;
         for (int kt = kt_begin; kt < kt_end; ++kt) {
+          if constexpr (FAM == T2_PLANES) {
+            if ((kt - kt_begin) % T2_SUB == 0) {  // a fresh accumulator
+              if (!mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              d_tmem = tmem_base + acc * T2_BN;
+            }
+          }
           if (!mbar_wait(&bars->full[stage], phase, abort_flag, p.err)) {
             ok = false;
             break;
@@ -308,18 +326,26 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
                                      : smem_desc_sw128(sa + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, TC_MN_BOX_BYTES, 1024)
                                      : smem_desc_sw128(sb + kk * 32, 16, 1024);
-            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (kt != kt_begin || kk != 0) ? 1u : 0u);
+            const bool first = FAM == T2_PLANES ? (kt - kt_begin) % T2_SUB == 0 : kt == kt_begin;
+            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
           }
           tc_commit_pair_mc(&bars->empty[stage], 0x3);  // frees the stage in both CTAs
           if (++stage == T2_STAGES) {
             stage = 0;
             phase ^= 1u;
           }
+          if (FAM == T2_PLANES && (kt + 1 == kt_end || (kt + 1 - kt_begin) % T2_SUB == 0)) {
+            tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);
+            acc ^= 1u;
+            if (acc == 0) acc_phase ^= 1u;
+          }
         }
         if (!ok) break;
-        tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);  // both CTAs' accumulators complete
-        acc ^= 1u;
-        if (acc == 0) acc_phase ^= 1u;
+        if (FAM != T2_PLANES) {
+          tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);  // both CTAs' accumulators complete
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
       }
       tc_commit_pair(&bars->drain);
       mbar_wait_drain(&bars->drain, 0, p.err);
@@ -356,8 +382,8 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
       // What the head cross entropy knows of this row, also before the wait.
       float4 ce_row = make_float4(0.0f, 0.0f, __int_as_float(-1), 0.0f);
       int64_t ce_y = -1;
-      if constexpr (FAM == T2_CE) {
-        if (row < p.M) {
+      if constexpr (FAM == T2_CE || FAM == T2_PLANES) {
+        if (row < p.M && e.mode != EPI_STORE) {
           if (e.mode == EPI_CE_GRAD)
             ce_row = __ldg(e.ce_rows + row);
           else
@@ -375,9 +401,10 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
           for (int i = 0; i < 32; ++i) a_next[i] = 0.0f;
         }
       }
-      if (p.ksplit > 1 && run > 0) {
-        // K split: the previous run of this tile (all 2 x 8 epilogue warps
-        // of its pair) must be in memory before this run adds to it.
+      // K split: the previous run of this tile (all 2 x 8 epilogue warps of its
+      // pair) must be in memory before this run adds to it.
+      auto my_turn = [&]() -> bool {
+        if (p.ksplit <= 1 || run == 0) return true;
         uint32_t ready = 1u;
         if (lane == 0) {
           const uint32_t need = static_cast<uint32_t>(2 * T2_EPI_WARPS * run);
@@ -395,12 +422,92 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
           }
           fence_async_global();
         }
-        if (!__shfl_sync(0xffffffffu, ready, 0)) break;
+        return __shfl_sync(0xffffffffu, ready, 0) != 0u;
+      };
+      if (FAM != T2_PLANES && !my_turn()) break;
+      const uint32_t t_col = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * warp_cols);
+      if constexpr (FAM == T2_PLANES) {
+        float sum[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
+        const int kt_begin = run * p.kt_run, kt_end = min(p.k_tiles, kt_begin + p.kt_run);
+        const int subs = (kt_end - kt_begin + T2_SUB - 1) / T2_SUB;
+        int sub = 0;
+        for (; sub < subs; ++sub) {
+          if (!mbar_wait(&bars->tmem_full[acc], acc_phase, abort_flag, p.err)) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {  // 16 columns at a time: registers
+            uint32_t r[16];
+            tmem_ld_32x32b_x16(t_col + acc * T2_BN + c * 16, r);
+            tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i) sum[c / 2][c % 2 * 16 + i] += __uint_as_float(r[i]);
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tmem_empty0_leader + acc * static_cast<uint32_t>(sizeof(uint64_t)));
+          acc ^= 1u;
+          if (acc == 0) acc_phase ^= 1u;
+        }
+        if (sub < subs || !my_turn()) break;  // the turn is awaited when the sums are complete, not before
+        const float none[32] = {};
+        if (e.mode == EPI_CE_LSE) {
+          if (nh0 < p.N)
+            ce_lse_tile(e, nh0, p.N, row < p.M, row, ce_y, [&](int c, float(&v)[32]) {
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (k == c) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) v[i] = sum[k][i];
+                }
+            });
+        } else {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int col0 = nh0 + c * 32;
+            if (col0 >= p.n_store) break;  // warp-uniform
+            float(&v)[32] = sum[c];
+            if (e.mode == EPI_CE_GRAD) {  // three bf16 planes whose sum is the fp32 gradient, zeros past column N
+              ce_grad32(ce_row, e.ce_col0 + col0, v);
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (col0 + i >= p.N) v[i] = 0.0f;
+              for (int pl = 0; pl < 3; ++pl) {
+                uint8_t* buf = stg + (chunk & 1u) * L::kBufBytes;
+                tc_store_chunk<L::kBufs - 1, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0 + pl * p.d_plane, v,
+                                                   none);
+                ++chunk;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+              }
+            } else if (!p.tma_store) {
+              if (row < p.M) epilogue_run32(e, row, col0, min(32, p.N - col0), v);
+            } else {
+              uint8_t* buf = stg + (chunk & 1u) * L::kBufBytes;
+              if (run > 0 || e.accumulate)
+                tc_store_chunk<L::kBufs - 1, true, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, none);
+              else
+                tc_store_chunk<L::kBufs - 1, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, none);
+              ++chunk;
+            }
+          }
+        }
+        if (p.ksplit > 1) {  // K split: this warp's part of the run is in memory
+          if (lane == 0) {
+            bulk_wait0();
+            fence_async_global();
+            red_release_gpu_add(p.kflags + tile, 1u);
+          }
+          __syncwarp();
+        }
+        continue;
       }
       if (!mbar_wait(&bars->tmem_full[acc], acc_phase, abort_flag, p.err)) break;
       tc_fence_after();
-      const uint32_t t_row =
-          tmem_base + (static_cast<uint32_t>(q * 32) << 16) + acc * T2_BN + static_cast<uint32_t>(h * warp_cols);
+      const uint32_t t_row = t_col + acc * T2_BN;
       bool ce_done = false;
       if constexpr (FAM == T2_PLAIN) {
         if (ce) {  // the warp's 128 columns are one statistics tile
@@ -426,12 +533,19 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
       if constexpr (FAM == T2_CE) {
         if (e.mode == EPI_CE_LSE) {
           ce_done = true;
-          if (nh0 < p.N) ce_lse_tile(e, t_row, nh0, p.N, row < p.M, row, ce_y);
+          if (nh0 < p.N)
+            ce_lse_tile(e, nh0, p.N, row < p.M, row, ce_y, [&](int c, float(&v)[32]) {
+              uint32_t r[32];
+              tmem_ld_32x32b_x32(t_row + c * 32, r);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+            });
         }
       }
       for (int c = 0; !ce_done && c < warp_cols / 32; ++c) {
         const int col0 = nh0 + c * 32;
-        if (col0 >= (FAM == T2_CE ? p.n_store : p.N)) break;  // warp-uniform
+        if (col0 >= p.N) break;  // warp-uniform
         uint32_t r[32];
         tmem_ld_32x32b_x32(t_row + c * 32, r);
         if constexpr (glu) {  // gate in r, the same hidden units' up projection 128 columns on
@@ -495,22 +609,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
         }
         // the fp32 and bf16 slots (store-only: one shared box), single- or double-buffered
         uint8_t* buf = stg + (L::kBufs == 2 ? (chunk & 1u) * L::kBufBytes : 0u);
-        if constexpr (FAM == T2_CE) {
-          ce_grad32(ce_row, e.ce_col0 + col0, v);
-          if (p.d_plane > 0) {  // three bf16 planes whose sum is the fp32 gradient, zeros past column N
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              if (i >= n) v[i] = 0.0f;
-            for (int pl = 0; pl < 3; ++pl) {
-              buf = stg + (chunk & 1u) * L::kBufBytes;
-              tc_store_chunk<L::kBufs - 1, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0 + pl * p.d_plane, v, a);
-              ++chunk;
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
-            }
-            continue;
-          }
-        }
+        if constexpr (FAM == T2_CE) ce_grad32(ce_row, e.ce_col0 + col0, v);
         if constexpr (FAM == T2_PLAIN) {
           if (run > 0 || e.accumulate) {  // K split (or a sum over pieces): add this partial tile to the output
             tc_store_chunk<L::kBufs - 1, true, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, a);
@@ -611,6 +710,7 @@ static int launch_pair_family(const GemmDesc& g, const T2Maps& m, const T2Params
     if (g.epi.mode != EPI_STORE) return TPS_ERR_ARG;
     return launch_pair_majors<T2_SEG>(g, m, p, pairs, a_mn, b_mn, stream);
   }
+  if (g.planes > 1) return launch_pair_majors<T2_PLANES>(g, m, p, pairs, a_mn, b_mn, stream);
   if (g.epi.mode == EPI_CE_LSE || g.epi.mode == EPI_CE_GRAD)
     return launch_pair_majors<T2_CE>(g, m, p, pairs, a_mn, b_mn, stream);
   const bool pre16 = (g.epi.mode == EPI_ACT_FWD && (g.epi.d == nullptr || g.epi.d_dtype == TPS_BF16)) ||

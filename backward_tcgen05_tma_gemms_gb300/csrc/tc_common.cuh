@@ -349,25 +349,24 @@ __device__ __forceinline__ void ce_stats_tile(const Epilogue& e, uint32_t t_col,
   if (row_ok) st.flush(e, row, tc0 / kStatsTileN);
 }
 
-// EPI_CE_LSE over the statistics tile that starts at column tc0 (TMEM address
-// t_col), for the row this thread owns (label y relative to column 0, or
+// EPI_CE_LSE over the statistics tile that starts at column tc0, for the row this thread owns (label y relative to column 0, or
 // negative): one read of the accumulator, 32 columns at a time, with the
 // running maximum m and the sum s of e^{z - m}, which is rescaled whenever m
 // grows.  Nothing is stored but (m, s) and, where the label lies here, its
 // logit.  A tile of -inf leaves (-inf, 0); a NaN makes s NaN.
-__device__ __forceinline__ void ce_lse_tile(const Epilogue& e, uint32_t t_col, int64_t tc0, int64_t N, bool row_ok,
-                                            int64_t row, int64_t y) {
+// load(c, v) brings the tile's 32 columns of chunk c.
+template <class Load>
+__device__ __forceinline__ void ce_lse_tile(const Epilogue& e, int64_t tc0, int64_t N, bool row_ok, int64_t row,
+                                            int64_t y, Load&& load) {
   constexpr int kChunks = kStatsTileN / 32;
   const int chunks = static_cast<int>((N - tc0) / 32 < kChunks ? (N - tc0 + 31) / 32 : kChunks);
   float m = -INFINITY, s = 0.0f, zy = 0.0f;
   bool have = false;
-  for (int c = 0; c < chunks; ++c) {
-    uint32_t r[32];
-    tmem_ld_32x32b_x32(t_col + c * 32, r);
-    tmem_ld_wait();
-    float v[32];
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+  for (int c = 0; c < kChunks; ++c) {
+    if (c >= chunks) break;
+    float v[32];
+    load(c, v);
     const int64_t col0 = tc0 + 32 * c;
     const int n = static_cast<int>(N - col0 < 32 ? N - col0 : 32);
     if (n < 32) {
