@@ -20,15 +20,21 @@
 // bf16, the type in which the tensor cores take it).  The piece is then the
 // K-major operand of dh += dz W_piece^T, summed over the pieces in fp32 by
 // TMA reductions in piece order, and the MN-major operand of dW_piece.
-// 8 T d V operations against the 6 T d V of a backward pass that is given
-// the logits: the quarter more is what not keeping them costs.
+// 6 T d V operations; forward and backward together take 8 T d V, where a
+// pass that keeps T x V logits takes 6: a third more is what not keeping them
+// costs.
+//
+// T = 8192, d = 4096, V = 128256, bf16: forward 4.84 ms (1780 TFLOP/s),
+// backward 15.2 ms (1700 TFLOP/s), the power cap's rate; workspace 66 MB and
+// 0.65 GB, where the logits would be 2.1 GB in bf16.
 //
 // fp32 operands take the tensor cores too: each value is the sum of three
 // bf16 values exactly (8 + 8 + 8 bits), and of the nine products of such
 // planes the six that reach fp32's 2^-24 are summed into one fp32
 // accumulator, smallest first (GemmDesc::planes); dz is split the same way in
 // the epilogue.  Six times the tensor-core work of bf16 is still a fraction of
-// the fp32 pipes' time.  These planes, and bf16 operands that TMA cannot
+// the fp32 pipes' time (T = 512, d = 1024, V = 8192 backward: 238 us, 2216 us
+// on the fp32 pipes).  These planes, and bf16 operands that TMA cannot
 // describe, are laid out in the workspace, Whead one piece at a time.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>

@@ -5,7 +5,9 @@
  * The library computes the forward and backward of a matrix product split
  * over P logical ranks, the column-then-row tensor-parallel MLP (plain and
  * gated), the head-split attention projections and the vocabulary-sharded
- * cross-entropy.  On one GPU the logical ranks are shard
+ * cross-entropy, and what a training step needs beside them: the head's
+ * cross-entropy without its logits, rotary positions and the AdamW step with
+ * the gradients' norm.  On one GPU the logical ranks are shard
  * partitions of the same device buffers: a result the pages concatenate is a
  * range of one output buffer, and a result the pages sum over ranks is
  * accumulated inside the producing kernel (the contraction loop runs over
@@ -41,8 +43,9 @@
  *     launches on one stream execute in issue order.
  *   - CUDA graphs.  tps_matmul_fwd_bwd, tps_mlp_fwd_bwd, tps_glu_mlp_fwd_bwd,
  *     tps_attn_qkv_fwd, tps_attn_qkv_bwd, tps_attn_out_fwd_bwd,
- *     tps_vocab_ce_fwd_bwd and tps_vocab_ce_fwd_bwd_ex enqueue only kernel
- *     launches and memsets on `cuda_stream`; their one-time set-up runs on
+ *     tps_vocab_ce_fwd_bwd, tps_vocab_ce_fwd_bwd_ex, tps_linear_ce_fwd,
+ *     tps_linear_ce_bwd, tps_rope_fwd, tps_rope_bwd, tps_grad_norm and
+ *     tps_adamw_step enqueue only kernel launches and memsets on `cuda_stream`; their one-time set-up runs on
  *     the first call on a device.  After one such call they may be captured
  *     into a CUDA graph; a replay reads and writes the buffers given at
  *     capture.  tps_last_device_error synchronizes and must not be captured.

@@ -267,6 +267,27 @@ def test_grad_norm(sizes, dtype):
     assert api.grad_norm(gs)[1].item() == 1.0
 
 
+def test_grad_norm_past_32_bit_offsets():
+    n = (1 << 31) + 12345
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-1], g[(1 << 31) + 5], g[7] = 3.0, 4.0, 12.0
+    assert api.grad_norm([g])[0].item() == 13.0
+
+
+def test_step_past_32_bit_offsets():
+    """A tensor of more than 2^32 bytes: its end is updated like a small one's."""
+    n, k = (1 << 31) + 512, 512
+    p, g = torch.zeros(n, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g[-k:] = tensors([k], torch.bfloat16, 40)[0]
+    plan = api.adamw_plan([p], E4M3)
+    api.adamw_step(plan, [g], step=1, **HP)
+    q = torch.zeros(k, dtype=torch.bfloat16, device="cuda")
+    small = api.adamw_plan([q], E4M3)
+    api.adamw_step(small, [g[-k:].clone()], step=1, **HP)
+    assert torch.equal(p[-k:], q) and not p[:1 << 20].any()
+    assert torch.equal(plan.m[0].view(torch.uint8)[-k:], small.m[0].view(torch.uint8))
+
+
 def test_gradient_scale_and_non_finite_gradients():
     p = tensors([1000], torch.float32, 12)
     plan = api.adamw_plan(p)

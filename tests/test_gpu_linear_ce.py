@@ -214,6 +214,12 @@ def test_bad_label_is_reported():
     assert torch.allclose(dh[4].double(), want, atol=2.0 ** -6)
 
 
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_more_tokens_than_one_forward_block(dtype):
+    """65536 rows go through one forward GEMM; the rest follow."""
+    check(*case(13, 65536 + 300, 16, 40, "in_out", dtype, ignored=1000), "in_out", "sum")
+
+
 def test_empty_batch():
     h, W, y = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(64, 512, dtype=torch.bfloat16,
                                                                                  device="cuda"), torch.empty(0, dtype=torch.int64, device="cuda")

@@ -150,6 +150,18 @@ def test_empty_and_neighbours_untouched():
     assert (big[:, 0] == 3).all() and (big[:, 3] == 3).all() and (big[..., :8] == 3).all() and (big[..., 40:] == 3).all()
 
 
+def test_past_32_bit_offsets():
+    """4.3 GB of heads: the last tokens turn like any others."""
+    T, H, D = 131072 + 3, 64, 256
+    q = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    q[-5:] = torch.randn(5, H, D, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(T, device="cuda")
+    plan = api.rope_plan(D)
+    want, bound = reference(q[-5:], pos[-5:], *frequencies(D), D, False, 1)
+    y, _ = api.rope_fwd(plan, q, None, pos, out=(q, None))
+    assert ((y[-5:].double() - want).abs() <= bound).all() and not y[:1000].any()
+
+
 def test_graph_and_stream():
     plan = api.rope_plan(128)
     q, k = torch.randn(64, 8, 128, device="cuda"), torch.randn(64, 2, 128, device="cuda")
