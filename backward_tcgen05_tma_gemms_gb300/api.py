@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import struct
+from array import array
 from typing import Optional, Sequence
 
 import numpy as np
@@ -609,7 +610,7 @@ def _rope(fn, plan, q, k, positions, head_dim, out):
             raise ValueError("shape")
         return t.unflatten(1, (t.shape[1] // head_dim, head_dim))
     if out is None:
-        out = (q.new_empty(q.shape), None if k is None else k.new_empty(k.shape))
+        out = (torch.empty_like(q), None if k is None else torch.empty_like(k))
     _check(fn(plan, _view(heads(q)), _view(heads(k)), _view(positions), _view(heads(out[0])), _view(heads(out[1])),
               _raw_stream(q)))
     return tuple(out)
@@ -637,7 +638,7 @@ class AdamWPlan:
     def __init__(self, params, master, m, v, m_scale, v_scale):
         self.params, self.master, self.m, self.v, self.m_scale, self.v_scale = params, master, m, v, m_scale, v_scale
         n = len(params)
-        self.numels = [p.numel() for p in params]
+        self.numels = array("q", (p.numel() for p in params))
         self.device = params[0].get_device() if n else 0
         t = np.zeros(n, _ADAMW_ROW)
         for name, ts in (("param", params), ("master", master), ("m", m), ("v", v), ("m_scale", m_scale),
@@ -708,8 +709,8 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
 
 
 def _grad_list(grads):
-    """Pointers, sizes and dtype codes of contiguous gradients, and the GPUs
-    they are on."""
+    """Pointers and sizes (as arrays), dtype codes of contiguous gradients, and
+    the GPUs they are on."""
     cls = torch.Tensor
     if not all(map(cls.is_contiguous, grads)):
         raise TpsError(ERR_LAYOUT, "gradients must be contiguous")
@@ -721,7 +722,7 @@ def _grad_list(grads):
     if not kinds <= {torch.float32, torch.bfloat16}:
         raise TypeError("gradients must be fp32 or bf16")
     codes = _DTYPES[dtypes[0]] if len(kinds) == 1 else [_DTYPES[d] for d in dtypes]
-    return list(map(cls.data_ptr, grads)), list(map(cls.numel, grads)), codes, devices
+    return array("Q", list(map(cls.data_ptr, grads))), array("q", list(map(cls.numel, grads))), codes, devices
 
 
 def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: Optional[torch.Tensor] = None,
@@ -732,13 +733,14 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: O
     ptrs, numels, codes, devices = _grad_list(grads)
     index = next(iter(devices)) if devices else torch.cuda.current_device()
     t = np.zeros(len(ptrs), _SPAN_ROW)
-    t["data"], t["numel"], t["dtype"] = ptrs, numels, codes
+    if len(ptrs):
+        t["data"], t["numel"], t["dtype"] = np.frombuffer(ptrs, np.uint64), np.frombuffer(numels, np.int64), codes
     lib = library()
     need = int(lib.tps_grad_norm_workspace_bytes(len(ptrs)))
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=torch.device("cuda", index))
+        workspace = torch.empty(need, dtype=torch.uint8, device=index)
     if out is None:
-        out = torch.empty(2, dtype=torch.float32, device=torch.device("cuda", index))
+        out = torch.empty(2, dtype=torch.float32, device=index)
     elif out.numel() != 2 or out.dtype != torch.float32 or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("shape")
     _check(lib.tps_grad_norm(t.ctypes.data, len(ptrs), float(max_norm), out.data_ptr(), workspace.data_ptr(),
@@ -776,7 +778,7 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
         if t is not None and (not t.is_cuda or t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
             raise ValueError("shape")
     t = plan._table.copy()
-    t["grad"], t["grad_dtype"] = ptrs, codes
+    t["grad"], t["grad_dtype"] = np.frombuffer(ptrs, np.uint64), codes
     h = TpsAdamwHyper(lr, beta1, beta2, eps, weight_decay, step, 0 if seed is None else seed & 0xffffffff,
                       0 if seed is None else 1)
     _check(library().tps_adamw_step(t.ctypes.data, len(ptrs), ctypes.byref(h),
