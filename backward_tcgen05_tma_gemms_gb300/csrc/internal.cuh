@@ -212,6 +212,7 @@ struct GemmDesc {
   int planes = 1;
   int64_t a_plane = 0, b_plane = 0, a_cols = 0, b_cols = 0;
   int64_t d_plane = 0, n_store = 0;
+  bool pair = false;  // CTA pairs whatever M is (a K split needs them)
   const char* name = "gemm";  // label used by the launch profiler
 };
 // Pair tiles of a GEMM on the CTA-pair kernel (the size of GemmDesc::kflags).

@@ -678,7 +678,7 @@ Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool direct, int planes, boo
     f.zy = take(4 * T);
   } else {
     f.rows = take(16 * T);
-    f.flags = take(4 * (pair_tile_count(T, d) + 1));
+    f.flags = take(4 * pair_tile_count(T, d));
     f.acc = take(4 * T * round_up(d, 4));
   }
   if (!direct) f.h = take(laid_bytes(T, d, planes));
@@ -921,11 +921,13 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
       const Split split = choose_split(c.T, c.d, (n + 63) / 64 * (l.planes > 1 ? 6 : 1), gemm_wide_supported(q));
       q.wide = split.wide;
       q.ksplit = split.runs;
-      const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
-      if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles + 1) * sizeof(uint32_t), s) != cudaSuccess)
-        return fail(TPS_ERR_CUDA, "memset failed");
-      q.kflags = flags;
-      q.unit_counter = flags + tiles;
+      if (q.ksplit > 1) {
+        const int64_t tiles = q.wide ? wide_tile_count(c.T, c.d) : pair_tile_count(c.T, c.d);
+        if (cudaMemsetAsync(flags, 0, static_cast<size_t>(tiles) * sizeof(uint32_t), s) != cudaSuccess)
+          return fail(TPS_ERR_CUDA, "memset failed");
+        q.kflags = flags;
+        q.pair = true;
+      }
       if ((rc = run_gemm(q, ld_acc, 1, s))) return rc;
     }
     if (want_dw) {  // dW_piece = h^T dz
