@@ -172,7 +172,8 @@ int launch_gemm_simt(const GemmDesc& g, uint32_t* /*dev_err*/, cudaStream_t stre
   // the fused gate/up form, the CE statistics form and column segments are
   // tensor-core only
   if (g.epi.mode == EPI_GLU_FWD || g.epi.mode == EPI_CE_STATS || g.epi.mode == EPI_CE_LSE ||
-      g.epi.mode == EPI_CE_GRAD || g.n_segs > 1 || (g.epi.accumulate && g.epi.d_dtype != TPS_F32))
+      g.epi.mode == EPI_CE_GRAD || g.n_segs > 1 || (g.epi.accumulate && g.epi.d_dtype != TPS_F32) ||
+      g.epi.alpha != nullptr)
     return TPS_ERR_ARG;
   p.epi = g.epi;
   const int64_t gx = (g.N + SG_BN - 1) / SG_BN, gy = (g.M + SG_BM - 1) / SG_BM;

@@ -385,6 +385,7 @@ bool gemm_tc_supported(const GemmDesc& g) {
   if (g.epi.mode == EPI_CE_LSE && (g.epi.stats == nullptr || g.epi.ce_labels == nullptr || g.epi.ce_zy == nullptr))
     return false;
   if (g.epi.mode == EPI_CE_GRAD && (g.epi.ce_rows == nullptr || g.epi.d_dtype != TPS_BF16)) return false;
+  if (g.epi.alpha != nullptr && (g.epi.mode != EPI_STORE || g.n_segs > 1 || k_segs || g.planes > 1)) return false;
   if (g.epi.accumulate && (g.epi.mode != EPI_STORE || g.epi.d_dtype != TPS_F32 || g.n_segs > 1 || k_segs ||
                            (reinterpret_cast<uintptr_t>(g.epi.d) & 15u) != 0 || (g.epi.ldd * 4) % 16 != 0 ||
                            g.epi.ldd < g.N))
@@ -530,7 +531,7 @@ int launch_gemm_tc(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   const int forced = kv ? atoi(kv) : 0;
   const bool pair_only =
       g.epi.mode == EPI_GLU_FWD || g.epi.mode == EPI_GLU_BWD || g.epi.mode == EPI_CE_LSE ||
-      g.epi.mode == EPI_CE_GRAD || g.epi.accumulate || g.pair || g.planes > 1 || g.a_cols > 0 || g.b_cols > 0 || g.K2 > 0 || g.K3 > 0 || g.n_segs > 1;
+      g.epi.mode == EPI_CE_GRAD || g.epi.accumulate || g.epi.alpha != nullptr || g.pair || g.planes > 1 || g.a_cols > 0 || g.b_cols > 0 || g.K2 > 0 || g.K3 > 0 || g.n_segs > 1;
   const bool pair = pair_only || forced == 2 || (forced != 1 && g.M >= 256);
   return pair ? launch_gemm_tc2(g, dev_err, stream) : launch_gemm_tc1(g, dev_err, stream);
 }

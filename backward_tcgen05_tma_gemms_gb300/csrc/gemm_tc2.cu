@@ -603,6 +603,13 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
         const int n = min(32, p.N - col0);
+        if constexpr (FAM == T2_PLAIN) {
+          if (e.alpha != nullptr) {
+            const float al = __ldg(e.alpha);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] *= al;
+          }
+        }
         if (FAM != T2_CE && !p.tma_store) {
           if (row < p.M) epilogue_run32(e, row, col0, n, v);
           continue;

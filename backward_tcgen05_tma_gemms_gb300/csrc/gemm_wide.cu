@@ -423,6 +423,11 @@ __global__ void __launch_bounds__(W_THREADS, 1) gemm_wide_kernel(const __grid_co
         float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+        if (e.alpha != nullptr) {
+          const float al = __ldg(e.alpha);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= al;
+        }
         if (run > 0 || e.accumulate)  // K split (or a sum over pieces): add this partial tile to the output
           tc_store_chunk<0, true, true>(e, &m.d, &m.d, stg, stg, lane, row0, col0, v, none);
         else

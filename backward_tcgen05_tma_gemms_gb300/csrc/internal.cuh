@@ -107,6 +107,9 @@ struct Epilogue {
   // EPI_STORE to fp32: add to D instead of storing (CTA-pair kernels with
   // TMA stores, and the SIMT kernel).
   int accumulate = 0;
+  // EPI_STORE on the CTA-pair kernels (no segments, no planes): a device
+  // float that multiplies the product, nullptr: 1.
+  const float* alpha = nullptr;
   // Debug builds: the output's extent (rows, columns) and the error word the
   // bounds checks report to.
   int64_t dbg_rows = 0, dbg_cols = 0;

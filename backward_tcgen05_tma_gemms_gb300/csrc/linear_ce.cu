@@ -179,10 +179,13 @@ __global__ void __launch_bounds__(1024) ce_total_kernel(const float* loss, int64
 
 // What the gradient epilogue knows of each row (Epilogue::ce_rows).  A mean
 // over this call's labels needs their count first: one block then does both,
-// else the rows are spread over blocks.
+// else the rows are spread over blocks.  alpha (a gradient that all rows
+// share: a sum's or a mean's): kept apart, and the products multiplied by it
+// in fp32 -- inside dz it would be rounded to bf16 with the one-hot term, the
+// same way in every row, and leave the whole gradient off by up to 2^-8.
 __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, const float* lse, const float* g,
                                                        int64_t g_step, int reduction, double denominator,
-                                                       float4* rows, uint32_t* err) {
+                                                       float4* rows, float* alpha, uint32_t* err) {
   __shared__ int64_t redi[32];
   __shared__ float share;
   if (reduction == TPS_REDUCE_MEAN && denominator == 0.0) {  // one block
@@ -200,7 +203,8 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, co
     if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
     const float up = g == nullptr ? 1.0f : g[t * g_step];
     const float l = lse[t];
-    rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : up * share,
+    if (alpha != nullptr && t == 0) *alpha = up * share;
+    rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : (alpha != nullptr ? 1.0f : up * share),
                           __int_as_float(kind == 0 ? static_cast<int>(y) : -1), l);
   }
 }
@@ -663,7 +667,7 @@ int64_t column_bytes(int64_t T, int64_t d, bool direct, int planes, bool backwar
 }
 
 struct Fixed {  // workspace before the pieces
-  size_t pairs, zy, rows, flags, acc, h, pieces;
+  size_t pairs, zy, rows, alpha, flags, acc, h, pieces;
 };
 Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool direct, int planes, bool backward) {
   Fixed f = {};
@@ -678,6 +682,7 @@ Fixed fixed_layout(int64_t T, int64_t d, int64_t V, bool direct, int planes, boo
     f.zy = take(4 * T);
   } else {
     f.rows = take(16 * T);
+    f.alpha = take(4);
     f.flags = take(4 * pair_tile_count(T, d));
     f.acc = take(4 * T * round_up(d, 4));
   }
@@ -874,13 +879,14 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
   char* ws = static_cast<char*>(workspace);
   float4* rows = reinterpret_cast<float4*>(ws + f.rows);
   uint32_t* flags = reinterpret_cast<uint32_t*>(ws + f.flags);
+  float* alpha = c.reduction != TPS_REDUCE_NONE && l.planes == 1 ? reinterpret_cast<float*>(ws + f.alpha) : nullptr;
   const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
 
   {
     const bool count = c.reduction == TPS_REDUCE_MEAN && c.denominator == 0.0;
     const int64_t blocks = count ? 1 : (c.T + 1023) / 1024;
     ce_rows_kernel<<<static_cast<unsigned>(blocks < 1024 ? blocks : 1024), 1024, 0, s>>>(
-        c.T, c.lab, static_cast<const float*>(lse->data), up, up_step, c.reduction, c.denominator, rows, err);
+        c.T, c.lab, static_cast<const float*>(lse->data), up, up_step, c.reduction, c.denominator, rows, alpha, err);
     if ((rc = launched("ce_rows"))) return rc;
   }
   // dh is summed over the pieces in fp32: in the caller's buffer where that
@@ -917,6 +923,7 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
       set_b(&q, w, true);
       q.epi.d = acc; q.epi.ldd = ld_acc;
       q.epi.accumulate = v0 > 0;
+      q.epi.alpha = alpha;
       q.wide = true;
       const Split split = choose_split(c.T, c.d, (n + 63) / 64 * (l.planes > 1 ? 6 : 1), gemm_wide_supported(q));
       q.wide = split.wide;
@@ -935,6 +942,7 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
       set_a(&q, x, true);
       set_b(&q, dz, false);
       q.epi.d = static_cast<char*>(dw.data) + v0 * dw_out * dw_es; q.epi.d_dtype = dw.dtype;
+      q.epi.alpha = alpha;
       if ((rc = run_gemm(q, dw_in, dw_out, s))) return rc;
     }
   }

@@ -173,6 +173,21 @@ def test_pieces(piece, grad):
     check(h, W, y, "in_out", "mean", grad=grad, piece=piece)
 
 
+@pytest.mark.parametrize("reduction", ["sum", "mean"])
+def test_a_shared_upstream_gradient_is_not_rounded_to_bf16(reduction):
+    """g = 1 + 2^-9 is half a bf16 step from 1.  Rounded with the one-hot term
+    it would leave the whole gradient 2^-9 off; as a factor in fp32 it leaves
+    what 1 - p of the label loses, p = 1 / 8192 on average, and roundings that
+    average out over 200 tokens."""
+    h, W, y = case(14, 200, 64, 8192, "in_out", torch.bfloat16, scale=0.05)
+    up = torch.tensor([1.0 + 2.0 ** -9], device="cuda")
+    _, _, lse = api.linear_ce_fwd(h, W, y, reduction=reduction)
+    dh, dW = api.linear_ce_bwd(h, W, y, lse, up, reduction=reduction)
+    ref = reference(h, W, y, "in_out", reduction, up=up)
+    for got, want in ((dh, ref["dh"][0]), (dW, ref["dW"][0])):
+        assert abs((got.double() * want).sum() / want.square().sum() - 1).item() <= 2.0 ** -11
+
+
 def test_all_ignored():
     h, W, y = case(6, 20, 64, 512, "in_out", torch.bfloat16, ignored=20)
     loss, total, _, dh, dW = check(h, W, y, "in_out", "mean")
