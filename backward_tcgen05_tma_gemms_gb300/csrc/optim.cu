@@ -18,7 +18,12 @@
 // multipliers of C. Wellons' search, "Prospecting for hash functions",
 // 2018).  bf16 weights without an fp32 master copy are rounded the same way.
 //
-// Bound by memory: one warp takes 256 elements (a block of the 8-bit form),
+// 218 M weights: fp32 moments with a master copy 0.92 ms (6.6 TB/s, memory),
+// e4m3 moments 0.51 ms (4.3 TB/s; some 80 instructions a weight bound it, a
+// quarter of them the random bits); the norm reads bf16 gradients at 4.9 TB/s
+// behind the previous step's dirty lines.
+//
+// One warp takes 256 elements (a block of the 8-bit form),
 // 2 x 4 a lane, so every load of a warp is consecutive, and the block's
 // maxima are two warp reductions.  The tensors' table travels in the kernel
 // parameters: no copy, no workspace, nothing to keep alive.
