@@ -9,6 +9,7 @@ built library or a GPU these functions raise.
 from __future__ import annotations
 
 import ctypes
+import itertools
 import os
 import struct
 from array import array
@@ -633,24 +634,68 @@ def rope_bwd(plan: RopePlan, dq: torch.Tensor, dk: Optional[torch.Tensor], posit
 # --------------------------------------------------------------------- optimizer step
 
 class AdamWPlan:
-    """The tensors an optimizer updates and their moments (adamw_plan)."""
+    """The tensors an optimizer updates and their moments (adamw_plan).  A
+    step updates the storage that each of them has by then: where it is another
+    one than the step before (p.data = ..., module.to(), a moved state), the
+    tensors are checked and their addresses taken again.  (Operations captured
+    into a CUDA graph keep those of the capture.)"""
 
     def __init__(self, params, master, m, v, m_scale, v_scale):
         self.params, self.master, self.m, self.v, self.m_scale, self.v_scale = params, master, m, v, m_scale, v_scale
-        n = len(params)
         self.numels = array("q", (p.numel() for p in params))
-        self.device = params[0].get_device() if n else 0
-        t = np.zeros(n, _ADAMW_ROW)
-        for name, ts in (("param", params), ("master", master), ("m", m), ("v", v), ("m_scale", m_scale),
-                         ("v_scale", v_scale)):
+        self.device = params[0].get_device() if params else 0
+        self._seen = None
+
+    def _columns(self):
+        """(field of the table, tensors, elements of a weight for each of theirs, dtypes) of what there is."""
+        state = (self.m[0].dtype,) if self.m else ()
+        for name, ts, per, dtypes in (("param", self.params, 1, (torch.float32, torch.bfloat16)),
+                                      ("master", self.master, 1, (torch.float32,)),
+                                      ("m", self.m, 1, state), ("v", self.v, 1, state),
+                                      ("m_scale", self.m_scale, ADAMW_BLOCK, (torch.float32,)),
+                                      ("v_scale", self.v_scale, ADAMW_BLOCK, (torch.float32,))):
             if ts is not None:
+                yield name, ts, per, dtypes
+
+    def _check(self):
+        if self.m and self.m[0].dtype not in _STATE_DTYPES:
+            raise TypeError(f"unsupported dtype {self.m[0].dtype}")
+        scaled = bool(self.m) and self.m[0].dtype == torch.float8_e4m3fn
+        if self.params and (scaled != (self.m_scale is not None) or scaled != (self.v_scale is not None)):
+            raise ValueError("argument")
+        for name, ts, per, dtypes in self._columns():
+            if len(ts) != len(self.params):
+                raise ValueError("shape")
+            for t, n in zip(ts, self.numels):
+                if t.numel() != -(-n // per):
+                    raise ValueError("shape")
+                if t.dtype not in dtypes:
+                    raise TypeError(f"unsupported dtype {t.dtype}")
+                if t.get_device() != self.device:
+                    raise ValueError("tensors must live on the GPU (no CPU path)" if t.get_device() < 0 else
+                                     "weights and state on different GPUs")
+                if not t.is_contiguous():
+                    raise TpsError(ERR_LAYOUT, "weights and state must be contiguous")
+
+    def rows(self):
+        """The tensors as rows of tps_adamw_tensor, without gradients."""
+        addresses = list(map(torch.Tensor.data_ptr, itertools.chain.from_iterable(c[1] for c in self._columns())))
+        if addresses != self._seen:
+            self._check()
+            n = len(self.params)
+            t = np.zeros(n, _ADAMW_ROW)
+            for name, ts, _, _ in self._columns():
                 t[name] = [x.data_ptr() for x in ts]
-        t["numel"] = self.numels
-        blocks = [-(-x // ADAMW_BLOCK) for x in self.numels]
-        t["place"] = ADAMW_BLOCK * np.concatenate(([0], np.cumsum(blocks)[:-1])) if n else []
-        t["param_dtype"] = [_DTYPES[p.dtype] for p in params]
-        t["state_dtype"] = [_STATE_DTYPES[x.dtype] for x in m]
-        self._table = t
+            t["numel"] = self.numels
+            blocks = [-(-x // ADAMW_BLOCK) for x in self.numels]
+            t["place"] = ADAMW_BLOCK * np.concatenate(([0], np.cumsum(blocks)[:-1])) if n else []
+            t["param_dtype"] = [_DTYPES[p.dtype] for p in self.params]
+            t["state_dtype"] = [_STATE_DTYPES[x.dtype] for x in self.m]
+            # These share the storages, so that none is freed (and its address given
+            # to another tensor) while the table names it.
+            self._kept = [x.detach() for c in self._columns() for x in c[1]]
+            self._table, self._seen = t, addresses
+        return self._table.copy()
 
 
 def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.float32, master=None,
@@ -666,10 +711,6 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
     for p in params:
         if not isinstance(p, torch.Tensor) or not p.is_cuda:
             raise ValueError("tensors must live on the GPU (no CPU path)")
-        if p.get_device() != params[0].get_device():
-            raise ValueError("weights on different GPUs")
-        if not p.is_contiguous():
-            raise TpsError(ERR_LAYOUT, "weights must be contiguous")
         if p.dtype not in (torch.float32, torch.bfloat16):
             raise TypeError(f"unsupported dtype {p.dtype}")
     if m is not None:
@@ -690,22 +731,9 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
         master = [p.detach().to(torch.float32).contiguous() for p in params]
     master = list(master) if master else None
     m_scale, v_scale = (list(x) if x is not None else None for x in (m_scale, v_scale))
-    if scaled != (m_scale is not None) or scaled != (v_scale is not None):
-        raise ValueError("argument")
-    for ts, dtype, per in ((m, state_dtype, 1), (v, state_dtype, 1), (master, torch.float32, 1),
-                           (m_scale, torch.float32, ADAMW_BLOCK), (v_scale, torch.float32, ADAMW_BLOCK)):
-        if ts is None:
-            continue
-        if len(ts) != len(params):
-            raise ValueError("shape")
-        for t, p in zip(ts, params):
-            if t.numel() != -(-p.numel() // per):
-                raise ValueError("shape")
-            if t.dtype != dtype:
-                raise TypeError(f"unsupported dtype {t.dtype}")
-            if not t.is_contiguous() or t.device != p.device:
-                raise TpsError(ERR_LAYOUT, "state must be contiguous, on the weights' GPU")
-    return AdamWPlan(params, master, m, v, m_scale, v_scale)
+    plan = AdamWPlan(params, master, m, v, m_scale, v_scale)
+    plan.rows()
+    return plan
 
 
 def _grad_list(grads):
@@ -777,7 +805,7 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
     for t, n, dtype in ((grad_scale, 1, torch.float32), (scalars, 4, torch.int32)):
         if t is not None and (not t.is_cuda or t.numel() != n or t.dtype != dtype or not t.is_contiguous()):
             raise ValueError("shape")
-    t = plan._table.copy()
+    t = plan.rows()
     t["grad"], t["grad_dtype"] = np.frombuffer(ptrs, np.uint64), codes
     h = TpsAdamwHyper(lr, beta1, beta2, eps, weight_decay, step, 0 if seed is None else seed & 0xffffffff,
                       0 if seed is None else 1)

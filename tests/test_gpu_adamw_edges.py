@@ -1,0 +1,32 @@
+"""AdamW and the gradient norm where they can go wrong beside the update
+itself: tensors that move, their types, and magnitudes near the ends of fp32.
+Bounds as in test_gpu_adamw.py."""
+import pytest
+import torch
+
+from backward_tcgen05_tma_gemms_gb300 import api
+from test_gpu_adamw import E4M3, HP, tensors
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("state", [torch.float32, E4M3])
+def test_a_step_follows_tensors_that_moved(state):
+    """Weights, master copies and moments whose storage was replaced are updated where they are now, and the old
+    storage stays as it was."""
+    sizes = [700, 256, 3]
+    ws = tensors(sizes, torch.bfloat16, 21)
+    a, b = [w.clone() for w in ws], [w.clone() for w in ws]
+    pa, pb = (api.adamw_plan(x, state, master=True) for x in (a, b))
+    for step in (1, 2, 3):
+        for ts in (b, pb.master, pb.m, pb.v, *((pb.m_scale, pb.v_scale) if state == E4M3 else ())):
+            old = ts[1].data
+            ts[1].data = ts[1].detach().clone()
+            old.view(torch.uint8).fill_(7)
+        gs = tensors(sizes, torch.bfloat16, 30 + step)
+        for plan in (pa, pb):
+            api.adamw_step(plan, gs, step=step, seed=step, **HP)
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
+        assert all(torch.equal(x, y) for x, y in zip(pa.master, pb.master))
+        for x, y in ((pa.m, pb.m), (pa.v, pb.v)):
+            assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(x, y))
