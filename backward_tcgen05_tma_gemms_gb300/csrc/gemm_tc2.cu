@@ -121,11 +121,33 @@ struct T2Params {
 //               steps a sum was 9e-6 off.  So the accumulator is drained every
 //               T2_SUB K tiles (32 steps) and added up, rounded, in the
 //               registers of the epilogue threads, 128 columns each, while the
-//               other accumulator fills.
+//               other accumulator fills.  The last product, of the planes 0,
+//               starts a fresh accumulator: it alone decides about infinities
+//               and NaN (see T2Drains).
 enum T2Family : int {
   T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6, T2_PLANES = 7
 };
 constexpr int T2_SUB = 8;
+
+// How the K tiles [begin, end) of a T2_PLANES unit are cut into accumulators:
+// every T2_SUB tiles, and where the product of the planes 0 begins (tile
+// `last`).  A value that is not finite lies whole in plane 0 and its other
+// planes are 0, while the planes 1 and 2 of a finite value are remainders of
+// either sign or 0: the first five products would make NaN (0 inf, inf - inf)
+// or the wrong infinity of h W = +-inf.  The product of the planes 0 has every
+// factor's sign and is 0 only where the factor is, so what it gives is what
+// fp32 gives, and entries of the other accumulators that are not finite are
+// left out.
+struct T2Drains {
+  int begin, end, last;
+  __device__ __forceinline__ T2Drains(int b, int e, int l) : begin(b), end(e), last(min(max(l, b), e)) {}
+  __device__ __forceinline__ bool starts(int kt) const {
+    return kt < last ? (kt - begin) % T2_SUB == 0 : (kt - last) % T2_SUB == 0;
+  }
+  __device__ __forceinline__ bool ends(int kt) const { return kt + 1 == end || starts(kt + 1); }
+  __device__ __forceinline__ int remainders() const { return (last - begin + T2_SUB - 1) / T2_SUB; }
+  __device__ __forceinline__ int count() const { return remainders() + (end - last + T2_SUB - 1) / T2_SUB; }
+};
 
 // Shared-memory layout per family: five operand stages of 32 KB and the
 // epilogue's staging.  With four stages the mainloop measured latency-bound
@@ -302,9 +324,10 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
         if (FAM != T2_PLANES && !mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
         tc_fence_after();
         uint32_t d_tmem = tmem_base + acc * T2_BN;
+        const T2Drains drains(kt_begin, kt_end, 5 * p.kt1);
         for (int kt = kt_begin; kt < kt_end; ++kt) {
           if constexpr (FAM == T2_PLANES) {
-            if ((kt - kt_begin) % T2_SUB == 0) {  // a fresh accumulator
+            if (drains.starts(kt)) {  // a fresh accumulator
               if (!mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) {
                 ok = false;
                 break;
@@ -326,7 +349,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
                                      : smem_desc_sw128(sa + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, TC_MN_BOX_BYTES, 1024)
                                      : smem_desc_sw128(sb + kk * 32, 16, 1024);
-            const bool first = FAM == T2_PLANES ? (kt - kt_begin) % T2_SUB == 0 : kt == kt_begin;
+            const bool first = FAM == T2_PLANES ? drains.starts(kt) : kt == kt_begin;
             tc_mma_f16_pair(d_tmem, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
           }
           tc_commit_pair_mc(&bars->empty[stage], 0x3);  // frees the stage in both CTAs
@@ -334,7 +357,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             stage = 0;
             phase ^= 1u;
           }
-          if (FAM == T2_PLANES && (kt + 1 == kt_end || (kt + 1 - kt_begin) % T2_SUB == 0)) {
+          if (FAM == T2_PLANES && drains.ends(kt)) {
             tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);
             acc ^= 1u;
             if (acc == 0) acc_phase ^= 1u;
@@ -433,7 +456,8 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) sum[c][i] = 0.0f;
         const int kt_begin = run * p.kt_run, kt_end = min(p.k_tiles, kt_begin + p.kt_run);
-        const int subs = (kt_end - kt_begin + T2_SUB - 1) / T2_SUB;
+        const T2Drains drains(kt_begin, kt_end, 5 * p.kt1);
+        const int subs = drains.count(), whole = drains.remainders();
         int sub = 0;
         for (; sub < subs; ++sub) {
           if (!mbar_wait(&bars->tmem_full[acc], acc_phase, abort_flag, p.err)) break;
@@ -443,6 +467,17 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             uint32_t r[16];
             tmem_ld_32x32b_x16(t_col + acc * T2_BN + c * 16, r);
             tmem_ld_wait();
+            if (sub < whole) {
+              float top = 0.0f;
+#pragma unroll
+              for (int i = 0; i < 16; i += 2)
+                top = max_nan(top, fabsf(__uint_as_float(r[i])), fabsf(__uint_as_float(r[i + 1])));
+              if (!(top < INFINITY)) {
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                  if (!(fabsf(__uint_as_float(r[i])) < INFINITY)) r[i] = 0u;
+              }
+            }
 #pragma unroll
             for (int i = 0; i < 16; ++i) sum[c / 2][c % 2 * 16 + i] += __uint_as_float(r[i]);
           }

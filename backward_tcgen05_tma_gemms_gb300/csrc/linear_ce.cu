@@ -240,7 +240,8 @@ __global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows,
         for (int j = 0; j < 8; ++j) {
           b[j] = __float2bfloat16_rn(x[j]);
           if (__hisinf(b[j]) && isfinite(x[j])) b[j] = __float2bfloat16_rz(x[j]);
-          x[j] = isfinite(x[j]) ? x[j] - __bfloat162float(b[j]) : 0.0f;  // infinities and NaN stay in plane 0
+          // infinities and NaN stay in plane 0, whose product alone decides about them (T2Drains)
+          x[j] = isfinite(x[j]) ? x[j] - __bfloat162float(b[j]) : 0.0f;
         }
         *reinterpret_cast<uint4*>(out + pl * plane) = *reinterpret_cast<const uint4*>(b);
       }

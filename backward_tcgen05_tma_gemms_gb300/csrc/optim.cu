@@ -179,12 +179,6 @@ __device__ __forceinline__ void write8(T* p, int lane, int n, const V (&x)[2][4]
     }
   }
 }
-// Largest of three that keeps a NaN (positive, as fabsf leaves it).
-__device__ __forceinline__ float max_nan(float a, float b, float c) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-  return r;
-}
 // The largest magnitude of the warp's block, 0 where it is next to nothing.
 __device__ __forceinline__ float block_top(const float (&x)[2][4]) {
   float part = 0.0f;

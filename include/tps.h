@@ -393,7 +393,8 @@ int tps_vocab_ce_fwd_bwd_ex(const tps_tensor* h, const tps_tensor* Whead, const 
  * about 512 MB); a call takes pieces as large as its workspace holds and
  * refuses one that does not hold 256 columns (TPS_ERR_WORKSPACE).  fp32
  * operands are taken as sums of three bf16 values each, exactly, and their
- * products to fp32's precision on the tensor cores; they, and bf16 operands
+ * products to fp32's precision on the tensor cores (with an infinity or a NaN
+ * among the factors they are what fp32 gives); they, and bf16 operands
  * that TMA cannot describe (a base or a row pitch that is not a multiple of
  * 16 bytes), are laid out in the workspace piece by piece, and such bf16
  * operands need the bytes given for TPS_F32.  Results do not depend on the

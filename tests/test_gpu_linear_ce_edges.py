@@ -1,0 +1,66 @@
+"""Head cross entropy (linear_ce_fwd / _bwd) where it can go wrong beside the
+sizes: infinite and missing logits.  Tolerances as in test_gpu_linear_ce.py."""
+import pytest
+import torch
+
+from backward_tcgen05_tma_gemms_gb300 import api
+from test_gpu_linear_ce import IGN, case, near, reference  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def lse_bound(h, W, lse):
+    """Of finite logits: d products in fp32, and the exponentials' 2^-19."""
+    return h.shape[1] * 2.0 ** -23 * (h.double().abs() @ W.double().abs().t()).amax(1) + 2.0 ** -19 * (1 + lse.abs())
+
+
+@pytest.mark.parametrize("layout", ["in_out", "out_in"])
+@pytest.mark.parametrize("T,d,off", [(1, 64, 0), (8, 64, 0), (9, 64, 0), (16, 600, 0), (300, 72, 0), (3, 64, 1), (5, 4096, 0)])
+def test_masked_vocabulary_entries_in_fp32(T, d, off, layout):
+    """-inf in a head entry that meets positive h makes its logit -inf and
+    leaves the row finite, whatever T, alignment or layout; so does +inf that
+    meets negative h.  The masked columns have no gradient."""
+    h, W, y = case(T + d, T, d, 301, "out_in", torch.float32)
+    h[:, 2], h[:, 3] = h[:, 2].abs() + 0.1, -h[:, 3].abs() - 0.1
+    W[:140, 2] = -float("inf")  # a whole tile of 128 columns and part of the next
+    W[170:180, 3] = float("inf")
+    kept = torch.ones(301, dtype=torch.bool, device="cuda")
+    kept[:140] = kept[170:180] = False
+    y = torch.where(kept[y], y, 200)
+    head = torch.zeros(301 * d + 4, device="cuda")[off:off + 301 * d].view(301, d)
+    head.copy_(W)
+    if layout == "in_out":
+        store = torch.zeros(301 * d + 4, device="cuda")[off:off + 301 * d].view(d, 301)
+        head = store.copy_(W.t())
+    loss, _, lse = api.linear_ce_fwd(h, head, y, weight_layout=layout)
+    want = torch.logsumexp(h.double() @ W[kept].double().t(), 1)
+    bound = lse_bound(h, W[kept], want)
+    assert ((lse.double() - want).abs() <= bound).all()
+    label = (h.double() * W[y].double()).sum(1)
+    assert ((loss.double() - (want - label)).abs() <= 2 * bound).all()
+    _, dW = api.linear_ce_bwd(h, head, y, lse, weight_layout=layout, want_dhidden=False)
+    dW = dW if layout == "out_in" else dW.t()
+    ref = reference(h, W[kept], kept.cumsum(0)[y] - 1, "out_in")["dW"]
+    near(dW[kept], ref, "dWhead")
+    assert not dW[~kept].any()
+    assert api.last_device_error() == 0
+
+
+@pytest.mark.parametrize("T", [4, 40])
+def test_infinite_and_missing_logits_follow_fp32(T):
+    """A row's logits are what fp32 products give: +inf, NaN for inf - inf, and NaN for a NaN in h or the head."""
+    h, W, _ = case(5, T, 64, 40, "out_in", torch.float32)
+    h = h.abs() + 0.1
+    y = torch.zeros(T, dtype=torch.int64, device="cuda")
+    W[7, 3] = float("inf")
+    _, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
+    assert not torch.isfinite(lse).any() and not (lse == -float("inf")).any()
+    W[7, 4] = -float("inf")
+    assert torch.isnan(api.linear_ce_fwd(h, W, y, weight_layout="out_in")[2]).all()
+    W[7, 3:5] = 1.0
+    h[2, 5] = float("inf")
+    h[1, 0] = float("nan")
+    _, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
+    assert torch.isnan(lse[1]) and not torch.isfinite(lse[2])
+    rest = [i for i in range(T) if i not in (1, 2)]
+    assert torch.isfinite(lse[rest]).all()
