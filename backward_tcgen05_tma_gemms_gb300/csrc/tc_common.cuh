@@ -349,11 +349,12 @@ __device__ __forceinline__ void ce_stats_tile(const Epilogue& e, uint32_t t_col,
   if (row_ok) st.flush(e, row, tc0 / kStatsTileN);
 }
 
-// EPI_CE_LSE over the statistics tile that starts at column tc0, for the row this thread owns (label y relative to column 0, or
-// negative): one read of the accumulator, 32 columns at a time, with the
-// running maximum m and the sum s of e^{z - m}, which is rescaled whenever m
-// grows.  Nothing is stored but (m, s) and, where the label lies here, its
-// logit.  A tile of -inf leaves (-inf, 0); a NaN makes s NaN.
+// EPI_CE_LSE over the statistics tile that starts at column tc0, for the row
+// this thread owns (label y relative to column 0, or negative): one read of
+// the accumulator, 32 columns at a time, with the running maximum m and the
+// sum s of e^{z - m}, which is rescaled whenever m grows.  Nothing is stored
+// but (m, s) and, where the label lies here, its logit.  A tile of -inf leaves
+// (-inf, 0); a NaN makes s NaN.
 // load(c, v) brings the tile's 32 columns of chunk c.
 template <class Load>
 __device__ __forceinline__ void ce_lse_tile(const Epilogue& e, int64_t tc0, int64_t N, bool row_ok, int64_t row,
@@ -383,10 +384,15 @@ __device__ __forceinline__ void ce_lse_tile(const Epilogue& e, int64_t tc0, int6
     }
     const float cm = ce_max32(v);
     if (!(cm <= m)) {
-      s = m == -INFINITY ? s : s * ex2_approx((m - cm) * kTcLog2e);
+      s = m == -INFINITY ? s : s * ex2_approx((m - cm) * kTcLog2e);  // (-inf, s): s is 0 or NaN
       m = cm;
     }
-    if (m != -INFINITY) s += ce_sum32(v, m);
+    if (m != -INFINITY) {
+      s += ce_sum32(v, m);
+    } else {  // all -inf so far, and perhaps a NaN, which a maximum does not show
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s = v[i] != v[i] ? v[i] : s;
+    }
   }
   if (!row_ok) return;
   const int64_t tile = tc0 / kStatsTileN;

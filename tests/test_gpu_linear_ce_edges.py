@@ -64,3 +64,16 @@ def test_infinite_and_missing_logits_follow_fp32(T):
     assert torch.isnan(lse[1]) and not torch.isfinite(lse[2])
     rest = [i for i in range(T) if i not in (1, 2)]
     assert torch.isfinite(lse[rest]).all()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("T", [2, 40])
+def test_a_nan_among_masked_logits_is_not_lost(T, dtype):
+    """Where everything before it in the row is -inf, a NaN still makes the row's sum NaN."""
+    h, W, _ = case(6, T, 64, 400, "out_in", dtype)
+    h = h.abs() + 0.1
+    W[:200, 2] = -float("inf")
+    W[133, 2] = float("nan")
+    y = torch.full((T,), 390, device="cuda")
+    loss, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
+    assert torch.isnan(lse).all() and torch.isnan(loss).all()
