@@ -9,7 +9,6 @@ built library or a GPU these functions raise.
 from __future__ import annotations
 
 import ctypes
-import itertools
 import os
 import struct
 from array import array
@@ -664,9 +663,13 @@ class AdamWPlan:
         if self.params and (scaled != (self.m_scale is not None) or scaled != (self.v_scale is not None)):
             raise ValueError("argument")
         for name, ts, per, dtypes in self._columns():
-            if len(ts) != len(self.params):
+            if len(ts) != len(self.numels):
                 raise ValueError("shape")
-            for t, n in zip(ts, self.numels):
+            for t, n, p in zip(ts, self.numels, self.params):
+                if t is None and name == "master":
+                    continue
+                if name == "master" and p.dtype != torch.bfloat16:
+                    raise TypeError("a master copy is for bf16 weights")
                 if t.numel() != -(-n // per):
                     raise ValueError("shape")
                 if t.dtype not in dtypes:
@@ -679,13 +682,15 @@ class AdamWPlan:
 
     def rows(self):
         """The tensors as rows of tps_adamw_tensor, without gradients."""
-        addresses = list(map(torch.Tensor.data_ptr, itertools.chain.from_iterable(c[1] for c in self._columns())))
+        address = torch.Tensor.data_ptr
+        addresses = [list(map(address, ts)) for ts in (self.params, self.m, self.v, self.m_scale or (), self.v_scale or ())]
+        addresses.append([0 if x is None else address(x) for x in self.master or ()])
         if addresses != self._seen:
             self._check()
             n = len(self.params)
             t = np.zeros(n, _ADAMW_ROW)
             for name, ts, _, _ in self._columns():
-                t[name] = [x.data_ptr() for x in ts]
+                t[name] = [0 if x is None else x.data_ptr() for x in ts]
             t["numel"] = self.numels
             blocks = [-(-x // ADAMW_BLOCK) for x in self.numels]
             t["place"] = ADAMW_BLOCK * np.concatenate(([0], np.cumsum(blocks)[:-1])) if n else []
@@ -693,7 +698,7 @@ class AdamWPlan:
             t["state_dtype"] = [_STATE_DTYPES[x.dtype] for x in self.m]
             # These share the storages, so that none is freed (and its address given
             # to another tensor) while the table names it.
-            self._kept = [x.detach() for c in self._columns() for x in c[1]]
+            self._kept = [x.detach() for c in self._columns() for x in c[1] if x is not None]
             self._table, self._seen = t, addresses
         return self._table.copy()
 
@@ -706,7 +711,8 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
     and their moments, fp32 or (state_dtype=torch.float8_e4m3fn) e4m3 numbers
     with a scale for every 256 elements, where v holds sqrt(v).  Moments are
     made here (zeros) unless given, as from a checkpoint.  master: True keeps
-    fp32 copies of bf16 weights (or the copies themselves, one each)."""
+    fp32 copies of the bf16 weights; or the copies themselves, one for each
+    weight, None for those without one (fp32 weights are their own)."""
     params = list(params)
     for p in params:
         if not isinstance(p, torch.Tensor) or not p.is_cuda:
@@ -728,7 +734,7 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
         m_scale = zeros(torch.float32, ADAMW_BLOCK) if scaled else None
         v_scale = zeros(torch.float32, ADAMW_BLOCK) if scaled else None
     if master is True:
-        master = [p.detach().to(torch.float32).contiguous() for p in params]
+        master = [p.detach().to(torch.float32).contiguous() if p.dtype == torch.bfloat16 else None for p in params]
     master = list(master) if master else None
     m_scale, v_scale = (list(x) if x is not None else None for x in (m_scale, v_scale))
     plan = AdamWPlan(params, master, m, v, m_scale, v_scale)

@@ -30,3 +30,25 @@ def test_a_step_follows_tensors_that_moved(state):
         assert all(torch.equal(x, y) for x, y in zip(pa.master, pb.master))
         for x, y in ((pa.m, pb.m), (pa.v, pb.v)):
             assert all(torch.equal(p.view(torch.uint8), q.view(torch.uint8)) for p, q in zip(x, y))
+
+
+@pytest.mark.parametrize("state", [torch.float32, E4M3])
+def test_master_copies_of_the_bf16_weights_of_a_mixed_model(state):
+    """bf16 matrices and fp32 norms in one plan: master=True keeps copies of the former alone, and every tensor is
+    updated as in a plan of its own."""
+    sizes, types = [300, 5000, 20, 1], [torch.float32, torch.bfloat16, torch.float32, torch.bfloat16]
+    ps = [tensors([n], t, 16 + i)[0] for i, (n, t) in enumerate(zip(sizes, types))]
+    gs = tensors(sizes, torch.float32, 18)
+    alone = []
+    for p, g in zip(ps, gs):
+        q = p.clone()
+        one = api.adamw_plan([q], state, master=p.dtype == torch.bfloat16)
+        api.adamw_step(one, [g], step=1, **HP)
+        alone.append((q, one.master))
+    plan = api.adamw_plan(ps, state, master=True)
+    assert [x is None for x in plan.master] == [True, False, True, False]
+    api.adamw_step(plan, gs, step=1, **HP)
+    for p, copy, (q, other) in zip(ps, plan.master, alone):
+        assert torch.equal(p, q) and (copy is None or torch.equal(copy, other[0]))
+    again = api.adamw_plan(ps, m=plan.m, v=plan.v, m_scale=plan.m_scale, v_scale=plan.v_scale, master=plan.master)
+    api.adamw_step(again, gs, step=2, **HP)

@@ -80,3 +80,20 @@ def test_released_storage_is_refused():
     rows["grad"] = 0x1000
     h = api.TpsAdamwHyper(1e-3, 0.9, 0.99, 1e-8, 0.0, 1, 0, 0)
     assert api.library().tps_adamw_step(rows.ctypes.data, 1, ctypes.byref(h), None, None, None) == api.ERR_ARG
+
+
+def test_master_copies_are_for_bf16_weights_alone():
+    params = [torch.zeros(300), torch.zeros(500, dtype=torch.bfloat16), torch.zeros(20, dtype=torch.bfloat16)]
+    moments = [[torch.zeros(p.numel()) for p in params] for _ in range(2)]
+    copies = [None, params[1].float(), None]
+    plan = api.AdamWPlan(params, copies, *moments, None, None)
+    assert [int(x) for x in plan.rows()["master"]] == [0, copies[1].data_ptr(), 0]
+    plan.master[1], plan.master[2] = None, params[2].float()
+    assert [int(x) for x in plan.rows()["master"]] == [0, 0, plan.master[2].data_ptr()]
+    with pytest.raises(TypeError, match="master"):
+        api.AdamWPlan(params, [params[0].clone(), None, None], *moments, None, None).rows()
+    with pytest.raises(ValueError, match="shape"):
+        api.AdamWPlan(params, [None, params[1].float()], *moments, None, None).rows()
+    plan.params.append(torch.zeros(3))
+    with pytest.raises(ValueError, match="shape"):
+        plan.rows()
