@@ -232,6 +232,12 @@ __device__ __forceinline__ void write8_codes(uint8_t* p, float inv, int lane, in
   }
 }
 
+// Smallest of three.
+__device__ __forceinline__ float min_of(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
 // Pairs of fp32 operations as one instruction, each rounded on its own.
 __device__ __forceinline__ uint64_t two(float a, float b) {
   uint64_t r;
@@ -258,15 +264,34 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
 // codes are those of the rounded root): Markstein's correction, P. Markstein,
 // "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990 -- with y near 1 / sqrt(x), r = x y is off by little and
-// r + (x - r^2) y / 2 by that squared before its one rounding.  Subnormals
-// count as 0.
+// r + (x - r^2) y / 2 by that squared before its one rounding.  For x of at
+// least kRootLeast, where x - r^2, some 2^-22 x, is a normal number; smaller
+// ones and zeros (whose y would be infinite) are for small_roots.
+constexpr float kRootLeast = 0x1p-100f;
 __device__ __forceinline__ uint64_t root2(uint64_t x) {
   float a, b;
-  both(add2(x, two(1e-36f, 1e-36f)), a, b);  // finite reciprocals for 0, whose root stays 0
+  both(x, a, b);
   asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(a));
   asm("rsqrt.approx.ftz.f32 %0, %0;" : "+f"(b));
   const uint64_t y = two(a, b), r = mul2(x, y);
   return fma2(fma2(mul2(r, two(-1.0f, -1.0f)), r, x), mul2(y, two(0.5f, 0.5f)), r);
+}
+// root2's results r of x, in place, where a lane has an x below kRootLeast.
+__device__ __forceinline__ void small_roots(const uint64_t (&x)[2][2], uint64_t (&r)[2][2]) {
+  float v[8], least;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) both(x[i / 2][i % 2], v[2 * i], v[2 * i + 1]);
+  least = fminf(v[0], v[1]);
+#pragma unroll
+  for (int i = 2; i < 8; i += 2) least = min_of(least, v[i], v[i + 1]);
+  if (!(least < kRootLeast)) return;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    float a, b;
+    both(r[i / 2][i % 2], a, b);
+    r[i / 2][i % 2] = two(v[2 * i] < kRootLeast ? __fsqrt_rn(v[2 * i]) : a,
+                          v[2 * i + 1] < kRootLeast ? __fsqrt_rn(v[2 * i + 1]) : b);
+  }
 }
 __device__ __forceinline__ float rcp_of(float x) {  // to one unit; subnormals count as 0
   float r;
@@ -362,19 +387,29 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
     // it would fuse a packed product and sum into one rounding
     const uint64_t zero = two(t.minus_zero, t.minus_zero);
     const uint64_t eps = two(t.eps, t.eps), dc = two(s.decay, s.decay), minus = two(-1.0f, -1.0f);
+    uint64_t mm[2][2], vv[2][2], rr[2][2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {
+      for (int k = 0; k < 2; ++k) {
+        const int i = 2 * k;
         const uint64_t gg = mul2(two(g[j][i], g[j][i + 1]), cc), r0 = two(root[j][i], root[j][i + 1]);
-        const uint64_t mm = add2(fma2(two(m[j][i], m[j][i + 1]), b1, zero), fma2(gg, c1, zero));
-        const uint64_t rr = root2(add2(fma2(mul2(r0, r0), b2, zero), fma2(mul2(gg, gg), c2, zero)));
+        mm[j][k] = add2(fma2(two(m[j][i], m[j][i + 1]), b1, zero), fma2(gg, c1, zero));
+        vv[j][k] = add2(fma2(mul2(r0, r0), b2, zero), fma2(mul2(gg, gg), c2, zero));
+        rr[j][k] = root2(vv[j][k]);
+      }
+    small_roots(vv, rr);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int i = 2 * k;
         float d0, d1;
-        both(fma2(rr, rs, eps), d0, d1);
-        const uint64_t step = mul2(mul2(mm, ss), two(rcp_of(d0), rcp_of(d1)));
+        both(fma2(rr[j][k], rs, eps), d0, d1);
+        const uint64_t step = mul2(mul2(mm[j][k], ss), two(rcp_of(d0), rcp_of(d1)));
         both(fma2(step, minus, mul2(two(w[j][i], w[j][i + 1]), dc)), w[j][i], w[j][i + 1]);
-        both(mm, m[j][i], m[j][i + 1]);
-        both(rr, root[j][i], root[j][i + 1]);
+        both(mm[j][k], m[j][i], m[j][i + 1]);
+        both(rr[j][k], root[j][i], root[j][i + 1]);
       }
   } else {
 #pragma unroll

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from backward_tcgen05_tma_gemms_gb300 import api
-from test_gpu_adamw import E4M3, HP, tensors
+from test_gpu_adamw import E4M3, HP, dither, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -52,3 +52,45 @@ def test_master_copies_of_the_bf16_weights_of_a_mixed_model(state):
         assert torch.equal(p, q) and (copy is None or torch.equal(copy, other[0]))
     again = api.adamw_plan(ps, m=plan.m, v=plan.v, m_scale=plan.m_scale, v_scale=plan.v_scale, master=plan.master)
     api.adamw_step(again, gs, step=2, **HP)
+
+
+def coded(x, rnd, keep):
+    """x as e4m3 numbers, scales and the values they stand for, in fp32 with one rounding an operation."""
+    x, rnd = x.view(-1, 256), rnd.view(-1, 256)
+    top = x.abs().amax(1)
+    y = (x.abs() * (448.0 / top)[:, None]).clamp(max=448.0)
+    big = ((y.view(torch.int32).long() + (rnd << 4)) >> 20) - 960
+    code = torch.where(y >= 2.0 ** -6, big, (y * 512 + rnd.float() / 65536).floor().long())
+    if keep:
+        code = torch.where((y > 0) & (code == 0), 1, code)
+    value = code.to(torch.uint8).view(E4M3).float() * torch.where(x < 0, -1.0, 1.0)
+    s = top * (1.0 / 448)
+    return value.flatten(), s, (value * s[:, None]).flatten()
+
+
+def check_codes(magnitude, zeros=False):
+    """Two steps' codes and scales against the same update in torch fp32: equal from 2^-5 on, at most one number apart
+    below (there the sum with the random bits is rounded elsewhere)."""
+    n, b1, b2 = 256 * 200, 0.9, 0.95
+    plan = api.adamw_plan([torch.zeros(n, device="cuda")], E4M3)
+    m, v = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+    for step in (1, 2):
+        g = torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(step)) * magnitude
+        if zeros:
+            g[::3] = 0
+        api.adamw_step(plan, [g], step=step, seed=step, lr=0.0, beta1=b1, beta2=b2)
+        m, v = m * b1 + g * (1 - b1), v * b2 + g * g * (1 - b2)
+        bits = dither(torch.arange(n, device="cuda"), step)
+        cm, sm, m = coded(m, bits & 0xffff, False)
+        cv, sv, root = coded(v.sqrt(), bits >> 16, True)
+        v = root * root
+        assert torch.equal(plan.m_scale[0], sm) and torch.equal(plan.v_scale[0], sv)
+        for got, want in ((plan.m[0].float(), cm), (plan.v[0].float(), cv)):
+            assert torch.equal(got[want.abs() >= 2.0 ** -5], want[want.abs() >= 2.0 ** -5])
+            assert (got - want).abs().max() <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("magnitude,zeros", [(1e-14, False), (1e-16, False), (1e-17, True), (1e-18, False), (3e-19, True)])
+def test_square_roots_of_small_second_moments(magnitude, zeros):
+    """v from 1e-28 down to subnormal numbers, and zeros beside them: the stored roots are those of sqrt in fp32."""
+    check_codes(magnitude, zeros)
