@@ -93,9 +93,12 @@ __device__ __forceinline__ uint32_t e4m3_by(float x, float s, uint32_t rnd) {
 // And back: the code's bits in place of a float's are the number times 2^-120;
 // s = scale * 2^120.
 __device__ __forceinline__ float e4m3_float(uint32_t bits, float s) { return __uint_as_float(bits) * s; }
-// Blocks whose scale times 2^120 would overflow, or whose 448 / a would lose
-// bits, are held 2^-40 smaller meanwhile; a whole warp agrees on it.
-constexpr float kSmaller = 0x1p-40f, kLarger = 0x1p40f, kLargeScale = 64.0f;
+// Blocks whose scale times 2^120 may overflow are read 2^-120 smaller: a code's
+// bits times the scale itself, which for a scale above 64 is a normal number,
+// then times 2^120.  Blocks whose 448 / a 2^-120 would lose bits are brought
+// down by 2^-40, up to three times, before they are written.  Both are exact,
+// and a whole warp agrees on them.
+constexpr float kSmaller = 0x1p-40f, kLarger = 0x1p120f, kLargeScale = 64.0f;
 // Bits of code i of four: exponent and mantissa from bit 26 down, and the sign
 // in bit 31.  (Shifts to the left are products here: they run beside the
 // logical operations, which this kernel has most of.)
@@ -191,7 +194,7 @@ __device__ __forceinline__ float block_top(const float (&x)[2][4]) {
 }
 // x with its block's largest magnitude a brought to where 448 / a keeps all its bits.
 __device__ __forceinline__ float bring_down(float a, float (&x)[2][4]) {
-  if (a > kLargeScale * 256.0f) {
+  for (int k = 0; k < 3 && a > kLargeScale * 256.0f; ++k) {
     a *= kSmaller;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
@@ -359,8 +362,8 @@ __device__ __forceinline__ void adamw_unit(const Table<N>& t, const Entry& e, in
   }
   if (E4M3) {
     const bool bm = r.ms > kLargeScale, bv = r.vs > kLargeScale;
-    const float sm = (bm ? r.ms * kSmaller : r.ms) * 0x1p120f;
-    const float sv = (bv ? r.vs * kSmaller : r.vs) * 0x1p120f;
+    const float sm = bm ? r.ms : r.ms * 0x1p120f;
+    const float sv = bv ? r.vs : r.vs * 0x1p120f;
 #pragma unroll
     for (int j = 0; j < 2; ++j)
 #pragma unroll

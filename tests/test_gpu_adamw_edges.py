@@ -94,3 +94,24 @@ def check_codes(magnitude, zeros=False):
 def test_square_roots_of_small_second_moments(magnitude, zeros):
     """v from 1e-28 down to subnormal numbers, and zeros beside them: the stored roots are those of sqrt in fp32."""
     check_codes(magnitude, zeros)
+
+
+@pytest.mark.parametrize("magnitude,zeros", [(1e5, False), (1e14, True), (1e17, False), (1e18, True), (3e18, False)])
+def test_moments_of_large_gradients(magnitude, zeros):
+    """Scales from 64 up to the largest root of a finite v, and zero codes beside them."""
+    check_codes(magnitude, zeros)
+
+
+def test_first_moments_up_to_the_end_of_fp32():
+    """Without gradients v stays 0, and m is halved wherever it lies in fp32."""
+    n = 256 * 8
+    x = torch.randn(n, device="cuda", generator=torch.Generator(device="cuda").manual_seed(3))
+    for top in (1e20, 1e30, 3.3e38):
+        m, ms, kept = coded(x / x.abs().max() * top, torch.full((n,), 0x8000, device="cuda"), False)
+        plan = api.adamw_plan([torch.zeros(n, device="cuda")], m=[m.to(E4M3)], v=[torch.zeros(n, device="cuda").to(E4M3)],
+                              m_scale=[ms], v_scale=[torch.zeros(n // 256, device="cuda")])
+        api.adamw_step(plan, [torch.zeros(n, device="cuda")], step=1, lr=0.0, beta1=0.5)
+        want, s, _ = coded(kept * 0.5, torch.full((n,), 0x8000, device="cuda"), False)
+        assert torch.equal(plan.m_scale[0], s)
+        big = want.abs() >= 2.0 ** -5
+        assert torch.equal(plan.m[0].float()[big], want[big]) and (plan.m[0].float() - want).abs().max() <= 2.0 ** -9
