@@ -178,16 +178,20 @@ __global__ void __launch_bounds__(1024) ce_total_kernel(const float* loss, int64
 }
 
 // What the gradient epilogue knows of each row (Epilogue::ce_rows).  A mean
-// over this call's labels needs their count first: one block then does both,
-// else the rows are spread over blocks.  alpha (a gradient that all rows
-// share: a sum's or a mean's): kept apart, and the products multiplied by it
-// in fp32 -- inside dz it would be rounded to bf16 with the one-hot term, the
-// same way in every row, and leave the whole gradient off by up to 2^-8.
+// over this call's labels needs their count first, and a gradient for each
+// token their largest: one block then does both, else the rows are spread
+// over blocks.  alpha (bf16 operands): the gradient that all rows share, a
+// sum's or a mean's, or the largest of the tokens' magnitudes, is kept apart
+// and the products multiplied by it in fp32; a row keeps its share of it.
+// Inside dz it would be rounded to bf16 with the one-hot term, the same way in
+// every row that has the same gradient, and leave the whole result off by up
+// to 2^-9.  (One that is not finite stays in its rows.)
 __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, const float* lse, const float* g,
                                                        int64_t g_step, int reduction, double denominator,
                                                        float4* rows, float* alpha, uint32_t* err) {
   __shared__ int64_t redi[32];
-  __shared__ float share;
+  __shared__ float redf[32];
+  __shared__ float share, common;
   if (reduction == TPS_REDUCE_MEAN && denominator == 0.0) {  // one block
     int64_t n = 0;
     for (int64_t t = threadIdx.x; t < T; t += 1024) n += lab.kind(lab.at(t)) == 0;
@@ -196,15 +200,38 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, co
   } else if (threadIdx.x == 0) {
     share = reduction == TPS_REDUCE_MEAN ? static_cast<float>(1.0 / denominator) : 1.0f;
   }
+  float most = 0.0f;
+  if (alpha != nullptr && g_step != 0) {  // one block: the largest finite magnitude
+    for (int64_t t = threadIdx.x; t < T; t += 1024) {
+      const float x = fabsf(g[t]);
+      if (x < INFINITY && lab.kind(lab.at(t)) != 1) most = fmaxf(most, x);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
+    if ((threadIdx.x & 31) == 0) redf[threadIdx.x >> 5] = most;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    common = 1.0f;
+    if (alpha != nullptr) {
+      if (g_step != 0) {
+        for (int i = 0; i < 32; ++i) most = fmaxf(most, redf[i]);
+        if (most > 0.0f) common = most;
+      } else {
+        const float x = (g == nullptr ? 1.0f : *g) * share;
+        if (fabsf(x) < INFINITY && x != 0.0f) common = x;
+      }
+      if (blockIdx.x == 0) *alpha = common;
+    }
+  }
   __syncthreads();
   for (int64_t t = blockIdx.x * int64_t(1024) + threadIdx.x; t < T; t += int64_t(gridDim.x) * 1024) {
     const int64_t y = lab.at(t);
     const int kind = lab.kind(y);
     if (kind == 2) atomicOr(err, TPS_DEVERR_LABEL);
-    const float up = g == nullptr ? 1.0f : g[t * g_step];
+    const float up = (g == nullptr ? 1.0f : g[t * g_step]) * share;
     const float l = lse[t];
-    if (alpha != nullptr && t == 0) *alpha = up * share;
-    rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : (alpha != nullptr ? 1.0f : up * share),
+    rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : (alpha != nullptr ? __fdiv_rn(up, common) : up),
                           __int_as_float(kind == 0 ? static_cast<int>(y) : -1), l);
   }
 }
@@ -880,11 +907,13 @@ extern "C" int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, c
   char* ws = static_cast<char*>(workspace);
   float4* rows = reinterpret_cast<float4*>(ws + f.rows);
   uint32_t* flags = reinterpret_cast<uint32_t*>(ws + f.flags);
-  float* alpha = c.reduction != TPS_REDUCE_NONE && l.planes == 1 ? reinterpret_cast<float*>(ws + f.alpha) : nullptr;
+  // without an upstream gradient each token's is 1, which dz holds exactly
+  float* alpha = l.planes == 1 && (c.reduction != TPS_REDUCE_NONE || up != nullptr) ? reinterpret_cast<float*>(ws + f.alpha)
+                                                                                    : nullptr;
   const int64_t cols = piece_columns(c.vreal, static_cast<int64_t>(workspace_bytes - f.pieces) - 256, per);
 
   {
-    const bool count = c.reduction == TPS_REDUCE_MEAN && c.denominator == 0.0;
+    const bool count = (c.reduction == TPS_REDUCE_MEAN && c.denominator == 0.0) || (alpha != nullptr && up_step != 0);
     const int64_t blocks = count ? 1 : (c.T + 1023) / 1024;
     ce_rows_kernel<<<static_cast<unsigned>(blocks < 1024 ? blocks : 1024), 1024, 0, s>>>(
         c.T, c.lab, static_cast<const float*>(lse->data), up, up_step, c.reduction, c.denominator, rows, alpha, err);

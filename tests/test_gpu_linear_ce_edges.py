@@ -77,3 +77,46 @@ def test_a_nan_among_masked_logits_is_not_lost(T, dtype):
     y = torch.full((T,), 390, device="cuda")
     loss, _, lse = api.linear_ce_fwd(h, W, y, weight_layout="out_in")
     assert torch.isnan(lse).all() and torch.isnan(loss).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 1e-6, 1e20])
+def test_a_gradient_that_all_tokens_share_is_not_rounded_to_bf16(scale):
+    """The mean of the tokens' losses taken outside sends the same gradient to each of them (and here nothing usable to
+    the ignored ones).  c = 1 + 2^-9 times a scale is up to half a bf16 step from what bf16 holds; as a factor in fp32
+    it leaves what 1 - p of the label loses (p = 1 / 8192 on average) and roundings that average out over 170 tokens."""
+    h, W, y = case(14, 200, 64, 8192, "in_out", torch.bfloat16, scale=0.05)
+    y[::7] = IGN
+    up = torch.full((200,), 1.0 + 2.0 ** -9, device="cuda") * scale
+    _, _, lse = api.linear_ce_fwd(h, W, y, ignore_index=IGN)
+    ref = reference(h, W, y, "in_out", up=up)
+    up[::7] = float("nan")
+    dh, dW = api.linear_ce_bwd(h, W, y, lse, up, ignore_index=IGN)
+    for got, want in ((dh, ref["dh"][0]), (dW, ref["dW"][0])):
+        assert abs((got.double() * want).sum() / want.square().sum() - 1).item() <= 2.0 ** -11
+    assert not dh[::7].any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("bad", [float("inf"), float("nan")])
+def test_a_gradient_that_is_not_finite_stays_with_its_token(bad, dtype):
+    h, W, y = case(15, 40, 64, 520, "in_out", dtype)
+    up = torch.randn(40, device="cuda", generator=torch.Generator(device="cuda").manual_seed(1)) * 1e-3
+    up[5], up[9] = bad, 0.0
+    y[7] = IGN
+    _, _, lse = api.linear_ce_fwd(h, W, y, ignore_index=IGN)
+    dh, _ = api.linear_ce_bwd(h, W, y, lse, up, ignore_index=IGN, want_dwhead=False)
+    rest = torch.arange(40, device="cuda") != 5
+    want, bound = reference(h, W, y, "in_out", up=torch.nan_to_num(up, 0.0, 0.0))["dh"]
+    near(dh[rest], (want[rest], bound[rest]), "dHidden")
+    assert not torch.isfinite(dh[5]).any() and not dh[7].any() and not dh[9].any()
+    for reduction in ("sum", "mean"):
+        dh, _ = api.linear_ce_bwd(h, W, y, lse, torch.tensor([bad], device="cuda"), ignore_index=IGN, reduction=reduction)
+        assert not dh[7].any() and not torch.isfinite(dh[rest.logical_and(torch.arange(40, device="cuda") != 7)]).any()
+
+
+def test_no_gradient_at_all():
+    h, W, y = case(16, 40, 64, 520, "in_out", torch.bfloat16)
+    _, _, lse = api.linear_ce_fwd(h, W, y)
+    for up, reduction in ((torch.zeros(40, device="cuda"), "none"), (torch.zeros(1, device="cuda"), "sum")):
+        dh, dW = api.linear_ce_bwd(h, W, y, lse, up, reduction=reduction)
+        assert not dh.any() and not dW.any()
