@@ -506,7 +506,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             if (col0 >= p.n_store) break;  // warp-uniform
             float(&v)[32] = sum[c];
             if (e.mode == EPI_CE_GRAD) {  // three bf16 planes whose sum is the fp32 gradient, zeros past column N
-              ce_grad32(ce_row, e.ce_col0 + col0, v);
+              ce_grad32<true>(ce_row, e.ce_col0 + col0, v);
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (col0 + i >= p.N) v[i] = 0.0f;
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
         }
         // the fp32 and bf16 slots (store-only: one shared box), single- or double-buffered
         uint8_t* buf = stg + (L::kBufs == 2 ? (chunk & 1u) * L::kBufBytes : 0u);
-        if constexpr (FAM == T2_CE) ce_grad32(ce_row, e.ce_col0 + col0, v);
+        if constexpr (FAM == T2_CE) ce_grad32<false>(ce_row, e.ce_col0 + col0, v);
         if constexpr (FAM == T2_PLAIN) {
           if (run > 0 || e.accumulate) {  // K split (or a sum over pieces): add this partial tile to the output
             tc_store_chunk<L::kBufs - 1, true, true>(e, &m.d[0], &m.d[1], buf, buf, lane, row0, col0, v, a);

@@ -118,7 +118,7 @@ struct Epilogue {
 
 // What EPI_CE_GRAD knows of a row (a float4): lse * log2(e), the upstream
 // gradient g (0: the whole row is 0, whatever the logits hold), the bits of
-// the int32 label (-1: no one-hot term) and lse itself.
+// the int32 label (-1: no one-hot term) and lse itself (for fp32 operands).
 constexpr float kCeLog2e = 1.4426950408889634f;
 
 // The vocabulary CE's gradient as the A operand of the dHidden GEMM, formed

@@ -401,10 +401,15 @@ __device__ __forceinline__ void ce_lse_tile(const Epilogue& e, int64_t tc0, int6
 }
 
 // EPI_CE_GRAD of 32 columns from col0: v becomes g (e^{v - lse} - [column = label]).
+// lse times log2(e) is rounded, which leaves e^{v - lse} |lse| 2^-24 off,
+// relatively: nothing where dz is rounded to bf16.  FP32: the difference is
+// formed first, exact where it matters.
+template <bool FP32>
 __device__ __forceinline__ void ce_grad32(float4 row, int64_t col0, float (&v)[32]) {
   const float g = row.y;
 #pragma unroll
-  for (int i = 0; i < 32; ++i) v[i] = ex2_approx(fmaf(v[i], kTcLog2e, -row.x)) * g;
+  for (int i = 0; i < 32; ++i)
+    v[i] = ex2_approx(FP32 ? (v[i] - row.w) * kTcLog2e : fmaf(v[i], kTcLog2e, -row.x)) * g;
   const int64_t dy = static_cast<int64_t>(__float_as_int(row.z)) - col0;
   if (dy >= 0 && dy < 32) {
 #pragma unroll

@@ -120,3 +120,15 @@ def test_no_gradient_at_all():
     for up, reduction in ((torch.zeros(40, device="cuda"), "none"), (torch.zeros(1, device="cuda"), "sum")):
         dh, dW = api.linear_ce_bwd(h, W, y, lse, up, reduction=reduction)
         assert not dh.any() and not dW.any()
+
+
+def test_fp32_gradients_of_rows_with_a_large_lse():
+    """z and lse near 1000 that fp32 holds exactly: e^{z - lse} is off by the hardware exponential's 2^-22 and two
+    roundings of the difference's at most 8 binary digits of exponent, 2^-20 together, not by lse's own magnitude."""
+    z = 1000 + 37.0 * torch.arange(8)[:, None] + torch.arange(64)[None] / 64.0
+    y = torch.arange(8) * 7
+    lse = torch.logsumexp(z.double(), 1).float()
+    _, dW = api.linear_ce_bwd(torch.eye(8).cuda(), z.cuda(), y.cuda(), lse.cuda(), want_dhidden=False)
+    p = torch.exp(z.double() - lse.double()[:, None])
+    want = p - torch.zeros_like(p).scatter_(1, y[:, None], 1.0)
+    assert ((dW.cpu().double() - want).abs() <= 2.0 ** -20 * p + 2.0 ** -23 * want.abs()).all()
