@@ -545,12 +545,49 @@ struct Spans {
 constexpr int kNormBlocks = 152 * 8;
 constexpr int kAhead = 8;  // units of a warp in flight
 
+// Whether a run's sum of squares is one: squares of fp32 numbers overflow from
+// 2^64 on, and each of the run's 64 may be off by 2^-150, which is next to
+// nothing of a sum above 2^-110.  `bits`: of all its values, signs apart.
+__device__ __forceinline__ bool sum_holds(float s, uint32_t bits) {
+  return (s >= 0x1p-110f && s < INFINITY) || bits == 0;
+}
+// What a warp of norm_kernel adds up, whatever the magnitudes: eight values of
+// a lane at a time, over a power of two near the largest of them.
+template <int N>
+__device__ __noinline__ double scaled_squares(const Spans<N>& t, int64_t r, int64_t step, int lane) {
+  double total = 0.0;
+  for (int k = 0; r * kAhead < t.units; r += step) {
+    for (int64_t u = r * kAhead; u < (r + 1) * kAhead && u < t.units; ++u) {
+      while (k + 1 < t.count && u >= t.e[k + 1].first) ++k;
+      const Span& e = t.e[k];
+      float x[8], top = 0.0f, sum = 0.0f;
+      for (int i = 0; i < 8; ++i) {
+        const int64_t at = (u - e.first) * kUnit + lane * 8 + i;
+        x[i] = 0.0f;
+        if (at < e.n)
+          x[i] = e.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.p)[at]) : static_cast<const float*>(e.p)[at];
+        top = max_nan(top, fabsf(x[i]), 0.0f);
+      }
+      if (!(top > 0.0f && top < INFINITY)) {  // 0, infinity or NaN
+        total += top;
+        continue;
+      }
+      const uint32_t f = __float_as_uint(top) >> 23, E = f < 1 ? 1 : f > 253 ? 253 : f;
+      const float down = __uint_as_float((254 - E) << 23), up = __uint_as_float(E << 23);  // 2^(127 - E), 2^(E - 127)
+      for (int i = 0; i < 8; ++i) sum = fmaf(x[i] * down, x[i] * down, sum);
+      total += static_cast<double>(sum) * up * up;
+    }
+  }
+  return total;
+}
+
 // Partial sums of squares, one for each block, of a fixed assignment of units.
 template <int N>
 __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant__ Spans<N> t, double* part) {
   __shared__ double red[kWarps];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   double total = 0.0;
+  bool holds = true;
   // kAhead consecutive units of a warp at a time: inside one tensor, all
   // their loads are in flight before the first sum
   const int64_t runs = (t.units + kAhead - 1) / kAhead;
@@ -561,6 +598,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
     // a run's 64 squares of a lane in fp32, runs in fp64: a long fp32 sum
     // would lose the small terms, always downwards
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    uint32_t bits = 0;
     while (k + 1 < t.count && u0 >= t.e[k + 1].first) ++k;
     const int64_t at0 = (u0 - t.e[k].first) * kUnit;
     if (t.e[k].wide && t.e[k].n - at0 >= kAhead * kUnit) {
@@ -576,6 +614,7 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
           for (int j = 0; j < 4; ++j) {
             const float lo = __uint_as_float(v[j] << 16), hi = __uint_as_float(v[j] & 0xffff0000u);
             acc[j] = fmaf(lo, lo, fmaf(hi, hi, acc[j]));
+            bits |= v[j] & 0x7fff7fffu;
           }
         }
       } else {
@@ -589,9 +628,13 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
           acc[1] = fmaf(q[i].y, q[i].y, acc[1]);
           acc[2] = fmaf(q[i].z, q[i].z, acc[2]);
           acc[3] = fmaf(q[i].w, q[i].w, acc[3]);
+          bits |= (__float_as_uint(q[i].x) | __float_as_uint(q[i].y) | __float_as_uint(q[i].z) | __float_as_uint(q[i].w)) &
+                  0x7fffffffu;
         }
       }
-      total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+      holds = holds && sum_holds(sum, bits);
+      total += sum;
       continue;
     }
     int kk = k;
@@ -613,10 +656,17 @@ __global__ void __launch_bounds__(32 * kWarps) norm_kernel(const __grid_constant
         unpack(f[1], x[1]);
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], acc[j]));
+      for (int j = 0; j < 4; ++j) {
+        acc[j] = fmaf(x[0][j], x[0][j], fmaf(x[1][j], x[1][j], acc[j]));
+        bits |= (__float_as_uint(x[0][j]) | __float_as_uint(x[1][j])) & 0x7fffffffu;
+      }
     }
-    total += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    const float sum = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+    holds = holds && sum_holds(sum, bits);
+    total += sum;
   }
+  if (__any_sync(0xffffffffu, !holds))
+    total = scaled_squares(t, static_cast<int64_t>(blockIdx.x) * kWarps + w, static_cast<int64_t>(gridDim.x) * kWarps, lane);
   double a = total;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o);

@@ -494,7 +494,8 @@ int tps_rope_bwd(const tps_rope_plan* plan, const tps_tensor* dQo, const tps_ten
  * launched when an argument is refused.
  *
  * tps_grad_norm: out[0] = the 2-norm of all gradients together (sums in
- * fp32 and fp64, in a fixed order), out[1] = min(1, max_norm / (norm + 1e-6))
+ * fp32 and fp64, in a fixed order; any norm that a float holds, also where
+ * squares leave fp32), out[1] = min(1, max_norm / (norm + 1e-6))
  * (1 for max_norm <= 0; NaN for a norm that is not finite).
  * ---------------------------------------------------------------------- */
 #define TPS_ADAMW_BLOCK 256

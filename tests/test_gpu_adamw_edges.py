@@ -115,3 +115,41 @@ def test_first_moments_up_to_the_end_of_fp32():
         assert torch.equal(plan.m_scale[0], s)
         big = want.abs() >= 2.0 ** -5
         assert torch.equal(plan.m[0].float()[big], want[big]) and (plan.m[0].float() - want).abs().max() <= 2.0 ** -9
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("magnitude", [1e-40, 1e-25, 1e-15, 1e15, 1e25, 1e36])
+@pytest.mark.parametrize("sizes", [[1], [3, 5000, 300], [100003, 0, 256]])
+def test_norms_whose_squares_leave_fp32(sizes, magnitude, dtype):
+    """Squares above 2^128 and below 2^-149, beside zeros and values of ordinary size: the norm of a float is a float.
+    Bound as in test_grad_norm; a subnormal norm is held to 2^-149."""
+    gs = [torch.randn(n, generator=torch.Generator().manual_seed(n)).double().mul_(magnitude).to(dtype).cuda() for n in sizes]
+    gs.append(torch.zeros(70000, dtype=dtype, device="cuda"))
+    for extra in ([], [torch.ones(2000, dtype=dtype, device="cuda")]):
+        both = [g for pair in zip(extra, gs) for g in pair] + gs[len(extra):]
+        want = sum(float(g.double().square().sum()) for g in both) ** 0.5
+        norm, coef = api.grad_norm(both, max_norm=0.5).tolist()
+        bound = (4 + (sum(sizes) + 72000) / (256 * 1216) + 40) * 2.0 ** -24
+        assert abs(norm - want) <= bound * want + 2.0 ** -149
+        assert abs(coef - min(1.0, 0.5 / (want + 1e-6))) <= (bound + 2.0 ** -23) * coef
+        assert api.grad_norm(both, max_norm=0.5).tolist() == [norm, coef]
+
+
+def test_norms_that_are_not_finite():
+    g = torch.ones(70000, device="cuda")
+    for bad in (float("inf"), float("nan"), -float("inf")):
+        g[12345] = bad
+        assert not torch.isfinite(api.grad_norm([g], max_norm=1.0)).any()
+    g.fill_(3e38)  # finite gradients, but a norm that fp32 does not hold
+    norm, coef = api.grad_norm([g], max_norm=1.0).tolist()
+    assert norm == float("inf") and coef != coef
+
+
+def test_a_step_with_large_gradients_is_clipped():
+    """A gradient of 1e25 scales to the norm that was asked for and the step is taken."""
+    p = torch.zeros(1000, device="cuda")
+    g = torch.full((1000,), 1e25, device="cuda")
+    norm = api.grad_norm([g], max_norm=1.0)
+    plan = api.adamw_plan([p])
+    api.adamw_step(plan, [g], lr=1.0, step=1, grad_scale=norm[1:])
+    assert torch.allclose(p, torch.full_like(p, -1.0), rtol=1e-5)  # m / sqrt(v) of equal gradients
