@@ -508,12 +508,23 @@ def linear_ce_workspace_bytes(T: int, d: int, V: int, dtype: torch.dtype, backwa
     return int(library().tps_linear_ce_workspace_bytes(T, d, V, _DTYPES[dtype], 1 if backward else 0, piece))
 
 
+def _room(workspace: torch.Tensor):
+    """Address and bytes of a workspace that the kernels may write."""
+    if not isinstance(workspace, torch.Tensor):
+        raise TypeError("expected a torch.Tensor")
+    if not workspace.is_cuda:
+        raise ValueError("tensors must live on the GPU (no CPU path)")
+    if not workspace.is_contiguous():
+        raise TpsError(ERR_LAYOUT, "workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _linear_ce_call(fn, T, d, V, dtype, backward, workspace, device):
     """Run fn(workspace pointer, bytes) with the given workspace, or with one
     for the tensor-core path; operands that do not qualify for it are refused
     before any launch and run again with the other path's size."""
     if workspace is not None:
-        _check(fn(workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        _check(fn(*_room(workspace)))
         return
     for dt in (dtype, torch.float32):
         n = max(linear_ce_workspace_bytes(T, d, V, dt, backward), 1)
@@ -777,8 +788,8 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: O
         out = torch.empty(2, dtype=torch.float32, device=index)
     elif out.numel() != 2 or out.dtype != torch.float32 or not out.is_contiguous() or not out.is_cuda:
         raise ValueError("shape")
-    _check(lib.tps_grad_norm(t.ctypes.data, len(ptrs), float(max_norm), out.data_ptr(), workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _raw_stream(out)))
+    _check(lib.tps_grad_norm(t.ctypes.data, len(ptrs), float(max_norm), out.data_ptr(), *_room(workspace),
+                             _raw_stream(out)))
     return out
 
 

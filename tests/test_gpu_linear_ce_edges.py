@@ -132,3 +132,16 @@ def test_fp32_gradients_of_rows_with_a_large_lse():
     p = torch.exp(z.double() - lse.double()[:, None])
     want = p - torch.zeros_like(p).scatter_(1, y[:, None], 1.0)
     assert ((dW.cpu().double() - want).abs() <= 2.0 ** -20 * p + 2.0 ** -23 * want.abs()).all()
+
+
+def test_workspaces_that_are_refused():
+    h, W, y = case(17, 20, 64, 520, "in_out", torch.bfloat16)
+    shared = torch.empty(1, dtype=torch.uint8, device="cuda").expand(1 << 24)
+    with pytest.raises(api.TpsError, match="contiguous"):
+        api.linear_ce_fwd(h, W, y, workspace=shared)
+    with pytest.raises(api.TpsError, match="contiguous"):
+        api.grad_norm([h], workspace=shared)
+    with pytest.raises(ValueError, match="GPU"):
+        api.linear_ce_fwd(h, W, y, workspace=torch.empty(1 << 24, dtype=torch.uint8))
+    with pytest.raises(ValueError, match="GPU"):
+        api.grad_norm([h], workspace=torch.empty(1 << 24, dtype=torch.uint8))

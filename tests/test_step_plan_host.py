@@ -97,3 +97,18 @@ def test_master_copies_are_for_bf16_weights_alone():
     plan.params.append(torch.zeros(3))
     with pytest.raises(ValueError, match="shape"):
         plan.rows()
+
+
+def test_a_workspace_the_kernels_cannot_write_is_refused(monkeypatch):
+    """One on the host, and one whose elements share storage, never reach the library."""
+    with pytest.raises(ValueError, match="GPU"):
+        api._room(torch.empty(1 << 20, dtype=torch.uint8))
+    with pytest.raises(TypeError):
+        api._room(bytearray(16))
+
+    def library():
+        raise AssertionError("reached the library")
+    monkeypatch.setattr(api, "library", library)
+    with pytest.raises(ValueError, match="GPU"):
+        api._linear_ce_call(lambda ws, n: library(), 1, 8, 8, torch.float32, False,
+                            torch.empty(1 << 20, dtype=torch.uint8), None)
