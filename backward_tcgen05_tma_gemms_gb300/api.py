@@ -690,6 +690,10 @@ class AdamWPlan:
                                      "weights and state on different GPUs")
                 if not t.is_contiguous():
                     raise TpsError(ERR_LAYOUT, "weights and state must be contiguous")
+        spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for c in self._columns() for t in c[1]
+                       if t is not None and t.numel())
+        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+            raise ValueError("weights or state given twice, or overlapping")
 
     def rows(self):
         """The tensors as rows of tps_adamw_tensor, without gradients."""

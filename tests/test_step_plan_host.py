@@ -112,3 +112,20 @@ def test_a_workspace_the_kernels_cannot_write_is_refused(monkeypatch):
     with pytest.raises(ValueError, match="GPU"):
         api._linear_ce_call(lambda ws, n: library(), 1, 8, 8, torch.float32, False,
                             torch.empty(1 << 20, dtype=torch.uint8), None)
+
+
+def test_a_tensor_given_twice_is_refused():
+    """Two warps would update the same elements at once (a weight that two layers share belongs in the list once)."""
+    w, flat = torch.zeros(300), torch.zeros(600)
+    moments = lambda n: [torch.zeros(n), torch.zeros(n)]  # noqa: E731
+    for params, m, v in (([w, w], moments(300), moments(300)), ([w.clone(), w], [flat[:300], flat[299:599]], moments(300)),
+                         ([flat[:300], flat[300:]], moments(300), [flat[:300], torch.zeros(300)])):
+        with pytest.raises(ValueError, match="twice"):
+            api.AdamWPlan(params, None, m, v, None, None).rows()
+    api.AdamWPlan([flat[:300], flat[300:]], None, moments(300), moments(300), None, None).rows()
+    plan = plan_of(n=2, size=300)
+    plan.rows()
+    plan.params[1].data = plan.params[0].data
+    with pytest.raises(ValueError):
+        plan.rows()
+    api.AdamWPlan([torch.zeros(0), torch.zeros(0)], None, [torch.zeros(0)] * 2, [torch.zeros(0)] * 2, None, None).rows()
