@@ -833,6 +833,8 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
     _check(library().tps_adamw_step(t.ctypes.data, len(ptrs), ctypes.byref(h),
                                     None if grad_scale is None else grad_scale.data_ptr(),
                                     None if scalars is None else scalars.data_ptr(), _raw_stream(grads[0])))
+    # what autograd saved of the weights is not what they are now
+    torch.autograd.graph.increment_version(plan.params)
 
 
 def selftest_wait_timeout(limit_ns: int = 50_000_000) -> None:

@@ -153,3 +153,19 @@ def test_a_step_with_large_gradients_is_clipped():
     plan = api.adamw_plan([p])
     api.adamw_step(plan, [g], lr=1.0, step=1, grad_scale=norm[1:])
     assert torch.allclose(p, torch.full_like(p, -1.0), rtol=1e-5)  # m / sqrt(v) of equal gradients
+
+
+def test_autograd_sees_that_a_step_changed_the_weights():
+    """A backward pass through weights that were updated since the forward pass is refused, as for any in-place change."""
+    w = torch.nn.Parameter(torch.ones(300, device="cuda"))
+    plan = api.adamw_plan([w])
+    loss = (w * w).sum()
+    api.adamw_step(plan, [torch.ones(300, device="cuda")], lr=0.1, step=1)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    (w * w).sum().backward()
+    assert torch.equal(w.grad, 2 * w.detach())
+    with torch.inference_mode():
+        p = torch.ones(300, device="cuda")
+        api.adamw_step(api.adamw_plan([p]), [torch.ones(300, device="cuda")], lr=0.1, step=1)
+    assert torch.equal(p, w.detach())
