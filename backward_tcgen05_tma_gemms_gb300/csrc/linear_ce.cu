@@ -730,13 +730,21 @@ size_t head_room(const Fixed& f, int64_t T, int planes, bool backward, int64_t c
 // before it.  Measured (us): T = 1000, d = 2048, 501 K tiles: wide with 1, 2,
 // 4, 5, 9 runs 278, 156, 107, 159, 133, narrow with 1, 2, 4, 9 runs 156, 94,
 // 100, 106; T = 8192, d = 4096, 512 K tiles: wide with 1, 2, 3, 4 runs 1286,
-// 1190, 1251, 1243.
+// 1190, 1251, 1243.  (fp32 planes are narrow and go by the same figures.)
+// TPS_LCE_SPLIT=wr forces wide (w = 0, 1) and the runs r, for tests: small
+// shapes would take neither wide tiles nor runs.
 struct Split {
   bool wide = false;
   int runs = 1;
 };
 Split choose_split(int64_t T, int64_t d, int64_t k_tiles, bool may_wide) {
   Split best;
+  const char* forced = getenv("TPS_LCE_SPLIT");
+  if (forced != nullptr && (forced[0] == '0' || forced[0] == '1') && atoi(forced + 1) >= 1) {
+    best.wide = forced[0] == '1' && may_wide;
+    best.runs = static_cast<int>(atoi(forced + 1) < k_tiles ? atoi(forced + 1) : k_tiles);
+    return best;
+  }
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 2)

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from backward_tcgen05_tma_gemms_gb300 import api
-from test_gpu_linear_ce import IGN, case, near, reference  # noqa: F401
+from test_gpu_linear_ce import IGN, case, check, near, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -145,3 +145,43 @@ def test_workspaces_that_are_refused():
         api.linear_ce_fwd(h, W, y, workspace=torch.empty(1 << 24, dtype=torch.uint8))
     with pytest.raises(ValueError, match="GPU"):
         api.grad_norm([h], workspace=torch.empty(1 << 24, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("split", ["01", "03", "11", "13", "116"])
+@pytest.mark.parametrize("reduction,dtype,grad", [("mean", torch.bfloat16, torch.float32), ("sum", torch.bfloat16, torch.bfloat16),
+                                                  ("none", torch.bfloat16, torch.float32), ("mean", torch.float32, torch.float32)])
+@pytest.mark.parametrize("T,d,V", [(300, 520, 1300), (70, 1032, 4100)])
+def test_every_way_to_sum_dhidden(T, d, V, reduction, dtype, grad, split, monkeypatch):
+    """dHidden on 256 x 256 and 256 x 512 tiles, in one and in several K runs, over pieces of 1024 columns and over one
+    piece, with an upstream gradient: the paths that large shapes take by themselves."""
+    monkeypatch.setenv("TPS_LCE_SPLIT", split)
+    for layout, piece in (("out_in", 1024), ("out_in", 0), ("in_out", 1024)):
+        V8 = V if layout == "out_in" else V - V % 8
+        h, W, y = case(T, T, d, V8, layout, dtype, ignored=T // 10)
+        up = torch.randn(T if reduction == "none" else 1, generator=torch.Generator().manual_seed(2)).cuda()
+        check(h, W, y, layout, reduction, grad=grad, piece=piece, up=up)
+
+
+@pytest.mark.parametrize("layout,T,d,V,dtype", [("out_in", 90, 72, 1031, torch.float32), ("in_out", 300, 40, 1027, torch.bfloat16),
+                                                ("in_out", 20, 64, 2000, torch.float32)])
+def test_pieces_leave_the_loss_as_it_is(layout, T, d, V, dtype):
+    """Operands that are laid out go piece by piece in the forward pass too: loss and lse are the same bits whatever the
+    piece, dWhead as well, and dHidden within the bounds."""
+    h, W, y = case(7, T, d, V, layout, dtype, ignored=3)
+    first = None
+    for piece in (256, 512, 1024, 0):
+        loss, _, lse, _, dW = check(h, W, y, layout, piece=piece)
+        first = first or (loss, lse, dW)
+        assert all(torch.equal(a, b) for a, b in zip(first, (loss, lse, dW)))
+
+
+@pytest.mark.parametrize("d", [4096, 32768])
+def test_long_fp32_sums_keep_their_precision(d):
+    """One vocabulary entry: lse is the logit, a sum of d positive products.  Tensor cores cut a partial sum at each
+    step of 16 products, at worst one 2^-23 of it, for 32 steps into an accumulator; the d / 512 accumulators are added
+    with 2^-24 each.  (One accumulator throughout would be off by about 2^-24 for each of d / 16 steps: 1e-4 at 32768.)"""
+    g = torch.Generator().manual_seed(1)
+    h, W = torch.rand(16, d, generator=g).cuda(), torch.rand(1, d, generator=g).cuda()
+    _, _, lse = api.linear_ce_fwd(h, W, torch.zeros(16, dtype=torch.int64, device="cuda"), weight_layout="out_in")
+    want = h.double() @ W[0].double()
+    assert ((lse.double() - want).abs() <= (32 * 2.0 ** -23 + (d / 512 + 4) * 2.0 ** -24) * want).all()
