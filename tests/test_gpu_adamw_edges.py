@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from backward_tcgen05_tma_gemms_gb300 import api
-from test_gpu_adamw import E4M3, HP, dither, tensors
+from test_gpu_adamw import E4M3, HP, dither, formula, tensors
 
 pytestmark = pytest.mark.gpu
 
@@ -169,3 +169,30 @@ def test_autograd_sees_that_a_step_changed_the_weights():
         p = torch.ones(300, device="cuda")
         api.adamw_step(api.adamw_plan([p]), [torch.ones(300, device="cuda")], lr=0.1, step=1)
     assert torch.equal(p, w.detach())
+
+
+@pytest.mark.parametrize("grad", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("sizes", [[1], [255, 0, 257, 5000]])
+def test_random_rounding_of_bf16_weights_with_fp32_moments(sizes, grad):
+    """bf16 weights without a master copy go up or down to a neighbour of the updated weight, by the bits of their
+    places, and keep its expectation: the mean of K draws lies within 6 standard deviations, a step / (2 sqrt(K)) each."""
+    K = 200
+    ws = tensors(sizes, torch.bfloat16, 50)
+    gs = tensors(sizes, grad, 51, 0.1)
+    zero = [torch.zeros(n, device="cuda", dtype=torch.float64) for n in sizes]
+    sums = [z.clone() for z in zero]
+    for k in range(K):
+        ps = [w.clone() for w in ws]
+        plan = api.adamw_plan(ps)
+        api.adamw_step(plan, gs, step=1, seed=100 + k, **HP)
+        for i, (p, w, g) in enumerate(zip(ps, ws, gs)):
+            w2, ew, *_ = formula(w, g, zero[i], zero[i], 1, **HP)
+            assert ((p.double() - w2).abs() <= ew + 2.0 ** -7 * (w2.abs() + ew)).all()
+            sums[i] += p.double()
+    for i, (w, g) in enumerate(zip(ws, gs)):
+        w2, ew, *_ = formula(w, g, zero[i], zero[i], 1, **HP)
+        assert ((sums[i] / K - w2).abs() <= ew + 6 * 2.0 ** -7 * (w2.abs() + ew) / (2 * K ** 0.5)).all()
+    ps, qs = [w.clone() for w in ws], [w.clone() for w in ws]
+    for x in (ps, qs):
+        api.adamw_step(api.adamw_plan(x), gs, step=1, seed=9, **HP)
+    assert all(torch.equal(a, b) for a, b in zip(ps, qs))
