@@ -7,11 +7,12 @@
 // x_{i + r/2}) or, interleaved, (x_{2i}, x_{2i+1}); the rest of the head is
 // copied.
 //
-// Angles without a table and without loss at far positions: the plan keeps
-// f_i / 2 pi, the turns a position, as a 64-bit binary fraction, so p times
-// it modulo 2^64 is the fraction of a turn, exactly; its upper 32 bits, as a
-// signed number of half turns / 2^31, go through sincospif.  The error is
-// 2^-34 of a turn at p = 2^30 and the 2^-25 of the conversion.
+// Angles without a table: the plan keeps f_i / 2 pi, the turns a position, as a
+// 64-bit binary fraction, so p times it modulo 2^64 is the fraction of a turn,
+// without a rounding; its upper 32 bits, as a signed number of half turns /
+// 2^31, go through sincospif.  The fraction comes from a double and is good to
+// 2^-55, which leaves an angle |p| 2^-55 of a turn off (2^-25 at p = 2^30, as
+// much as the conversion to a float).
 //
 // A block takes a few tokens: each thread forms the cosine and sine of one
 // (token, pair), which all heads of the token share through shared memory,

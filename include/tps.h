@@ -427,8 +427,10 @@ size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dt
  * attention_factor > 0 replaces that multiplier (1 for the other scalings).
  *
  * tps_rope_plan_init fills a plan on the host (no device work): the turns a
- * position of each pair as 64-bit fractions, so that angles are exact to
- * 2^-24 of a turn at any position (int32 or int64, negative ones too).
+ * position of each pair as 64-bit fractions, formed from a double and good to
+ * 2^-55.  The angle of position p (int32 or int64, negative ones too) is then
+ * off by at most |p| 2^-55 + 2^-25 of a turn: 2^-24 up to p = 2^30, one bit
+ * more for each doubling beyond.
  * Errors: TPS_ERR_SHAPE (rotary_dim odd, below 2 or above 512), TPS_ERR_ARG.
  *
  * tps_rope_fwd: Q (T, H, D) or (B, S, H, D), K (T, Hkv, D) or (B, S, Hkv, D)
