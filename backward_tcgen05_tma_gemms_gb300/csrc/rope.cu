@@ -324,7 +324,10 @@ extern "C" int tps_rope_plan_init(const tps_rope_options* o, tps_rope_plan* plan
   if (o->scaling == TPS_ROPE_NTK) {
     if (o->rotary_dim < 4) return fail(TPS_ERR_SHAPE, "this scaling needs a rotary_dim of 4 or more");
     base *= std::pow(factor, r / (r - 2.0));
+    if (!std::isfinite(base)) return fail(TPS_ERR_ARG, "base times the factor's power is not finite");
   }
+  if (std::isinf(o->attention_factor) || std::isnan(o->attention_factor))
+    return fail(TPS_ERR_ARG, "attention_factor must be finite");
   if (o->scaling == TPS_ROPE_YARN) {
     const double fast = o->beta_fast > 0 ? o->beta_fast : 32.0, slow = o->beta_slow > 0 ? o->beta_slow : 1.0;
     if (!(o->original_context > 0) || !std::isfinite(o->original_context) || !(fast >= slow) || !std::isfinite(fast))

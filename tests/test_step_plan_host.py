@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from backward_tcgen05_tma_gemms_gb300 import api
+from test_abi_host import lib  # noqa: F401  (fixture)
 
 
 def plan_of(n=5, size=300, state=torch.float32, master=False):
@@ -70,7 +71,7 @@ def test_moved_tensors_are_checked_again():
         moved("m_scale", torch.zeros(1), state=torch.float8_e4m3fn).rows()
 
 
-def test_released_storage_is_refused():
+def test_released_storage_is_refused(lib):  # noqa: F811
     """A storage that was resized away has no address: the library refuses the row before any launch."""
     import ctypes
     plan = plan_of(n=1)
@@ -79,7 +80,7 @@ def test_released_storage_is_refused():
     rows = plan.rows()
     rows["grad"] = 0x1000
     h = api.TpsAdamwHyper(1e-3, 0.9, 0.99, 1e-8, 0.0, 1, 0, 0)
-    assert api.library().tps_adamw_step(rows.ctypes.data, 1, ctypes.byref(h), None, None, None) == api.ERR_ARG
+    assert lib.tps_adamw_step(rows.ctypes.data, 1, ctypes.byref(h), None, None, None) == api.ERR_ARG
 
 
 def test_master_copies_are_for_bf16_weights_alone():
