@@ -658,54 +658,58 @@ class AdamWPlan:
 
     def _columns(self):
         """(field of the table, tensors, elements of a weight for each of theirs, dtypes) of what there is."""
-        state = (self.m[0].dtype,) if self.m else ()
-        for name, ts, per, dtypes in (("param", self.params, 1, (torch.float32, torch.bfloat16)),
-                                      ("master", self.master, 1, (torch.float32,)),
-                                      ("m", self.m, 1, state), ("v", self.v, 1, state),
-                                      ("m_scale", self.m_scale, ADAMW_BLOCK, (torch.float32,)),
-                                      ("v_scale", self.v_scale, ADAMW_BLOCK, (torch.float32,))):
+        state = {self.m[0].dtype} if self.m else set()
+        for name, ts, per, dtypes in (("param", self.params, 1, {torch.float32, torch.bfloat16}), ("m", self.m, 1, state),
+                                      ("v", self.v, 1, state), ("m_scale", self.m_scale, ADAMW_BLOCK, {torch.float32}),
+                                      ("v_scale", self.v_scale, ADAMW_BLOCK, {torch.float32}),
+                                      ("master", self.master, 1, {torch.float32})):
             if ts is not None:
                 yield name, ts, per, dtypes
 
-    def _check(self):
+    def _check(self, addresses):
         if self.m and self.m[0].dtype not in _STATE_DTYPES:
             raise TypeError(f"unsupported dtype {self.m[0].dtype}")
         scaled = bool(self.m) and self.m[0].dtype == torch.float8_e4m3fn
         if self.params and (scaled != (self.m_scale is not None) or scaled != (self.v_scale is not None)):
             raise ValueError("argument")
-        for name, ts, per, dtypes in self._columns():
+        cls, spans = torch.Tensor, []
+        for (name, ts, per, dtypes), at in zip(self._columns(), addresses):
             if len(ts) != len(self.numels):
                 raise ValueError("shape")
-            for t, n, p in zip(ts, self.numels, self.params):
-                if t is None and name == "master":
-                    continue
-                if name == "master" and p.dtype != torch.bfloat16:
+            numels = self.numels if per == 1 else [-(-n // per) for n in self.numels]
+            if name == "master":  # None: no copy
+                if any(t is not None and p.dtype != torch.bfloat16 for t, p in zip(ts, self.params)):
                     raise TypeError("a master copy is for bf16 weights")
-                if t.numel() != -(-n // per):
-                    raise ValueError("shape")
-                if t.dtype not in dtypes:
-                    raise TypeError(f"unsupported dtype {t.dtype}")
-                if t.get_device() != self.device:
-                    raise ValueError("tensors must live on the GPU (no CPU path)" if t.get_device() < 0 else
-                                     "weights and state on different GPUs")
-                if not t.is_contiguous():
-                    raise TpsError(ERR_LAYOUT, "weights and state must be contiguous")
-        spans = sorted((t.data_ptr(), t.numel() * t.element_size()) for c in self._columns() for t in c[1]
-                       if t is not None and t.numel())
-        if any(a + n > b for (a, n), (b, _) in zip(spans, spans[1:])):
+                numels = [n for n, t in zip(numels, ts) if t is not None]
+                at = [x for x, t in zip(at, ts) if t is not None]
+                ts = [t for t in ts if t is not None]
+            if list(map(cls.numel, ts)) != list(numels):
+                raise ValueError("shape")
+            if not {t.dtype for t in ts} <= dtypes:
+                raise TypeError(f"unsupported dtype among {[t.dtype for t in ts]}")
+            devices = set(map(cls.get_device, ts))
+            if not devices <= {self.device}:
+                raise ValueError("tensors must live on the GPU (no CPU path)" if -1 in devices else
+                                 "weights and state on different GPUs")
+            if not all(map(cls.is_contiguous, ts)):
+                raise TpsError(ERR_LAYOUT, "weights and state must be contiguous")
+            spans += [(x, x + t.nbytes) for x, t in zip(at, ts) if x]
+        spans.sort()
+        if any(end > first for (_, end), (first, _) in zip(spans, spans[1:])):
             raise ValueError("weights or state given twice, or overlapping")
 
     def rows(self):
         """The tensors as rows of tps_adamw_tensor, without gradients."""
         address = torch.Tensor.data_ptr
-        addresses = [list(map(address, ts)) for ts in (self.params, self.m, self.v, self.m_scale or (), self.v_scale or ())]
-        addresses.append([0 if x is None else address(x) for x in self.master or ()])
+        addresses = [list(map(address, ts)) for ts in (self.params, self.m, self.v, self.m_scale, self.v_scale) if ts is not None]
+        if self.master is not None:
+            addresses.append([0 if x is None else address(x) for x in self.master])
         if addresses != self._seen:
-            self._check()
+            self._check(addresses)
             n = len(self.params)
             t = np.zeros(n, _ADAMW_ROW)
-            for name, ts, _, _ in self._columns():
-                t[name] = [0 if x is None else x.data_ptr() for x in ts]
+            for (name, _, _, _), at in zip(self._columns(), addresses):
+                t[name] = at
             t["numel"] = self.numels
             blocks = [-(-x // ADAMW_BLOCK) for x in self.numels]
             t["place"] = ADAMW_BLOCK * np.concatenate(([0], np.cumsum(blocks)[:-1])) if n else []
