@@ -762,9 +762,11 @@ def adamw_plan(params: Sequence[torch.Tensor], state_dtype: torch.dtype = torch.
 
 
 def _grad_list(grads):
-    """Pointers and sizes (as arrays), dtype codes of contiguous gradients, and
-    the GPUs they are on."""
+    """The gradients as a list (they may come one by one), pointers and sizes (as
+    arrays), dtype codes of contiguous gradients, and the GPUs they are on."""
     cls = torch.Tensor
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)
     if not all(map(cls.is_contiguous, grads)):
         raise TpsError(ERR_LAYOUT, "gradients must be contiguous")
     devices = set(map(cls.get_device, grads))
@@ -775,7 +777,7 @@ def _grad_list(grads):
     if not kinds <= {torch.float32, torch.bfloat16}:
         raise TypeError("gradients must be fp32 or bf16")
     codes = _DTYPES[dtypes[0]] if len(kinds) == 1 else [_DTYPES[d] for d in dtypes]
-    return array("Q", list(map(cls.data_ptr, grads))), array("q", list(map(cls.numel, grads))), codes, devices
+    return grads, array("Q", list(map(cls.data_ptr, grads))), array("q", list(map(cls.numel, grads))), codes, devices
 
 
 def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: Optional[torch.Tensor] = None,
@@ -783,7 +785,7 @@ def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: O
     """fp32 tensor (norm, coefficient): the 2-norm of all gradients together
     and what brings it to max_norm (1 if it is below, or max_norm is 0; NaN
     for a norm that is not finite), both on the device."""
-    ptrs, numels, codes, devices = _grad_list(grads)
+    grads, ptrs, numels, codes, devices = _grad_list(grads)
     index = next(iter(devices)) if devices else torch.cuda.current_device()
     t = np.zeros(len(ptrs), _SPAN_ROW)
     if len(ptrs):
@@ -820,7 +822,7 @@ def adamw_step(plan: AdamWPlan, grads: Sequence[torch.Tensor], lr: float, step: 
     coefficient); nothing changes if it is not finite.  seed: rounds e4m3
     moments, and bf16 weights without a master copy, at random (another seed
     each step); None rounds to nearest.  scalars: see adamw_scalars."""
-    ptrs, numels, codes, devices = _grad_list(grads)
+    grads, ptrs, numels, codes, devices = _grad_list(grads)
     if numels != plan.numels:
         raise ValueError("shape")
     if not ptrs:

@@ -196,3 +196,12 @@ def test_random_rounding_of_bf16_weights_with_fp32_moments(sizes, grad):
     for x in (ps, qs):
         api.adamw_step(api.adamw_plan(x), gs, step=1, seed=9, **HP)
     assert all(torch.equal(a, b) for a, b in zip(ps, qs))
+
+
+def test_gradients_from_a_generator():
+    ws, gs = tensors([300, 20], torch.float32, 60), tensors([300, 20], torch.float32, 61)
+    assert torch.equal(api.grad_norm((g for g in gs), max_norm=1.0), api.grad_norm(gs, max_norm=1.0))
+    a, b = [w.clone() for w in ws], [w.clone() for w in ws]
+    api.adamw_step(api.adamw_plan(a), gs, step=1, **HP)
+    api.adamw_step(api.adamw_plan(w for w in b), (g for g in gs), step=1, **HP)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))

@@ -130,3 +130,13 @@ def test_a_tensor_given_twice_is_refused():
     with pytest.raises(ValueError):
         plan.rows()
     api.AdamWPlan([torch.zeros(0), torch.zeros(0)], None, [torch.zeros(0)] * 2, [torch.zeros(0)] * 2, None, None).rows()
+
+
+def test_gradients_that_come_one_by_one(monkeypatch):
+    """A generator was walked several times: after the first walk there were no gradients, and their norm was 0."""
+    with pytest.raises(ValueError, match="GPU"):
+        api.grad_norm(g for g in [torch.zeros(3)])
+    g = [torch.zeros(3), torch.zeros(4)]
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda t: 0)
+    again, ptrs, numels, _, _ = api._grad_list(x for x in g)
+    assert list(numels) == [3, 4] and list(ptrs) == [x.data_ptr() for x in g] and again[1] is g[1]
