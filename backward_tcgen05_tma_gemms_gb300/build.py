@@ -5,9 +5,11 @@ then linked into a shared library with the CUDA runtime linked statically,
 so loading the library needs no GPU and no libcuda at load time (the driver
 entry points are resolved through the runtime on first use).
 
-`debug=True` builds libtps_debug.so instead (TPS_DEBUG=1: every epilogue
-and cross-entropy store is checked against the bounds of its output, and a
-store outside is skipped and reported as TPS_ERR_BOUNDS).  Set
+`debug=True` builds libtps_debug.so instead (TPS_DEBUG=1: every direct store
+of the GEMMs' epilogues and of the vocabulary-sharded cross-entropy is checked
+against the bounds of its output, and a store outside is skipped and reported
+as TPS_ERR_BOUNDS; the kernels around the GEMMs of linear_ce.cu, rope.cu and
+optim.cu have no such check).  Set
 TPS_LIBRARY to its path to make the Python binding load it.
 
     python -m backward_tcgen05_tma_gemms_gb300.build [--force] [--debug]

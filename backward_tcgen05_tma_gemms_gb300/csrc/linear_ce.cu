@@ -17,23 +17,26 @@
 // Backward, bf16: nothing but lse is kept, so each piece of the vocabulary
 // has its logits formed again, and the epilogue turns them into dz at once
 // (EPI_CE_GRAD: one exponential and one product an element; dz leaves as
-// bf16, the type in which the tensor cores take it).  The piece is then the
+// bf16, the type in which the tensor cores take it: gradients are then 3e-4
+// (T = 8192) to 3e-3 (a few tokens) from those of an fp32 dz, where their own
+// rounding to bf16 is 1.7e-3; dz in two planes would double both products that
+// read it).  The piece is then the
 // K-major operand of dh += dz W_piece^T, summed over the pieces in fp32 by
 // TMA reductions in piece order, and the MN-major operand of dW_piece.
 // 6 T d V operations; forward and backward together take 8 T d V, where a
 // pass that keeps T x V logits takes 6: a third more is what not keeping them
 // costs.
 //
-// T = 8192, d = 4096, V = 128256, bf16: forward 4.84 ms (1780 TFLOP/s),
-// backward 15.2 ms (1700 TFLOP/s), the power cap's rate; workspace 66 MB and
-// 0.65 GB, where the logits would be 2.1 GB in bf16.
+// T = 8192, d = 4096, V = 128256, bf16: forward 4.9-5.0 ms (1720-1750
+// TFLOP/s), backward 15.1-15.4 ms (1680-1710 TFLOP/s), the power cap's rate;
+// workspace 66 MB and 0.65 GB, where the logits would be 2.1 GB in bf16.
 //
 // fp32 operands take the tensor cores too: each value is the sum of three
 // bf16 values exactly (8 + 8 + 8 bits), and of the nine products of such
 // planes the six that reach fp32's 2^-24 are summed into one fp32
 // accumulator, smallest first (GemmDesc::planes); dz is split the same way in
 // the epilogue.  Six times the tensor-core work of bf16 is still a fraction of
-// the fp32 pipes' time (T = 512, d = 1024, V = 8192 backward: 238 us, 2216 us
+// the fp32 pipes' time (T = 512, d = 1024, V = 8192 backward: 247 us, 2216 us
 // on the fp32 pipes).  These planes, and bf16 operands that TMA cannot
 // describe, are laid out in the workspace, Whead one piece at a time.
 #include <cuda_bf16.h>
@@ -283,10 +286,12 @@ __global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows,
 // are not enough bytes in flight).  Here a block takes 128 columns, 16 bytes
 // a thread and load with eight loads in flight, fp32 sums on the fp32 pipes,
 // and leaves the pair of its columns for each token.
-// Measured (us, d = 4096; bf16 V = 128256, fp32 V = 65536, the GEMM's time
-// after the stroke): bf16 1 token 185 / 250, 2 tokens 245 / 274, from 4 on the
-// GEMM is ahead; fp32 1 token 179 / 1600, 4 tokens 267 / 1600, 8 tokens
-// 276 / 1500 (the GEMM has 256 rows of six products to do for them).
+// Measured (us, d = 4096; bf16 V = 128256, fp32 V = 65536, (d, V) and (V, d)
+// layout, the GEMM's time after the stroke): bf16 1 token 182 / 251 and
+// 192 / 276, 2 tokens 243 / 270 and 240 / 237, from 4 on the GEMM is ahead;
+// fp32 1 token 181 / 1720 and 206 / 1760, 4 tokens 271 / 1640 and 320 / 1740,
+// 8 tokens 281 / 1530 (the GEMM lays the head out and has 256 rows of six
+// products to do for them).
 constexpr int kFewTokens = 8, kFewTokensBf16 = 2;
 constexpr int kFewWarps = 8;
 constexpr int kFewChunk = 1024;       // rows of Whead whose h is in shared memory

@@ -18,10 +18,14 @@
 // multipliers of C. Wellons' search, "Prospecting for hash functions",
 // 2018).  bf16 weights without an fp32 master copy are rounded the same way.
 //
+// With fp32 moments the root and the quotient of the step are the hardware's
+// approximations, to two units each; the state holds neither.  With e4m3
+// moments the root is state, and correctly rounded.
+//
 // 218 M weights: fp32 moments with a master copy 0.92 ms (6.6 TB/s, memory),
-// e4m3 moments 0.51 ms (4.3 TB/s; some 80 instructions a weight bound it, a
-// quarter of them the random bits); the norm reads bf16 gradients at 4.9 TB/s
-// behind the previous step's dirty lines.
+// e4m3 moments 0.51 ms (4.3 TB/s; 80 instructions a weight bound it, about
+// fourteen of them for the random bits); the norm reads bf16 gradients at
+// 5.6 TB/s one call behind the other, 4.8 TB/s after other work.
 //
 // One warp takes 256 elements (a block of the 8-bit form),
 // 2 x 4 a lane, so every load of a warp is consecutive, and the block's

@@ -372,7 +372,8 @@ int tps_vocab_ce_fwd_bwd_ex(const tps_tensor* h, const tps_tensor* Whead, const 
  * the pieces' maxima and sums and the gradient of the logits.
  *   lse_t = log sum_{j < vocab} e^{z_tj},  loss_t = lse_t - z_{t, y_t};
  *   dz_tj = g_t (e^{z_tj - lse_t} - 1[j = y_t]) (formed again from h and
- *   Whead, piece by piece; bf16 for bf16 operands),
+ *   Whead, piece by piece; bf16 for bf16 operands, over the largest |g_t|,
+ *   which multiplies the products in fp32),
  *   dHidden = dz Whead^T (summed over the pieces in fp32),
  *   dWhead = h^T dz.
  * h (..., d) and Whead (d x V, or V x d for TPS_W_OUT_IN): both F32 or both
@@ -487,7 +488,8 @@ int tps_rope_bwd(const tps_rope_plan* plan, const tps_tensor* dQo, const tps_ten
  * element's place = tensor.place (a multiple of TPS_ADAMW_BLOCK) + its index.
  * Otherwise they are rounded to
  * nearest, which leaves e4m3 moments where they are once they change by less
- * than half a step.
+ * than half a step.  A block whose largest magnitude is below 1e-30 is held as
+ * zeros.  No two of the tensors' buffers may overlap.
  * device_scalars (device, 16-byte aligned, NULL: computed from `hyper`): the
  * four numbers that change from step to step, as tps_adamw_prepare gives
  * them on the host; a captured CUDA graph then replays with whatever the
