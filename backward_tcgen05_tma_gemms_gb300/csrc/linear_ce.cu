@@ -17,12 +17,12 @@
 // Backward, bf16: nothing but lse is kept, so each piece of the vocabulary
 // has its logits formed again, and the epilogue turns them into dz at once
 // (EPI_CE_GRAD: one exponential and one product an element; dz leaves as
-// bf16, the type in which the tensor cores take it: gradients are then 3e-4
-// (T = 8192) to 3e-3 (a few tokens) from those of an fp32 dz, where their own
-// rounding to bf16 is 1.7e-3; dz in two planes would double both products that
-// read it).  The piece is then the
-// K-major operand of dh += dz W_piece^T, summed over the pieces in fp32 by
-// TMA reductions in piece order, and the MN-major operand of dW_piece.
+// bf16, the type in which the tensor cores take it.  That leaves fp32 gradients
+// 3e-5 to 3e-4 off, in the norm, where the rows share their upstream gradient,
+// and 1.6e-3 where each token has one of its own, as much as bf16 gradients
+// are; dz in two planes would double both products that read it).  The piece is
+// then the K-major operand of dh += dz W_piece^T, summed over the pieces in
+// fp32 by TMA reductions in piece order, and the MN-major operand of dW_piece.
 // 6 T d V operations; forward and backward together take 8 T d V, where a
 // pass that keeps T x V logits takes 6: a third more is what not keeping them
 // costs.
