@@ -31,6 +31,7 @@ ACTS = {"gelu": 0, "gelu_erf": 0, "gelu_tanh": 1, "tanh": 2, "silu": 3}
 LAYOUTS = {"in_out": 0, "out_in": 1}
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32, torch.int64: I64}
+_CODE_DTYPES = {**_DTYPES, torch.float8_e4m3fn: E4M3}  # where e4m3 numbers may stand
 _STATE_DTYPES = {torch.float32: F32, torch.float8_e4m3fn: E4M3}
 
 
@@ -138,6 +139,14 @@ def library():
     lib.tps_grad_norm.argtypes = [vp, i32, ctypes.c_double, vp, vp, sz, vp]
     lib.tps_grad_norm_workspace_bytes.argtypes = [i32]
     lib.tps_grad_norm_workspace_bytes.restype = sz
+    D = ctypes.c_char_p  # a tps_dropout packed by _dropout
+    lib.tps_rmsnorm_fwd.argtypes = [V, V, V, ctypes.c_double, D, V, V, V, V, vp]
+    lib.tps_rmsnorm_bwd.argtypes = [V, V, V, V, V, D, V, V, V, vp, sz, vp]
+    lib.tps_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    lib.tps_rmsnorm_workspace_bytes.restype = sz
+    lib.tps_dropout_fwd.argtypes = [V, V, D, V, vp]
+    lib.tps_dropout_bwd.argtypes = [V, D, V, vp]
+    lib.tps_quantize_e4m3.argtypes = [V, V, V, vp]
     lib.tps_last_device_error.argtypes = [vp]
     lib.tps_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.tps_strerror.argtypes = [ctypes.c_int]
@@ -184,7 +193,7 @@ _VIEW = struct.Struct("=Qii8q")  # tps_tensor
 _PAD = (0, 0, 0, 0)
 
 
-def _view(t: Optional[torch.Tensor]):
+def _view(t: Optional[torch.Tensor], dtypes=_DTYPES):
     """tps_tensor view of a CUDA tensor as bytes (None -> NULL): the same
     checks as _tt, packed in one step for the short calls."""
     if t is None:
@@ -193,7 +202,7 @@ def _view(t: Optional[torch.Tensor]):
         raise TypeError("expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU (no CPU path)")
-    code = _DTYPES.get(t.dtype)
+    code = dtypes.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     n = t.dim()
@@ -639,6 +648,154 @@ def rope_bwd(plan: RopePlan, dq: torch.Tensor, dk: Optional[torch.Tensor], posit
              head_dim: Optional[int] = None, out: Optional[Sequence[torch.Tensor]] = None):
     """Gradients of q and k from those of rope_fwd's results."""
     return _rope(library().tps_rope_bwd, plan, dq, dk, positions, head_dim, out)
+
+
+# --------------------------------------------------------------------- norm and dropout
+
+_DROPOUT = struct.Struct("=dQQQ")  # tps_dropout
+
+
+def _dropout(p: float, seed, site: int, like: torch.Tensor):
+    """tps_dropout as bytes, None for none.  seed: a number, or one int64 on
+    `like`'s GPU."""
+    if p == 0.0:
+        return None
+    if isinstance(seed, torch.Tensor):
+        if seed.dtype != torch.int64 or seed.numel() != 1:
+            raise ValueError("seed: one int64")
+        if seed.get_device() != like.get_device():
+            raise ValueError("seed on another GPU than the tensors")
+        return _DROPOUT.pack(p, 0, seed.data_ptr(), site & (2 ** 64 - 1))
+    return _DROPOUT.pack(p, seed & (2 ** 64 - 1), 0, site & (2 ** 64 - 1))
+
+
+def _one_gpu(*tensors):
+    """Everything on the current GPU, where the kernels are going to run."""
+    here = {t.get_device() for t in tensors if t is not None}
+    if -1 in here:
+        raise ValueError("tensors must live on the GPU (no CPU path)")
+    if here != {torch.cuda.current_device()}:
+        raise ValueError("tensors on different GPUs" if len(here) > 1 else "tensors on another GPU than the current one")
+
+
+def _rows(t: Optional[torch.Tensor]):
+    """A vector as one row."""
+    return t if t is None or t.dim() != 1 else t.unsqueeze(0)
+
+
+def rmsnorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
+                eps: float = 1e-6, dropout: float = 0.0, seed=0, site: int = 0,
+                out_dtype: Optional[torch.dtype] = None, out: Optional[Sequence] = None):
+    """Residual addition and root-mean-square norm of rows (..., d):
+    h = residual + dropout(x), y = h weight / sqrt(mean h^2 + eps).  Returns
+    (y, scale, h, rstd): y in out_dtype (x's by default), with one scale for
+    each row when that is torch.float8_e4m3fn (else None); h in the residual's
+    type, None where it is x (no residual, no dropout); rstd for rmsnorm_bwd.
+    seed: a number, or one int64 on the GPU, which a captured CUDA graph reads
+    at every replay; site: which dropout of the model this is.  `out` may
+    supply the four; h may be the residual and y may be x."""
+    if out is not None:
+        y, scale, h, rstd = out
+    else:
+        T = x.shape[:-1]
+        y = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
+        scale = torch.empty(T, dtype=torch.float32, device=x.device) if y.dtype == torch.float8_e4m3fn else None
+        h = None
+        if residual is not None or dropout != 0.0:
+            h = torch.empty_like(x if residual is None else residual, memory_format=torch.contiguous_format)
+        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
+    _one_gpu(x, weight, residual, y, scale, h, rstd)
+    _check(library().tps_rmsnorm_fwd(_view(_rows(x)), _view(_rows(residual)), _view(weight), eps,
+                                     _dropout(dropout, seed, site, x), _view(_rows(h)),
+                                     _view(_rows(y), _CODE_DTYPES), _flat(scale),
+                                     _flat(rstd), _raw_stream(x)))
+    return y, scale, h, rstd
+
+
+def _flat(t: Optional[torch.Tensor]):
+    """One number a row, whatever the shape of the rows."""
+    return None if t is None else _view(t.reshape(-1) if t.is_contiguous() else t)
+
+
+def rmsnorm_workspace_bytes(T: int, d: int) -> int:
+    return int(library().tps_rmsnorm_workspace_bytes(T, d))
+
+
+def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor], rstd: torch.Tensor,
+                dh: Optional[torch.Tensor] = None, dropout: float = 0.0, seed=0, site: int = 0,
+                x_dtype: Optional[torch.dtype] = None, want_dweight: bool = True,
+                workspace: Optional[torch.Tensor] = None, out: Optional[Sequence] = None):
+    """Backward of rmsnorm_fwd from its h (x where it gave none) and rstd:
+    (dx, dresidual, dweight).  dh: the gradient that reaches h past the norm.
+    dx has x_dtype (h's by default), dresidual h's type; without dropout and
+    with one type the two are one tensor.  dweight is fp32.  dropout, seed and
+    site as in the forward call.  `out` may supply the three."""
+    if out is not None:
+        dx, dres, dw = out
+    else:
+        dres = torch.empty_like(h, memory_format=torch.contiguous_format)
+        dx = dres
+        if dropout != 0.0 or (x_dtype or h.dtype) != h.dtype:
+            dx = torch.empty_like(dres, dtype=x_dtype or h.dtype)
+        dw = None
+        if want_dweight:
+            dw = torch.empty(h.shape[-1], dtype=torch.float32, device=h.device)
+    _one_gpu(dy, h, weight, rstd, dh, dx, dres, dw, workspace)
+    lib = library()
+    room = (None, 0)
+    if dw is not None:
+        if workspace is None:
+            d = h.shape[-1]
+            need = int(lib.tps_rmsnorm_workspace_bytes(h.numel() // d if d else 0, d))
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
+        room = _room(workspace)
+    second = None if dx is dres and dropout == 0.0 else _view(_rows(dx))
+    _check(lib.tps_rmsnorm_bwd(_view(_rows(dy)), _view(_rows(h)), _view(weight), _flat(rstd), _view(_rows(dh)),
+                               _dropout(dropout, seed, site, h), _view(_rows(dres)), second, _view(dw), *room,
+                               _raw_stream(h)))
+    return dx, dres, dw
+
+
+def dropout_fwd(x: torch.Tensor, p: float, seed, site: int = 0, residual: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """x with each element dropped with probability p (in steps of 2^-16) and
+    multiplied by 1 / (1 - p) otherwise, plus the residual.  The mask is a
+    function of seed, site and the element's place, and is not stored."""
+    if out is None:
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
+    _one_gpu(x, residual, out)
+    _check(library().tps_dropout_fwd(_view(_rows(x)), _view(_rows(residual)), _dropout_always(p, seed, site, x),
+                                     _view(_rows(out)), _raw_stream(x)))
+    return out
+
+
+def dropout_bwd(dy: torch.Tensor, p: float, seed, site: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gradient of dropout_fwd's x from that of its result (which is the
+    residual's too)."""
+    if out is None:
+        out = torch.empty_like(dy, memory_format=torch.contiguous_format)
+    _one_gpu(dy, out)
+    _check(library().tps_dropout_bwd(_view(_rows(dy)), _dropout_always(p, seed, site, dy), _view(_rows(out)),
+                                     _raw_stream(dy)))
+    return out
+
+
+def _dropout_always(p, seed, site, like):
+    return _dropout(p, seed, site, like) or _DROPOUT.pack(p, 0, 0, 0)
+
+
+def quantize_e4m3(x: torch.Tensor, out: Optional[Sequence] = None):
+    """(q, scale): the rows of x (..., d) as e4m3 numbers, the largest
+    magnitude of each row being 448, and one fp32 scale for each row:
+    x = q scale."""
+    if out is not None:
+        q, scale = out
+    else:
+        q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
+        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+    _one_gpu(x, q, scale)
+    _check(library().tps_quantize_e4m3(_view(_rows(x)), _view(_rows(q), _CODE_DTYPES), _flat(scale), _raw_stream(x)))
+    return q, scale
 
 
 # --------------------------------------------------------------------- optimizer step

@@ -412,6 +412,66 @@ int tps_linear_ce_bwd(const tps_tensor* h, const tps_tensor* Whead, const tps_te
 size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dtype, int32_t backward, int64_t piece);
 
 /* ------------------------------------------------------------------------
+ * What stands between the products of a layer: residual addition, dropout and
+ * the root-mean-square norm (no counterpart on the source pages, whose layers
+ * are the products alone).
+ *
+ * tps_dropout: element i (its place in row-major order) of the tensor is
+ * multiplied by 1 / (1 - p), or dropped: made 0, whatever it held.  Nothing
+ * of the mask is stored.  The draw of an element is a function of the seed,
+ * the site (which dropout of a model it is, so that one seed a step is
+ * enough) and i: 16 bits of Philox 4x32-10 with key `seed` and counter
+ * (i / 8, site); kept where they are at least round(65536 p), so that p holds
+ * to 2^-17 (the multiplier is that of the p that is used).  seed_ptr (device,
+ * NULL: `seed`): the seed is read there, for CUDA graphs whose replays draw
+ * anew.  Errors: TPS_ERR_ARG for p outside [0, 1].
+ *
+ * tps_rmsnorm_fwd: for every row of d elements
+ *   h = residual + dropout(x), rounded to the residual's type,
+ *   rstd = (mean h^2 + eps)^(-1/2),  y_i = h_i weight_i rstd.
+ * X (..., d), residual (..., d) or NULL, H and Y (..., d): F32 or BF16, each
+ * of its own (H: the residual's type); rows of unit stride, any pitch.  H is
+ * NULL without a residual and without dropout (h is then x; with dropout alone
+ * H has X's type).  weight (d) F32 or BF16, NULL: ones.  rstd: T floats, for
+ * the backward pass.  Y may be E4M3 with scale (T floats): y = number * scale,
+ * the row's largest magnitude being 448 (a row whose largest |h weight| is
+ * below 1e-30 is zeros; a NaN or an infinity makes its row's scale and what the
+ * numbers stand for NaN or infinite).  H may be the residual itself, and Y may
+ * be X itself; otherwise outputs overlap nothing.  Squares are summed in fp32.
+ * tps_rmsnorm_bwd: with g = dy weight,
+ *   dsum = dH + rstd (g - h rstd mean(g h rstd)),  dx = dropout(dsum),
+ *   dweight = sum over the rows of dy h rstd.
+ * H: the h of the forward pass.  dH (NULL: none): the gradient that reaches h
+ * on the residual's own way.  dY, dX: F32 or BF16, each of its own; dH, dSum:
+ * H's type; dweight (d): F32.  dSum, dX and dweight may each be NULL.  dSum may
+ * be dH, dX may be dY.  dweight needs a workspace
+ * of tps_rmsnorm_workspace_bytes, 256-byte aligned; its sums are taken in a
+ * fixed order.
+ * tps_dropout_fwd: Y = dropout(X) + residual (NULL: none); tps_dropout_bwd:
+ * dX = dropout(dY).  (..., d), F32 or BF16, each of its own; Y may be X or the
+ * residual.
+ * tps_quantize_e4m3: rows of X (..., d) as E4M3 numbers Q and scale, as above.
+ * Extents below 2^31.  All of them may be captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+typedef struct tps_dropout {
+  double p;
+  uint64_t seed;
+  const int64_t* seed_ptr;
+  uint64_t site;
+} tps_dropout;
+int tps_rmsnorm_fwd(const tps_tensor* X, const tps_tensor* residual, const tps_tensor* weight, double eps,
+                    const tps_dropout* dropout, const tps_tensor* H, const tps_tensor* Y, const tps_tensor* scale,
+                    const tps_tensor* rstd, void* cuda_stream);
+int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const tps_tensor* weight, const tps_tensor* rstd,
+                    const tps_tensor* dH, const tps_dropout* dropout, const tps_tensor* dSum, const tps_tensor* dX,
+                    const tps_tensor* dweight, void* workspace, size_t workspace_bytes, void* cuda_stream);
+size_t tps_rmsnorm_workspace_bytes(int64_t T, int64_t d);
+int tps_dropout_fwd(const tps_tensor* X, const tps_tensor* residual, const tps_dropout* dropout, const tps_tensor* Y,
+                    void* cuda_stream);
+int tps_dropout_bwd(const tps_tensor* dY, const tps_dropout* dropout, const tps_tensor* dX, void* cuda_stream);
+int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor* scale, void* cuda_stream);
+
+/* ------------------------------------------------------------------------
  * Rotary positions of the query and key heads, between tps_attn_qkv_fwd and
  * the attention core ([TP] core concept 2.B leaves the core to the caller;
  * no counterpart on the source pages).  Pair i of the first rotary_dim
