@@ -28,6 +28,7 @@ F32, BF16, I32, I64, E4M3 = 0, 1, 2, 3, 4
 BUILD_DEBUG = 1  # bit of tps_build_flags()
 AXES = {"rows": 0, "columns": 1, "inner": 2}
 ACTS = {"gelu": 0, "gelu_erf": 0, "gelu_tanh": 1, "tanh": 2, "silu": 3}
+LINEAR_ACTS = {**ACTS, None: -1}
 LAYOUTS = {"in_out": 0, "out_in": 1}
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32, torch.int64: I64}
@@ -147,6 +148,10 @@ def library():
     lib.tps_dropout_fwd.argtypes = [V, V, D, V, vp]
     lib.tps_dropout_bwd.argtypes = [V, D, V, vp]
     lib.tps_quantize_e4m3.argtypes = [V, V, V, vp]
+    lib.tps_linear_fwd.argtypes = [V, V, V, V, i32, i32, V, V, V, V, vp, sz, vp]
+    lib.tps_linear_bwd.argtypes = [V, V, V, V, i32, i32, V, V, V, vp, sz, vp]
+    lib.tps_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
+    lib.tps_linear_workspace_bytes.restype = sz
     lib.tps_last_device_error.argtypes = [vp]
     lib.tps_selftest_wait_timeout.argtypes = [ctypes.c_uint64, vp]
     lib.tps_strerror.argtypes = [ctypes.c_int]
@@ -796,6 +801,88 @@ def quantize_e4m3(x: torch.Tensor, out: Optional[Sequence] = None):
     _one_gpu(x, q, scale)
     _check(library().tps_quantize_e4m3(_view(_rows(x)), _view(_rows(q), _CODE_DTYPES), _flat(scale), _raw_stream(x)))
     return q, scale
+
+
+# --------------------------------------------------------------------- product with its epilogue
+
+def linear_workspace_bytes(T: int, K: int, N: int, dtype: torch.dtype, backward: bool) -> int:
+    """Workspace bytes of linear_fwd / linear_bwd for operands of `dtype`; bf16
+    operands that are not 16-byte aligned need those of fp32."""
+    return int(library().tps_linear_workspace_bytes(T, K, N, _CODE_DTYPES[dtype], 1 if backward else 0))
+
+
+def _linear_call(fn, T, K, N, x, backward, workspace):
+    """Run fn(workspace pointer, bytes) with the given workspace, or with one
+    for aligned operands; others are refused before any launch and run again
+    with the size that holds them laid out."""
+    if workspace is not None:
+        _check(fn(*_room(workspace)))
+        return
+    for dt in (x.dtype, torch.float32):
+        n = linear_workspace_bytes(T, K, N, dt, backward)
+        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
+        rc = fn(ws.data_ptr() if n else None, n)
+        if rc != ERR_WORKSPACE:
+            break
+    _check(rc)
+
+
+def _linear_args(x, W, act, weight_layout):
+    if act not in LINEAR_ACTS or weight_layout not in LAYOUTS:
+        raise ValueError("argument")
+    if W.dim() != 2:
+        raise ValueError("shape")
+    K = x.shape[-1]
+    return (x.numel() // K if K else 0), K, W.shape[1] if weight_layout == "in_out" else W.shape[0]
+
+
+def linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
+               residual: Optional[torch.Tensor] = None, act: Optional[str] = None, weight_layout: str = "in_out",
+               x_scale: Optional[torch.Tensor] = None, w_scale: Optional[torch.Tensor] = None,
+               want_pre: bool = False, out_dtype: Optional[torch.dtype] = None,
+               workspace: Optional[torch.Tensor] = None, out: Optional[Sequence] = None):
+    """(y, z): z = x W + bias and y = act(z) + residual of x (..., K), in
+    out_dtype (x's by default, bf16 for e4m3); z, the pre-activation that
+    linear_bwd needs, only with want_pre.  x and W are fp32, bf16, or e4m3 with
+    x_scale and w_scale, one for each row of x and of W (quantize_e4m3), W then
+    being (out, in).  `out` may supply (y, z); y may be the residual."""
+    T, K, N = _linear_args(x, W, act, weight_layout)
+    if out is not None:
+        y, z = out
+    else:
+        dt = out_dtype or (torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype)
+        y = torch.empty(*x.shape[:-1], N, dtype=dt, device=x.device)
+        z = torch.empty_like(y) if want_pre else None
+    _one_gpu(x, W, bias, residual, x_scale, w_scale, y, z, workspace)
+    a = (_view(_rows(x), _CODE_DTYPES), _view(W, _CODE_DTYPES), _view(bias), _view(_rows(residual)))
+    b = (_flat(x_scale), _flat(w_scale), _view(_rows(z)), _view(_rows(y)))
+    stream = _raw_stream(x)
+    _linear_call(lambda ws, n: library().tps_linear_fwd(*a, LINEAR_ACTS[act], LAYOUTS[weight_layout], *b, ws, n, stream),
+                 T, K, N, x, False, workspace)
+    return y, z
+
+
+def linear_bwd(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, pre: Optional[torch.Tensor] = None,
+               act: Optional[str] = None, weight_layout: str = "in_out", want_dx: bool = True, want_dw: bool = True,
+               want_dbias: bool = True, grad_dtype: torch.dtype = torch.float32,
+               workspace: Optional[torch.Tensor] = None, out: Optional[Sequence] = None):
+    """Gradients of linear_fwd's x, W and bias from that of its y (which is the
+    residual's too): (dx, dW, dbias) in `grad_dtype` (fp32 or bf16), None for
+    one that is not wanted.  pre: the pre-activation, with an activation."""
+    T, K, N = _linear_args(x, W, act, weight_layout)
+    if out is not None:
+        dx, dW, db = out
+    else:
+        dx = torch.empty(x.shape, dtype=grad_dtype, device=x.device) if want_dx else None
+        dW = torch.empty(W.shape, dtype=grad_dtype, device=x.device) if want_dw else None
+        db = torch.empty(N, dtype=grad_dtype, device=x.device) if want_dbias else None
+    _one_gpu(x, W, dy, pre, dx, dW, db, workspace)
+    a = (_view(_rows(x)), _view(W), _view(_rows(dy)), _view(_rows(pre)))
+    b = (_view(_rows(dx)), _view(dW), _view(db))
+    stream = _raw_stream(x)
+    _linear_call(lambda ws, n: library().tps_linear_bwd(*a, LINEAR_ACTS[act], LAYOUTS[weight_layout], *b, ws, n, stream),
+                 T, K, N, x, True, workspace)
+    return dx, dW, db
 
 
 # --------------------------------------------------------------------- optimizer step

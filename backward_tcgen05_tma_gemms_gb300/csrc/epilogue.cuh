@@ -175,6 +175,124 @@ __device__ __forceinline__ void epilogue_glu_run32(const Epilogue& e, int64_t ro
   store_run32(e.d2, e.d2_dtype, row * e.ldd2 + col0, n, u);
 }
 
+// ---- EPI_LINEAR -------------------------------------------------------------
+__device__ __forceinline__ float any_elem(const void* base, int dtype, int64_t i) {
+  return dtype == TPS_F32 ? static_cast<const float*>(base)[i]
+                          : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
+}
+__device__ __forceinline__ float linear_act(int act, float z) { return act == kActNone ? z : act_fwd(act, z); }
+// z of one row's columns [col0, col0 + n), n <= C, from the accumulators.
+template <int C>
+__device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64_t col0, int n, float (&v)[C]) {
+  if (e.row_scale != nullptr) {
+    const float rs = __ldg(e.row_scale + row);
+    const float* p = e.col_scale + col0;
+    if (n == C && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < C / 4; ++i) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+        v[4 * i] *= rs * q.x;
+        v[4 * i + 1] *= rs * q.y;
+        v[4 * i + 2] *= rs * q.z;
+        v[4 * i + 3] *= rs * q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < n) v[i] *= rs * __ldg(p + i);
+    }
+  }
+  if (e.bias == nullptr) return;
+  if (e.bias_dtype == TPS_F32) {
+    const float* p = static_cast<const float*>(e.bias) + col0;
+    if (n == C && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+#pragma unroll
+      for (int i = 0; i < C / 4; ++i) {
+        const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+        v[4 * i] += q.x;
+        v[4 * i + 1] += q.y;
+        v[4 * i + 2] += q.z;
+        v[4 * i + 3] += q.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < n) v[i] += __ldg(p + i);
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(e.bias) + col0;
+    if (n == C && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+#pragma unroll
+      for (int i = 0; i < C / 4; ++i) {
+        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p) + i);
+        v[4 * i] += __uint_as_float(q.x << 16);
+        v[4 * i + 1] += __uint_as_float(q.x & 0xffff0000u);
+        v[4 * i + 2] += __uint_as_float(q.y << 16);
+        v[4 * i + 3] += __uint_as_float(q.y & 0xffff0000u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (i < n) v[i] += __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16);
+    }
+  }
+}
+// act(z) in place.
+template <int C>
+__device__ __forceinline__ void linear_acted(const Epilogue& e, float (&v)[C]) {
+  if (e.act == kActNone) return;
+  act_dispatch(e.act, [&](auto A) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = act_fwd_c<decltype(A)::value>(v[i]);
+  });
+}
+// The residual's run of 32 columns as loaded (before its conversion, so that
+// the loads stay in flight), where it is whole and 16-byte aligned.
+struct Residual32 {
+  uint4 q[8];
+  bool have;
+  __device__ __forceinline__ void load(const Epilogue& e, int64_t row, int64_t col0, int n, bool live) {
+    have = false;
+    if (e.res == nullptr || !live || n < 32) return;
+    const char* p = static_cast<const char*>(e.res) + (row * e.ld_res + col0) * (e.res_dtype == TPS_F32 ? 4 : 2);
+    if ((reinterpret_cast<uintptr_t>(p) & 15u) != 0) return;
+    have = true;
+    const uint4* s = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) q[i] = s[i];
+    if (e.res_dtype == TPS_F32) {
+#pragma unroll
+      for (int i = 4; i < 8; ++i) q[i] = s[i];
+    }
+  }
+  __device__ __forceinline__ void add(const Epilogue& e, int64_t row, int64_t col0, int n, bool live, float (&v)[32]) const {
+    if (e.res == nullptr || !live) return;
+    if (!have) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) v[i] += any_elem(e.res, e.res_dtype, row * e.ld_res + col0 + i);
+    } else if (e.res_dtype == TPS_F32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[4 * i] += __uint_as_float(q[i].x);
+        v[4 * i + 1] += __uint_as_float(q[i].y);
+        v[4 * i + 2] += __uint_as_float(q[i].z);
+        v[4 * i + 3] += __uint_as_float(q[i].w);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w[4] = {q[i].x, q[i].y, q[i].z, q[i].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[8 * i + 2 * j] += __uint_as_float(w[j] << 16);
+          v[8 * i + 2 * j + 1] += __uint_as_float(w[j] & 0xffff0000u);
+        }
+      }
+    }
+  }
+};
+
 // Scalar form used by the SIMT kernel.
 __device__ __forceinline__ void epilogue_elem(const Epilogue& e, int64_t row, int64_t col, float v) {
   if (!dbg_store_ok(e, row, col, 1)) return;
@@ -192,6 +310,12 @@ __device__ __forceinline__ void epilogue_elem(const Epilogue& e, int64_t row, in
     act_fwd_grad(e.act, e.aux[row * e.ld_aux + col], f, g);
     store_elem(e.d, e.d_dtype, row * e.ldd + col, v * e.aux2[row * e.ld_aux2 + col] * g);
     store_elem(e.d2, e.d2_dtype, row * e.ldd2 + col, v * f);
+  } else if (e.mode == EPI_LINEAR) {
+    if (e.bias != nullptr) v += any_elem(e.bias, e.bias_dtype, col);
+    if (e.d2 != nullptr) store_elem(e.d2, e.d2_dtype, row * e.ldd2 + col, v);
+    v = linear_act(e.act, v);
+    if (e.res != nullptr) v += any_elem(e.res, e.res_dtype, row * e.ld_res + col);
+    store_elem(e.d, e.d_dtype, row * e.ldd + col, v);
   } else {
     const int64_t i = row * e.ld_aux + col;
     const float pre = e.aux_bf16 != nullptr ? __uint_as_float(static_cast<uint32_t>(e.aux_bf16[i]) << 16) : e.aux[i];

@@ -1,0 +1,591 @@
+// gemm_rows.cu -- Y = X W for a few rows of X (tokens), with the linear
+// epilogue: the weights are read once, and that bounds it.
+//
+//   z = x w row_scale col_scale + bias,  y = act(z) + residual
+//
+// The roles of the operands are swapped: 128 output features are the rows of
+// the tensor core's tile and up to 256 tokens its columns, so that the 128
+// lanes of tensor memory are full of features however few tokens there are
+// (tiles of tokens x features would leave all but a few of their rows empty).
+// W is the A operand in either layout, X, K-major, the B operand; the
+// accumulator holds Y transposed.
+//
+// The 128-feature tiles alone are too few for the SMs and for the bytes in
+// flight that memory wants, so a cluster of up to eight CTAs splits K: each
+// accumulates its run, writes its partial tile to shared memory as [token][feature],
+// and the CTAs of the cluster add up the eight partials of their share of the
+// tokens in rank order, out of each other's shared memory, with the epilogue
+// on the sums.  No workspace, no flags, results do not depend on timing.
+//
+// Warp roles (192 threads): warp 0 loads (TMA), warp 1 issues the MMAs, warps
+// 2..5 drain tensor memory; all of them add and store.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cstring>
+#include <mutex>
+
+#include "api_common.cuh"
+#include "tc_common.cuh"
+
+namespace tps {
+
+namespace {
+
+constexpr int GR_THREADS = 192;
+constexpr int GR_FEATURES = 128;
+constexpr int GR_W_BYTES = GR_FEATURES * 128;  // 128 bytes of K for each feature
+constexpr int GR_MAX_STAGES = 8, GR_MAX_SPLIT = 8;
+constexpr int GR_TOKENS = 256;                 // columns of a tile at most
+
+struct GrBarriers {
+  uint64_t full[GR_MAX_STAGES];
+  uint64_t empty[GR_MAX_STAGES];
+  uint64_t done;
+  uint32_t tmem_slot;
+  uint32_t abort;
+};
+
+struct GrParams {
+  int T, N;
+  int k_tiles, bn, t_tiles, stages, splits;
+  uint32_t tmem_cols;
+  Epilogue epi;
+  uint32_t* err;
+};
+
+// Epilogue of four columns of one row.
+__device__ __forceinline__ void rows_store4(void* base, int dtype, int64_t idx, int n, const float (&v)[4]) {
+  if (dtype == TPS_F32) {
+    float* p = static_cast<float*>(base) + idx;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = v[i];
+    }
+  } else {
+    __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + idx;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+      const __nv_bfloat162 a = __floats2bfloat162_rn(v[0], v[1]), b = __floats2bfloat162_rn(v[2], v[3]);
+      *reinterpret_cast<uint2*>(p) =
+          make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (i < n) p[i] = __float2bfloat16_rn(v[i]);
+    }
+  }
+}
+__device__ __forceinline__ void rows_load4(const void* base, int dtype, int64_t idx, int n, float (&a)[4]) {
+  if (dtype == TPS_F32) {
+    const float* p = static_cast<const float*>(base) + idx;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
+      const float4 q = *reinterpret_cast<const float4*>(p);
+      a[0] = q.x, a[1] = q.y, a[2] = q.z, a[3] = q.w;
+      return;
+    }
+  } else {
+    const uint16_t* p = static_cast<const uint16_t*>(base) + idx;
+    if (n == 4 && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
+      const uint2 q = *reinterpret_cast<const uint2*>(p);
+      a[0] = __uint_as_float(q.x << 16), a[1] = __uint_as_float(q.x & 0xffff0000u);
+      a[2] = __uint_as_float(q.y << 16), a[3] = __uint_as_float(q.y & 0xffff0000u);
+      return;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) a[i] = i < n ? any_elem(base, dtype, idx + i) : 0.0f;
+}
+
+// Adds up the cluster's partial tiles [token][128] (at the same shared-memory
+// address in every CTA) and stores this CTA's share of the tokens.
+__device__ __forceinline__ void rows_join(const Epilogue& e, uint32_t part, uint32_t rank, int splits, int t0, int tokens,
+                                          int64_t n0, int64_t N) {
+  const int first = tokens * static_cast<int>(rank) / splits * 32, last = tokens * (static_cast<int>(rank) + 1) / splits * 32;
+  for (int i = first + threadIdx.x; i < last; i += blockDim.x) {
+    const int t = i / 32, f = i % 32 * 4;
+    const int64_t row = t0 + t, col = n0 + f;
+    if (col >= N) continue;
+    const int n = N - col < 4 ? static_cast<int>(N - col) : 4;
+    float res[4];
+    if (e.res != nullptr) rows_load4(e.res, e.res_dtype, row * e.ld_res + col, n, res);
+    const uint32_t at = part + static_cast<uint32_t>((t * GR_FEATURES + f) * 4);
+    float4 q[GR_MAX_SPLIT];
+#pragma unroll
+    for (int s = 0; s < GR_MAX_SPLIT; ++s)
+      if (s < splits) q[s] = ld_cluster_f32x4(cluster_map(at, s));
+    float v[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
+#pragma unroll
+    for (int s = 1; s < GR_MAX_SPLIT; ++s)
+      if (s < splits) {
+        v[0] += q[s].x;
+        v[1] += q[s].y;
+        v[2] += q[s].z;
+        v[3] += q[s].w;
+      }
+    if (!dbg_store_ok(e, row, col, n)) continue;
+    if (e.mode == EPI_LINEAR) {
+      linear_pre(e, row, col, n, v);
+      if (e.d2 != nullptr) rows_store4(e.d2, e.d2_dtype, row * e.ldd2 + col, n, v);
+      if (e.act != kActNone) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = act_fwd(e.act, v[k]);
+      }
+      if (e.res != nullptr) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] += res[k];
+      }
+    }
+    rows_store4(e.d, e.d_dtype, row * e.ldd + col, n, v);
+  }
+}
+
+// W_MN: W's unit stride is along the features.  CODES: e4m3 operands.
+template <bool W_MN, bool CODES>
+__global__ void __launch_bounds__(GR_THREADS)
+    gemm_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const GrParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t raw_addr = smem_u32(smem_raw);
+  uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const int stage_bytes = GR_W_BYTES + p.bn * 128;
+  GrBarriers* bars = reinterpret_cast<GrBarriers*>(smem + p.stages * stage_bytes);
+  volatile uint32_t* abort_flag = &bars->abort;
+  constexpr int kBK = CODES ? 128 : 64;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
+  const int tile = static_cast<int>(blockIdx.x) / p.splits;
+  const int n0 = tile / p.t_tiles * GR_FEATURES, t0 = tile % p.t_tiles * p.bn;
+  const int tokens = min(p.bn, p.T - t0);
+  const int kt_begin = static_cast<int>(static_cast<int64_t>(p.k_tiles) * rank / p.splits);
+  const int kt_end = static_cast<int>(static_cast<int64_t>(p.k_tiles) * (rank + 1) / p.splits);
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&bars->full[s], 1);
+      mbar_init(&bars->empty[s], 1);
+    }
+    mbar_init(&bars->done, 1);
+    bars->abort = 0u;
+    fence_mbar_init();
+    tma_prefetch_desc(&tw);
+    tma_prefetch_desc(&tx);
+  }
+  if (warp == 1) {
+    tmem_alloc(&bars->tmem_slot, p.tmem_cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bars->tmem_slot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int issued = 0;
+      for (int kt = kt_begin; kt < kt_end; ++kt, ++issued) {
+        const int stage = issued % p.stages;
+        if (!mbar_wait(&bars->empty[stage], ((issued / p.stages) & 1) ^ 1u, abort_flag, p.err)) break;
+        uint8_t* sw = smem + stage * stage_bytes;
+        mbar_expect_tx(&bars->full[stage], stage_bytes);
+        if (W_MN) {
+#pragma unroll
+          for (int j = 0; j < GR_FEATURES / 64; ++j)
+            tma_load_2d(sw + j * TC_MN_BOX_BYTES, &tw, &bars->full[stage], n0 + 64 * j, kt * kBK);
+        } else {
+          tma_load_2d(sw, &tw, &bars->full[stage], kt * kBK, n0);
+        }
+        tma_load_2d(sw + GR_W_BYTES, &tx, &bars->full[stage], kt * kBK, t0);
+      }
+      // Copies in flight finish before the block ends, whatever the MMA thread did.
+      for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
+        mbar_wait_drain(&bars->full[i % p.stages], static_cast<uint32_t>((i / p.stages) & 1), p.err);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      const uint32_t idesc = CODES ? idesc_e4m3_f32(GR_FEATURES, p.bn) : idesc_bf16_f32(GR_FEATURES, p.bn, W_MN, false);
+      int i = 0;
+      for (int kt = kt_begin; kt < kt_end; ++kt, ++i) {
+        const int stage = i % p.stages;
+        if (!mbar_wait(&bars->full[stage], (i / p.stages) & 1, abort_flag, p.err)) break;
+        tc_fence_after();
+        const uint32_t sw = smem_u32(smem + stage * stage_bytes), sx = sw + GR_W_BYTES;
+#pragma unroll
+        for (int kk = 0; kk < 4; ++kk) {
+          const uint64_t ad = W_MN ? smem_desc_sw128(sw + kk * 2048, TC_MN_BOX_BYTES, 1024)
+                                   : smem_desc_sw128(sw + kk * 32, 16, 1024);
+          const uint64_t bd = smem_desc_sw128(sx + kk * 32, 16, 1024);
+          if (CODES)
+            tc_mma_f8(tmem, ad, bd, idesc, (i != 0 || kk != 0) ? 1u : 0u);
+          else
+            tc_mma_f16(tmem, ad, bd, idesc, (i != 0 || kk != 0) ? 1u : 0u);
+        }
+        tc_commit(&bars->empty[stage]);
+      }
+      tc_commit(&bars->done);
+      mbar_wait_drain(&bars->done, 0, p.err);
+    }
+  }
+  __syncwarp();
+  __syncthreads();  // the MMAs have completed: nothing reads or writes the stages any more
+  tc_fence_after();
+  if (warp >= 2) {
+    const int q = warp & 3;
+    float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
+    const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
+    for (int c = 0; c < tokens; c += 16) {
+      uint32_t r[16];
+      tmem_ld_32x32b_x16(t_row + c, r);
+      tmem_ld_wait();
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        if (c + i < tokens) part[(c + i) * GR_FEATURES] = __uint_as_float(r[i]);
+    }
+    tc_fence_before();
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  if (!*abort_flag)
+    rows_join(p.epi, smem_u32(smem), rank, p.splits, t0, tokens, n0, p.N);
+  if (p.splits > 1) cluster_sync();  // the others have read this CTA's partial tile
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, p.tmem_cols);
+  }
+}
+
+// ---- fp32, up to eight rows ---------------------------------------------------
+// The fp32 pipes do it: 2 T operations a weight of four bytes.  A block takes
+// 128 features of the cluster's run of K, with that run of X in shared memory.
+constexpr int GF_ROWS = 8, GF_WARPS = 8;
+constexpr int GF_SHARED = 96 << 10;
+
+struct GfParams {
+  const float* x;
+  int64_t ldx;
+  const float* w;
+  int64_t ldw;
+  int64_t T, N, K;
+  int splits;
+  Epilogue epi;
+};
+
+// OUT_IN: W's unit stride is along K, a warp takes four features at a time with its
+// lanes along K; else lanes are along the features and warps along K.
+template <int TT, bool OUT_IN>
+__global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams p) {
+  extern __shared__ __align__(16) float xs[];  // OUT_IN: [t][kn], else [k][t]; then [warp][t][128] sums
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) / p.splits * GR_FEATURES;
+  const int64_t quads = (p.K + 3) / 4;  // runs of K start on 16 bytes
+  const int64_t k0 = quads * rank / p.splits * 4, k1 = quads * (rank + 1) / p.splits * 4;
+  const int kn = static_cast<int>((k1 < p.K ? k1 : p.K) - k0), kp = (kn + 3) & ~3;
+  for (int i = threadIdx.x; i < TT * kp; i += 32 * GF_WARPS) {
+    const int t = i / kp, k = i - t * kp;
+    xs[OUT_IN ? i : k * TT + t] = t < p.T && k < kn ? p.x[t * p.ldx + k0 + k] : 0.0f;
+  }
+  __syncthreads();
+  if constexpr (OUT_IN) {
+    constexpr int F = 4, kWarpFeatures = GR_FEATURES / GF_WARPS;
+    float out[kWarpFeatures / F][F][TT];
+#pragma unroll
+    for (int g = 0; g < kWarpFeatures / F; ++g) {
+      const int64_t n = n0 + w * kWarpFeatures + g * F;
+      const float* src[F];  // features past N read the last one
+#pragma unroll
+      for (int f = 0; f < F; ++f) src[f] = p.w + (n + f < p.N ? n + f : p.N - 1) * p.ldw + k0;
+      float acc[F][TT];
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) acc[f][t] = 0.0f;
+      auto add = [&](const float4(&q)[F], int k) {
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const float4 y = *reinterpret_cast<const float4*>(xs + t * kp + k);
+#pragma unroll
+          for (int f = 0; f < F; ++f)
+            acc[f][t] = fmaf(q[f].x, y.x, fmaf(q[f].y, y.y, fmaf(q[f].z, y.z, fmaf(q[f].w, y.w, acc[f][t]))));
+        }
+      };
+      int k = lane * 4;
+      for (; k + 128 + 4 <= kn; k += 256) {  // two runs of each feature in flight
+        float4 q[2][F];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int f = 0; f < F; ++f) q[u][f] = __ldg(reinterpret_cast<const float4*>(src[f] + k + u * 128));
+        add(q[0], k);
+        add(q[1], k + 128);
+      }
+      for (; k < kn; k += 128) {
+        float4 q[F];
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          if (k + 4 <= kn) {
+            q[f] = __ldg(reinterpret_cast<const float4*>(src[f] + k));
+          } else {  // the end of K
+            q[f].x = src[f][k];
+            q[f].y = k + 1 < kn ? src[f][k + 1] : 0.0f;
+            q[f].z = k + 2 < kn ? src[f][k + 2] : 0.0f;
+            q[f].w = 0.0f;
+          }
+        }
+        add(q, k);
+      }
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+#pragma unroll
+          for (int o = 16; o > 0; o >>= 1) acc[f][t] += __shfl_xor_sync(0xffffffffu, acc[f][t], o);
+          out[g][f][t] = acc[f][t];
+        }
+    }
+    __syncthreads();  // X is done with
+    if (lane == 0) {
+#pragma unroll
+      for (int g = 0; g < kWarpFeatures / F; ++g)
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int t = 0; t < TT; ++t) xs[t * GR_FEATURES + w * kWarpFeatures + g * F + f] = out[g][f][t];
+    }
+  } else {
+    constexpr int U = 8;  // loads in flight
+    const int64_t col = n0 + lane * 4;
+    float acc[TT][4];
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[t][i] = 0.0f;
+    const float* src = p.w + k0 * p.ldw + col;
+    for (int k = w; k < kn && col < p.N; k += GF_WARPS * U) {
+      float4 q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = k + u * GF_WARPS;
+        const float* a = src + kk * p.ldw;
+        if (kk < kn) {
+          if (col + 4 <= p.N) {
+            q[u] = __ldg(reinterpret_cast<const float4*>(a));
+          } else {
+            q[u].x = a[0];
+            q[u].y = col + 1 < p.N ? a[1] : 0.0f;
+            q[u].z = col + 2 < p.N ? a[2] : 0.0f;
+            q[u].w = 0.0f;
+          }
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int kk = k + u * GF_WARPS;
+        if (kk >= kn) continue;
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+          const float x = xs[kk * TT + t];
+          acc[t][0] = fmaf(q[u].x, x, acc[t][0]);
+          acc[t][1] = fmaf(q[u].y, x, acc[t][1]);
+          acc[t][2] = fmaf(q[u].z, x, acc[t][2]);
+          acc[t][3] = fmaf(q[u].w, x, acc[t][3]);
+        }
+      }
+    }
+    __syncthreads();  // X is done with
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+      *reinterpret_cast<float4*>(xs + (w * TT + t) * GR_FEATURES + lane * 4) =
+          make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
+    __syncthreads();
+    for (int i = threadIdx.x; i < TT * GR_FEATURES; i += 32 * GF_WARPS) {
+      float a = 0.0f;
+#pragma unroll
+      for (int q = 0; q < GF_WARPS; ++q) a += xs[q * TT * GR_FEATURES + i];
+      xs[i] = a;  // warp 0's part, read and written by this thread alone
+    }
+  }
+  if (p.splits > 1)
+    cluster_sync();
+  else
+    __syncthreads();
+  rows_join(p.epi, smem_u32(xs), rank, p.splits, 0, static_cast<int>(p.T), n0, p.N);
+  if (p.splits > 1) cluster_sync();
+}
+
+// ------------------------------------------------------------------ host
+
+struct GrPlan {
+  int bn, t_tiles, n_tiles, k_tiles, splits, stages;
+  size_t shared;
+};
+constexpr int64_t kSms = 152;
+
+// The tile's tokens, the split of K and the stages.  Tiles of up to 64 tokens
+// leave room for two CTAs on an SM.  The split is the one whose CTAs make the
+// least K tiles a CTA in turn.
+GrPlan plan_of(const GemmDesc& g) {
+  GrPlan r;
+  r.t_tiles = static_cast<int>((g.M + GR_TOKENS - 1) / GR_TOKENS);
+  r.bn = static_cast<int>(((g.M + r.t_tiles - 1) / r.t_tiles + 15) / 16 * 16);
+  r.n_tiles = static_cast<int>((g.N + GR_FEATURES - 1) / GR_FEATURES);
+  const int bk = g.in_dtype == TPS_E4M3 ? 128 : 64;
+  r.k_tiles = static_cast<int>((g.K + bk - 1) / bk);
+  const int64_t per_sm = r.bn <= 64 ? 2 : 1, slots = kSms * per_sm;
+  const int64_t tiles = int64_t(r.t_tiles) * r.n_tiles;
+  r.splits = 1;
+  int64_t least = -1;
+  for (int s = 1; s <= GR_MAX_SPLIT && s <= r.k_tiles; s *= 2) {
+    const int64_t turns = (tiles * s + slots - 1) / slots * ((r.k_tiles + s - 1) / s);
+    if (least < 0 || turns < least) {
+      least = turns;
+      r.splits = s;
+    }
+  }
+  const int stage = GR_W_BYTES + r.bn * 128;
+  const int budget = per_sm == 2 ? (104 << 10) : (208 << 10);
+  r.stages = budget / stage < GR_MAX_STAGES ? budget / stage : GR_MAX_STAGES;
+  r.shared = 1024 + static_cast<size_t>(r.stages) * stage + sizeof(GrBarriers);
+  return r;
+}
+
+template <bool W_MN, bool CODES>
+int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx, const GrParams& p, const GrPlan& plan,
+                 cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+  });
+  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(plan.t_tiles * plan.n_tiles * plan.splits), 1, 1);
+  cfg.blockDim = dim3(GR_THREADS, 1, 1);
+  cfg.dynamicSmemBytes = plan.shared;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(plan.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope prof("gemm_rows", g.name, 2.0 * double(g.M) * double(g.N) * double(g.K),
+                 double(g.K) * double(g.N) * (CODES ? 1 : 2), stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_rows_kernel<W_MN, CODES>, tw, tx, p);
+  note_launch();
+  return e == cudaSuccess ? TPS_OK : TPS_ERR_CUDA;
+}
+
+}  // namespace
+
+// fp32 rows of X and W's rows in either layout, 16-byte aligned.
+bool gemm_few_supported(const GemmDesc& g) {
+  if (g.in_dtype != TPS_F32 || g.M < 1 || g.M > GF_ROWS || g.N < 1 || g.K < 1) return false;
+  if (g.epi.mode != EPI_LINEAR && g.epi.mode != EPI_STORE) return false;
+  if (g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1 || g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.planes > 1)
+    return false;
+  const int64_t ldw = g.b_sk == 1 ? g.b_sn : g.b_sk;
+  if (g.a_sk != 1 || (g.b_sk != 1 && g.b_sn != 1) || ldw % 4 != 0 || (reinterpret_cast<uintptr_t>(g.b) & 15u) != 0) return false;
+  const int64_t tt = g.M <= 1 ? 1 : g.M <= 2 ? 2 : g.M <= 4 ? 4 : 8;
+  return tt * ((g.K + GR_MAX_SPLIT - 1) / GR_MAX_SPLIT + 8) * 4 <= GF_SHARED;
+}
+
+template <int TT, bool OUT_IN>
+static int launch_few(const GemmDesc& g, const GfParams& p, cudaStream_t stream) {
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [] {
+    attr_err = cudaFuncSetAttribute(gemm_few_kernel<TT, OUT_IN>, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SHARED);
+  });
+  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  const int64_t run = ((p.K + 3) / 4 + p.splits - 1) / p.splits * 4;
+  const int64_t floats = TT * run > GF_WARPS * TT * GR_FEATURES ? TT * run : GF_WARPS * TT * GR_FEATURES;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>((p.N + GR_FEATURES - 1) / GR_FEATURES * p.splits), 1, 1);
+  cfg.blockDim = dim3(32 * GF_WARPS, 1, 1);
+  cfg.dynamicSmemBytes = static_cast<size_t>(4 * floats);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(p.splits);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  ProfScope prof("gemm_few", g.name, 2.0 * double(p.T) * double(p.N) * double(p.K), 4.0 * double(p.K) * double(p.N), stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_few_kernel<TT, OUT_IN>, p);
+  note_launch();
+  return e == cudaSuccess ? TPS_OK : TPS_ERR_CUDA;
+}
+
+int launch_gemm_few(const GemmDesc& g, cudaStream_t stream) {
+  GfParams p;
+  p.x = static_cast<const float*>(g.a);
+  p.ldx = g.a_sm;
+  p.w = static_cast<const float*>(g.b);
+  const bool out_in = g.b_sk == 1;
+  p.ldw = out_in ? g.b_sn : g.b_sk;
+  p.T = g.M;
+  p.N = g.N;
+  p.K = g.K;
+  p.epi = g.epi;
+  // Enough blocks for four on every SM, as far as a cluster goes; every run holds some of K.
+  const int64_t tiles = (g.N + GR_FEATURES - 1) / GR_FEATURES;
+  p.splits = 1;
+  while (p.splits < GR_MAX_SPLIT && tiles * p.splits < 4 * kSms && (g.K + 3) / 4 >= 2 * p.splits) p.splits *= 2;
+  const int64_t tt = g.M <= 1 ? 1 : g.M <= 2 ? 2 : g.M <= 4 ? 4 : 8;
+  while (p.splits < GR_MAX_SPLIT && tt * (((g.K + 3) / 4 + p.splits - 1) / p.splits * 4) * 4 > GF_SHARED) p.splits *= 2;
+  if (tiles * p.splits >= (1ll << 31)) return TPS_ERR_SHAPE;
+  if (g.M <= 1) return out_in ? launch_few<1, true>(g, p, stream) : launch_few<1, false>(g, p, stream);
+  if (g.M <= 2) return out_in ? launch_few<2, true>(g, p, stream) : launch_few<2, false>(g, p, stream);
+  if (g.M <= 4) return out_in ? launch_few<4, true>(g, p, stream) : launch_few<4, false>(g, p, stream);
+  return out_in ? launch_few<8, true>(g, p, stream) : launch_few<8, false>(g, p, stream);
+}
+
+// X K-major; everything else as the CTA-pair kernel wants it.
+bool gemm_rows_supported(const GemmDesc& g) {
+  if (g.epi.mode != EPI_LINEAR && g.epi.mode != EPI_STORE) return false;
+  if (g.planes > 1 || g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1 ||
+      g.a_cols > 0 || g.b_cols > 0 || g.a_sk != 1)
+    return false;
+  if (g.in_dtype == TPS_E4M3 && g.epi.mode != EPI_LINEAR) return false;
+  if (!gemm_tc_supported(g)) return false;
+  const GrPlan r = plan_of(g);
+  return int64_t(r.t_tiles) * r.n_tiles * r.splits < (1ll << 31);
+}
+
+bool gemm_rows_preferred(const GemmDesc& g) { return g.M <= GR_TOKENS; }
+
+int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
+  const bool w_mn = g.b_sk != 1, codes = g.in_dtype == TPS_E4M3;
+  const GrPlan plan = plan_of(g);
+  CUtensorMap tw, tx;
+  bool ok;
+  if (codes)
+    ok = !w_mn && tc_make_map8(&tw, g.b, g.N, g.K, g.b_sn, 128, GR_FEATURES) &&
+         tc_make_map8(&tx, g.a, g.M, g.K, g.a_sm, 128, plan.bn);
+  else
+    ok = (w_mn ? tc_make_map(&tw, g.b, g.K, g.N, g.b_sk, 64, TC_BK) : tc_make_map(&tw, g.b, g.N, g.K, g.b_sn, TC_BK, GR_FEATURES)) &&
+         tc_make_map(&tx, g.a, g.M, g.K, g.a_sm, TC_BK, plan.bn);
+  if (!ok) return TPS_ERR_CUDA;
+  GrParams p;
+  p.T = static_cast<int>(g.M);
+  p.N = static_cast<int>(g.N);
+  p.k_tiles = plan.k_tiles;
+  p.bn = plan.bn;
+  p.t_tiles = plan.t_tiles;
+  p.stages = plan.stages;
+  p.splits = plan.splits;
+  p.tmem_cols = 32;
+  while (p.tmem_cols < static_cast<uint32_t>(plan.bn)) p.tmem_cols *= 2;
+  p.epi = g.epi;
+  p.err = dev_err;
+  if (codes) return launch_typed<false, true>(g, tw, tx, p, plan, stream);
+  return w_mn ? launch_typed<true, false>(g, tw, tx, p, plan, stream) : launch_typed<false, false>(g, tw, tx, p, plan, stream);
+}
+
+}  // namespace tps

@@ -304,18 +304,25 @@ static PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   return fn;
 }
 
-bool tc_make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
-                 int box_rows) {
+static bool make_operand_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                             int box_rows, CUtensorMapDataType type, int es) {
   auto fn = encode_fn();
   if (fn == nullptr) return false;
   cuuint64_t dims[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows)};
-  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * 2)};
+  cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld * es)};
   cuuint32_t box[2] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows)};
   cuuint32_t estr[2] = {1, 1};
-  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  CUresult r = fn(map, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS;
+}
+bool tc_make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                 int box_rows) {
+  return make_operand_map(map, base, rows, cols, ld, box_cols, box_rows, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2);
+}
+bool tc_make_map8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                  int box_rows) {
+  return make_operand_map(map, base, rows, cols, ld, box_cols, box_rows, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1);
 }
 
 bool tc_make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int dtype) {
@@ -373,7 +380,9 @@ void tc_raster_choice(int m_tiles, int* raster_n, int* group, int* pol_a, int* p
 // The gated forms need their second operands to qualify too, with the same
 // contiguous dimension.
 bool gemm_tc_supported(const GemmDesc& g) {
-  if (g.in_dtype != TPS_BF16) return false;
+  const bool codes = g.in_dtype == TPS_E4M3;
+  if (g.in_dtype != TPS_BF16 && !codes) return false;
+  if (codes && (g.epi.mode != EPI_LINEAR || g.a_sk != 1 || g.b_sk != 1)) return false;
   if (g.M < 1 || g.N < 1 || g.K < 1 || g.K2 < 0 || g.K3 < 0) return false;
   if (g.M >= (1ll << 31) || g.N >= (1ll << 31) || g.K + g.K2 + g.K3 >= (1ll << 31)) return false;
   const bool k_segs = g.K2 > 0 || g.K3 > 0;
@@ -390,16 +399,19 @@ bool gemm_tc_supported(const GemmDesc& g) {
                            (reinterpret_cast<uintptr_t>(g.epi.d) & 15u) != 0 || (g.epi.ldd * 4) % 16 != 0 ||
                            g.epi.ldd < g.N))
     return false;
-  if (g.planes > 1 && ((g.epi.mode != EPI_STORE && g.epi.mode != EPI_CE_LSE && g.epi.mode != EPI_CE_GRAD) ||
-                       g.planes != 3 || g.n_segs > 1 || k_segs || 6 * g.K >= (1ll << 31)))
+  if (g.epi.mode == EPI_LINEAR && (g.n_segs > 1 || k_segs)) return false;
+  if (g.planes > 1 && ((g.epi.mode != EPI_STORE && g.epi.mode != EPI_CE_LSE && g.epi.mode != EPI_CE_GRAD &&
+                        g.epi.mode != EPI_LINEAR) ||
+                       codes || g.planes != 3 || g.n_segs > 1 || k_segs || 6 * g.K >= (1ll << 31)))
     return false;
   if (g.n_segs < 1 || g.n_segs > 3 || (g.n_segs > 1 && k_segs)) return false;
   if ((g.n_segs > 1 || k_segs) && g.epi.mode != EPI_STORE) return false;  // segments: plain stores only
-  auto ok_operand = [](const void* ptr, int64_t s_outer, int64_t s_inner, int64_t inner_extent) {
+  const int64_t es = codes ? 1 : 2;
+  auto ok_operand = [es](const void* ptr, int64_t s_outer, int64_t s_inner, int64_t inner_extent) {
     if ((reinterpret_cast<uintptr_t>(ptr) & 15u) != 0) return false;
     if (s_inner != 1) return false;
-    if ((s_outer * 2) % 16 != 0 || s_outer < inner_extent) return false;
-    return s_outer * 2 < (1ll << 40);
+    if ((s_outer * es) % 16 != 0 || s_outer < inner_extent) return false;
+    return s_outer * es < (1ll << 40);
   };
   const bool a_ok = (g.a_sk == 1) ? ok_operand(g.a, g.a_sm, g.a_sk, g.K) : ok_operand(g.a, g.a_sk, g.a_sm, g.M);
   if (!a_ok) return false;
@@ -462,6 +474,9 @@ bool tc_make_output_maps(const GemmDesc& g, CUtensorMap* td, CUtensorMap* td2, C
            tc_make_out_map(td, g.epi.d, g.M, g.N, g.epi.ldd, TPS_BF16) &&
            tc_make_out_map(td2, g.epi.d2, g.M, g.N, g.epi.ldd2, TPS_BF16);
   }
+  if (g.epi.mode == EPI_LINEAR)  // z beside the result
+    return tc_make_out_map(td, g.epi.d, g.M, g.N, g.epi.ldd, g.epi.d_dtype) &&
+           (g.epi.d2 == nullptr || tc_make_out_map(td2, g.epi.d2, g.M, g.N, g.epi.ldd2, g.epi.d2_dtype));
   if (g.epi.mode == EPI_ACT_FWD || g.epi.mode == EPI_GLU_UP) {
     bool ok = true;
     const int pre_dtype = g.epi.mode == EPI_ACT_FWD ? g.epi.d_dtype : TPS_F32;  // U of EPI_GLU_UP is fp32
@@ -531,7 +546,7 @@ int launch_gemm_tc(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   const int forced = kv ? atoi(kv) : 0;
   const bool pair_only =
       g.epi.mode == EPI_GLU_FWD || g.epi.mode == EPI_GLU_BWD || g.epi.mode == EPI_CE_LSE ||
-      g.epi.mode == EPI_CE_GRAD || g.epi.accumulate || g.epi.alpha != nullptr || g.pair || g.planes > 1 || g.a_cols > 0 || g.b_cols > 0 || g.K2 > 0 || g.K3 > 0 || g.n_segs > 1;
+      g.epi.mode == EPI_CE_GRAD || g.epi.mode == EPI_LINEAR || g.epi.accumulate || g.epi.alpha != nullptr || g.pair || g.planes > 1 || g.a_cols > 0 || g.b_cols > 0 || g.K2 > 0 || g.K3 > 0 || g.n_segs > 1;
   const bool pair = pair_only || forced == 2 || (forced != 1 && g.M >= 256);
   return pair ? launch_gemm_tc2(g, dev_err, stream) : launch_gemm_tc1(g, dev_err, stream);
 }

@@ -124,9 +124,17 @@ struct T2Params {
 //               other accumulator fills.  The last product, of the planes 0,
 //               starts a fresh accumulator: it alone decides about infinities
 //               and NaN (see T2Drains).
+//   T2_LIN      EPI_LINEAR of bf16 operands: z and the result leave one after
+//               the other through the same two boxes
+//   T2_LIN8     EPI_LINEAR of e4m3 operands: a K tile is 128 elements, the same
+//               bytes, and the instruction takes 32 of them
+//   T2_PLANES_LIN  EPI_LINEAR of operands in bf16 planes, as T2_PLANES
 enum T2Family : int {
-  T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6, T2_PLANES = 7
+  T2_PLAIN = 0, T2_GLU_FWD = 1, T2_GLU_BWD = 2, T2_SEG = 3, T2_ACT = 4, T2_ACT16 = 5, T2_CE = 6, T2_PLANES = 7,
+  T2_LIN = 8, T2_LIN8 = 9, T2_PLANES_LIN = 10
 };
+constexpr bool t2_planes(int fam) { return fam == T2_PLANES || fam == T2_PLANES_LIN; }
+constexpr bool t2_linear(int fam) { return fam == T2_LIN || fam == T2_LIN8; }
 constexpr int T2_SUB = 8;
 
 // How the K tiles [begin, end) of a T2_PLANES unit are cut into accumulators:
@@ -162,7 +170,7 @@ struct T2Drains {
 //                     (6 KB), single-buffered                -> 5 stages
 template <int FAM>
 struct T2Layout {
-  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG || FAM == T2_CE || FAM == T2_PLANES;
+  static constexpr bool kStoreOnly = FAM == T2_PLAIN || FAM == T2_SEG || FAM == T2_CE || t2_planes(FAM) || t2_linear(FAM);
   static constexpr int kStages = 5;
   static constexpr bool kTwoBf16 = FAM == T2_GLU_BWD || FAM == T2_ACT16;  // two bf16 boxes per buffer
   static constexpr int kBufBytes = kStoreOnly ? TC_STG_F32_BYTES : (kTwoBf16 ? 2 * TC_STG_BF16_BYTES : T2_STG_BUF);
@@ -193,6 +201,7 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
   uint8_t* smem = smem_raw + ((1024u - (raw_addr & 1023u)) & 1023u);
   using L = T2Layout<FAM>;
   constexpr int T2_STAGES = L::kStages;
+  constexpr int kBK = FAM == T2_LIN8 ? 2 * TC_BK : TC_BK;  // elements of a K tile, 128 bytes
   uint8_t* staging = smem + T2_STAGES * T2_STAGE_BYTES;  // 1024-aligned
   T2Barriers* bars = reinterpret_cast<T2Barriers*>(staging + T2_EPI_WARPS * L::kWarpStaging);
   volatile uint32_t* abort_flag = &bars->abort;
@@ -276,9 +285,9 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             while (ks < 2 && kt >= p.k_end[ks]) ++ks;
           const CUtensorMap* ma = &m.a[ks];
           const CUtensorMap* mb = ks > 0 ? &m.b[ks] : mb0;
-          int k0 = (kt - (ks > 0 ? p.k_end[ks - 1] : 0)) * TC_BK;
+          int k0 = (kt - (ks > 0 ? p.k_end[ks - 1] : 0)) * kBK;
           int xa = 0, xb = 0;  // the operands' planes along their contiguous dimensions
-          if constexpr (FAM == T2_PLANES) {
+          if constexpr (t2_planes(FAM)) {
             const int prod = kt / p.kt1;  // planes of A: 2 1 0 1 0 0, of B: 0 1 2 0 1 0
             k0 = (kt - prod * p.kt1) * TC_BK;
             xa = ((0x046 >> (2 * prod)) & 3) * p.a_plane;
@@ -315,18 +324,19 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
   } else if (warp == 1) {
     if (lane == 0 && rank == 0) {
       // ------------------------------------------------ MMA issuer
-      constexpr uint32_t idesc = idesc_bf16_f32(2 * T2_BM, T2_BN, A_MN, B_MN);
+      constexpr uint32_t idesc =
+          FAM == T2_LIN8 ? idesc_e4m3_f32(2 * T2_BM, T2_BN) : idesc_bf16_f32(2 * T2_BM, T2_BN, A_MN, B_MN);
       uint32_t stage = 0, phase = 0, acc = 0, acc_phase = 0;
       bool ok = true;
       for (int u = units.take(); ok && u >= 0; u = units.take()) {
         const int run = u / p.num_tiles;
         const int kt_begin = run * p.kt_run, kt_end = min(p.k_tiles, kt_begin + p.kt_run);
-        if (FAM != T2_PLANES && !mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
+        if (!t2_planes(FAM) && !mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) break;
         tc_fence_after();
         uint32_t d_tmem = tmem_base + acc * T2_BN;
         const T2Drains drains(kt_begin, kt_end, 5 * p.kt1);
         for (int kt = kt_begin; kt < kt_end; ++kt) {
-          if constexpr (FAM == T2_PLANES) {
+          if constexpr (t2_planes(FAM)) {
             if (drains.starts(kt)) {  // a fresh accumulator
               if (!mbar_wait(&bars->tmem_empty[acc], acc_phase ^ 1u, abort_flag, p.err)) {
                 ok = false;
@@ -349,22 +359,25 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
                                      : smem_desc_sw128(sa + kk * 32, 16, 1024);
             const uint64_t bd = B_MN ? smem_desc_sw128(sb + kk * 2048, TC_MN_BOX_BYTES, 1024)
                                      : smem_desc_sw128(sb + kk * 32, 16, 1024);
-            const bool first = FAM == T2_PLANES ? drains.starts(kt) : kt == kt_begin;
-            tc_mma_f16_pair(d_tmem, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
+            const bool first = t2_planes(FAM) ? drains.starts(kt) : kt == kt_begin;
+            if constexpr (FAM == T2_LIN8)
+              tc_mma_f8_pair(d_tmem, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
+            else
+              tc_mma_f16_pair(d_tmem, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
           }
           tc_commit_pair_mc(&bars->empty[stage], 0x3);  // frees the stage in both CTAs
           if (++stage == T2_STAGES) {
             stage = 0;
             phase ^= 1u;
           }
-          if (FAM == T2_PLANES && drains.ends(kt)) {
+          if (t2_planes(FAM) && drains.ends(kt)) {
             tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);
             acc ^= 1u;
             if (acc == 0) acc_phase ^= 1u;
           }
         }
         if (!ok) break;
-        if (FAM != T2_PLANES) {
+        if (!t2_planes(FAM)) {
           tc_commit_pair_mc(&bars->tmem_full[acc], 0x3);  // both CTAs' accumulators complete
           acc ^= 1u;
           if (acc == 0) acc_phase ^= 1u;
@@ -413,8 +426,10 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             ce_y = ce_row_label(e, row) - e.ce_col0;
         }
       }
-      // The first chunk's AUX input does not depend on the accumulator: it
-      // is loaded before waiting for it.
+      // The first chunk's residual or AUX input does not depend on the
+      // accumulator: it is loaded before waiting for it.
+      Residual32 res;
+      if constexpr (t2_linear(FAM)) res.load(e, row, nh0, min(32, p.N - nh0), row < p.M);
       float a_next[32];
       if (bwd) {
         if (row < p.M && nh0 < p.N) {
@@ -447,9 +462,9 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
         }
         return __shfl_sync(0xffffffffu, ready, 0) != 0u;
       };
-      if (FAM != T2_PLANES && !my_turn()) break;
+      if (!t2_planes(FAM) && !my_turn()) break;
       const uint32_t t_col = tmem_base + (static_cast<uint32_t>(q * 32) << 16) + static_cast<uint32_t>(h * warp_cols);
-      if constexpr (FAM == T2_PLANES) {
+      if constexpr (t2_planes(FAM)) {
         float sum[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c)
@@ -505,6 +520,28 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
             const int col0 = nh0 + c * 32;
             if (col0 >= p.n_store) break;  // warp-uniform
             float(&v)[32] = sum[c];
+            if constexpr (FAM == T2_PLANES_LIN) {
+              const int n = min(32, p.N - col0);
+              const bool live = row < p.M;
+              Residual32 res;
+              res.load(e, row, col0, n, live);
+              linear_pre(e, live ? row : 0, col0, n, v);
+              if (e.d2 != nullptr) {
+                if (p.tma_store) {
+                  tc_store_box(&m.d[1], e.d2_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
+                } else if (live && dbg_store_ok(e, row, col0, n)) {
+                  store_run32(e.d2, e.d2_dtype, row * e.ldd2 + col0, n, v);
+                }
+              }
+              linear_acted(e, v);
+              res.add(e, row, col0, n, live, v);
+              if (p.tma_store) {
+                tc_store_box(&m.d[0], e.d_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
+              } else if (live && dbg_store_ok(e, row, col0, n)) {
+                store_run32(e.d, e.d_dtype, row * e.ldd + col0, n, v);
+              }
+              continue;
+            }
             if (e.mode == EPI_CE_GRAD) {  // three bf16 planes whose sum is the fp32 gradient, zeros past column N
               ce_grad32<true>(ce_row, e.ce_col0 + col0, v);
 #pragma unroll
@@ -577,6 +614,37 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
               for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
             });
         }
+      }
+      if constexpr (t2_linear(FAM)) {
+        const bool live = row < p.M;
+        for (int c = 0; c < warp_cols / 32; ++c) {
+          const int col0 = nh0 + c * 32;
+          if (col0 >= p.N) break;  // warp-uniform
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(t_row + c * 32, r);
+          tmem_ld_wait();
+          float v[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
+          const int n = min(32, p.N - col0);
+          linear_pre(e, live ? row : 0, col0, n, v);
+          if (e.d2 != nullptr) {
+            if (p.tma_store) {
+              tc_store_box(&m.d[1], e.d2_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
+            } else if (live && dbg_store_ok(e, row, col0, n)) {
+              store_run32(e.d2, e.d2_dtype, row * e.ldd2 + col0, n, v);
+            }
+          }
+          linear_acted(e, v);
+          res.add(e, row, col0, n, live, v);
+          if (c + 1 < warp_cols / 32) res.load(e, row, col0 + 32, min(32, p.N - col0 - 32), live);
+          if (p.tma_store) {
+            tc_store_box(&m.d[0], e.d_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
+          } else if (live && dbg_store_ok(e, row, col0, n)) {
+            store_run32(e.d, e.d_dtype, row * e.ldd + col0, n, v);
+          }
+        }
+        ce_done = true;
       }
       for (int c = 0; !ce_done && c < warp_cols / 32; ++c) {
         const int col0 = nh0 + c * 32;
@@ -752,6 +820,12 @@ static int launch_pair_family(const GemmDesc& g, const T2Maps& m, const T2Params
     if (g.epi.mode != EPI_STORE) return TPS_ERR_ARG;
     return launch_pair_majors<T2_SEG>(g, m, p, pairs, a_mn, b_mn, stream);
   }
+  if (g.epi.mode == EPI_LINEAR) {
+    if (g.planes > 1) return launch_pair_majors<T2_PLANES_LIN>(g, m, p, pairs, a_mn, b_mn, stream);
+    if (g.in_dtype == TPS_E4M3)
+      return a_mn || b_mn ? TPS_ERR_LAYOUT : launch_pair_typed<false, false, T2_LIN8>(g, m, p, pairs, stream);
+    return launch_pair_majors<T2_LIN>(g, m, p, pairs, a_mn, b_mn, stream);
+  }
   if (g.planes > 1) return launch_pair_majors<T2_PLANES>(g, m, p, pairs, a_mn, b_mn, stream);
   if (g.epi.mode == EPI_CE_LSE || g.epi.mode == EPI_CE_GRAD)
     return launch_pair_majors<T2_CE>(g, m, p, pairs, a_mn, b_mn, stream);
@@ -765,7 +839,8 @@ static int launch_pair_family(const GemmDesc& g, const T2Maps& m, const T2Params
 
 // `cols` > 0: the extent of the contiguous dimension, where it is not the operand's own (planes).
 static bool pair_operand_map(CUtensorMap* map, const void* base, bool mn, int64_t K, int64_t MN, int64_t ld,
-                             int box_mn, int64_t cols = 0) {
+                             int box_mn, int64_t cols = 0, bool codes = false) {
+  if (codes) return !mn && tc_make_map8(map, base, MN, K, ld, 2 * TC_BK, box_mn);
   return mn ? tc_make_map(map, base, K, cols > 0 ? cols : MN, ld, 64, TC_BK)       // stored K x MN
             : tc_make_map(map, base, MN, cols > 0 ? cols : K, ld, TC_BK, box_mn);  // stored MN x K
 }
@@ -774,6 +849,7 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   const bool a_mn = (g.a_sk != 1);
   const bool b_mn = (g.b_sk != 1);
   const bool glu = g.epi.mode == EPI_GLU_FWD;
+  const bool codes = g.in_dtype == TPS_E4M3;
   const int64_t ks[3] = {g.K, g.K2, g.K3};
   const void* as[3] = {g.a, g.a2, g.a3};
   const void* bs[3] = {g.b, g.b2, g.b3};
@@ -792,9 +868,10 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   bool ok = true;
   for (int s = 0; s < 3; ++s) {
     if (s > 0 && ks[s] == 0) continue;
-    ok = ok && pair_operand_map(&m.a[s], as[s], a_mn, ks[s], g.M, a_mn ? a_sk[s] : a_sm[s], T2_BM, g.a_cols);
+    ok = ok && pair_operand_map(&m.a[s], as[s], a_mn, ks[s], g.M, a_mn ? a_sk[s] : a_sm[s], T2_BM, g.a_cols, codes);
     if (!n_segs)
-      ok = ok && pair_operand_map(&m.b[s], bs[s], b_mn, ks[s], g.N, b_mn ? b_sk[s] : b_sn[s], T2_BN_CTA, g.b_cols);
+      ok = ok && pair_operand_map(&m.b[s], bs[s], b_mn, ks[s], g.N, b_mn ? b_sk[s] : b_sn[s], T2_BN_CTA, g.b_cols,
+                                  codes);
   }
   if (glu) ok = ok && pair_operand_map(&m.b[1], g.b_up, b_mn, g.K, g.N, b_mn ? g.b_sk : g.b_sn, T2_BN_CTA);
   if (n_segs)
@@ -812,7 +889,8 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   p.n_tiles = static_cast<int>(glu ? (g.N + T2_BN_CTA - 1) / T2_BN_CTA : (g.N + T2_BN - 1) / T2_BN);
   int kt = 0;
   for (int s = 0; s < 3; ++s) {
-    kt += static_cast<int>((ks[s] + TC_BK - 1) / TC_BK);
+    const int64_t bk = codes ? 2 * TC_BK : TC_BK;
+    kt += static_cast<int>((ks[s] + bk - 1) / bk);
     p.k_end[s] = kt;
   }
   p.kt1 = p.a_plane = p.b_plane = p.d_plane = 0;
@@ -857,7 +935,7 @@ int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
   // count of distinct panels, about group + 76 / group, is smallest at 8.
   if (getenv("TPS_GEMM_GROUP") == nullptr) {
     const int64_t k_total = static_cast<int64_t>(g.K) + g.K2 + g.K3;
-    if (16ll * 2 * T2_BM * k_total * 2 <= (40ll << 20)) p.group = 16;
+    if (16ll * 2 * T2_BM * k_total * (codes ? 1 : 2) <= (40ll << 20)) p.group = 16;
   }
   if (p.group < 1) p.group = 1;
   if (p.group > p.m_tiles) p.group = p.m_tiles;

@@ -44,6 +44,10 @@ constexpr uint32_t TPS_DEVERR_BOUNDS = 4u;  // debug builds: a store outside its
 // EPI_CE_LSE   per (row, 128-column tile) the max and the sum of
 //              e^{acc - max}, and per row the logit at its label column
 // EPI_CE_GRAD  D = bf16(g_row (e^{acc - lse_row} - [column = label_row]))
+// Product with bias, activation and residual (CTA-pair, few-row and SIMT
+// kernels):
+// EPI_LINEAR   z = acc row_scale[row] col_scale[column] + bias[column], D2 = z
+//              (may be null), D = act(z) + residual
 enum EpiMode : int {
   EPI_STORE = 0,
   EPI_ACT_FWD = 1,
@@ -53,8 +57,10 @@ enum EpiMode : int {
   EPI_GLU_UP = 5,
   EPI_GLU_BWD = 6,
   EPI_CE_LSE = 7,
-  EPI_CE_GRAD = 8
+  EPI_CE_GRAD = 8,
+  EPI_LINEAR = 9
 };
+constexpr int kActNone = TPS_ACT_NONE;
 
 // Width of the column tiles the CE statistics are kept for (the GEMM
 // epilogue thread that owns a row folds this many columns at a time).
@@ -110,6 +116,15 @@ struct Epilogue {
   // EPI_STORE on the CTA-pair kernels (no segments, no planes): a device
   // float that multiplies the product, nullptr: 1.
   const float* alpha = nullptr;
+  // EPI_LINEAR: each may be null; act may be kActNone.  The residual may be D
+  // itself: every element is read by the thread that stores it, before.
+  const float* row_scale = nullptr;
+  const float* col_scale = nullptr;
+  const void* bias = nullptr;
+  int bias_dtype = TPS_F32;
+  const void* res = nullptr;
+  int64_t ld_res = 0;
+  int res_dtype = TPS_F32;
   // Debug builds: the output's extent (rows, columns) and the error word the
   // bounds checks report to.
   int64_t dbg_rows = 0, dbg_cols = 0;
@@ -228,6 +243,11 @@ int launch_gemm_tc1(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream); 
 int launch_gemm_tc2(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream);  // CTA pairs
 int launch_gemm_simt(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream);
 int launch_gemm_wide(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream);  // wide CTA-pair tiles
+int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream);  // few rows (gemm_rows.cu)
+bool gemm_rows_supported(const GemmDesc& g);
+bool gemm_rows_preferred(const GemmDesc& g);  // over CTA pairs, for a supported call
+int launch_gemm_few(const GemmDesc& g, cudaStream_t stream);  // fp32, up to eight rows (gemm_rows.cu)
+bool gemm_few_supported(const GemmDesc& g);
 bool gemm_wide_supported(const GemmDesc& g);
 bool gemm_tc_supported(const GemmDesc& g);
 

@@ -47,6 +47,7 @@
 #include <mutex>
 
 #include "api_common.cuh"
+#include "operand.cuh"
 #include "ptx.cuh"
 
 namespace tps {
@@ -236,46 +237,6 @@ __global__ void __launch_bounds__(1024) ce_rows_kernel(int64_t T, Labels lab, co
     const float l = lse[t];
     rows[t] = make_float4(l * kCeLog2e, kind == 1 ? 0.0f : (alpha != nullptr ? __fdiv_rn(up, common) : up),
                           __int_as_float(kind == 0 ? static_cast<int>(y) : -1), l);
-  }
-}
-
-// Lays an operand out for TMA: rows x cols of bf16, or three planes of an
-// fp32 one side by side, each `plane` columns with zeros from `cols` on.
-// Plane 1 holds what plane 0's rounding left, plane 2 what both left: exactly
-// the value, unless its last bits are below bf16's smallest number.
-template <class T>
-__global__ void __launch_bounds__(256) ce_lay_kernel(const T* src, int64_t rows, int64_t cols, int64_t ld,
-                                                     __nv_bfloat16* dst, int64_t plane) {
-  constexpr int kPlanes = sizeof(T) == 4 ? 3 : 1;
-  const int64_t per = plane / 8;
-  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < rows * per; i += int64_t(gridDim.x) * 256) {
-    const int64_t r = i / per, c = (i - r * per) * 8;
-    const T* p = src + r * ld + c;
-    T x[8];
-    if (c + 8 <= cols && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
-#pragma unroll
-      for (int q = 0; q < static_cast<int>(sizeof(x)) / 16; ++q) reinterpret_cast<uint4*>(x)[q] = reinterpret_cast<const uint4*>(p)[q];
-    } else {
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = c + j < cols ? p[j] : T(0.0f);
-    }
-    __nv_bfloat16* out = dst + r * kPlanes * plane + c;
-    if constexpr (kPlanes == 1) {
-      *reinterpret_cast<uint4*>(out) = *reinterpret_cast<const uint4*>(x);
-    } else {
-#pragma unroll
-      for (int pl = 0; pl < 3; ++pl) {
-        __align__(16) __nv_bfloat16 b[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          b[j] = __float2bfloat16_rn(x[j]);
-          if (__hisinf(b[j]) && isfinite(x[j])) b[j] = __float2bfloat16_rz(x[j]);
-          // infinities and NaN stay in plane 0, whose product alone decides about them (T2Drains)
-          x[j] = isfinite(x[j]) ? x[j] - __bfloat162float(b[j]) : 0.0f;
-        }
-        *reinterpret_cast<uint4*>(out + pl * plane) = *reinterpret_cast<const uint4*>(b);
-      }
-    }
   }
 }
 
@@ -561,23 +522,11 @@ int check_call(const tps_tensor* h, const tps_tensor* Whead, const tps_tensor* l
   return TPS_OK;
 }
 
-int64_t round_up(int64_t x, int64_t m) { return (x + m - 1) / m * m; }
-
-// An operand X(i, j) as the GEMMs take it: the caller's, or laid out anew.
-struct Operand {
-  const char* p = nullptr;
-  int64_t si = 0, sj = 0;         // strides of i and j, one of them 1
-  int64_t plane = 0, cols = 0;    // GemmDesc::a_plane, a_cols when laid out
-};
 struct Layout {  // of all operands of a call
   bool direct = true;  // bf16 as TMA takes it
   int planes = 1;
 };
 
-bool tma_can(const void* p, int64_t si, int64_t sj) {
-  const int64_t outer = sj == 1 ? si : sj;
-  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0 && (si == 1 || sj == 1) && outer % 8 == 0;
-}
 Layout layout_of(const Call& c) {
   Layout l;
   l.planes = c.dt == TPS_F32 ? 3 : 1;
@@ -588,39 +537,15 @@ Layout layout_of(const Call& c) {
   l.direct = c.dt == TPS_BF16 && tma_can(g.a, g.a_sm, g.a_sk) && tma_can(g.b, g.b_sk, g.b_sn) && gemm_tc_supported(g);
   return l;
 }
-// Bytes of X (ni x nj) laid out, in either orientation.
-int64_t laid_bytes(int64_t ni, int64_t nj, int planes) {
-  const int64_t a = ni * round_up(nj, 64), b = nj * round_up(ni, 64);
-  return 2 * planes * (a > b ? a : b);
-}
-
 int launched(const char* what) {
   note_launch();
   const cudaError_t e = cudaPeekAtLastError();
   return e == cudaSuccess ? TPS_OK : fail(TPS_ERR_CUDA, "%s: launch failed: %s", what, cudaGetErrorString(cudaGetLastError()));
 }
 
-// X (ni x nj, strides si, sj, of the call's dtype) laid out at `dst`.
 int lay_out(const Call& c, const char* src, int64_t ni, int64_t nj, int64_t si, int64_t sj, char* dst, cudaStream_t s,
             Operand* o) {
-  const bool j_inner = sj == 1;
-  const int64_t rows = j_inner ? ni : nj, cols = j_inner ? nj : ni, ld = j_inner ? si : sj;
-  const int64_t plane = round_up(cols, 64), blocks = (rows * plane / 8 + 255) / 256;
-  const int planes = c.dt == TPS_F32 ? 3 : 1;
-  const unsigned grid = static_cast<unsigned>(blocks < 152 * 16 ? blocks : 152 * 16);
-  ProfScope prof("ce_lay", "lce", 0.0, double(rows) * (double(cols) * (c.dt == TPS_F32 ? 4 : 2) + 2.0 * planes * double(plane)), s);
-  if (planes == 3)
-    ce_lay_kernel<float><<<grid, 256, 0, s>>>(reinterpret_cast<const float*>(src), rows, cols, ld,
-                                              reinterpret_cast<__nv_bfloat16*>(dst), plane);
-  else
-    ce_lay_kernel<__nv_bfloat16><<<grid, 256, 0, s>>>(reinterpret_cast<const __nv_bfloat16*>(src), rows, cols, ld,
-                                                      reinterpret_cast<__nv_bfloat16*>(dst), plane);
-  o->p = dst;
-  o->si = j_inner ? planes * plane : 1;
-  o->sj = j_inner ? 1 : planes * plane;
-  o->plane = plane;
-  o->cols = planes * plane;
-  return launched("ce_lay");
+  return lay_operand(c.dt, src, ni, nj, si, sj, dst, "lce", s, o);
 }
 // The piece [v0, v0 + n) of Whead as Operand(d, v).
 int head_piece(const Call& c, const Layout& l, int64_t v0, int64_t n, char* room, cudaStream_t s, Operand* o) {
@@ -634,13 +559,6 @@ int hidden(const Call& c, const Layout& l, char* room, cudaStream_t s, Operand* 
   if (!l.direct) return lay_out(c, static_cast<const char*>(c.h.data), c.T, c.d, c.h.sr, c.h.sc, room, s, o);
   *o = Operand{static_cast<const char*>(c.h.data), c.h.sr, c.h.sc, 0, 0};
   return TPS_OK;
-}
-// A(m, k) = X(i, j) or, transposed, X(j, i); B(k, n) alike.
-void set_a(GemmDesc* g, const Operand& x, bool t) {
-  g->a = x.p; g->a_sm = t ? x.sj : x.si; g->a_sk = t ? x.si : x.sj; g->a_plane = x.plane; g->a_cols = x.cols;
-}
-void set_b(GemmDesc* g, const Operand& x, bool t) {
-  g->b = x.p; g->b_sk = t ? x.sj : x.si; g->b_sn = t ? x.si : x.sj; g->b_plane = x.plane; g->b_cols = x.cols;
 }
 GemmDesc gemm_of(const char* name, const Layout& l, int64_t M, int64_t N, int64_t K) {
   GemmDesc g;

@@ -120,6 +120,24 @@ __device__ __forceinline__ void tc_store_chunk(const Epilogue& e, const CUtensor
   }
 }
 
+// One 32 x 32 box of v (lane = row) through one of the warp's two staging
+// buffers, for the kernels that store several boxes a chunk.
+__device__ __forceinline__ void tc_store_box(const CUtensorMap* map, int dtype, uint8_t* buf, int lane, int row0,
+                                             int col0, const float (&v)[32]) {
+  if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+  __syncwarp();
+  if (dtype == TPS_F32)
+    stage_f32_sw128(buf, lane, v);
+  else
+    stage_bf16_sw64(buf, lane, v);
+  fence_async_smem();
+  __syncwarp();
+  if (lane == 0) {
+    tma_store_2d(map, buf, col0, row0);
+    bulk_commit();
+  }
+}
+
 // EPI_GLU_BWD chunk through TMA stores, double-buffered like
 // tc_store_chunk<1>: dHg = v * U * phi'(Hg) leaves from the bf16 slot and
 // dU = v * phi(Hg) from the start of the fp32 slot, both as bf16 boxes.
@@ -535,6 +553,9 @@ __device__ __forceinline__ void tma_load_maybe_hint(void* dst, const CUtensorMap
 // box_cols x box_rows box, 128-byte swizzle, zero fill out of bounds.
 bool tc_make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                  int box_rows);
+// The same of e4m3 operands (box_cols: 128, one swizzle row).
+bool tc_make_map8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                  int box_rows);
 // Row-major output view (fp32 or bf16) with a 32 x 32 box whose swizzle
 // matches the staging layout.
 bool tc_make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int dtype);

@@ -99,7 +99,8 @@ enum { TPS_AXIS_ROWS = 0, TPS_AXIS_COLUMNS = 1, TPS_AXIS_INNER = 2 };
  *   TANH     : tanh, with phi' = 1 - H^2 as [MC] "02 / BACKWARD" writes.
  *   SILU     : x sigma(x), one of the element-wise activations [TP] core
  *              concept 2.A step 3 names (SwiGLU's gate). */
-enum { TPS_ACT_GELU_ERF = 0, TPS_ACT_GELU_TANH = 1, TPS_ACT_TANH = 2, TPS_ACT_SILU = 3 };
+enum { TPS_ACT_GELU_ERF = 0, TPS_ACT_GELU_TANH = 1, TPS_ACT_TANH = 2, TPS_ACT_SILU = 3,
+       TPS_ACT_NONE = -1 /* tps_linear_fwd, tps_linear_bwd: no activation */ };
 
 /* Weight layouts.  IN_OUT: W1 is d x F and W2 is F x d (math notation
  * Y = phi(X W1) W2 of [MC] "01 / COLUMN THEN ROW").  OUT_IN: torch
@@ -470,6 +471,45 @@ int tps_dropout_fwd(const tps_tensor* X, const tps_tensor* residual, const tps_d
                     void* cuda_stream);
 int tps_dropout_bwd(const tps_tensor* dY, const tps_dropout* dropout, const tps_tensor* dX, void* cuda_stream);
 int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor* scale, void* cuda_stream);
+
+/* ------------------------------------------------------------------------
+ * tps_linear_fwd / tps_linear_bwd -- one matrix product with what stands
+ * around it fused into its epilogue ([SG] "解题路线" step 1 gives the
+ * product and its gradients; bias, activation and residual are the usual ones):
+ *   z = X W + bias,  y = act(z) + residual;
+ *   dz = dy act'(z),  dX = dz W^T,  dW = X^T dz,  dbias = sum over rows of dz.
+ * X (..., K); W: K x N (TPS_W_IN_OUT) or N x K (TPS_W_OUT_IN); both F32, both
+ * BF16, or (forward) both E4M3 with x_scale (T floats) and w_scale (N floats),
+ * one for each row as tps_quantize_e4m3 gives them:
+ *   z = x_scale_t w_scale_n (X W) + bias;
+ * E4M3 weights are TPS_W_OUT_IN, and rows of both start on 16 bytes
+ * (TPS_ERR_LAYOUT otherwise).  bias (N) and residual (..., N) may be NULL.
+ * act: TPS_ACT_*, TPS_ACT_NONE for none.  Y (..., N); Z (..., N) or NULL: the
+ * pre-activation, which the backward pass needs when there is an activation.
+ * bias, residual, Y, Z: F32 or BF16, each of its own; rows of unit stride, any
+ * pitch.  Y may be the residual itself; otherwise outputs overlap nothing.
+ * Sums and the epilogue are fp32 (fp32 operands to fp32's precision, also where
+ * they pass the tensor cores as three bf16 values each); Y and Z are rounded
+ * once.  Backward: dY and Z F32 or BF16 (Z NULL without an activation); dX,
+ * dW, dbias F32 or BF16, each of its own, each may be NULL.  dz is rounded to
+ * the operands' type where it enters the products; dbias sums it unrounded, in
+ * a fixed order.  The residual's gradient is dY itself.
+ * `workspace`: 256-byte aligned.  tps_linear_workspace_bytes gives what a call
+ * of F32 or BF16 operands needs at most (0: none, as for E4M3); BF16 operands
+ * that TMA cannot describe (a base or a row pitch that is not a multiple of 16
+ * bytes) are laid out there and need the bytes given for TPS_F32; a call that
+ * needs more than it was given is refused with TPS_ERR_WORKSPACE before
+ * anything is launched.  K, N >= 1; extents below 2^31, 2^29 for F32.  Both may
+ * be captured into a CUDA graph.
+ * ---------------------------------------------------------------------- */
+int tps_linear_fwd(const tps_tensor* X, const tps_tensor* W, const tps_tensor* bias, const tps_tensor* residual,
+                   int32_t act, int32_t weight_layout, const tps_tensor* x_scale, const tps_tensor* w_scale,
+                   const tps_tensor* Z, const tps_tensor* Y, void* workspace, size_t workspace_bytes,
+                   void* cuda_stream);
+int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tps_tensor* dY, const tps_tensor* Z, int32_t act,
+                   int32_t weight_layout, const tps_tensor* dX, const tps_tensor* dW, const tps_tensor* dbias,
+                   void* workspace, size_t workspace_bytes, void* cuda_stream);
+size_t tps_linear_workspace_bytes(int64_t T, int64_t K, int64_t N, int32_t dtype, int32_t backward);
 
 /* ------------------------------------------------------------------------
  * Rotary positions of the query and key heads, between tps_attn_qkv_fwd and
