@@ -1,4 +1,5 @@
-"""ctypes binding of libtps.so (include/tps.h).
+"""Python binding of libtps.so (include/tps.h), through ctypes; the short calls
+(norm, dropout, linear product) through the extension of csrc/binding.cpp.
 
 Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  Tensors must be CUDA tensors on the current device;
@@ -32,7 +33,6 @@ LINEAR_ACTS = {**ACTS, None: -1}
 LAYOUTS = {"in_out": 0, "out_in": 1}
 
 _DTYPES = {torch.float32: F32, torch.bfloat16: BF16, torch.int32: I32, torch.int64: I64}
-_CODE_DTYPES = {**_DTYPES, torch.float8_e4m3fn: E4M3}  # where e4m3 numbers may stand
 _STATE_DTYPES = {torch.float32: F32, torch.float8_e4m3fn: E4M3}
 
 
@@ -140,16 +140,16 @@ def library():
     lib.tps_grad_norm.argtypes = [vp, i32, ctypes.c_double, vp, vp, sz, vp]
     lib.tps_grad_norm_workspace_bytes.argtypes = [i32]
     lib.tps_grad_norm_workspace_bytes.restype = sz
-    D = ctypes.c_char_p  # a tps_dropout packed by _dropout
+    D = ctypes.c_char_p  # a tps_dropout as bytes
     lib.tps_rmsnorm_fwd.argtypes = [V, V, V, ctypes.c_double, D, V, V, V, V, vp]
     lib.tps_rmsnorm_bwd.argtypes = [V, V, V, V, V, D, V, V, V, vp, sz, vp]
-    lib.tps_rmsnorm_workspace_bytes.argtypes = [i64, i64]
-    lib.tps_rmsnorm_workspace_bytes.restype = sz
     lib.tps_dropout_fwd.argtypes = [V, V, D, V, vp]
     lib.tps_dropout_bwd.argtypes = [V, D, V, vp]
     lib.tps_quantize_e4m3.argtypes = [V, V, V, vp]
     lib.tps_linear_fwd.argtypes = [V, V, V, V, i32, i32, V, V, V, V, vp, sz, vp]
     lib.tps_linear_bwd.argtypes = [V, V, V, V, i32, i32, V, V, V, vp, sz, vp]
+    lib.tps_rmsnorm_workspace_bytes.argtypes = [i64, i64]
+    lib.tps_rmsnorm_workspace_bytes.restype = sz
     lib.tps_linear_workspace_bytes.argtypes = [i64, i64, i64, i32, i32]
     lib.tps_linear_workspace_bytes.restype = sz
     lib.tps_last_device_error.argtypes = [vp]
@@ -164,6 +164,28 @@ def library():
     lib.tps_launch_count.restype = i64
     _lib = lib
     return lib
+
+
+_fast = None
+_FAST_ENTRIES = ("tps_rmsnorm_fwd", "tps_rmsnorm_bwd", "tps_rmsnorm_workspace_bytes", "tps_dropout_fwd",
+                 "tps_dropout_bwd", "tps_quantize_e4m3", "tps_linear_fwd", "tps_linear_bwd",
+                 "tps_linear_workspace_bytes")  # in the order of Entries in csrc/binding.cpp
+
+
+def _native():
+    """The extension behind norm, dropout and the linear product, calling the
+    library that is loaded."""
+    global _fast
+    if _fast is None:
+        lib = library()
+        try:
+            from . import _binding
+        except ImportError as e:
+            raise RuntimeError(f"_binding.so is not built or does not fit the installed torch ({e}); run "
+                               "`python -m backward_tcgen05_tma_gemms_gb300.build` first") from e
+        _binding.init(*(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in _FAST_ENTRIES))
+        _fast = _binding
+    return _fast
 
 
 # --------------------------------------------------------------------- helpers
@@ -198,7 +220,7 @@ _VIEW = struct.Struct("=Qii8q")  # tps_tensor
 _PAD = (0, 0, 0, 0)
 
 
-def _view(t: Optional[torch.Tensor], dtypes=_DTYPES):
+def _view(t: Optional[torch.Tensor]):
     """tps_tensor view of a CUDA tensor as bytes (None -> NULL): the same
     checks as _tt, packed in one step for the short calls."""
     if t is None:
@@ -207,7 +229,7 @@ def _view(t: Optional[torch.Tensor], dtypes=_DTYPES):
         raise TypeError("expected a torch.Tensor")
     if not t.is_cuda:
         raise ValueError("tensors must live on the GPU (no CPU path)")
-    code = dtypes.get(t.dtype)
+    code = _DTYPES.get(t.dtype)
     if code is None:
         raise TypeError(f"unsupported dtype {t.dtype}")
     n = t.dim()
@@ -657,37 +679,6 @@ def rope_bwd(plan: RopePlan, dq: torch.Tensor, dk: Optional[torch.Tensor], posit
 
 # --------------------------------------------------------------------- norm and dropout
 
-_DROPOUT = struct.Struct("=dQQQ")  # tps_dropout
-
-
-def _dropout(p: float, seed, site: int, like: torch.Tensor):
-    """tps_dropout as bytes, None for none.  seed: a number, or one int64 on
-    `like`'s GPU."""
-    if p == 0.0:
-        return None
-    if isinstance(seed, torch.Tensor):
-        if seed.dtype != torch.int64 or seed.numel() != 1:
-            raise ValueError("seed: one int64")
-        if seed.get_device() != like.get_device():
-            raise ValueError("seed on another GPU than the tensors")
-        return _DROPOUT.pack(p, 0, seed.data_ptr(), site & (2 ** 64 - 1))
-    return _DROPOUT.pack(p, seed & (2 ** 64 - 1), 0, site & (2 ** 64 - 1))
-
-
-def _one_gpu(*tensors):
-    """Everything on the current GPU, where the kernels are going to run."""
-    here = {t.get_device() for t in tensors if t is not None}
-    if -1 in here:
-        raise ValueError("tensors must live on the GPU (no CPU path)")
-    if here != {torch.cuda.current_device()}:
-        raise ValueError("tensors on different GPUs" if len(here) > 1 else "tensors on another GPU than the current one")
-
-
-def _rows(t: Optional[torch.Tensor]):
-    """A vector as one row."""
-    return t if t is None or t.dim() != 1 else t.unsqueeze(0)
-
-
 def rmsnorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual: Optional[torch.Tensor] = None,
                 eps: float = 1e-6, dropout: float = 0.0, seed=0, site: int = 0,
                 out_dtype: Optional[torch.dtype] = None, out: Optional[Sequence] = None):
@@ -699,27 +690,8 @@ def rmsnorm_fwd(x: torch.Tensor, weight: Optional[torch.Tensor] = None, residual
     seed: a number, or one int64 on the GPU, which a captured CUDA graph reads
     at every replay; site: which dropout of the model this is.  `out` may
     supply the four; h may be the residual and y may be x."""
-    if out is not None:
-        y, scale, h, rstd = out
-    else:
-        T = x.shape[:-1]
-        y = torch.empty_like(x, dtype=out_dtype, memory_format=torch.contiguous_format)
-        scale = torch.empty(T, dtype=torch.float32, device=x.device) if y.dtype == torch.float8_e4m3fn else None
-        h = None
-        if residual is not None or dropout != 0.0:
-            h = torch.empty_like(x if residual is None else residual, memory_format=torch.contiguous_format)
-        rstd = torch.empty(T, dtype=torch.float32, device=x.device)
-    _one_gpu(x, weight, residual, y, scale, h, rstd)
-    _check(library().tps_rmsnorm_fwd(_view(_rows(x)), _view(_rows(residual)), _view(weight), eps,
-                                     _dropout(dropout, seed, site, x), _view(_rows(h)),
-                                     _view(_rows(y), _CODE_DTYPES), _flat(scale),
-                                     _flat(rstd), _raw_stream(x)))
-    return y, scale, h, rstd
-
-
-def _flat(t: Optional[torch.Tensor]):
-    """One number a row, whatever the shape of the rows."""
-    return None if t is None else _view(t.reshape(-1) if t.is_contiguous() else t)
+    r = (_fast or _native()).rmsnorm_fwd(x, weight, residual, eps, dropout, seed, site, out_dtype, out)
+    return r if type(r) is tuple else _check(r)
 
 
 def rmsnorm_workspace_bytes(T: int, d: int) -> int:
@@ -735,30 +707,9 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor
     dx has x_dtype (h's by default), dresidual h's type; without dropout and
     with one type the two are one tensor.  dweight is fp32.  dropout, seed and
     site as in the forward call.  `out` may supply the three."""
-    if out is not None:
-        dx, dres, dw = out
-    else:
-        dres = torch.empty_like(h, memory_format=torch.contiguous_format)
-        dx = dres
-        if dropout != 0.0 or (x_dtype or h.dtype) != h.dtype:
-            dx = torch.empty_like(dres, dtype=x_dtype or h.dtype)
-        dw = None
-        if want_dweight:
-            dw = torch.empty(h.shape[-1], dtype=torch.float32, device=h.device)
-    _one_gpu(dy, h, weight, rstd, dh, dx, dres, dw, workspace)
-    lib = library()
-    room = (None, 0)
-    if dw is not None:
-        if workspace is None:
-            d = h.shape[-1]
-            need = int(lib.tps_rmsnorm_workspace_bytes(h.numel() // d if d else 0, d))
-            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=h.device)
-        room = _room(workspace)
-    second = None if dx is dres and dropout == 0.0 else _view(_rows(dx))
-    _check(lib.tps_rmsnorm_bwd(_view(_rows(dy)), _view(_rows(h)), _view(weight), _flat(rstd), _view(_rows(dh)),
-                               _dropout(dropout, seed, site, h), _view(_rows(dres)), second, _view(dw), *room,
-                               _raw_stream(h)))
-    return dx, dres, dw
+    r = (_fast or _native()).rmsnorm_bwd(dy, h, weight, rstd, dh, dropout, seed, site, x_dtype, want_dweight, workspace,
+                                         out)
+    return r if type(r) is tuple else _check(r)
 
 
 def dropout_fwd(x: torch.Tensor, p: float, seed, site: int = 0, residual: Optional[torch.Tensor] = None,
@@ -766,41 +717,23 @@ def dropout_fwd(x: torch.Tensor, p: float, seed, site: int = 0, residual: Option
     """x with each element dropped with probability p (in steps of 2^-16) and
     multiplied by 1 / (1 - p) otherwise, plus the residual.  The mask is a
     function of seed, site and the element's place, and is not stored."""
-    if out is None:
-        out = torch.empty_like(x, memory_format=torch.contiguous_format)
-    _one_gpu(x, residual, out)
-    _check(library().tps_dropout_fwd(_view(_rows(x)), _view(_rows(residual)), _dropout_always(p, seed, site, x),
-                                     _view(_rows(out)), _raw_stream(x)))
-    return out
+    r = (_fast or _native()).dropout(x, p, seed, site, residual, out, False)
+    return _check(r) if type(r) is int else r
 
 
 def dropout_bwd(dy: torch.Tensor, p: float, seed, site: int = 0, out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The gradient of dropout_fwd's x from that of its result (which is the
     residual's too)."""
-    if out is None:
-        out = torch.empty_like(dy, memory_format=torch.contiguous_format)
-    _one_gpu(dy, out)
-    _check(library().tps_dropout_bwd(_view(_rows(dy)), _dropout_always(p, seed, site, dy), _view(_rows(out)),
-                                     _raw_stream(dy)))
-    return out
-
-
-def _dropout_always(p, seed, site, like):
-    return _dropout(p, seed, site, like) or _DROPOUT.pack(p, 0, 0, 0)
+    r = (_fast or _native()).dropout(dy, p, seed, site, None, out, True)
+    return _check(r) if type(r) is int else r
 
 
 def quantize_e4m3(x: torch.Tensor, out: Optional[Sequence] = None):
     """(q, scale): the rows of x (..., d) as e4m3 numbers, the largest
     magnitude of each row being 448, and one fp32 scale for each row:
     x = q scale."""
-    if out is not None:
-        q, scale = out
-    else:
-        q = torch.empty_like(x, dtype=torch.float8_e4m3fn, memory_format=torch.contiguous_format)
-        scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
-    _one_gpu(x, q, scale)
-    _check(library().tps_quantize_e4m3(_view(_rows(x)), _view(_rows(q), _CODE_DTYPES), _flat(scale), _raw_stream(x)))
-    return q, scale
+    r = (_fast or _native()).quantize_e4m3(x, out)
+    return r if type(r) is tuple else _check(r)
 
 
 # --------------------------------------------------------------------- product with its epilogue
@@ -808,32 +741,14 @@ def quantize_e4m3(x: torch.Tensor, out: Optional[Sequence] = None):
 def linear_workspace_bytes(T: int, K: int, N: int, dtype: torch.dtype, backward: bool) -> int:
     """Workspace bytes of linear_fwd / linear_bwd for operands of `dtype`; bf16
     operands that are not 16-byte aligned need those of fp32."""
-    return int(library().tps_linear_workspace_bytes(T, K, N, _CODE_DTYPES[dtype], 1 if backward else 0))
+    code = E4M3 if dtype == torch.float8_e4m3fn else _DTYPES[dtype]
+    return int(library().tps_linear_workspace_bytes(T, K, N, code, 1 if backward else 0))
 
 
-def _linear_call(fn, T, K, N, x, backward, workspace):
-    """Run fn(workspace pointer, bytes) with the given workspace, or with one
-    for aligned operands; others are refused before any launch and run again
-    with the size that holds them laid out."""
-    if workspace is not None:
-        _check(fn(*_room(workspace)))
-        return
-    for dt in (x.dtype, torch.float32):
-        n = linear_workspace_bytes(T, K, N, dt, backward)
-        ws = torch.empty(n, dtype=torch.uint8, device=x.device) if n else None
-        rc = fn(ws.data_ptr() if n else None, n)
-        if rc != ERR_WORKSPACE:
-            break
-    _check(rc)
-
-
-def _linear_args(x, W, act, weight_layout):
+def _linear_codes(act, weight_layout):
     if act not in LINEAR_ACTS or weight_layout not in LAYOUTS:
         raise ValueError("argument")
-    if W.dim() != 2:
-        raise ValueError("shape")
-    K = x.shape[-1]
-    return (x.numel() // K if K else 0), K, W.shape[1] if weight_layout == "in_out" else W.shape[0]
+    return LINEAR_ACTS[act], LAYOUTS[weight_layout]
 
 
 def linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = None,
@@ -846,20 +761,10 @@ def linear_fwd(x: torch.Tensor, W: torch.Tensor, bias: Optional[torch.Tensor] = 
     linear_bwd needs, only with want_pre.  x and W are fp32, bf16, or e4m3 with
     x_scale and w_scale, one for each row of x and of W (quantize_e4m3), W then
     being (out, in).  `out` may supply (y, z); y may be the residual."""
-    T, K, N = _linear_args(x, W, act, weight_layout)
-    if out is not None:
-        y, z = out
-    else:
-        dt = out_dtype or (torch.bfloat16 if x.dtype == torch.float8_e4m3fn else x.dtype)
-        y = torch.empty(*x.shape[:-1], N, dtype=dt, device=x.device)
-        z = torch.empty_like(y) if want_pre else None
-    _one_gpu(x, W, bias, residual, x_scale, w_scale, y, z, workspace)
-    a = (_view(_rows(x), _CODE_DTYPES), _view(W, _CODE_DTYPES), _view(bias), _view(_rows(residual)))
-    b = (_flat(x_scale), _flat(w_scale), _view(_rows(z)), _view(_rows(y)))
-    stream = _raw_stream(x)
-    _linear_call(lambda ws, n: library().tps_linear_fwd(*a, LINEAR_ACTS[act], LAYOUTS[weight_layout], *b, ws, n, stream),
-                 T, K, N, x, False, workspace)
-    return y, z
+    a, layout = _linear_codes(act, weight_layout)
+    r = (_fast or _native()).linear_fwd(x, W, bias, residual, a, layout, x_scale, w_scale, want_pre, out_dtype, workspace,
+                                        out)
+    return r if type(r) is tuple else _check(r)
 
 
 def linear_bwd(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, pre: Optional[torch.Tensor] = None,
@@ -869,20 +774,9 @@ def linear_bwd(x: torch.Tensor, W: torch.Tensor, dy: torch.Tensor, pre: Optional
     """Gradients of linear_fwd's x, W and bias from that of its y (which is the
     residual's too): (dx, dW, dbias) in `grad_dtype` (fp32 or bf16), None for
     one that is not wanted.  pre: the pre-activation, with an activation."""
-    T, K, N = _linear_args(x, W, act, weight_layout)
-    if out is not None:
-        dx, dW, db = out
-    else:
-        dx = torch.empty(x.shape, dtype=grad_dtype, device=x.device) if want_dx else None
-        dW = torch.empty(W.shape, dtype=grad_dtype, device=x.device) if want_dw else None
-        db = torch.empty(N, dtype=grad_dtype, device=x.device) if want_dbias else None
-    _one_gpu(x, W, dy, pre, dx, dW, db, workspace)
-    a = (_view(_rows(x)), _view(W), _view(_rows(dy)), _view(_rows(pre)))
-    b = (_view(_rows(dx)), _view(dW), _view(db))
-    stream = _raw_stream(x)
-    _linear_call(lambda ws, n: library().tps_linear_bwd(*a, LINEAR_ACTS[act], LAYOUTS[weight_layout], *b, ws, n, stream),
-                 T, K, N, x, True, workspace)
-    return dx, dW, db
+    a, layout = _linear_codes(act, weight_layout)
+    r = (_fast or _native()).linear_bwd(x, W, dy, pre, a, layout, want_dx, want_dw, want_dbias, grad_dtype, workspace, out)
+    return r if type(r) is tuple else _check(r)
 
 
 # --------------------------------------------------------------------- optimizer step

@@ -3,7 +3,9 @@
 Each translation unit in csrc/ is compiled by nvcc for sm_103a in parallel,
 then linked into a shared library with the CUDA runtime linked statically,
 so loading the library needs no GPU and no libcuda at load time (the driver
-entry points are resolved through the runtime on first use).
+entry points are resolved through the runtime on first use).  Beside it the
+CPython extension _binding.so (csrc/binding.cpp), the Python side of the
+short calls, is compiled by the host compiler against the installed torch.
 
 `debug=True` builds libtps_debug.so instead (TPS_DEBUG=1: every direct store
 of the GEMMs' epilogues and of the vocabulary-sharded cross-entropy is checked
@@ -20,6 +22,7 @@ import argparse
 import os
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -28,6 +31,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtps.so")
+BINDING = os.path.join(PKG, "_binding.so")
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libtps_debug.so")
 
@@ -62,19 +66,43 @@ def _compile(src: str, extra, build_dir: str = BUILD) -> str:
     return obj
 
 
+def _compile_binding() -> None:
+    import torch
+    at = os.path.dirname(torch.__file__)
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I", INCLUDE, "-isystem", os.path.join(at, "include"), "-isystem", sysconfig.get_paths()["include"],
+           "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
+           "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           f"-Wl,-rpath,{os.path.join(at, 'lib')}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
-    """Compile and link libtps.so (libtps_debug.so with debug=True) if any
-    source is newer than it; return its path."""
+    """Compile and link libtps.so (libtps_debug.so with debug=True) and the
+    extension if any source is newer than they; return the library's path."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
-    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+
+    def current(path):
+        return not force and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
+    if current(lib):
+        if not current(BINDING):
+            _compile_binding()
         return lib
     os.makedirs(build_dir, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     if debug:
         extra += ["-DTPS_DEBUG=1"]
     srcs = sources()
-    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs), os.cpu_count() or 1))) as ex:
+    with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
+        binding = None if current(BINDING) else ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
+        if binding is not None:
+            binding.result()
     tmp = lib + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-Xcompiler", "-fPIC", "-cudart", "static", *objs, "-o", tmp]
     r = subprocess.run(cmd, capture_output=True, text=True)

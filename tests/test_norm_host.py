@@ -1,10 +1,8 @@
 """The generator behind the dropout mask against its published vectors, and
 refusals of the norm, dropout and e4m3 rows: decided on the host, before any launch."""
-import ctypes
 import math
 import struct
 
-import numpy as np
 import pytest
 import torch
 
@@ -139,9 +137,10 @@ def test_binding_refusals(lib):  # noqa: F811
                  lambda: api.rmsnorm_bwd(x, x, None, torch.zeros(4))):
         with pytest.raises(ValueError, match="no CPU path"):
             call()
-    with pytest.raises(ValueError, match="seed"):
-        api._dropout(0.5, torch.zeros(2, dtype=torch.int64), 0, x)
-    with pytest.raises(ValueError, match="seed"):
-        api._dropout(0.5, torch.zeros(1), 0, x)
-    assert np.frombuffer(api._dropout(0.5, -1, -2, x)[8:], np.uint64).tolist() == [2 ** 64 - 1, 0, 2 ** 64 - 2]
-    assert ctypes.sizeof(ctypes.c_double) + 24 == len(api._dropout(0.5, 1, 2, x))
+    for seed in (torch.zeros(2, dtype=torch.int64), torch.zeros(1)):
+        with pytest.raises(ValueError, match="seed"):
+            api.dropout_fwd(x, 0.5, seed)
+    for call in (lambda: api.rmsnorm_fwd(None), lambda: api.rmsnorm_fwd(x, weight=3), lambda: api.dropout_fwd(x, 0.5, "1"),
+                 lambda: api.quantize_e4m3([1.0]), lambda: api.rmsnorm_fwd(x, out_dtype="f32")):
+        with pytest.raises((TypeError, ValueError)):
+            call()
