@@ -10,18 +10,21 @@
 // it, differentiates what the forward pass computed.
 //
 // All of it is bound by memory.  A row passes through the registers of a group
-// of threads once, 16 bytes a load, and the group joins its sums by shuffles
-// and one round through shared memory; blocks walk the rows, and the loads of
-// the next row are issued before the sums of the present one.  The weights,
-// and in the backward pass the sums of dw, lie in shared memory as floats.  The
-// e4m3 output needs the largest |h w| of the row, which is reduced together
-// with the sum of squares: the codes do not depend on r.
+// of threads once, and the group joins its sums by shuffles and one round
+// through shared memory.  Many rows: blocks walk them, and bulk copies keep a
+// ring of the next rows in shared memory full, whatever the threads wait for
+// (loads into registers, also those of the next row ahead of the sums, left the
+// memory idle during the joins: 8192 x 4096 with residual in 52 us).  Few rows:
+// a block a row, loads into registers.  The e4m3 output needs the largest |h w|
+// of the row, which is reduced together with the sum of squares: the codes do
+// not depend on r.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 #include <cmath>
 
 #include "api_common.cuh"
+#include "ptx.cuh"
 #include "rows.cuh"
 #include "rows_host.cuh"
 
@@ -31,9 +34,11 @@ namespace {
 
 constexpr int kMaxGroup = 512;     // threads of a row at most
 constexpr int kMaxWarps = kMaxGroup / 32;
-constexpr int kLongThreads = 512;  // of a row that does not fit into registers
+constexpr int kRingThreads = 256;  // of a block with a ring at most
+constexpr int kLongThreads = 256;  // of a row that does not fit into registers
 static_assert(kLongThreads <= kMaxGroup, "the warps' sums fit");
-constexpr int64_t kDwCols = 256;   // columns of a block of the wide weight gradient
+constexpr int64_t kDwCols = 256;   // columns of a block of the long rows' weight gradient
+constexpr int64_t kSplits = 152;   // and the runs of rows it is split into
 
 struct NormParams {
   Rows x, res, h, y;  // p of res, h: nullptr when absent
@@ -44,6 +49,8 @@ struct NormParams {
   int64_t rows, d;
   float eps, inv_d;
   Dropout drop;
+  int stages;         // of a ring
+  uint32_t* err;
 };
 
 // Sums (and the NaN-keeping maximum of magnitudes) over the G threads of a
@@ -52,14 +59,17 @@ struct NormParams {
 struct Joined {
   float sum, top;
 };
-template <bool TOP>
+template <bool TOP, bool SYNC = false>  // SYNC: a barrier of the block in any case
 __device__ __forceinline__ Joined join_group(Joined v, int G, float2 (&buf)[kMaxWarps]) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     v.sum += __shfl_xor_sync(0xffffffffu, v.sum, o);
     if (TOP) v.top = max_nan(v.top, __shfl_xor_sync(0xffffffffu, v.top, o), 0.0f);
   }
-  if (G <= 32) return v;
+  if (G <= 32) {
+    if (SYNC) __syncthreads();
+    return v;
+  }
   const int warp = threadIdx.x >> 5, per = G >> 5, first = warp / per * per;
   if ((threadIdx.x & 31) == 0) buf[warp] = make_float2(v.sum, v.top);
   __syncthreads();
@@ -75,29 +85,36 @@ __device__ __forceinline__ Joined join_group(Joined v, int G, float2 (&buf)[kMax
 // ---- rows that fit into a group's registers --------------------------------
 // R runs of N elements a thread, lane + k G in the row; blockDim.x / G rows at a
 // time.  TX: x; TR: the residual and h (x's type without a residual).
-template <class TX, class TR, int N, int R, bool CODES>
-__global__ void __launch_bounds__(kMaxGroup, R <= 2 || N == 1 ? 2 : 1) norm_fwd_kernel(const NormParams p, const int G) {
+template <class TX, class TR, class TY, int N, int R>
+__global__ void __launch_bounds__(kMaxGroup, 2) norm_fwd_kernel(const NormParams p, const int G) {
+  constexpr bool CODES = sizeof(TY) == 1;
   __shared__ float2 buf[2][kMaxWarps];
   extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any
   const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
-  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, weighted = p.w != nullptr;
+  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, weighted = p.w != nullptr, joined = p.res.p != nullptr;
+  // This thread's first column of the group's row, which moves on by `step` rows.
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
+  const TX* xp = reinterpret_cast<const TX*>(p.x.p) + row * p.x.ld + lane * N;
+  const TR* rp = reinterpret_cast<const TR*>(p.res.p) + row * p.res.ld + lane * N;
+  TR* hp = reinterpret_cast<TR*>(p.h.p) + row * p.h.ld + lane * N;
+  TY* yp = reinterpret_cast<TY*>(p.y.p) + row * p.y.ld + lane * N;
+  bool mine[R];  // the row has these columns
+#pragma unroll
+  for (int k = 0; k < R; ++k) mine[k] = (lane + k * G) * N < d;
   Typed<TX, N> x[R];
   Typed<TR, N> r[R];
-  auto fetch = [&](int64_t row) {
-    const TX* xp = reinterpret_cast<const TX*>(p.x.p) + row * p.x.ld;
-    const TR* rp = reinterpret_cast<const TR*>(p.res.p) + row * p.res.ld;
+  auto fetch = [&] {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (c < d) {
-        x[k].load(xp + c);
-        if (p.res.p != nullptr) r[k].load(rp + c);
+    for (int k = 0; k < R; ++k)
+      if (mine[k]) {
+        x[k].load(xp + k * G * N);
+        if (joined) r[k].load(rp + k * G * N);
       }
-    }
+    xp += step * p.x.ld;
+    rp += step * p.res.ld;
   };
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups;
-  if (row0 + group < p.rows) fetch(row0 + group);
+  if (row < p.rows) fetch();
   if (weighted) {
     if (p.w_dtype == TPS_F32)
       for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = reinterpret_cast<const float*>(p.w)[i];
@@ -108,81 +125,99 @@ __global__ void __launch_bounds__(kMaxGroup, R <= 2 || N == 1 ? 2 : 1) norm_fwd_
   }
   const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
   int turn = 0;
-  for (; row0 < p.rows; row0 += step) {
-    const int64_t row = row0 + group;
+  for (; row0 < p.rows; row0 += step, row += step) {
     const bool live = row < p.rows;
-    float v[R][N];
+    Typed<TR, N> h[R];  // the row, as it is stored
     Joined own = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (live && c < d) {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[k][i] = x[k].at(i);
-        if (p.drop.step != 0u) drop(p.drop, key, row * d + c, v[k]);
-        if (p.res.p != nullptr) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[k][i] += r[k].at(i);
+      if (!live || !mine[k]) continue;
+      bool have = false;
+      if constexpr (sizeof(TX) == sizeof(TR)) {
+        if (p.drop.step == 0u && !joined) {
+          h[k] = x[k];
+          have = true;
         }
-        if (summed) {
-          run_round<N>(dtype_of<TR>(), v[k]);
-          run_store(reinterpret_cast<char*>(reinterpret_cast<TR*>(p.h.p) + row * p.h.ld + c), dtype_of<TR>(), v[k]);
+        if constexpr (N == 8 && sizeof(TX) == 2) {
+          if (p.drop.step == 0u && joined) {  // one rounding, two values an instruction
+            h[k] = x[k];
+            add_bf16(h[k], r[k]);
+            have = true;
+          }
         }
-#pragma unroll
-        for (int i = 0; i < N; ++i) own.sum = fmaf(v[k][i], v[k][i], own.sum);
-      } else {
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[k][i] = 0.0f;
       }
-    }
-    if (row + step < p.rows) fetch(row + step);
-    auto weigh = [&](int k, float(&u)[N]) {
-      const int c = (lane + k * G) * N;
+      if (!have) {
+        float v[N];
 #pragma unroll
-      for (int i = 0; i < N; ++i) u[i] = v[k][i];
+        for (int i = 0; i < N; ++i) v[i] = x[k].at(i);
+        if (p.drop.step != 0u) drop(p.drop, key, row * d + (lane + k * G) * N, v);
+        if (joined) {
+#pragma unroll
+          for (int i = 0; i < N; ++i) v[i] += r[k].at(i);
+        }
+        h[k].set(v);
+      }
+      if (summed) h[k].store(hp + k * G * N);
+    }
+    hp += step * p.h.ld;
+    if (row + step < p.rows) fetch();
+    // the row's values times their weights
+    auto weigh = [&](int k, float(&v)[N]) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = h[k].at(i);
       if (weighted) {
+        const int c = (lane + k * G) * N;
         if constexpr (N == 8) {
           const float4 a = *reinterpret_cast<const float4*>(ws + c), b = *reinterpret_cast<const float4*>(ws + c + 4);
-          u[0] *= a.x; u[1] *= a.y; u[2] *= a.z; u[3] *= a.w;
-          u[4] *= b.x; u[5] *= b.y; u[6] *= b.z; u[7] *= b.w;
+          v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
+          v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
         } else {
-          u[0] *= ws[c];
+          v[0] *= ws[c];
         }
       }
     };
-    if (CODES) {
 #pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if ((lane + k * G) * N >= d) continue;
-        float u[N];
-        weigh(k, u);
+    for (int k = 0; k < R; ++k) {
+      if (!live || !mine[k]) continue;
 #pragma unroll
-        for (int i = 0; i < N; ++i) own.top = max_nan(own.top, fabsf(u[i]), 0.0f);
+      for (int i = 0; i < N; ++i) own.sum = fmaf(h[k].at(i), h[k].at(i), own.sum);
+      if (CODES) {
+        float v[N];
+        weigh(k, v);
+        if constexpr (N == 8) {
+#pragma unroll
+          for (int i = 0; i < N; i += 2) own.top = max_nan(own.top, fabsf(v[i]), fabsf(v[i + 1]));
+        } else {
+          own.top = max_nan(own.top, fabsf(v[0]), 0.0f);
+        }
       }
     }
     own = join_group<CODES>(own, G, buf[turn]);
     turn ^= 1;
-    const float rstd = normed ? __frcp_rn(__fsqrt_rn(fmaf(own.sum, p.inv_d, p.eps))) : 1.0f;
-    const RowCodes codes(own.top);
-    if (!live) continue;
-    if (lane == 0) {
-      if (normed) p.rstd[row] = rstd;
-      if (CODES) p.scale[row] = codes.scale() * rstd;
-    }
+    const float rstd = normed ? rsqrtf(fmaf(own.sum, p.inv_d, p.eps)) : 1.0f;
+    if (live) {
+      const RowCodes codes(own.top);
+      if (lane == 0) {
+        if (normed) p.rstd[row] = rstd;
+        if (CODES) p.scale[row] = codes.scale() * rstd;
+      }
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (c >= d) continue;
-      float u[N];
-      weigh(k, u);
-      if (CODES) {
-        codes_store(p.y.p + row * p.y.ld + c, codes, u);
-      } else {
+      for (int k = 0; k < R; ++k) {
+        if (!mine[k]) continue;
+        float v[N];
+        weigh(k, v);
+        if constexpr (CODES) {
+          codes_store(reinterpret_cast<char*>(yp + k * G * N), codes, v);
+        } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) u[i] *= rstd;
-        run_store(p.y.at(row, c), p.y.dtype, u);
+          for (int i = 0; i < N; ++i) v[i] *= rstd;
+          Typed<TY, N> y;
+          y.set(v);
+          y.store(yp + k * G * N);
+        }
       }
     }
+    yp += step * p.y.ld;
   }
 }
 
@@ -195,111 +230,417 @@ struct NormBwdParams {
   int64_t rows, d;
   float inv_d;
   Dropout drop;
+  int stages;
+  uint32_t* err;
 };
 
-// TD: dy; TH: h, dh and dsum.
-template <class TD, class TH, int N, int R>
-__global__ void __launch_bounds__(kMaxGroup, R <= 2 || N == 1 ? 2 : 1) norm_bwd_kernel(const NormBwdParams p, const int G) {
+// TD: dy; TH: h, dh and dsum; TX: dx.  The sums of dw stay in registers.
+template <class TD, class TH, class TX, int N, int R>
+__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(const NormBwdParams p, const int G) {
   __shared__ float2 buf[2][kMaxWarps];
-  extern __shared__ __align__(16) float ws[];  // [d] weights, then [row group][d] sums of dw
+  extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any; at last [row group][d] sums of dw
   const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
-  float* sums = ws + d + group * d;
-  if (p.w_dtype == TPS_F32)
-    for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = p.w != nullptr ? reinterpret_cast<const float*>(p.w)[i] : 1.0f;
-  else
-    for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
-  if (p.part != nullptr)
-    for (int i = threadIdx.x; i < groups * d; i += blockDim.x) ws[d + i] = 0.0f;
-  __syncthreads();
+  const bool past = p.dh.p != nullptr, weighted = p.w != nullptr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
+  const TD* dyp = reinterpret_cast<const TD*>(p.dy.p) + row * p.dy.ld + lane * N;
+  const TH* hp = reinterpret_cast<const TH*>(p.h.p) + row * p.h.ld + lane * N;
+  const TH* dhp = reinterpret_cast<const TH*>(p.dh.p) + row * p.dh.ld + lane * N;
+  TH* dsp = reinterpret_cast<TH*>(p.dsum.p) + row * p.dsum.ld + lane * N;
+  TX* dxp = reinterpret_cast<TX*>(p.dx.p) + row * p.dx.ld + lane * N;
+  bool mine[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) mine[k] = (lane + k * G) * N < d;
+  if (weighted) {
+    if (p.w_dtype == TPS_F32)
+      for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = reinterpret_cast<const float*>(p.w)[i];
+    else
+      for (int i = threadIdx.x; i < d; i += blockDim.x)
+        ws[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
+    __syncthreads();
+  }
   const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  float dw[R][N];
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) dw[k][i] = 0.0f;
   int turn = 0;
-  for (int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups; row0 < p.rows; row0 += static_cast<int64_t>(gridDim.x) * groups) {
-    const int64_t row = row0 + group;
+  for (; row0 < p.rows; row0 += step, row += step) {
     const bool live = row < p.rows;
     const float r = live ? __ldg(p.rstd + row) : 0.0f;
     Typed<TD, N> a[R];
     Typed<TH, N> b[R], in[R];
-    const TD* dyp = reinterpret_cast<const TD*>(p.dy.p) + row * p.dy.ld;
-    const TH* hp = reinterpret_cast<const TH*>(p.h.p) + row * p.h.ld;
-    const TH* dhp = reinterpret_cast<const TH*>(p.dh.p) + row * p.dh.ld;
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (live && c < d) {
-        a[k].load(dyp + c);
-        b[k].load(hp + c);
-        if (p.dh.p != nullptr) in[k].load(dhp + c);
+    for (int k = 0; k < R; ++k)
+      if (live && mine[k]) {
+        a[k].load(dyp + k * G * N);
+        b[k].load(hp + k * G * N);
+        if (past) in[k].load(dhp + k * G * N);
       }
-    }
-    // of the columns of run k: g = dy w and n = h r
-    auto terms = [&](int k, float(&g)[N], float(&n)[N]) {
-      const int c = (lane + k * G) * N;
-      if constexpr (N == 8) {
-        const float4 x = *reinterpret_cast<const float4*>(ws + c), y = *reinterpret_cast<const float4*>(ws + c + 4);
-        const float w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+    dyp += step * p.dy.ld;
+    hp += step * p.h.ld;
+    dhp += step * p.dh.ld;
+    // dy times the weights
+    auto weigh = [&](int k, float(&g)[N]) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) g[i] = a[k].at(i) * w[i];
-      } else {
-        g[0] = a[k].at(0) * ws[c];
+      for (int i = 0; i < N; ++i) g[i] = a[k].at(i);
+      if (weighted) {
+        const int c = (lane + k * G) * N;
+        if constexpr (N == 8) {
+          const float4 x = *reinterpret_cast<const float4*>(ws + c), y = *reinterpret_cast<const float4*>(ws + c + 4);
+          g[0] *= x.x; g[1] *= x.y; g[2] *= x.z; g[3] *= x.w;
+          g[4] *= y.x; g[5] *= y.y; g[6] *= y.z; g[7] *= y.w;
+        } else {
+          g[0] *= ws[c];
+        }
       }
-#pragma unroll
-      for (int i = 0; i < N; ++i) n[i] = b[k].at(i) * r;
     };
     Joined own = {0.0f, 0.0f};
 #pragma unroll
     for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (!live || c >= d) continue;
-      float g[N], n[N];
-      terms(k, g, n);
+      if (!live || !mine[k]) continue;
+      float g[N];
+      weigh(k, g);
 #pragma unroll
-      for (int i = 0; i < N; ++i) own.sum = fmaf(g[i], n[i], own.sum);
-      if (p.part != nullptr) {
-        if constexpr (N == 8) {
-          float4 x = *reinterpret_cast<const float4*>(sums + c), y = *reinterpret_cast<const float4*>(sums + c + 4);
-          x.x = fmaf(a[k].at(0), n[0], x.x);
-          x.y = fmaf(a[k].at(1), n[1], x.y);
-          x.z = fmaf(a[k].at(2), n[2], x.z);
-          x.w = fmaf(a[k].at(3), n[3], x.w);
-          y.x = fmaf(a[k].at(4), n[4], y.x);
-          y.y = fmaf(a[k].at(5), n[5], y.y);
-          y.z = fmaf(a[k].at(6), n[6], y.z);
-          y.w = fmaf(a[k].at(7), n[7], y.w);
-          *reinterpret_cast<float4*>(sums + c) = x;
-          *reinterpret_cast<float4*>(sums + c + 4) = y;
-        } else {
-          sums[c] = fmaf(a[k].at(0), n[0], sums[c]);
-        }
+      for (int i = 0; i < N; ++i) {
+        const float n = b[k].at(i) * r;
+        dw[k][i] = fmaf(a[k].at(i), n, dw[k][i]);
+        own.sum = fmaf(g[i], n, own.sum);
       }
     }
     own = join_group<false>(own, G, buf[turn]);
     turn ^= 1;
-    const float mean = own.sum * p.inv_d;
+    const float pull = -own.sum * p.inv_d * r;  // what h r is multiplied by
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < R; ++k) {
-      const int c = (lane + k * G) * N;
-      if (!live || c >= d) continue;
-      float v[N], n[N];
-      terms(k, v, n);
+      for (int k = 0; k < R; ++k) {
+        if (!mine[k]) continue;
+        float v[N];
+        weigh(k, v);
 #pragma unroll
-      for (int i = 0; i < N; ++i) {
-        v[i] = fmaf(-n[i], mean, v[i]) * r;
-        if (p.dh.p != nullptr) v[i] += in[k].at(i);
-      }
-      if (p.dsum.p != nullptr)
-        run_store(reinterpret_cast<char*>(reinterpret_cast<TH*>(p.dsum.p) + row * p.dsum.ld + c), dtype_of<TH>(), v);
-      if (p.dx.p != nullptr) {
-        if (p.drop.step != 0u) drop(p.drop, key, row * d + c, v);
-        run_store(p.dx.at(row, c), p.dx.dtype, v);
+        for (int i = 0; i < N; ++i) v[i] = fmaf(v[i], r, fmaf(b[k].at(i) * r, pull, past ? in[k].at(i) : 0.0f));
+        if (p.dsum.p != nullptr) {
+          Typed<TH, N> o;
+          o.set(v);
+          o.store(dsp + k * G * N);
+        }
+        if (p.dx.p != nullptr) {
+          if (p.drop.step != 0u) drop(p.drop, key, row * d + (lane + k * G) * N, v);
+          Typed<TX, N> o;
+          o.set(v);
+          o.store(dxp + k * G * N);
+        }
       }
     }
+    dsp += step * p.dsum.ld;
+    dxp += step * p.dx.ld;
   }
   if (p.part == nullptr) return;
-  __syncthreads();
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
+  __syncthreads();  // the weights are done with
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (mine[k]) ws[group * d + (lane + k * G) * N + i] = dw[k][i];
+  __syncthreads();
   for (int c = threadIdx.x; c < d; c += blockDim.x) {
     float s = 0.0f;
-    for (int q = 0; q < groups; ++q) s += ws[d + q * d + c];
+    for (int q = 0; q < groups; ++q) s += ws[q * d + c];
+    out[c] = s;
+  }
+}
+
+// ---- many rows, through a ring ---------------------------------------------
+// The next rows of up to three tensors in shared memory: a stage holds one row
+// of each for every group of the block.  A stage is filled again once the whole
+// block has taken its rows into registers.
+constexpr int kMaxStages = 8;
+struct RowRing {
+  uint64_t full[kMaxStages];
+  uint32_t abort;
+};
+struct RingSource {
+  const char* p[3];
+  int64_t pitch[3];  // bytes
+  int bytes[3];      // of a row, a multiple of 16; 0: no such tensor
+};
+__device__ __forceinline__ int ring_row_bytes(const RingSource& s) { return s.bytes[0] + s.bytes[1] + s.bytes[2]; }
+// By the first warp: the rows from row0 on into a stage.
+__device__ __forceinline__ void ring_fill(const RingSource& s, RowRing* ring, char* at, int stage, int groups, int64_t row0,
+                                          int64_t rows) {
+  if (row0 >= rows) return;
+  const int lane = threadIdx.x & 31, n = static_cast<int>(rows - row0 < groups ? rows - row0 : groups);
+  const int one = ring_row_bytes(s);
+  if (lane == 0) mbar_expect_tx(&ring->full[stage], static_cast<uint32_t>(n * one));
+  __syncwarp();
+  if (lane < n) {
+    char* to = at + (stage * groups + lane) * one;
+#pragma unroll
+    for (int t = 0; t < 3; ++t)
+      if (s.bytes[t] > 0) {
+        bulk_load(to, s.p[t] + (row0 + lane) * s.pitch[t], static_cast<uint32_t>(s.bytes[t]), &ring->full[stage]);
+        to += s.bytes[t];
+      }
+  }
+}
+__device__ __forceinline__ void ring_start(const RingSource& s, RowRing* ring, char* at, int stages, int groups, int64_t row0,
+                                           int64_t step, int64_t rows) {
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&ring->full[i], 1);
+    ring->abort = 0u;
+    fence_mbar_init();
+  }
+  __syncthreads();
+  if (threadIdx.x < 32)
+    for (int i = 0; i < stages; ++i) ring_fill(s, ring, at, i, groups, row0 + i * step, rows);
+}
+// A stage whose copies did not arrive in time: what it holds is not used, but
+// they must be over when the block ends.
+__device__ __forceinline__ void ring_wait(RowRing* ring, int stage, uint32_t phase, uint32_t* err) {
+  if (!mbar_wait(&ring->full[stage], phase, &ring->abort, err)) mbar_wait_drain(&ring->full[stage], phase, err);
+}
+
+
+// The weights of a thread's columns, as floats in registers: ones without weights and past the row.
+template <int R>
+__device__ __forceinline__ void ring_weights(const char* w, int dtype, int c0, int stride, int d, float (&v)[R][8]) {
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    const int c = c0 + k * stride;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[k][i] = 1.0f;
+    if (w != nullptr && c < d) {
+      Raw<8> q;
+      raw_load(w + c * (dtype == TPS_F32 ? 4 : 2), dtype, q);
+      raw_value(q, dtype, v[k]);
+    }
+  }
+}
+// Blocks of kRingThreads threads on an SM that the registers are to allow, by
+// the floats of a thread that live through a row.
+constexpr int ring_blocks(int floats) { return floats <= 32 ? 3 : floats <= 72 ? 2 : 1; }
+constexpr int ring_fwd_blocks(int R, bool wide_h) { return ring_blocks(R * 8 + R * (wide_h ? 8 : 4)); }
+constexpr int ring_bwd_blocks(int R) { return ring_blocks(2 * R * 8); }
+
+// R runs of eight elements a thread, lane + k G in the row.
+template <class TX, class TR, class TY, int R>
+__global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) == 4))
+    norm_fwd_ring_kernel(const NormParams p, const int G) {
+  constexpr bool CODES = sizeof(TY) == 1;
+  __shared__ float2 buf[2][kMaxWarps];
+  __shared__ RowRing ring;
+  extern __shared__ __align__(128) char stages_at[];
+  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
+  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, joined = p.res.p != nullptr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups;
+  const RingSource src = {{p.x.p, p.res.p, nullptr},
+                          {p.x.ld * int(sizeof(TX)), p.res.ld * int(sizeof(TR)), 0},
+                          {d * int(sizeof(TX)), joined ? d * int(sizeof(TR)) : 0, 0}};
+  ring_start(src, &ring, stages_at, p.stages, groups, row0, step, p.rows);
+  const int c0 = lane * 8, stride = G * 8;
+  float w[R][8];
+  ring_weights(p.w, p.w_dtype, c0, stride, d, w);
+  TR* hp = reinterpret_cast<TR*>(p.h.p) + (row0 + group) * p.h.ld + c0;
+  TY* yp = reinterpret_cast<TY*>(p.y.p) + (row0 + group) * p.y.ld + c0;
+  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  for (; row0 < p.rows; row0 += step) {
+    const bool live = row0 + group < p.rows;
+    ring_wait(&ring, stage, phase, p.err);
+    const char* at = stages_at + (stage * groups + group) * ring_row_bytes(src);
+    const TX* xs = reinterpret_cast<const TX*>(at) + c0;
+    const TR* rs = reinterpret_cast<const TR*>(at + src.bytes[0]) + c0;
+    Typed<TR, 8> h[R];  // the row, as it is stored
+    Joined own = {0.0f, 0.0f};
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (c0 + k * stride >= d) continue;
+        Typed<TX, 8> x;
+        Typed<TR, 8> r;
+        x.load(xs + k * stride);
+        if (joined) r.load(rs + k * stride);
+        bool have = false;
+        if constexpr (sizeof(TX) == sizeof(TR)) {
+          if (p.drop.step == 0u && !joined) {
+            h[k] = x;
+            have = true;
+          }
+          if constexpr (sizeof(TX) == 2) {
+            if (p.drop.step == 0u && joined) {  // one rounding, two values an instruction
+              h[k] = x;
+              add_bf16(h[k], r);
+              have = true;
+            }
+          }
+        }
+        if (!have) {
+          float v[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = x.at(i);
+          if (p.drop.step != 0u) drop(p.drop, key, (row0 + group) * d + c0 + k * stride, v);
+          if (joined) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) v[i] += r.at(i);
+          }
+          h[k].set(v);
+        }
+        if (summed) h[k].store(hp + k * stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float v = h[k].at(i);
+          own.sum = fmaf(v, v, own.sum);
+          if (CODES) own.top = max_nan(own.top, fabsf(v * w[k][i]), 0.0f);
+        }
+      }
+    }
+    own = join_group<CODES, true>(own, G, buf[turn]);
+    turn ^= 1;
+    // everyone has the stage's rows
+    if (threadIdx.x < 32) ring_fill(src, &ring, stages_at, stage, groups, row0 + p.stages * step, p.rows);
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    if (live) {
+      const float rstd = normed ? rsqrtf(fmaf(own.sum, p.inv_d, p.eps)) : 1.0f;
+      const RowCodes codes(own.top);
+      if (lane == 0) {
+        if (normed) p.rstd[row0 + group] = rstd;
+        if (CODES) p.scale[row0 + group] = codes.scale() * rstd;
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (c0 + k * stride >= d) continue;
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = h[k].at(i) * w[k][i];
+        if constexpr (CODES) {
+          codes_store(reinterpret_cast<char*>(yp + k * stride), codes, v);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] *= rstd;
+          Typed<TY, 8> y;
+          y.set(v);
+          y.store(yp + k * stride);
+        }
+      }
+    }
+    hp += step * p.h.ld;
+    yp += step * p.y.ld;
+  }
+}
+
+// The rows are taken out of the stage twice, before and after the join, and the
+// stage is filled again at the next row's join.
+template <class TD, class TH, class TX, int R>
+__global__ void __launch_bounds__(kRingThreads, ring_bwd_blocks(R)) norm_bwd_ring_kernel(const NormBwdParams p, const int G) {
+  __shared__ float2 buf[2][kMaxWarps];
+  __shared__ RowRing ring;
+  extern __shared__ __align__(128) char stages_at[];  // at last [row group][d] sums of dw
+  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
+  const bool past = p.dh.p != nullptr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups;
+  const RingSource src = {{p.dy.p, p.h.p, p.dh.p},
+                          {p.dy.ld * int(sizeof(TD)), p.h.ld * int(sizeof(TH)), p.dh.ld * int(sizeof(TH))},
+                          {d * int(sizeof(TD)), d * int(sizeof(TH)), past ? d * int(sizeof(TH)) : 0}};
+  ring_start(src, &ring, stages_at, p.stages, groups, row0, step, p.rows);
+  const int c0 = lane * 8, stride = G * 8;
+  float w[R][8], dw[R][8];
+  ring_weights(p.w, p.w_dtype, c0, stride, d, w);
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) dw[k][i] = 0.0f;
+  TH* dsp = reinterpret_cast<TH*>(p.dsum.p) + (row0 + group) * p.dsum.ld + c0;
+  TX* dxp = reinterpret_cast<TX*>(p.dx.p) + (row0 + group) * p.dx.ld + c0;
+  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  int stage = 0, turn = 0;
+  uint32_t phase = 0;
+  bool first = true;
+  for (; row0 < p.rows; row0 += step) {
+    const bool live = row0 + group < p.rows;
+    const float r = live ? __ldg(p.rstd + row0 + group) : 0.0f;
+    ring_wait(&ring, stage, phase, p.err);
+    const char* at = stages_at + (stage * groups + group) * ring_row_bytes(src);
+    const TD* as = reinterpret_cast<const TD*>(at) + c0;
+    const TH* bs = reinterpret_cast<const TH*>(at + src.bytes[0]) + c0;
+    const TH* is = reinterpret_cast<const TH*>(at + src.bytes[0] + src.bytes[1]) + c0;
+    Joined own = {0.0f, 0.0f};
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (c0 + k * stride >= d) continue;
+        Typed<TD, 8> a;
+        Typed<TH, 8> b;
+        a.load(as + k * stride);
+        b.load(bs + k * stride);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float n = b.at(i) * r, g = a.at(i) * n;
+          dw[k][i] += g;
+          own.sum = fmaf(g, w[k][i], own.sum);
+        }
+      }
+    }
+    own = join_group<false, true>(own, G, buf[turn]);
+    turn ^= 1;
+    // everyone is done with the row before
+    if (!first && threadIdx.x < 32)
+      ring_fill(src, &ring, stages_at, (stage == 0 ? p.stages : stage) - 1, groups, row0 + (p.stages - 1) * step, p.rows);
+    first = false;
+    if (++stage == p.stages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+    const float pull = -own.sum * p.inv_d * r;  // what h r is multiplied by
+    if (live) {
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (c0 + k * stride >= d) continue;
+        Typed<TD, 8> a;
+        Typed<TH, 8> b, in;
+        a.load(as + k * stride);
+        b.load(bs + k * stride);
+        if (past) in.load(is + k * stride);
+        float v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+          v[i] = fmaf(a.at(i) * w[k][i], r, fmaf(b.at(i) * r, pull, past ? in.at(i) : 0.0f));
+        if (p.dsum.p != nullptr) {
+          Typed<TH, 8> o;
+          o.set(v);
+          o.store(dsp + k * stride);
+        }
+        if (p.dx.p != nullptr) {
+          if (p.drop.step != 0u) drop(p.drop, key, (row0 + group) * d + c0 + k * stride, v);
+          Typed<TX, 8> o;
+          o.set(v);
+          o.store(dxp + k * stride);
+        }
+      }
+    }
+    dsp += step * p.dsum.ld;
+    dxp += step * p.dx.ld;
+  }
+  if (p.part == nullptr) return;
+  float* sums = reinterpret_cast<float*>(stages_at);
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
+  __syncthreads();  // the rows are done with
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (c0 + k * stride < d) sums[group * d + c0 + k * stride + i] = dw[k][i];
+  __syncthreads();
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    float s = 0.0f;
+    for (int q = 0; q < groups; ++q) s += sums[q * d + c];
     out[c] = s;
   }
 }
@@ -350,7 +691,7 @@ __global__ void __launch_bounds__(kLongThreads) norm_fwd_long_kernel(const NormP
     }
   }
   own = join_group<CODES>(own, kLongThreads, buf);
-  const float rstd = normed ? __frcp_rn(__fsqrt_rn(fmaf(own.sum, p.inv_d, p.eps))) : 1.0f;
+  const float rstd = normed ? rsqrtf(fmaf(own.sum, p.inv_d, p.eps)) : 1.0f;
   const RowCodes codes(own.top);
   if (threadIdx.x == 0) {
     if (normed) p.rstd[row] = rstd;
@@ -450,71 +791,113 @@ int round_pow2(int64_t x) {
   while (r < x) r *= 2;
   return r;
 }
-// How a row is spread over threads: runs of N elements, R of them a thread, G
-// threads a row; N = 0: the kernels of long rows.
-// 16-byte loads where every row of every tensor starts on one and holds whole
-// runs of eight; else single elements, eight a thread, where the types agree.
-// Two runs a thread in bf16, one where fp32 is among the types (as many bytes),
-// up to kMaxGroup threads; then more runs, up to 16384 columns.
+// How a call is run: runs of N elements, R of them a thread, G threads a row,
+// blocks of `threads`.  N = 0: the kernels of long rows.
+// ring > 0: through a ring of so many stages, `per_sm` blocks an SM walking the
+// rows; where every row of every tensor starts on 16 bytes and holds whole runs of
+// eight, and where there are more rows than two for each group of the
+// blocks that the device holds, or more columns than the other form's registers
+// do.  Four runs a thread in bf16, two where fp32 is among the types (as many
+// bytes), more for more than 256 threads' worth.
+// Otherwise loads into registers, two runs a thread (one) and up to kMaxGroup
+// threads a row; single elements, eight a thread, where runs do not fit and the
+// types agree.
+constexpr int64_t kSms = 152, kMostBlocks = kSms * 16;
+constexpr int kRingShared = 216 << 10;  // of an SM
 struct Spread {
-  int N, R, G, threads;
+  int N, R, G, threads, ring, per_sm;
 };
-Spread spread_of(int64_t d, bool wide, bool fp32, bool mixed) {
-  Spread s = {0, 0, 0, 0};
+// row_bytes: of one row of all tensors that are read.  heavy: the backward pass, whose threads hold dw too.
+Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int64_t row_bytes, int heavy) {
+  Spread s = {0, 0, 0, 0, 0, 0};
+  if (wide) {
+    const int64_t runs = (d + 7) / 8;
+    Spread r = {8, fp32 ? 2 : 4, 0, 0, 0, 0};
+    while (runs > int64_t(r.R) * kRingThreads && r.R < 8) r.R *= 2;
+    if (runs <= int64_t(r.R) * kRingThreads) {
+      const int64_t need = (runs + r.R - 1) / r.R;
+      r.G = need <= 32 ? 32 : round_pow2(need);
+      r.threads = r.G < 128 ? 128 : r.G;
+      const int64_t stage = row_bytes * (r.threads / r.G);
+      // registers: floats of a thread that live through a row
+      const int floats = heavy ? 2 * r.R * 8 : r.R * 8 + r.R * (fp32 ? 8 : 4);
+      const int most = ring_blocks(floats) * kRingThreads / r.threads;
+      for (int per = most; per >= 1 && r.ring == 0; --per) {
+        const int64_t n = (kRingShared / per - 2048) / stage;
+        if (n >= 2) {
+          r.ring = static_cast<int>(n < kMaxStages ? n : kMaxStages);
+          r.per_sm = per;
+        }
+      }
+      const int64_t groups = kSms * r.per_sm * (r.threads / r.G);
+      if (r.ring > 0 && (rows > 2 * groups || runs > int64_t(fp32 ? 1 : 2) * kMaxGroup)) return r;
+    }
+  }
   if (!wide && (mixed || d > 8 * kMaxGroup)) return s;
   s.N = wide ? 8 : 1;
   s.R = wide ? (fp32 ? 1 : 2) : 8;
   const int64_t runs = (d + s.N - 1) / s.N;
-  while (wide && runs > int64_t(s.R) * kMaxGroup && s.R < 4) s.R *= 2;
-  if (runs > int64_t(s.R) * kMaxGroup) return Spread{0, 0, 0, 0};
+  if (runs > int64_t(s.R) * kMaxGroup) return Spread{0, 0, 0, 0, 0, 0};
   const int64_t need = (runs + s.R - 1) / s.R;
   s.G = need <= 32 ? 32 : round_pow2(need);
   s.threads = s.G < 256 ? 256 : s.G;
+  while (s.threads > s.G && (rows * s.G + s.threads - 1) / s.threads < 2 * kSms) s.threads /= 2;  // few rows: a block each
+  s.per_sm = (heavy ? 512 : 1024) / s.threads;
   return s;
 }
 
-// Blocks that walk the rows: as many as the launch bounds (1024 threads an SM,
-// 512 with four runs a thread) and shared memory let be resident.
-constexpr int64_t kSms = 152, kMostBlocks = kSms * 4;
+// Blocks of `f`, and its shared memory.
 template <class F>
-int resident(F f, const Spread& sp, size_t shared, int64_t* blocks) {
-  if (shared > (48u << 10) &&
+int prepare_launch(F f, const Spread& sp, int64_t rows, size_t shared, int64_t* blocks) {
+  if (shared > (40u << 10) &&  // with the static part, beyond 48 KB
       cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared)) != cudaSuccess)
     return fail(TPS_ERR_CUDA, "norm: %s", cudaGetErrorString(cudaGetLastError()));
-  const int64_t by_threads = (sp.N == 8 && sp.R > 2 ? 512 : 1024) / sp.threads, by_shared = (224 << 10) / (int64_t(shared) + 2048);
-  const int64_t per = by_threads < by_shared ? by_threads : by_shared;
-  *blocks = kSms * (per < 1 ? 1 : per);
+  int64_t per = sp.per_sm;
+  if (sp.ring == 0 && per * (int64_t(shared) + 2048) > kRingShared) per = kRingShared / (int64_t(shared) + 2048);
+  const int64_t groups = sp.threads / sp.G, need = (rows + groups - 1) / groups, most = kSms * (per < 1 ? 1 : per);
+  *blocks = need < most ? need : most;
   return TPS_OK;
 }
+int ring_ready(const Spread& sp, int* stages, uint32_t** err) {
+  *stages = sp.ring;
+  *err = device_error_word();
+  return *err != nullptr ? TPS_OK : fail(TPS_ERR_CUDA, "cannot resolve the device error word");
+}
 
-template <class TX, class TR, int N, int R, bool CODES>
-int launch_fwd(const NormParams& p, const Spread& sp, cudaStream_t s) {
-  const size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
-  const int64_t per = sp.threads / sp.G, blocks = (p.rows + per - 1) / per;
-  int64_t most = 0;
-  const int rc = resident(norm_fwd_kernel<TX, TR, N, R, CODES>, sp, shared, &most);
-  if (rc) return rc;
-  norm_fwd_kernel<TX, TR, N, R, CODES>
-      <<<static_cast<unsigned>(blocks < most ? blocks : most), sp.threads, shared, s>>>(p, sp.G);
+template <class TX, class TR, class TY, int N, int R, bool RING>
+int launch_fwd(NormParams p, const Spread& sp, cudaStream_t s) {
+  int64_t blocks = 0;
+  int rc;
+  if constexpr (RING) {
+    const size_t shared = static_cast<size_t>(sp.ring) * (sp.threads / sp.G) * p.d * (sizeof(TX) + (p.res.p ? sizeof(TR) : 0));
+    if ((rc = ring_ready(sp, &p.stages, &p.err)) ||
+        (rc = prepare_launch(norm_fwd_ring_kernel<TX, TR, TY, R>, sp, p.rows, shared, &blocks)))
+      return rc;
+    norm_fwd_ring_kernel<TX, TR, TY, R><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
+  } else {
+    const size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
+    if ((rc = prepare_launch(norm_fwd_kernel<TX, TR, TY, N, R>, sp, p.rows, shared, &blocks))) return rc;
+    norm_fwd_kernel<TX, TR, TY, N, R><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
+  }
   return launched("norm");
 }
-template <class TX, class TR, bool CODES>
+template <class TX, class TR, class TY>
 int launch_fwd_typed(const NormParams& p, const Spread& sp, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(TX) == 2 && sizeof(TR) == 2;
   if (sp.N == 1) {
-    if constexpr (sizeof(TX) == sizeof(TR)) return launch_fwd<TX, TR, 1, 8, CODES>(p, sp, s);
+    if constexpr (sizeof(TX) == sizeof(TR)) return launch_fwd<TX, TR, TY, 1, 8, false>(p, sp, s);
     return fail(TPS_ERR_DTYPE, "norm: single elements of two types");
   }
+  if (sp.ring == 0) return launch_fwd<TX, TR, TY, 8, kBf16 ? 2 : 1, false>(p, sp, s);
   if constexpr (!kBf16)
-    if (sp.R == 1) return launch_fwd<TX, TR, 8, 1, CODES>(p, sp, s);
-  if (sp.R == 2) return launch_fwd<TX, TR, 8, 2, CODES>(p, sp, s);
-  return launch_fwd<TX, TR, 8, 4, CODES>(p, sp, s);
+    if (sp.R == 2) return launch_fwd<TX, TR, TY, 8, 2, true>(p, sp, s);
+  if (sp.R == 4) return launch_fwd<TX, TR, TY, 8, 4, true>(p, sp, s);
+  return launch_fwd<TX, TR, TY, 8, 8, true>(p, sp, s);
 }
-template <bool CODES>
-int launch_fwd_codes(const NormParams& p, const Spread& sp, int tx, int tr, cudaStream_t s) {
-  using bf16 = __nv_bfloat16;
-  if (tx == TPS_F32) return tr == TPS_F32 ? launch_fwd_typed<float, float, CODES>(p, sp, s) : launch_fwd_typed<float, bf16, CODES>(p, sp, s);
-  return tr == TPS_F32 ? launch_fwd_typed<bf16, float, CODES>(p, sp, s) : launch_fwd_typed<bf16, bf16, CODES>(p, sp, s);
+template <class TX, class TR>
+int launch_fwd_out(const NormParams& p, const Spread& sp, cudaStream_t s) {
+  if (p.y.dtype == TPS_E4M3) return launch_fwd_typed<TX, TR, uint8_t>(p, sp, s);
+  return p.y.dtype == TPS_F32 ? launch_fwd_typed<TX, TR, float>(p, sp, s) : launch_fwd_typed<TX, TR, __nv_bfloat16>(p, sp, s);
 }
 
 int launch_norm_fwd(const NormParams& p, const char* label, cudaStream_t s) {
@@ -522,11 +905,15 @@ int launch_norm_fwd(const NormParams& p, const char* label, cudaStream_t s) {
                     starts_runs(p.y, p.rows) && (p.w == nullptr || starts_runs(p.w, 0, p.w_dtype, 1));
   const int tx = p.x.dtype, tr = p.res.p != nullptr ? p.res.dtype : tx;
   const bool codes = p.y.dtype == TPS_E4M3;
-  const Spread sp = spread_of(p.d, wide, tx == TPS_F32 || tr == TPS_F32, tx != tr);
+  const int64_t row_bytes = p.d * (es_of(tx) + (p.res.p != nullptr ? es_of(tr) : 0));
+  const Spread sp = spread_of(p.rows, p.d, wide, tx == TPS_F32 || tr == TPS_F32, tx != tr, row_bytes, 0);
   const double bytes = double(p.rows) * double(p.d) *
                        (es_of(p.x.dtype) + (p.res.p ? es_of(p.res.dtype) : 0) + (p.h.p ? es_of(p.h.dtype) : 0) + es_of(p.y.dtype));
   ProfScope prof("norm", label, 0.0, bytes, s);
-  if (sp.N != 0) return codes ? launch_fwd_codes<true>(p, sp, tx, tr, s) : launch_fwd_codes<false>(p, sp, tx, tr, s);
+  using bf16 = __nv_bfloat16;
+  if (sp.N != 0)
+    return tx == TPS_F32 ? (tr == TPS_F32 ? launch_fwd_out<float, float>(p, sp, s) : launch_fwd_out<float, bf16>(p, sp, s))
+                         : (tr == TPS_F32 ? launch_fwd_out<bf16, float>(p, sp, s) : launch_fwd_out<bf16, bf16>(p, sp, s));
   const unsigned grid = static_cast<unsigned>(p.rows);
   if (wide)
     codes ? norm_fwd_long_kernel<8, true><<<grid, kLongThreads, 0, s>>>(p) : norm_fwd_long_kernel<8, false><<<grid, kLongThreads, 0, s>>>(p);
@@ -535,56 +922,69 @@ int launch_norm_fwd(const NormParams& p, const char* label, cudaStream_t s) {
   return launched("norm_long");
 }
 
-template <class TD, class TH, int N, int R>
-int launch_bwd(const NormBwdParams& p, const Spread& sp, int64_t* parts, cudaStream_t s) {
-  const int64_t per = sp.threads / sp.G, blocks = (p.rows + per - 1) / per;
-  const size_t shared = sizeof(float) * p.d * (1 + (p.part != nullptr ? per : 0));
-  int64_t most = 0;
-  const int rc = resident(norm_bwd_kernel<TD, TH, N, R>, sp, shared, &most);
-  if (rc) return rc;
-  *parts = blocks < most ? blocks : most;
-  norm_bwd_kernel<TD, TH, N, R><<<static_cast<unsigned>(*parts), sp.threads, shared, s>>>(p, sp.G);
+template <class TD, class TH, class TX, int N, int R, bool RING>
+int launch_bwd(NormBwdParams p, const Spread& sp, int64_t* parts, cudaStream_t s) {
+  const int64_t per = sp.threads / sp.G;
+  const size_t sums = p.part != nullptr ? sizeof(float) * p.d * per : 0;
+  int rc;
+  if constexpr (RING) {
+    size_t shared = static_cast<size_t>(sp.ring) * per * p.d * (sizeof(TD) + sizeof(TH) * (p.dh.p ? 2 : 1));
+    if (shared < sums) shared = sums;
+    if ((rc = ring_ready(sp, &p.stages, &p.err)) ||
+        (rc = prepare_launch(norm_bwd_ring_kernel<TD, TH, TX, R>, sp, p.rows, shared, parts)))
+      return rc;
+    norm_bwd_ring_kernel<TD, TH, TX, R><<<static_cast<unsigned>(*parts), sp.threads, shared, s>>>(p, sp.G);
+  } else {
+    size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
+    if (shared < sums) shared = sums;
+    if ((rc = prepare_launch(norm_bwd_kernel<TD, TH, TX, N, R>, sp, p.rows, shared, parts))) return rc;
+    norm_bwd_kernel<TD, TH, TX, N, R><<<static_cast<unsigned>(*parts), sp.threads, shared, s>>>(p, sp.G);
+  }
   return launched("norm_bwd");
 }
-template <class TD, class TH>
+template <class TD, class TH, class TX>
 int launch_bwd_typed(const NormBwdParams& p, const Spread& sp, int64_t* parts, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(TD) == 2 && sizeof(TH) == 2;
   if (sp.N == 1) {
-    if constexpr (sizeof(TD) == sizeof(TH)) return launch_bwd<TD, TH, 1, 8>(p, sp, parts, s);
+    if constexpr (sizeof(TD) == sizeof(TH)) return launch_bwd<TD, TH, TX, 1, 8, false>(p, sp, parts, s);
     return fail(TPS_ERR_DTYPE, "norm: single elements of two types");
   }
+  if (sp.ring == 0) return launch_bwd<TD, TH, TX, 8, kBf16 ? 2 : 1, false>(p, sp, parts, s);
   if constexpr (!kBf16)
-    if (sp.R == 1) return launch_bwd<TD, TH, 8, 1>(p, sp, parts, s);
-  if (sp.R == 2) return launch_bwd<TD, TH, 8, 2>(p, sp, parts, s);
-  return launch_bwd<TD, TH, 8, 4>(p, sp, parts, s);
+    if (sp.R == 2) return launch_bwd<TD, TH, TX, 8, 2, true>(p, sp, parts, s);
+  if (sp.R == 4) return launch_bwd<TD, TH, TX, 8, 4, true>(p, sp, parts, s);
+  return launch_bwd<TD, TH, TX, 8, 8, true>(p, sp, parts, s);
+}
+template <class TD, class TH>
+int launch_bwd_out(const NormBwdParams& p, const Spread& sp, int64_t* parts, cudaStream_t s) {
+  return p.dx.dtype == TPS_F32 ? launch_bwd_typed<TD, TH, float>(p, sp, parts, s)
+                               : launch_bwd_typed<TD, TH, __nv_bfloat16>(p, sp, parts, s);
 }
 
 }  // namespace
 
 // Sum of `n` rows of d floats to out (f32 or bf16), in row order.
-__global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_t n, int64_t d, void* out, int dtype) {
-  __shared__ float s[8][33];
+__global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64_t n, int64_t d, void* out, int dtype) {
+  __shared__ float s[32][33];
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float acc = 0.0f;
   if (c < d) {
     constexpr int U = 8;  // loads in flight
-    int64_t i = w;
-    for (; i + (U - 1) * 8 < n; i += U * 8) {
+    for (int64_t i = w; i < n; i += U * 32) {
       float x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = __ldg(part + (i + u * 8) * d + c);
+      for (int u = 0; u < U; ++u) x[u] = i + u * 32 < n ? __ldg(part + (i + u * 32) * d + c) : 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) acc += x[u];
     }
-    for (; i < n; i += 8) acc += __ldg(part + i * d + c);
   }
   s[w][lane] = acc;
   __syncthreads();
   if (w != 0 || c >= d) return;
   acc = 0.0f;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc += s[i][lane];
+  for (int i = 0; i < 32; ++i) acc += s[i][lane];
   if (dtype == TPS_F32)
     static_cast<float*>(out)[c] = acc;
   else
@@ -593,7 +993,7 @@ __global__ void __launch_bounds__(256) sum_rows_kernel(const float* part, int64_
 
 int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, cudaStream_t s) {
   ProfScope prof("sum_rows", "dw", 0.0, 4.0 * double(n) * double(d), s);
-  sum_rows_kernel<<<static_cast<unsigned>((d + 31) / 32), 256, 0, s>>>(part, n, d, out, dtype);
+  sum_rows_kernel<<<static_cast<unsigned>((d + 31) / 32), 1024, 0, s>>>(part, n, d, out, dtype);
   return launched("sum_rows");
 }
 
@@ -700,8 +1100,10 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
                     starts_runs(p.dsum, rows) && starts_runs(p.dx, rows) &&
                     (p.w == nullptr || starts_runs(p.w, 0, p.w_dtype, 1));
   const int td = p.dy.dtype, th = p.h.dtype;
-  const Spread sp = spread_of(d, wide, td == TPS_F32 || th == TPS_F32, td != th);
-  int64_t parts = rows < kMostBlocks ? rows : kMostBlocks;
+  if (dX == nullptr) p.dx.dtype = th;
+  const int64_t row_bytes = d * (es_of(td) + es_of(th) * (p.dh.p != nullptr ? 2 : 1));
+  const Spread sp = spread_of(rows, d, wide, td == TPS_F32 || th == TPS_F32, td != th, row_bytes, 1);
+  int64_t parts = rows < kSplits ? rows : kSplits;
   if (p.part != nullptr || p.dsum.p != nullptr || p.dx.p != nullptr) {
     using bf16 = __nv_bfloat16;
     const double bytes = double(rows) * double(d) *
@@ -709,8 +1111,8 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
                           (p.dsum.p ? es_of(p.dsum.dtype) : 0) + (p.dx.p ? es_of(p.dx.dtype) : 0));
     ProfScope prof("norm", "bwd", 0.0, bytes, s);
     if (sp.N != 0) {
-      rc = td == TPS_F32 ? (th == TPS_F32 ? launch_bwd_typed<float, float>(p, sp, &parts, s) : launch_bwd_typed<float, bf16>(p, sp, &parts, s))
-                         : (th == TPS_F32 ? launch_bwd_typed<bf16, float>(p, sp, &parts, s) : launch_bwd_typed<bf16, bf16>(p, sp, &parts, s));
+      rc = td == TPS_F32 ? (th == TPS_F32 ? launch_bwd_out<float, float>(p, sp, &parts, s) : launch_bwd_out<float, bf16>(p, sp, &parts, s))
+                         : (th == TPS_F32 ? launch_bwd_out<bf16, float>(p, sp, &parts, s) : launch_bwd_out<bf16, bf16>(p, sp, &parts, s));
     } else {
       if (p.part != nullptr) {  // before the rows' kernel, which may write over dY
         norm_dw_kernel<<<dim3(static_cast<unsigned>((d + kDwCols - 1) / kDwCols), static_cast<unsigned>(parts)), kDwCols, 0, s>>>(p);

@@ -101,24 +101,54 @@ struct Typed {
       w[4 * i + 3] = q.w;
     }
   }
+  __device__ __forceinline__ void store(T* p) const {
+#pragma unroll
+    for (int i = 0; i < kWords / 4; ++i)
+      *(reinterpret_cast<uint4*>(p) + i) = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+  }
   __device__ __forceinline__ float at(int i) const {
     if constexpr (sizeof(T) == 4)
       return __uint_as_float(w[i]);
     else
       return __uint_as_float(i % 2 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
   }
+  __device__ __forceinline__ void set(const float (&v)[N]) {  // rounds
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) w[i] = __float_as_uint(v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / 2; ++i) w[i] = pack_bf16(v[2 * i], v[2 * i + 1]);
+    }
+  }
 };
 template <class T>
 struct Typed<T, 1> {
   T x;
   __device__ __forceinline__ void load(const T* p) { x = *p; }
+  __device__ __forceinline__ void store(T* p) const { *p = x; }
   __device__ __forceinline__ float at(int) const {
     if constexpr (sizeof(T) == 4)
       return x;
     else
       return __bfloat162float(x);
   }
+  __device__ __forceinline__ void set(const float (&v)[1]) {
+    if constexpr (sizeof(T) == 4)
+      x = v[0];
+    else
+      x = __float2bfloat16_rn(v[0]);
+  }
 };
+// a + b of two bf16 runs, rounded once.
+__device__ __forceinline__ void add_bf16(Typed<__nv_bfloat16, 8>& a, const Typed<__nv_bfloat16, 8>& b) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const __nv_bfloat162 x = __hadd2(*reinterpret_cast<const __nv_bfloat162*>(&a.w[i]),
+                                     *reinterpret_cast<const __nv_bfloat162*>(&b.w[i]));
+    a.w[i] = *reinterpret_cast<const uint32_t*>(&x);
+  }
+}
 template <class T>
 constexpr int dtype_of() { return sizeof(T) == 4 ? TPS_F32 : TPS_BF16; }
 
@@ -169,48 +199,59 @@ __device__ __forceinline__ void codes_store(char* p, const RowCodes& c, const fl
 // products are then shared by eight elements, and a pass stays bound by memory;
 // a probability in steps of 2^-16 is off by at most 2^-17, and the multiplier
 // goes with the probability that is used.
+constexpr uint32_t kPhiloxW0 = 0x9e3779b9u, kPhiloxW1 = 0xbb67ae85u;  // what a round adds to the key
 struct Dropout {
   uint64_t seed;
   const int64_t* seed_ptr;  // when set, the seed is read from here
   uint64_t site;
   uint32_t step;   // 0: everything is kept
+  uint32_t keys[20];  // of a seed that the host knows: the two words of each round
+  uint32_t below;  // (step << 16) - 1: 16 bits in the upper half of a word are kept where the word is larger
   float scale;
   __device__ __forceinline__ uint64_t key() const { return seed_ptr != nullptr ? static_cast<uint64_t>(*seed_ptr) : seed; }
 };
 
-__device__ __forceinline__ uint4 philox(uint64_t key, uint64_t index, uint64_t site) {
+__device__ __forceinline__ uint4 philox(const Dropout& d, uint64_t key, uint64_t index) {
   uint32_t c0 = static_cast<uint32_t>(index), c1 = static_cast<uint32_t>(index >> 32);
-  uint32_t c2 = static_cast<uint32_t>(site), c3 = static_cast<uint32_t>(site >> 32);
-  uint32_t k0 = static_cast<uint32_t>(key), k1 = static_cast<uint32_t>(key >> 32);
-#pragma unroll
-  for (int i = 0; i < 10; ++i) {
+  uint32_t c2 = static_cast<uint32_t>(d.site), c3 = static_cast<uint32_t>(d.site >> 32);
+  auto round = [&](uint32_t k0, uint32_t k1) {
     const uint64_t a = static_cast<uint64_t>(c0) * 0xd2511f53u, b = static_cast<uint64_t>(c2) * 0xcd9e8d57u;
     const uint32_t n0 = static_cast<uint32_t>(b >> 32) ^ c1 ^ k0, n2 = static_cast<uint32_t>(a >> 32) ^ c3 ^ k1;
     c1 = static_cast<uint32_t>(b);
     c3 = static_cast<uint32_t>(a);
     c0 = n0;
     c2 = n2;
-    k0 += 0x9e3779b9u;
-    k1 += 0xbb67ae85u;
+  };
+  if (d.seed_ptr == nullptr) {  // the words are operands from the parameters
+#pragma unroll
+    for (int i = 0; i < 10; ++i) round(d.keys[2 * i], d.keys[2 * i + 1]);
+  } else {
+    uint32_t k0 = static_cast<uint32_t>(key), k1 = static_cast<uint32_t>(key >> 32);
+#pragma unroll 1
+    for (int i = 0; i < 10; ++i) {
+      round(k0, k1);
+      k0 += kPhiloxW0;
+      k1 += kPhiloxW1;
+    }
   }
   return make_uint4(c0, c1, c2, c3);
 }
 // v times the mask of the elements from `index` on (N = 8: a multiple of 8).
 // What is dropped is 0 whatever it held.
 __device__ __forceinline__ void drop(const Dropout& d, uint64_t key, int64_t index, float (&v)[8]) {
-  const uint4 u = philox(key, static_cast<uint64_t>(index) >> 3, d.site);
+  const uint4 u = philox(d, key, static_cast<uint64_t>(index) >> 3);
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    v[2 * i] = (w[i] & 0xffffu) >= d.step ? v[2 * i] * d.scale : 0.0f;
-    v[2 * i + 1] = (w[i] >> 16) >= d.step ? v[2 * i + 1] * d.scale : 0.0f;
+    v[2 * i] = (w[i] << 16) > d.below ? v[2 * i] * d.scale : 0.0f;
+    v[2 * i + 1] = w[i] > d.below ? v[2 * i + 1] * d.scale : 0.0f;
   }
 }
 __device__ __forceinline__ void drop(const Dropout& d, uint64_t key, int64_t index, float (&v)[1]) {
-  const uint4 u = philox(key, static_cast<uint64_t>(index) >> 3, d.site);
+  const uint4 u = philox(d, key, static_cast<uint64_t>(index) >> 3);
   const int j = static_cast<int>(index & 7);
   const uint32_t w = j < 4 ? (j < 2 ? u.x : u.y) : (j < 6 ? u.z : u.w);
-  v[0] = (j & 1 ? w >> 16 : w & 0xffffu) >= d.step ? v[0] * d.scale : 0.0f;
+  v[0] = (j & 1 ? w : w << 16) > d.below ? v[0] * d.scale : 0.0f;
 }
 
 }  // namespace tps
