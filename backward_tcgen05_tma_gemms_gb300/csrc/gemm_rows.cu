@@ -17,11 +17,17 @@
 // tokens in rank order, out of each other's shared memory, with the epilogue
 // on the sums.  No workspace, no flags, results do not depend on timing.
 //
+// fp32 operands come as three bf16 planes (GemmDesc::planes): every CTA runs the
+// six products over its part of K, the five that hold remainders into one
+// accumulator and the product of the planes 0 into another, which alone
+// decides about infinities and NaN (T2Drains in gemm_tc2.cu).
+//
 // Warp roles (192 threads): warp 0 loads (TMA), warp 1 issues the MMAs, warps
 // 2..5 drain tensor memory; all of them add and store.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cstdlib>
 #include <cstring>
 #include <mutex>
 
@@ -50,6 +56,7 @@ struct GrParams {
   int T, N;
   int k_tiles, bn, t_tiles, stages, splits;
   uint32_t tmem_cols;
+  int x_plane, w_plane;  // PLANES: elements between planes
   Epilogue epi;
   uint32_t* err;
 };
@@ -142,8 +149,13 @@ __device__ __forceinline__ void rows_join(const Epilogue& e, uint32_t part, uint
   }
 }
 
-// W_MN: W's unit stride is along the features.  CODES: e4m3 operands.
-template <bool W_MN, bool CODES>
+enum GrKind : int { GR_BF16 = 0, GR_CODES = 1, GR_PLANES = 2 };  // e4m3 operands; fp32 as bf16 planes
+// Planes of X and of W in product i, two bits each: 2 1 0 1 0 0 and 0 1 2 0 1 0.
+__device__ __forceinline__ int gr_x_plane(int i) { return (0x046 >> (2 * i)) & 3; }
+__device__ __forceinline__ int gr_w_plane(int i) { return (0x124 >> (2 * i)) & 3; }
+
+// W_MN: W's unit stride is along the features.
+template <bool W_MN, int KIND>
 __global__ void __launch_bounds__(GR_THREADS)
     gemm_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const GrParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -152,7 +164,8 @@ __global__ void __launch_bounds__(GR_THREADS)
   const int stage_bytes = GR_W_BYTES + p.bn * 128;
   GrBarriers* bars = reinterpret_cast<GrBarriers*>(smem + p.stages * stage_bytes);
   volatile uint32_t* abort_flag = &bars->abort;
-  constexpr int kBK = CODES ? 128 : 64;
+  constexpr bool CODES = KIND == GR_CODES, PLANES = KIND == GR_PLANES;
+  constexpr int kBK = CODES ? 128 : 64, kProducts = PLANES ? 6 : 1;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
   const int tile = static_cast<int>(blockIdx.x) / p.splits;
@@ -161,7 +174,26 @@ __global__ void __launch_bounds__(GR_THREADS)
   const int kt_begin = static_cast<int>(static_cast<int64_t>(p.k_tiles) * rank / p.splits);
   const int kt_end = static_cast<int>(static_cast<int64_t>(p.k_tiles) * (rank + 1) / p.splits);
 
+  const int run = kt_end - kt_begin, total = run * kProducts;  // K tiles of a product, and of all
+  auto load = [&](int i) {  // K tile i of this CTA into its stage
+    const int stage = i % p.stages, prod = PLANES ? i / run : 0;
+    const int k0 = (kt_begin + (PLANES ? i - prod * run : i)) * kBK;
+    const int xa = PLANES ? gr_x_plane(prod) * p.x_plane : 0, wa = PLANES ? gr_w_plane(prod) * p.w_plane : 0;
+    uint8_t* sw = smem + stage * stage_bytes;
+    mbar_expect_tx(&bars->full[stage], stage_bytes);
+    if (W_MN) {
+#pragma unroll
+      for (int j = 0; j < GR_FEATURES / 64; ++j)
+        tma_load_2d(sw + j * TC_MN_BOX_BYTES, &tw, &bars->full[stage], n0 + wa + 64 * j, k0);
+    } else {
+      tma_load_2d(sw, &tw, &bars->full[stage], k0 + wa, n0);
+    }
+    tma_load_2d(sw + GR_W_BYTES, &tx, &bars->full[stage], k0 + xa, t0);
+  };
+  int issued = 0;
   if (threadIdx.x == 0) {
+    tma_prefetch_desc(&tw);
+    tma_prefetch_desc(&tx);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(&bars->full[s], 1);
       mbar_init(&bars->empty[s], 1);
@@ -169,8 +201,8 @@ __global__ void __launch_bounds__(GR_THREADS)
     mbar_init(&bars->done, 1);
     bars->abort = 0u;
     fence_mbar_init();
-    tma_prefetch_desc(&tw);
-    tma_prefetch_desc(&tx);
+    // the first loads do not wait for tensor memory
+    for (; issued < total && issued < p.stages; ++issued) load(issued);
   }
   if (warp == 1) {
     tmem_alloc(&bars->tmem_slot, p.tmem_cols);
@@ -180,23 +212,13 @@ __global__ void __launch_bounds__(GR_THREADS)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bars->tmem_slot;
+  const uint32_t main_at = PLANES ? p.tmem_cols / 2 : 0;  // the accumulator of the planes 0
 
   if (warp == 0) {
     if (lane == 0) {
-      int issued = 0;
-      for (int kt = kt_begin; kt < kt_end; ++kt, ++issued) {
-        const int stage = issued % p.stages;
-        if (!mbar_wait(&bars->empty[stage], ((issued / p.stages) & 1) ^ 1u, abort_flag, p.err)) break;
-        uint8_t* sw = smem + stage * stage_bytes;
-        mbar_expect_tx(&bars->full[stage], stage_bytes);
-        if (W_MN) {
-#pragma unroll
-          for (int j = 0; j < GR_FEATURES / 64; ++j)
-            tma_load_2d(sw + j * TC_MN_BOX_BYTES, &tw, &bars->full[stage], n0 + 64 * j, kt * kBK);
-        } else {
-          tma_load_2d(sw, &tw, &bars->full[stage], kt * kBK, n0);
-        }
-        tma_load_2d(sw + GR_W_BYTES, &tx, &bars->full[stage], kt * kBK, t0);
+      for (; issued < total; ++issued) {
+        if (!mbar_wait(&bars->empty[issued % p.stages], ((issued / p.stages) & 1) ^ 1u, abort_flag, p.err)) break;
+        load(issued);
       }
       // Copies in flight finish before the block ends, whatever the MMA thread did.
       for (int i = issued > p.stages ? issued - p.stages : 0; i < issued; ++i)
@@ -205,11 +227,13 @@ __global__ void __launch_bounds__(GR_THREADS)
   } else if (warp == 1) {
     if (lane == 0) {
       const uint32_t idesc = CODES ? idesc_e4m3_f32(GR_FEATURES, p.bn) : idesc_bf16_f32(GR_FEATURES, p.bn, W_MN, false);
-      int i = 0;
-      for (int kt = kt_begin; kt < kt_end; ++kt, ++i) {
+      for (int i = 0; i < total; ++i) {
         const int stage = i % p.stages;
         if (!mbar_wait(&bars->full[stage], (i / p.stages) & 1, abort_flag, p.err)) break;
         tc_fence_after();
+        const bool last = PLANES && i >= 5 * run;  // the product of the planes 0
+        const bool first = i == 0 || (PLANES && i == 5 * run);
+        const uint32_t acc = tmem + (last ? main_at : 0);
         const uint32_t sw = smem_u32(smem + stage * stage_bytes), sx = sw + GR_W_BYTES;
 #pragma unroll
         for (int kk = 0; kk < 4; ++kk) {
@@ -217,9 +241,9 @@ __global__ void __launch_bounds__(GR_THREADS)
                                    : smem_desc_sw128(sw + kk * 32, 16, 1024);
           const uint64_t bd = smem_desc_sw128(sx + kk * 32, 16, 1024);
           if (CODES)
-            tc_mma_f8(tmem, ad, bd, idesc, (i != 0 || kk != 0) ? 1u : 0u);
+            tc_mma_f8(acc, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
           else
-            tc_mma_f16(tmem, ad, bd, idesc, (i != 0 || kk != 0) ? 1u : 0u);
+            tc_mma_f16(acc, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
         }
         tc_commit(&bars->empty[stage]);
       }
@@ -238,6 +262,16 @@ __global__ void __launch_bounds__(GR_THREADS)
       uint32_t r[16];
       tmem_ld_32x32b_x16(t_row + c, r);
       tmem_ld_wait();
+      if constexpr (PLANES) {  // remainders that are not finite are left out
+        uint32_t m[16];
+        tmem_ld_32x32b_x16(t_row + main_at + c, m);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float rest = __uint_as_float(r[i]);
+          r[i] = __float_as_uint(__uint_as_float(m[i]) + (fabsf(rest) < INFINITY ? rest : 0.0f));
+        }
+      }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
         if (c + i < tokens) part[(c + i) * GR_FEATURES] = __uint_as_float(r[i]);
@@ -261,7 +295,7 @@ __global__ void __launch_bounds__(GR_THREADS)
 // The fp32 pipes do it: 2 T operations a weight of four bytes.  A block takes
 // 128 features of the cluster's run of K, with that run of X in shared memory.
 constexpr int GF_ROWS = 8, GF_WARPS = 8;
-constexpr int GF_SHARED = 96 << 10;
+constexpr int GF_SHARED = 96 << 10;  // of X
 
 struct GfParams {
   const float* x;
@@ -277,7 +311,8 @@ struct GfParams {
 // lanes along K; else lanes are along the features and warps along K.
 template <int TT, bool OUT_IN>
 __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams p) {
-  extern __shared__ __align__(16) float xs[];  // OUT_IN: [t][kn], else [k][t]; then [warp][t][128] sums
+  extern __shared__ __align__(16) float part[];  // [t][128] sums (else [warp][t][128]), then X: OUT_IN [t][kn], else [k][t]
+  float* xs = part + (OUT_IN ? 1 : GF_WARPS) * TT * GR_FEATURES;
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = p.splits > 1 ? cluster_ctarank() : 0;
   const int64_t n0 = static_cast<int64_t>(blockIdx.x) / p.splits * GR_FEATURES;
@@ -291,8 +326,6 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
   __syncthreads();
   if constexpr (OUT_IN) {
     constexpr int F = 4, kWarpFeatures = GR_FEATURES / GF_WARPS;
-    float out[kWarpFeatures / F][F][TT];
-#pragma unroll
     for (int g = 0; g < kWarpFeatures / F; ++g) {
       const int64_t n = n0 + w * kWarpFeatures + g * F;
       const float* src[F];  // features past N read the last one
@@ -343,17 +376,8 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
         for (int t = 0; t < TT; ++t) {
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) acc[f][t] += __shfl_xor_sync(0xffffffffu, acc[f][t], o);
-          out[g][f][t] = acc[f][t];
+          if (lane == 0) part[t * GR_FEATURES + w * kWarpFeatures + g * F + f] = acc[f][t];
         }
-    }
-    __syncthreads();  // X is done with
-    if (lane == 0) {
-#pragma unroll
-      for (int g = 0; g < kWarpFeatures / F; ++g)
-#pragma unroll
-        for (int f = 0; f < F; ++f)
-#pragma unroll
-          for (int t = 0; t < TT; ++t) xs[t * GR_FEATURES + w * kWarpFeatures + g * F + f] = out[g][f][t];
     }
   } else {
     constexpr int U = 8;  // loads in flight
@@ -395,24 +419,23 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
         }
       }
     }
-    __syncthreads();  // X is done with
 #pragma unroll
     for (int t = 0; t < TT; ++t)
-      *reinterpret_cast<float4*>(xs + (w * TT + t) * GR_FEATURES + lane * 4) =
+      *reinterpret_cast<float4*>(part + (w * TT + t) * GR_FEATURES + lane * 4) =
           make_float4(acc[t][0], acc[t][1], acc[t][2], acc[t][3]);
     __syncthreads();
     for (int i = threadIdx.x; i < TT * GR_FEATURES; i += 32 * GF_WARPS) {
       float a = 0.0f;
 #pragma unroll
-      for (int q = 0; q < GF_WARPS; ++q) a += xs[q * TT * GR_FEATURES + i];
-      xs[i] = a;  // warp 0's part, read and written by this thread alone
+      for (int q = 0; q < GF_WARPS; ++q) a += part[q * TT * GR_FEATURES + i];
+      part[i] = a;  // warp 0's part, read and written by this thread alone
     }
   }
   if (p.splits > 1)
     cluster_sync();
   else
     __syncthreads();
-  rows_join(p.epi, smem_u32(xs), rank, p.splits, 0, static_cast<int>(p.T), n0, p.N);
+  rows_join(p.epi, smem_u32(part), rank, p.splits, 0, static_cast<int>(p.T), n0, p.N);
   if (p.splits > 1) cluster_sync();
 }
 
@@ -421,12 +444,58 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
 struct GrPlan {
   int bn, t_tiles, n_tiles, k_tiles, splits, stages;
   size_t shared;
+  double cost;  // microseconds
 };
 constexpr int64_t kSms = 152;
+constexpr int GR_SHARED_TWO = 106 << 10, GR_SHARED_ONE = 212 << 10;  // of a CTA, two or one on an SM
 
 // The tile's tokens, the split of K and the stages.  Tiles of up to 64 tokens
-// leave room for two CTAs on an SM.  The split is the one whose CTAs make the
-// least K tiles a CTA in turn.
+// leave room for two CTAs on an SM.  The split (powers of two, up to a portable
+// cluster) is the one whose time, in microseconds, is least:
+//   start and join of a CTA, its K tiles in turn or the reading of W at the
+//   copy's rate, whichever is longer, and what further waves of clusters add.
+// Fitted to calls of 1 to 512 tokens with K and N from 1024 to 14336, which it
+// gives within about 10 %.  With (K, N) = (14336, 4096), (4096, 14336) and
+// (4096, 1024), 1 token takes 78, 27, 25 us with one run, 42, 23, 15 with 2, 25, 26, 10 with 4 and
+// 23, 32, 7.5 with 8, where reading W takes 17.3, 17.3 and 1.2 us.
+double tile_us(int bn) { return 0.32 + 0.0003 * bn; }
+double start_us(int bn, int s) { return 5.5 + 0.01 * bn + 0.04 * bn / s; }
+constexpr double kWaveUs = 3.0;        // a further wave where memory bounds the call
+constexpr double kBytesPerUs = 6.776e6;
+// K tiles of one accumulator of planes: the tensor cores cut each partial sum
+// where fp32 would round it, so that chains stay as short as the drains of
+// gemm_tc2.cu (T2_SUB).
+constexpr int64_t kPlaneRun = 8;
+// Clusters of s CTAs that the device holds at once with one CTA on an SM, by
+// what the driver says of the kernel: an SM group holds whole clusters only (on
+// a GB300 76, 36 and 15 of 2, 4 and 8).
+int64_t clusters_at_once(int s) {
+  static std::mutex mu;
+  static int64_t known[GR_MAX_SPLIT + 1] = {};
+  std::lock_guard<std::mutex> lock(mu);
+  int64_t& n = known[s];
+  if (n == 0) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
+    cfg.blockDim = dim3(GR_THREADS, 1, 1);
+    cfg.dynamicSmemBytes = GR_SHARED_ONE;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int m = 0;
+    if (cudaFuncSetAttribute(gemm_rows_kernel<false, GR_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&m, gemm_rows_kernel<false, GR_BF16>, &cfg) != cudaSuccess || m < 1) {
+      cudaGetLastError();
+      m = static_cast<int>(kSms / s);
+    }
+    n = m;
+  }
+  return n;
+}
 GrPlan plan_of(const GemmDesc& g) {
   GrPlan r;
   r.t_tiles = static_cast<int>((g.M + GR_TOKENS - 1) / GR_TOKENS);
@@ -434,31 +503,43 @@ GrPlan plan_of(const GemmDesc& g) {
   r.n_tiles = static_cast<int>((g.N + GR_FEATURES - 1) / GR_FEATURES);
   const int bk = g.in_dtype == TPS_E4M3 ? 128 : 64;
   r.k_tiles = static_cast<int>((g.K + bk - 1) / bk);
-  const int64_t per_sm = r.bn <= 64 ? 2 : 1, slots = kSms * per_sm;
-  const int64_t tiles = int64_t(r.t_tiles) * r.n_tiles;
+  const int64_t products = g.planes > 1 ? 6 : 1;
+  const int64_t per_sm = r.bn <= 64 ? 2 : 1, tiles = int64_t(r.t_tiles) * r.n_tiles;
   r.splits = 1;
-  int64_t least = -1;
+  r.cost = -1.0;
   for (int s = 1; s <= GR_MAX_SPLIT && s <= r.k_tiles; s *= 2) {
-    const int64_t turns = (tiles * s + slots - 1) / slots * ((r.k_tiles + s - 1) / s);
-    if (least < 0 || turns < least) {
-      least = turns;
+    const int64_t run = (r.k_tiles + s - 1) / s;
+    if (products > 1 && run > kPlaneRun && 2 * s <= GR_MAX_SPLIT && 2 * s <= r.k_tiles) continue;
+    const int64_t clusters = clusters_at_once(s) * per_sm;
+    const double w_us = double(g.N) * double(g.K) * (g.in_dtype == TPS_E4M3 ? 1.0 : 2.0 * double(g.planes)) / kBytesPerUs;
+    const double own = double(run * products) * tile_us(r.bn);
+    double cost;
+    if (per_sm > 1) {  // two CTAs share an SM: waves run into each other
+      const double waves = tiles > clusters ? double(tiles) / double(clusters) : 1.0;
+      cost = start_us(r.bn, s) + (waves * own > w_us ? waves * own : w_us) + (waves - 1.0) * kWaveUs;
+    } else {
+      const double waves = double((tiles + clusters - 1) / clusters), all = waves * (start_us(r.bn, s) + own);
+      cost = all > w_us ? all : w_us;
+    }
+    if (r.cost < 0.0 || cost < r.cost) {
+      r.cost = cost;
       r.splits = s;
     }
   }
   const int stage = GR_W_BYTES + r.bn * 128;
-  const int budget = per_sm == 2 ? (104 << 10) : (208 << 10);
+  const int budget = (per_sm == 2 ? GR_SHARED_TWO : GR_SHARED_ONE) - 2048;
   r.stages = budget / stage < GR_MAX_STAGES ? budget / stage : GR_MAX_STAGES;
   r.shared = 1024 + static_cast<size_t>(r.stages) * stage + sizeof(GrBarriers);
   return r;
 }
 
-template <bool W_MN, bool CODES>
+template <bool W_MN, int KIND>
 int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx, const GrParams& p, const GrPlan& plan,
                  cudaStream_t stream) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, CODES>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   });
   if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -473,9 +554,9 @@ int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  ProfScope prof("gemm_rows", g.name, 2.0 * double(g.M) * double(g.N) * double(g.K),
-                 double(g.K) * double(g.N) * (CODES ? 1 : 2), stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_rows_kernel<W_MN, CODES>, tw, tx, p);
+  ProfScope prof("gemm_rows", g.name, 2.0 * double(g.M) * double(g.N) * double(g.K) * (KIND == GR_PLANES ? 6.0 : 1.0),
+                 double(g.K) * double(g.N) * (KIND == GR_CODES ? 1.0 : 2.0), stream);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_rows_kernel<W_MN, KIND>, tw, tx, p);
   note_launch();
   return e == cudaSuccess ? TPS_OK : TPS_ERR_CUDA;
 }
@@ -499,11 +580,12 @@ static int launch_few(const GemmDesc& g, const GfParams& p, cudaStream_t stream)
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_few_kernel<TT, OUT_IN>, cudaFuncAttributeMaxDynamicSharedMemorySize, GF_SHARED);
+    attr_err = cudaFuncSetAttribute(gemm_few_kernel<TT, OUT_IN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    GF_SHARED + 4 * GF_WARPS * GF_ROWS * GR_FEATURES);
   });
   if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
   const int64_t run = ((p.K + 3) / 4 + p.splits - 1) / p.splits * 4;
-  const int64_t floats = TT * run > GF_WARPS * TT * GR_FEATURES ? TT * run : GF_WARPS * TT * GR_FEATURES;
+  const int64_t floats = TT * run + (OUT_IN ? 1 : GF_WARPS) * TT * GR_FEATURES;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((p.N + GR_FEATURES - 1) / GR_FEATURES * p.splits), 1, 1);
   cfg.blockDim = dim3(32 * GF_WARPS, 1, 1);
@@ -549,28 +631,43 @@ int launch_gemm_few(const GemmDesc& g, cudaStream_t stream) {
 // X K-major; everything else as the CTA-pair kernel wants it.
 bool gemm_rows_supported(const GemmDesc& g) {
   if (g.epi.mode != EPI_LINEAR && g.epi.mode != EPI_STORE) return false;
-  if (g.planes > 1 || g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1 ||
-      g.a_cols > 0 || g.b_cols > 0 || g.a_sk != 1)
+  if (g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1 || g.a_sk != 1)
     return false;
+  if (g.planes == 1 && (g.a_cols > 0 || g.b_cols > 0)) return false;
   if (g.in_dtype == TPS_E4M3 && g.epi.mode != EPI_LINEAR) return false;
   if (!gemm_tc_supported(g)) return false;
   const GrPlan r = plan_of(g);
+  if (g.planes > 1 && (r.k_tiles + r.splits - 1) / r.splits > kPlaneRun) return false;
   return int64_t(r.t_tiles) * r.n_tiles * r.splits < (1ll << 31);
 }
 
-bool gemm_rows_preferred(const GemmDesc& g) { return g.M <= GR_TOKENS; }
+// By what either kernel takes: a pair tile's K tile costs 0.31 us, whatever
+// fills its 256 x 256.  Measured (us, this kernel / pairs, bf16): K = 14336, N =
+// 4096: 256 tokens 35 / 72, 512 55 / 72, 1024 96 / 72; K = 4096, N = 4096: 19 / 26, 26 / 26,
+// 41 / 26; K = 4096, N = 14336: 47 / 31, 77 / 48; K = 1024, N = 4096: 13.5 / 11.9, 17.6 / 12.0.
+// TPS_LINEAR_ROWS=n takes this kernel for up to n rows and no others.
+bool gemm_rows_preferred(const GemmDesc& g) {
+  const char* most = getenv("TPS_LINEAR_ROWS");
+  if (most != nullptr) return g.M <= atoll(most);
+  const GrPlan r = plan_of(g);
+  const int64_t waves = (pair_tile_count(g.M, g.N) + kSms / 2 - 1) / (kSms / 2);
+  return r.cost < 6.0 + 0.31 * double(waves) * double(r.k_tiles) * (g.planes > 1 ? 6.0 : 1.0);
+}
 
 int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
-  const bool w_mn = g.b_sk != 1, codes = g.in_dtype == TPS_E4M3;
+  const bool w_mn = g.b_sk != 1, codes = g.in_dtype == TPS_E4M3, planes = g.planes > 1;
   const GrPlan plan = plan_of(g);
   CUtensorMap tw, tx;
   bool ok;
-  if (codes)
+  if (codes) {
     ok = !w_mn && tc_make_map8(&tw, g.b, g.N, g.K, g.b_sn, 128, GR_FEATURES) &&
          tc_make_map8(&tx, g.a, g.M, g.K, g.a_sm, 128, plan.bn);
-  else
-    ok = (w_mn ? tc_make_map(&tw, g.b, g.K, g.N, g.b_sk, 64, TC_BK) : tc_make_map(&tw, g.b, g.N, g.K, g.b_sn, TC_BK, GR_FEATURES)) &&
-         tc_make_map(&tx, g.a, g.M, g.K, g.a_sm, TC_BK, plan.bn);
+  } else {
+    const int64_t w_cols = planes ? g.b_cols : w_mn ? g.N : g.K, x_cols = planes ? g.a_cols : g.K;
+    ok = (w_mn ? tc_make_map(&tw, g.b, g.K, w_cols, g.b_sk, 64, TC_BK)
+               : tc_make_map(&tw, g.b, g.N, w_cols, g.b_sn, TC_BK, GR_FEATURES)) &&
+         tc_make_map(&tx, g.a, g.M, x_cols, g.a_sm, TC_BK, plan.bn);
+  }
   if (!ok) return TPS_ERR_CUDA;
   GrParams p;
   p.T = static_cast<int>(g.M);
@@ -580,12 +677,19 @@ int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) 
   p.t_tiles = plan.t_tiles;
   p.stages = plan.stages;
   p.splits = plan.splits;
+  p.x_plane = static_cast<int>(g.a_plane);
+  p.w_plane = static_cast<int>(g.b_plane);
   p.tmem_cols = 32;
   while (p.tmem_cols < static_cast<uint32_t>(plan.bn)) p.tmem_cols *= 2;
+  if (planes) p.tmem_cols *= 2;
   p.epi = g.epi;
   p.err = dev_err;
-  if (codes) return launch_typed<false, true>(g, tw, tx, p, plan, stream);
-  return w_mn ? launch_typed<true, false>(g, tw, tx, p, plan, stream) : launch_typed<false, false>(g, tw, tx, p, plan, stream);
+  if (codes) return launch_typed<false, GR_CODES>(g, tw, tx, p, plan, stream);
+  if (planes)
+    return w_mn ? launch_typed<true, GR_PLANES>(g, tw, tx, p, plan, stream)
+                : launch_typed<false, GR_PLANES>(g, tw, tx, p, plan, stream);
+  return w_mn ? launch_typed<true, GR_BF16>(g, tw, tx, p, plan, stream)
+              : launch_typed<false, GR_BF16>(g, tw, tx, p, plan, stream);
 }
 
 }  // namespace tps
