@@ -10,8 +10,9 @@ short calls, is compiled by the host compiler against the installed torch.
 `debug=True` builds libtps_debug.so instead (TPS_DEBUG=1: every direct store
 of the GEMMs' epilogues and of the vocabulary-sharded cross-entropy is checked
 against the bounds of its output, and a store outside is skipped and reported
-as TPS_ERR_BOUNDS; the kernels around the GEMMs of linear_ce.cu, rope.cu and
-optim.cu have no such check).  Set
+as TPS_ERR_BOUNDS, those of the linear product among them; the kernels around
+the GEMMs of linear_ce.cu and linear.cu, rope.cu, optim.cu, norm.cu and
+dropout.cu have no such check).  Set
 TPS_LIBRARY to its path to make the Python binding load it.
 
     python -m backward_tcgen05_tma_gemms_gb300.build [--force] [--debug]

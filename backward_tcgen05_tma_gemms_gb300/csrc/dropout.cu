@@ -49,29 +49,30 @@ struct DropUnit {
 };
 
 // Units of eight consecutive elements, the last one of a row perhaps shorter
-// (FLAT: one row), or of one element (N = 1); kUnits of a thread are in flight
-// together.  The generator and the masking take some hundred instructions a
-// unit, two thirds of the time that memory takes.
-// (Four in flight: 87 us for 8192 x 14336 in bf16, two 84.)
+// (FLAT: one row), or of one element (N = 1).  Two units of a thread are in
+// flight together (8192 x 14336 in bf16: 84 us; four 87).  The generator and the
+// masking take some hundred instructions a unit, two thirds of the time that
+// memory takes.
 constexpr int kUnits = 2;
 template <class TX, class TR, class TY, int N, bool FLAT>
 __global__ void __launch_bounds__(256) dropout_kernel(const DropParams p) {
   const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
   const int64_t units = FLAT ? p.per_row : p.rows * p.per_row, step = int64_t(gridDim.x) * 256;
+  auto row_of = [&](int64_t i) { return FLAT ? 0 : i / p.per_row; };
   const int64_t whole = FLAT ? p.d / N : units;  // FLAT: units before the end
-  for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < whole; i += kUnits * step) {
-    DropUnit<TX, TR, TY, N> u[kUnits];
-    int64_t row[kUnits], col[kUnits];
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-      const int64_t j = i + k * step;
-      row[k] = FLAT ? 0 : j / p.per_row;
-      col[k] = (j - row[k] * p.per_row) * N;
-      if (j < whole) u[k].load(p, row[k], col[k]);
+  int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
+  for (; i < whole; i += kUnits * step) {
+    DropUnit<TX, TR, TY, N> a, b;
+    const int64_t ra = row_of(i), ca = (i - ra * p.per_row) * N, j = i + step;
+    a.load(p, ra, ca);
+    if (j < whole) {
+      const int64_t rb = row_of(j), cb = (j - rb * p.per_row) * N;
+      b.load(p, rb, cb);
+      a.finish(p, key, ra, ca);
+      b.finish(p, key, rb, cb);
+    } else {
+      a.finish(p, key, ra, ca);
     }
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k)
-      if (i + k * step < whole) u[k].finish(p, key, row[k], col[k]);
   }
   if (FLAT && N > 1 && blockIdx.x == 0 && threadIdx.x < p.d - whole * N) {  // the end of the row
     const int64_t c = whole * N + threadIdx.x;

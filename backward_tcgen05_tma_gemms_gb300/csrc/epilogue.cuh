@@ -180,7 +180,27 @@ __device__ __forceinline__ float any_elem(const void* base, int dtype, int64_t i
   return dtype == TPS_F32 ? static_cast<const float*>(base)[i]
                           : __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
 }
-__device__ __forceinline__ float linear_act(int act, float z) { return act == kActNone ? z : act_fwd(act, z); }
+// The activation and its slope, also far from 0: act_fwd holds the sigmoid of
+// SiLU and of the tanh GELU at e^-80 and multiplies it by z, which shows from |z| = 1e33
+// on, and act_grad squares z.  Below -100 both are under 1e-40, above 100 the
+// slope is 1 in fp32.
+constexpr float kActFar = 100.0f;
+template <int ACT>
+__device__ __forceinline__ float linear_act_c(float z) {
+  const float y = act_fwd_c<ACT>(z);
+  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) return z < -kActFar ? 0.0f : y;
+  return y;
+}
+template <int ACT>
+__device__ __forceinline__ float linear_slope_c(float z) {
+  const float y = act_grad_c<ACT>(z);
+  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) return z < -kActFar ? 0.0f : z > kActFar ? 1.0f : y;
+  return y;
+}
+__device__ __forceinline__ float linear_act(int act, float z) {
+  if (act != kActNone) act_dispatch(act, [&](auto A) { z = linear_act_c<decltype(A)::value>(z); });
+  return z;
+}
 // z of one row's columns [col0, col0 + n), n <= C, from the accumulators.
 template <int C>
 __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64_t col0, int n, float (&v)[C]) {
@@ -243,7 +263,7 @@ __device__ __forceinline__ void linear_acted(const Epilogue& e, float (&v)[C]) {
   if (e.act == kActNone) return;
   act_dispatch(e.act, [&](auto A) {
 #pragma unroll
-    for (int i = 0; i < C; ++i) v[i] = act_fwd_c<decltype(A)::value>(v[i]);
+    for (int i = 0; i < C; ++i) v[i] = linear_act_c<decltype(A)::value>(v[i]);
   });
 }
 // The residual's run of 32 columns as loaded (before its conversion, so that

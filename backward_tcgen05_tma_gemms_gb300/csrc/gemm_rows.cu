@@ -106,46 +106,65 @@ __device__ __forceinline__ void rows_load4(const void* base, int dtype, int64_t 
   for (int i = 0; i < 4; ++i) a[i] = i < n ? any_elem(base, dtype, idx + i) : 0.0f;
 }
 
-// Adds up the cluster's partial tiles [token][128] (at the same shared-memory
-// address in every CTA) and stores this CTA's share of the tokens.
+// Adds up the cluster's S partial tiles [token][128] (at the same shared-memory
+// address in every CTA) and stores this CTA's share of the tokens.  A load from
+// another CTA takes about a microsecond: the loads of U items of a thread are
+// in flight together.
+template <int S>
+__device__ __forceinline__ void rows_join_of(const Epilogue& e, uint32_t part, uint32_t rank, int t0, int tokens, int64_t n0,
+                                             int64_t N) {
+  constexpr int U = S <= 2 ? 4 : 2;
+  const int first = tokens * static_cast<int>(rank) / S * 32, last = tokens * (static_cast<int>(rank) + 1) / S * 32;
+  uint32_t from[S];
+#pragma unroll
+  for (int s = 0; s < S; ++s) from[s] = cluster_map(part, s);
+  for (int i0 = first + threadIdx.x; i0 < last; i0 += U * blockDim.x) {
+    float4 q[U][S];
+    float res[U][4];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * blockDim.x, t = i / 32, f = i % 32 * 4;
+      const int64_t row = t0 + t, col = n0 + f;
+      if (i >= last || col >= N) continue;
+#pragma unroll
+      for (int s = 0; s < S; ++s) q[u][s] = ld_cluster_f32x4(from[s] + static_cast<uint32_t>((t * GR_FEATURES + f) * 4));
+      if (e.res != nullptr) rows_load4(e.res, e.res_dtype, row * e.ld_res + col, N - col < 4 ? static_cast<int>(N - col) : 4, res[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int i = i0 + u * blockDim.x, t = i / 32, f = i % 32 * 4;
+      const int64_t row = t0 + t, col = n0 + f;
+      if (i >= last || col >= N) continue;
+      const int n = N - col < 4 ? static_cast<int>(N - col) : 4;
+      float v[4] = {q[u][0].x, q[u][0].y, q[u][0].z, q[u][0].w};
+#pragma unroll
+      for (int s = 1; s < S; ++s) {
+        v[0] += q[u][s].x;
+        v[1] += q[u][s].y;
+        v[2] += q[u][s].z;
+        v[3] += q[u][s].w;
+      }
+      if (!dbg_store_ok(e, row, col, n)) continue;
+      if (e.mode == EPI_LINEAR) {
+        linear_pre(e, row, col, n, v);
+        if (e.d2 != nullptr) rows_store4(e.d2, e.d2_dtype, row * e.ldd2 + col, n, v);
+        linear_acted(e, v);
+        if (e.res != nullptr) {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] += res[u][k];
+        }
+      }
+      rows_store4(e.d, e.d_dtype, row * e.ldd + col, n, v);
+    }
+  }
+}
 __device__ __forceinline__ void rows_join(const Epilogue& e, uint32_t part, uint32_t rank, int splits, int t0, int tokens,
                                           int64_t n0, int64_t N) {
-  const int first = tokens * static_cast<int>(rank) / splits * 32, last = tokens * (static_cast<int>(rank) + 1) / splits * 32;
-  for (int i = first + threadIdx.x; i < last; i += blockDim.x) {
-    const int t = i / 32, f = i % 32 * 4;
-    const int64_t row = t0 + t, col = n0 + f;
-    if (col >= N) continue;
-    const int n = N - col < 4 ? static_cast<int>(N - col) : 4;
-    float res[4];
-    if (e.res != nullptr) rows_load4(e.res, e.res_dtype, row * e.ld_res + col, n, res);
-    const uint32_t at = part + static_cast<uint32_t>((t * GR_FEATURES + f) * 4);
-    float4 q[GR_MAX_SPLIT];
-#pragma unroll
-    for (int s = 0; s < GR_MAX_SPLIT; ++s)
-      if (s < splits) q[s] = ld_cluster_f32x4(cluster_map(at, s));
-    float v[4] = {q[0].x, q[0].y, q[0].z, q[0].w};
-#pragma unroll
-    for (int s = 1; s < GR_MAX_SPLIT; ++s)
-      if (s < splits) {
-        v[0] += q[s].x;
-        v[1] += q[s].y;
-        v[2] += q[s].z;
-        v[3] += q[s].w;
-      }
-    if (!dbg_store_ok(e, row, col, n)) continue;
-    if (e.mode == EPI_LINEAR) {
-      linear_pre(e, row, col, n, v);
-      if (e.d2 != nullptr) rows_store4(e.d2, e.d2_dtype, row * e.ldd2 + col, n, v);
-      if (e.act != kActNone) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = act_fwd(e.act, v[k]);
-      }
-      if (e.res != nullptr) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] += res[k];
-      }
-    }
-    rows_store4(e.d, e.d_dtype, row * e.ldd + col, n, v);
+  switch (splits) {
+    case 1: rows_join_of<1>(e, part, rank, t0, tokens, n0, N); break;
+    case 2: rows_join_of<2>(e, part, rank, t0, tokens, n0, N); break;
+    case 4: rows_join_of<4>(e, part, rank, t0, tokens, n0, N); break;
+    default: rows_join_of<8>(e, part, rank, t0, tokens, n0, N); break;
   }
 }
 
@@ -201,6 +220,7 @@ __global__ void __launch_bounds__(GR_THREADS)
     mbar_init(&bars->done, 1);
     bars->abort = 0u;
     fence_mbar_init();
+    fence_async_smem();  // this thread's copies count on them at once
     // the first loads do not wait for tensor memory
     for (; issued < total && issued < p.stages; ++issued) load(issued);
   }

@@ -41,16 +41,19 @@ struct DzParams {
 };
 
 // A warp takes 32 runs of N elements of a row, a block eight rows at a time, every
-// gridDim.y-th group of eight; the columns' sums stay in registers.
-template <int N>
-__global__ void __launch_bounds__(32 * kDzRows) linear_dz_kernel(const DzParams p) {
+// gridDim.y-th group of eight; the columns' sums stay in registers.  Some 25
+// instructions an element with an activation (two of them on the special function
+// unit), nearly the time that memory takes: the activation is a type, and four blocks an SM
+// leave loads in flight.
+template <int N, int ACT>
+__global__ void __launch_bounds__(32 * kDzRows, 4) linear_dz_kernel(const DzParams p) {
   __shared__ float sums[kDzRows][32 * N + 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int64_t c0 = static_cast<int64_t>(blockIdx.x) * 32 * N, c = c0 + lane * N;
   float s[N];
 #pragma unroll
   for (int i = 0; i < N; ++i) s[i] = 0.0f;
-  constexpr int U = N == 8 ? 2 : 4;  // rows whose loads are in flight
+  constexpr int U = 2;  // rows whose loads are in flight
   const int64_t step = static_cast<int64_t>(gridDim.y) * kDzRows;
   if (c < p.N) {
     for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + w; r0 < p.T; r0 += U * step) {
@@ -60,7 +63,7 @@ __global__ void __launch_bounds__(32 * kDzRows) linear_dz_kernel(const DzParams 
         const int64_t r = r0 + u * step;
         if (r < p.T) {
           raw_load(p.dy.at(r, c), p.dy.dtype, a[u]);
-          if (p.z.p != nullptr) raw_load(p.z.at(r, c), p.z.dtype, b[u]);
+          if (ACT != kActNone) raw_load(p.z.at(r, c), p.z.dtype, b[u]);
         }
       }
 #pragma unroll
@@ -69,13 +72,11 @@ __global__ void __launch_bounds__(32 * kDzRows) linear_dz_kernel(const DzParams 
         if (r >= p.T) continue;
         float v[N];
         raw_value(a[u], p.dy.dtype, v);
-        if (p.z.p != nullptr) {
+        if constexpr (ACT != kActNone) {
           float z[N];
           raw_value(b[u], p.z.dtype, z);
-          act_dispatch(p.act, [&](auto A) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) v[i] *= act_grad_c<decltype(A)::value>(z[i]);
-          });
+          for (int i = 0; i < N; ++i) v[i] *= linear_slope_c<ACT>(z[i]);
         }
         if (p.dz.p != nullptr) run_store(p.dz.at(r, c), p.dz.dtype, v);
 #pragma unroll
@@ -93,6 +94,16 @@ __global__ void __launch_bounds__(32 * kDzRows) linear_dz_kernel(const DzParams 
 #pragma unroll
     for (int q = 0; q < kDzRows; ++q) t += sums[q][i];
     p.part[static_cast<int64_t>(blockIdx.y) * p.N + c0 + i] = t;
+  }
+}
+template <int N>
+void launch_dz(const DzParams& p, dim3 grid, cudaStream_t s) {
+  switch (p.act) {
+    case TPS_ACT_GELU_ERF: linear_dz_kernel<N, TPS_ACT_GELU_ERF><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_GELU_TANH: linear_dz_kernel<N, TPS_ACT_GELU_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_TANH: linear_dz_kernel<N, TPS_ACT_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_SILU: linear_dz_kernel<N, TPS_ACT_SILU><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    default: linear_dz_kernel<N, kActNone><<<grid, 32 * kDzRows, 0, s>>>(p); break;
   }
 }
 
@@ -338,17 +349,15 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
   if (p.dz.p != nullptr || p.part != nullptr) {
     const bool wide = c.N % 8 == 0 && starts_runs(p.dy, c.T) && starts_runs(p.z, c.T) && starts_runs(p.dz, c.T);
     const int64_t gx = (c.N + (wide ? 256 : 32) - 1) / (wide ? 256 : 32), groups = (c.T + kDzRows - 1) / kDzRows;
-    // about eight blocks an SM; every block several groups of rows
-    int64_t gy = (152 * 8 + gx - 1) / gx;
+    // four waves of four blocks an SM, as far as there are groups of rows
+    int64_t gy = 152 * 16 / gx;
     if (gy > groups) gy = groups;
     if (gy > kParts) gy = kParts;
+    if (gy < 1) gy = 1;
     ProfScope prof("linear_dz", "bwd", 0.0,
                    double(c.T) * double(c.N) * (es_of(p.dy.dtype) + (p.z.p ? es_of(p.z.dtype) : 0) + (p.dz.p ? es : 0)), s);
     const dim3 grid(static_cast<unsigned>(gx), static_cast<unsigned>(gy));
-    if (wide)
-      linear_dz_kernel<8><<<grid, 32 * kDzRows, 0, s>>>(p);
-    else
-      linear_dz_kernel<1><<<grid, 32 * kDzRows, 0, s>>>(p);
+    wide ? launch_dz<8>(p, grid, s) : launch_dz<1>(p, grid, s);
     if ((rc = launched("linear_dz"))) return rc;
     if (p.part != nullptr && (rc = launch_sum_rows(p.part, gy, c.N, dbias->data, dbias->dtype, s))) return rc;
   }

@@ -391,6 +391,7 @@ __device__ __forceinline__ void ring_start(const RingSource& s, RowRing* ring, c
     for (int i = 0; i < stages; ++i) mbar_init(&ring->full[i], 1);
     ring->abort = 0u;
     fence_mbar_init();
+    fence_async_smem();
   }
   __syncthreads();
   if (threadIdx.x < 32)
@@ -420,20 +421,22 @@ __device__ __forceinline__ void ring_weights(const char* w, int dtype, int c0, i
 }
 // Blocks of kRingThreads threads on an SM that the registers are to allow, by
 // the floats of a thread that live through a row.
-constexpr int ring_blocks(int floats) { return floats <= 32 ? 3 : floats <= 72 ? 2 : 1; }
+constexpr int ring_blocks(int floats) { return floats <= 16 ? 4 : floats <= 32 ? 3 : floats <= 72 ? 2 : 1; }
 constexpr int ring_fwd_blocks(int R, bool wide_h) { return ring_blocks(R * 8 + R * (wide_h ? 8 : 4)); }
 constexpr int ring_bwd_blocks(int R) { return ring_blocks(2 * R * 8); }
 
-// R runs of eight elements a thread, lane + k G in the row.
-template <class TX, class TR, class TY, int R>
-__global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) == 4))
+// R runs of eight elements a thread, lane + k G in the row.  BARE: codes of x
+// alone, without weights, norm and sum.
+template <class TX, class TR, class TY, int R, bool BARE>
+__global__ void __launch_bounds__(kRingThreads, BARE ? ring_blocks(R * (sizeof(TR) == 4 ? 8 : 4)) : ring_fwd_blocks(R, sizeof(TR) == 4))
     norm_fwd_ring_kernel(const NormParams p, const int G) {
   constexpr bool CODES = sizeof(TY) == 1;
   __shared__ float2 buf[2][kMaxWarps];
   __shared__ RowRing ring;
   extern __shared__ __align__(128) char stages_at[];
   const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
-  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, joined = p.res.p != nullptr;
+  const bool normed = !BARE && p.rstd != nullptr, summed = !BARE && p.h.p != nullptr, joined = !BARE && p.res.p != nullptr;
+  const bool drops = !BARE && p.drop.step != 0u;
   const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
   int64_t row0 = static_cast<int64_t>(blockIdx.x) * groups;
   const RingSource src = {{p.x.p, p.res.p, nullptr},
@@ -442,10 +445,10 @@ __global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) ==
   ring_start(src, &ring, stages_at, p.stages, groups, row0, step, p.rows);
   const int c0 = lane * 8, stride = G * 8;
   float w[R][8];
-  ring_weights(p.w, p.w_dtype, c0, stride, d, w);
+  if constexpr (!BARE) ring_weights(p.w, p.w_dtype, c0, stride, d, w);
   TR* hp = reinterpret_cast<TR*>(p.h.p) + (row0 + group) * p.h.ld + c0;
   TY* yp = reinterpret_cast<TY*>(p.y.p) + (row0 + group) * p.y.ld + c0;
-  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  const uint64_t key = drops ? p.drop.key() : 0;
   int stage = 0, turn = 0;
   uint32_t phase = 0;
   for (; row0 < p.rows; row0 += step) {
@@ -466,12 +469,12 @@ __global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) ==
         if (joined) r.load(rs + k * stride);
         bool have = false;
         if constexpr (sizeof(TX) == sizeof(TR)) {
-          if (p.drop.step == 0u && !joined) {
+          if (!drops && !joined) {
             h[k] = x;
             have = true;
           }
           if constexpr (sizeof(TX) == 2) {
-            if (p.drop.step == 0u && joined) {  // one rounding, two values an instruction
+            if (!drops && joined) {  // one rounding, two values an instruction
               h[k] = x;
               add_bf16(h[k], r);
               have = true;
@@ -482,7 +485,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) ==
           float v[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) v[i] = x.at(i);
-          if (p.drop.step != 0u) drop(p.drop, key, (row0 + group) * d + c0 + k * stride, v);
+          if (drops) drop(p.drop, key, (row0 + group) * d + c0 + k * stride, v);
           if (joined) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) v[i] += r.at(i);
@@ -490,11 +493,17 @@ __global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) ==
           h[k].set(v);
         }
         if (summed) h[k].store(hp + k * stride);
+        if constexpr (!BARE) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float v = h[k].at(i);
-          own.sum = fmaf(v, v, own.sum);
-          if (CODES) own.top = max_nan(own.top, fabsf(v * w[k][i]), 0.0f);
+          for (int i = 0; i < 8; ++i) own.sum = fmaf(h[k].at(i), h[k].at(i), own.sum);
+        }
+        if constexpr (CODES) {
+#pragma unroll
+          for (int i = 0; i < 8; i += 2) {
+            const float u = h[k].at(i), v = h[k].at(i + 1);
+            own.top = BARE ? max_nan(own.top, fabsf(u), fabsf(v))
+                           : max_nan(own.top, fabsf(u * w[k][i]), fabsf(v * w[k][i + 1]));
+          }
         }
       }
     }
@@ -518,7 +527,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_fwd_blocks(R, sizeof(TR) ==
         if (c0 + k * stride >= d) continue;
         float v[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = h[k].at(i) * w[k][i];
+        for (int i = 0; i < 8; ++i) v[i] = BARE ? h[k].at(i) : h[k].at(i) * w[k][i];
         if constexpr (CODES) {
           codes_store(reinterpret_cast<char*>(yp + k * stride), codes, v);
         } else {
@@ -807,8 +816,9 @@ constexpr int kRingShared = 216 << 10;  // of an SM
 struct Spread {
   int N, R, G, threads, ring, per_sm;
 };
-// row_bytes: of one row of all tensors that are read.  heavy: the backward pass, whose threads hold dw too.
-Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int64_t row_bytes, int heavy) {
+// row_bytes: of one row of all tensors that are read.
+enum Pass { FORWARD, BACKWARD, CODES_ONLY };
+Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int64_t row_bytes, Pass kind) {
   Spread s = {0, 0, 0, 0, 0, 0};
   if (wide) {
     const int64_t runs = (d + 7) / 8;
@@ -820,7 +830,7 @@ Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int6
       r.threads = r.G < 128 ? 128 : r.G;
       const int64_t stage = row_bytes * (r.threads / r.G);
       // registers: floats of a thread that live through a row
-      const int floats = heavy ? 2 * r.R * 8 : r.R * 8 + r.R * (fp32 ? 8 : 4);
+      const int floats = (kind == BACKWARD ? 16 : kind == FORWARD ? 8 : 0) * r.R + (kind == BACKWARD ? 0 : r.R * (fp32 ? 8 : 4));
       const int most = ring_blocks(floats) * kRingThreads / r.threads;
       for (int per = most; per >= 1 && r.ring == 0; --per) {
         const int64_t n = (kRingShared / per - 2048) / stage;
@@ -842,7 +852,7 @@ Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int6
   s.G = need <= 32 ? 32 : round_pow2(need);
   s.threads = s.G < 256 ? 256 : s.G;
   while (s.threads > s.G && (rows * s.G + s.threads - 1) / s.threads < 2 * kSms) s.threads /= 2;  // few rows: a block each
-  s.per_sm = (heavy ? 512 : 1024) / s.threads;
+  s.per_sm = (kind == BACKWARD ? 512 : 1024) / s.threads;
   return s;
 }
 
@@ -870,10 +880,16 @@ int launch_fwd(NormParams p, const Spread& sp, cudaStream_t s) {
   int rc;
   if constexpr (RING) {
     const size_t shared = static_cast<size_t>(sp.ring) * (sp.threads / sp.G) * p.d * (sizeof(TX) + (p.res.p ? sizeof(TR) : 0));
-    if ((rc = ring_ready(sp, &p.stages, &p.err)) ||
-        (rc = prepare_launch(norm_fwd_ring_kernel<TX, TR, TY, R>, sp, p.rows, shared, &blocks)))
-      return rc;
-    norm_fwd_ring_kernel<TX, TR, TY, R><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
+    if ((rc = ring_ready(sp, &p.stages, &p.err))) return rc;
+    if constexpr (sizeof(TY) == 1 && sizeof(TX) == sizeof(TR)) {
+      if (p.rstd == nullptr) {
+        if ((rc = prepare_launch(norm_fwd_ring_kernel<TX, TR, TY, R, true>, sp, p.rows, shared, &blocks))) return rc;
+        norm_fwd_ring_kernel<TX, TR, TY, R, true><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
+        return launched("quantize");
+      }
+    }
+    if ((rc = prepare_launch(norm_fwd_ring_kernel<TX, TR, TY, R, false>, sp, p.rows, shared, &blocks))) return rc;
+    norm_fwd_ring_kernel<TX, TR, TY, R, false><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
   } else {
     const size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
     if ((rc = prepare_launch(norm_fwd_kernel<TX, TR, TY, N, R>, sp, p.rows, shared, &blocks))) return rc;
@@ -906,7 +922,7 @@ int launch_norm_fwd(const NormParams& p, const char* label, cudaStream_t s) {
   const int tx = p.x.dtype, tr = p.res.p != nullptr ? p.res.dtype : tx;
   const bool codes = p.y.dtype == TPS_E4M3;
   const int64_t row_bytes = p.d * (es_of(tx) + (p.res.p != nullptr ? es_of(tr) : 0));
-  const Spread sp = spread_of(p.rows, p.d, wide, tx == TPS_F32 || tr == TPS_F32, tx != tr, row_bytes, 0);
+  const Spread sp = spread_of(p.rows, p.d, wide, tx == TPS_F32 || tr == TPS_F32, tx != tr, row_bytes, p.rstd == nullptr ? CODES_ONLY : FORWARD);
   const double bytes = double(p.rows) * double(p.d) *
                        (es_of(p.x.dtype) + (p.res.p ? es_of(p.res.dtype) : 0) + (p.h.p ? es_of(p.h.dtype) : 0) + es_of(p.y.dtype));
   ProfScope prof("norm", label, 0.0, bytes, s);
@@ -966,15 +982,15 @@ int launch_bwd_out(const NormBwdParams& p, const Spread& sp, int64_t* parts, cud
 // Sum of `n` rows of d floats to out (f32 or bf16), in row order.
 __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64_t n, int64_t d, void* out, int dtype) {
   __shared__ float s[32][33];
-  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float acc = 0.0f;
   if (c < d) {
     constexpr int U = 8;  // loads in flight
-    for (int64_t i = w; i < n; i += U * 32) {
+    for (int64_t i = w; i < n; i += U * warps) {
       float x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = i + u * 32 < n ? __ldg(part + (i + u * 32) * d + c) : 0.0f;
+      for (int u = 0; u < U; ++u) x[u] = i + u * warps < n ? __ldg(part + (i + u * warps) * d + c) : 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) acc += x[u];
     }
@@ -983,8 +999,7 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64
   __syncthreads();
   if (w != 0 || c >= d) return;
   acc = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) acc += s[i][lane];
+  for (int i = 0; i < warps; ++i) acc += s[i][lane];
   if (dtype == TPS_F32)
     static_cast<float*>(out)[c] = acc;
   else
@@ -993,7 +1008,8 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64
 
 int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, cudaStream_t s) {
   ProfScope prof("sum_rows", "dw", 0.0, 4.0 * double(n) * double(d), s);
-  sum_rows_kernel<<<static_cast<unsigned>((d + 31) / 32), 1024, 0, s>>>(part, n, d, out, dtype);
+  const int64_t warps = (n + 7) / 8 < 32 ? (n + 7) / 8 : 32;  // eight rows a warp at a time
+  sum_rows_kernel<<<static_cast<unsigned>((d + 31) / 32), static_cast<unsigned>(32 * warps), 0, s>>>(part, n, d, out, dtype);
   return launched("sum_rows");
 }
 
@@ -1102,7 +1118,7 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
   const int td = p.dy.dtype, th = p.h.dtype;
   if (dX == nullptr) p.dx.dtype = th;
   const int64_t row_bytes = d * (es_of(td) + es_of(th) * (p.dh.p != nullptr ? 2 : 1));
-  const Spread sp = spread_of(rows, d, wide, td == TPS_F32 || th == TPS_F32, td != th, row_bytes, 1);
+  const Spread sp = spread_of(rows, d, wide, td == TPS_F32 || th == TPS_F32, td != th, row_bytes, BACKWARD);
   int64_t parts = rows < kSplits ? rows : kSplits;
   if (p.part != nullptr || p.dsum.p != nullptr || p.dx.p != nullptr) {
     using bf16 = __nv_bfloat16;

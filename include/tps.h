@@ -7,7 +7,9 @@
  * gated), the head-split attention projections and the vocabulary-sharded
  * cross-entropy, and what a training step needs beside them: the head's
  * cross-entropy without its logits, rotary positions and the AdamW step with
- * the gradients' norm.  On one GPU the logical ranks are shard
+ * the gradients' norm; and what stands between the products of a layer: the
+ * norm with residual and dropout, and the product with bias, activation and
+ * residual, also on 8-bit numbers.  On one GPU the logical ranks are shard
  * partitions of the same device buffers: a result the pages concatenate is a
  * range of one output buffer, and a result the pages sum over ranks is
  * accumulated inside the producing kernel (the contraction loop runs over
@@ -44,8 +46,10 @@
  *   - CUDA graphs.  tps_matmul_fwd_bwd, tps_mlp_fwd_bwd, tps_glu_mlp_fwd_bwd,
  *     tps_attn_qkv_fwd, tps_attn_qkv_bwd, tps_attn_out_fwd_bwd,
  *     tps_vocab_ce_fwd_bwd, tps_vocab_ce_fwd_bwd_ex, tps_linear_ce_fwd,
- *     tps_linear_ce_bwd, tps_rope_fwd, tps_rope_bwd, tps_grad_norm and
- *     tps_adamw_step enqueue only kernel launches and memsets on `cuda_stream`; their one-time set-up runs on
+ *     tps_linear_ce_bwd, tps_rope_fwd, tps_rope_bwd, tps_grad_norm,
+ *     tps_adamw_step, tps_rmsnorm_fwd, tps_rmsnorm_bwd, tps_dropout_fwd,
+ *     tps_dropout_bwd, tps_quantize_e4m3, tps_linear_fwd and tps_linear_bwd
+ *     enqueue only kernel launches and memsets on `cuda_stream`; their one-time set-up runs on
  *     the first call on a device.  After one such call they may be captured
  *     into a CUDA graph; a replay reads and writes the buffers given at
  *     capture.  tps_last_device_error synchronizes and must not be captured.

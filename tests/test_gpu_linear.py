@@ -197,6 +197,27 @@ def test_not_finite():
             assert torch.isfinite(y[~bad]).all() and torch.isinf(y[1, :7]).all() and torch.isnan(y[:, 7]).all()
 
 
+@pytest.mark.parametrize("act", ACTS)
+def test_far_from_zero(act):
+    """Pre-activations up to the end of the types: the activation is z or 0, its slope 1 or 0 (tanh: 1 and 0)."""
+    far = torch.tensor([1e38, 1e30, 1e20, 1e10, 300.0, 150.0, 101.0, 99.0, 60.0], device="cuda")
+    far = torch.cat((far, -far)).to(BF)
+    for T in (1, 40, 300):
+        for t in (BF, FP):
+            x = torch.zeros(T, 64, device="cuda").to(t)
+            x[:, 0] = 1
+            W = torch.zeros(64, 24, device="cuda").to(t)
+            W[0, :18] = far.to(t)
+            y, z = api.linear_fwd(x, W, act=act, want_pre=True)
+            assert torch.equal(z[:, :18], far.to(t).expand(T, 18))
+            want = act64(far.double(), act)
+            assert ((y[:, :18].double() - want).abs() <= (half(t) + 2.0 ** -18) * want.abs() + 1e-20).all()
+            if act:
+                _, _, db = api.linear_bwd(x, W, torch.ones_like(z), pre=z, act=act)
+                slope = (far > 0).double() if act != "tanh" else torch.zeros(18, device="cuda").double()
+                assert ((db[:18].double() - T * slope).abs() <= 2.0 ** -18 * T).all()
+
+
 def backward(T, K, N, t, layout="in_out", act=None, yt=None, grads=None, want=(1, 1, 1), extra=0, shift=0):
     g = gen(T, K, N, 7)
     x, W, _, _, x64, W64 = operands(T, K, N, t, layout, g, extra, shift)
