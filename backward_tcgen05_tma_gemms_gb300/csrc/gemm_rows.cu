@@ -7,8 +7,9 @@
 // the tensor core's tile and up to 256 tokens its columns, so that the 128
 // lanes of tensor memory are full of features however few tokens there are
 // (tiles of tokens x features would leave all but a few of their rows empty).
-// W is the A operand in either layout, X, K-major, the B operand; the
-// accumulator holds Y transposed.
+// W is the A operand in either layout, X the B operand; the accumulator holds Y
+// transposed.  X is K-major, or, for a weight gradient, has its unit stride
+// along the rows, as W then has along the features.
 //
 // The 128-feature tiles alone are too few for the SMs and for the bytes in
 // flight that memory wants, so a cluster of up to eight CTAs splits K: each
@@ -173,8 +174,8 @@ enum GrKind : int { GR_BF16 = 0, GR_CODES = 1, GR_PLANES = 2 };  // e4m3 operand
 __device__ __forceinline__ int gr_x_plane(int i) { return (0x046 >> (2 * i)) & 3; }
 __device__ __forceinline__ int gr_w_plane(int i) { return (0x124 >> (2 * i)) & 3; }
 
-// W_MN: W's unit stride is along the features.
-template <bool W_MN, int KIND>
+// W_MN: W's unit stride is along the features.  X_MN: X's along the rows.
+template <bool W_MN, bool X_MN, int KIND>
 __global__ void __launch_bounds__(GR_THREADS)
     gemm_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const GrParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -207,7 +208,12 @@ __global__ void __launch_bounds__(GR_THREADS)
     } else {
       tma_load_2d(sw, &tw, &bars->full[stage], k0 + wa, n0);
     }
-    tma_load_2d(sw + GR_W_BYTES, &tx, &bars->full[stage], k0 + xa, t0);
+    if (X_MN) {  // boxes of 64 rows of X
+      for (int j = 0; j < p.bn / 64; ++j)
+        tma_load_2d(sw + GR_W_BYTES + j * TC_MN_BOX_BYTES, &tx, &bars->full[stage], t0 + xa + 64 * j, k0);
+    } else {
+      tma_load_2d(sw + GR_W_BYTES, &tx, &bars->full[stage], k0 + xa, t0);
+    }
   };
   int issued = 0;
   if (threadIdx.x == 0) {
@@ -246,7 +252,7 @@ __global__ void __launch_bounds__(GR_THREADS)
     }
   } else if (warp == 1) {
     if (lane == 0) {
-      const uint32_t idesc = CODES ? idesc_e4m3_f32(GR_FEATURES, p.bn) : idesc_bf16_f32(GR_FEATURES, p.bn, W_MN, false);
+      const uint32_t idesc = CODES ? idesc_e4m3_f32(GR_FEATURES, p.bn) : idesc_bf16_f32(GR_FEATURES, p.bn, W_MN, X_MN);
       for (int i = 0; i < total; ++i) {
         const int stage = i % p.stages;
         if (!mbar_wait(&bars->full[stage], (i / p.stages) & 1, abort_flag, p.err)) break;
@@ -259,7 +265,8 @@ __global__ void __launch_bounds__(GR_THREADS)
         for (int kk = 0; kk < 4; ++kk) {
           const uint64_t ad = W_MN ? smem_desc_sw128(sw + kk * 2048, TC_MN_BOX_BYTES, 1024)
                                    : smem_desc_sw128(sw + kk * 32, 16, 1024);
-          const uint64_t bd = smem_desc_sw128(sx + kk * 32, 16, 1024);
+          const uint64_t bd = X_MN ? smem_desc_sw128(sx + kk * 2048, TC_MN_BOX_BYTES, 1024)
+                                   : smem_desc_sw128(sx + kk * 32, 16, 1024);
           if (CODES)
             tc_mma_f8(acc, ad, bd, idesc, (!first || kk != 0) ? 1u : 0u);
           else
@@ -507,8 +514,8 @@ int64_t clusters_at_once(int s) {
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     int m = 0;
-    if (cudaFuncSetAttribute(gemm_rows_kernel<false, GR_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&m, gemm_rows_kernel<false, GR_BF16>, &cfg) != cudaSuccess || m < 1) {
+    if (cudaFuncSetAttribute(gemm_rows_kernel<false, false, GR_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&m, gemm_rows_kernel<false, false, GR_BF16>, &cfg) != cudaSuccess || m < 1) {
       cudaGetLastError();
       m = static_cast<int>(kSms / s);
     }
@@ -519,7 +526,8 @@ int64_t clusters_at_once(int s) {
 GrPlan plan_of(const GemmDesc& g) {
   GrPlan r;
   r.t_tiles = static_cast<int>((g.M + GR_TOKENS - 1) / GR_TOKENS);
-  r.bn = static_cast<int>(((g.M + r.t_tiles - 1) / r.t_tiles + 15) / 16 * 16);
+  const int64_t unit = g.a_sk == 1 ? 16 : 64;  // boxes of 64 rows where X's unit stride is along them
+  r.bn = static_cast<int>(((g.M + r.t_tiles - 1) / r.t_tiles + unit - 1) / unit * unit);
   r.n_tiles = static_cast<int>((g.N + GR_FEATURES - 1) / GR_FEATURES);
   const int bk = g.in_dtype == TPS_E4M3 ? 128 : 64;
   r.k_tiles = static_cast<int>((g.K + bk - 1) / bk);
@@ -553,13 +561,13 @@ GrPlan plan_of(const GemmDesc& g) {
   return r;
 }
 
-template <bool W_MN, int KIND>
+template <bool W_MN, bool X_MN, int KIND>
 int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx, const GrParams& p, const GrPlan& plan,
                  cudaStream_t stream) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
+    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, X_MN, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
   });
   if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
@@ -576,7 +584,7 @@ int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx
   cfg.numAttrs = 1;
   ProfScope prof("gemm_rows", g.name, 2.0 * double(g.M) * double(g.N) * double(g.K) * (KIND == GR_PLANES ? 6.0 : 1.0),
                  double(g.K) * double(g.N) * (KIND == GR_CODES ? 1.0 : 2.0), stream);
-  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_rows_kernel<W_MN, KIND>, tw, tx, p);
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, gemm_rows_kernel<W_MN, X_MN, KIND>, tw, tx, p);
   note_launch();
   return e == cudaSuccess ? TPS_OK : TPS_ERR_CUDA;
 }
@@ -648,11 +656,11 @@ int launch_gemm_few(const GemmDesc& g, cudaStream_t stream) {
   return out_in ? launch_few<8, true>(g, p, stream) : launch_few<8, false>(g, p, stream);
 }
 
-// X K-major; everything else as the CTA-pair kernel wants it.
+// X K-major, or both operands the other way; everything else as the CTA-pair kernel wants it.
 bool gemm_rows_supported(const GemmDesc& g) {
   if (g.epi.mode != EPI_LINEAR && g.epi.mode != EPI_STORE) return false;
-  if (g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1 || g.a_sk != 1)
-    return false;
+  if (g.n_segs > 1 || g.K2 > 0 || g.K3 > 0 || g.epi.accumulate || g.epi.alpha != nullptr || g.kparts > 1) return false;
+  if (g.a_sk != 1 && (g.a_sm != 1 || g.b_sk == 1)) return false;
   if (g.planes == 1 && (g.a_cols > 0 || g.b_cols > 0)) return false;
   if (g.in_dtype == TPS_E4M3 && g.epi.mode != EPI_LINEAR) return false;
   if (!gemm_tc_supported(g)) return false;
@@ -675,7 +683,7 @@ bool gemm_rows_preferred(const GemmDesc& g) {
 }
 
 int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) {
-  const bool w_mn = g.b_sk != 1, codes = g.in_dtype == TPS_E4M3, planes = g.planes > 1;
+  const bool w_mn = g.b_sk != 1, x_mn = g.a_sk != 1, codes = g.in_dtype == TPS_E4M3, planes = g.planes > 1;
   const GrPlan plan = plan_of(g);
   CUtensorMap tw, tx;
   bool ok;
@@ -683,10 +691,10 @@ int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) 
     ok = !w_mn && tc_make_map8(&tw, g.b, g.N, g.K, g.b_sn, 128, GR_FEATURES) &&
          tc_make_map8(&tx, g.a, g.M, g.K, g.a_sm, 128, plan.bn);
   } else {
-    const int64_t w_cols = planes ? g.b_cols : w_mn ? g.N : g.K, x_cols = planes ? g.a_cols : g.K;
+    const int64_t w_cols = planes ? g.b_cols : w_mn ? g.N : g.K, x_cols = planes ? g.a_cols : x_mn ? g.M : g.K;
     ok = (w_mn ? tc_make_map(&tw, g.b, g.K, w_cols, g.b_sk, 64, TC_BK)
                : tc_make_map(&tw, g.b, g.N, w_cols, g.b_sn, TC_BK, GR_FEATURES)) &&
-         tc_make_map(&tx, g.a, g.M, x_cols, g.a_sm, TC_BK, plan.bn);
+         (x_mn ? tc_make_map(&tx, g.a, g.K, x_cols, g.a_sk, 64, TC_BK) : tc_make_map(&tx, g.a, g.M, x_cols, g.a_sm, TC_BK, plan.bn));
   }
   if (!ok) return TPS_ERR_CUDA;
   GrParams p;
@@ -704,12 +712,14 @@ int launch_gemm_rows(const GemmDesc& g, uint32_t* dev_err, cudaStream_t stream) 
   if (planes) p.tmem_cols *= 2;
   p.epi = g.epi;
   p.err = dev_err;
-  if (codes) return launch_typed<false, GR_CODES>(g, tw, tx, p, plan, stream);
+  if (codes) return launch_typed<false, false, GR_CODES>(g, tw, tx, p, plan, stream);
   if (planes)
-    return w_mn ? launch_typed<true, GR_PLANES>(g, tw, tx, p, plan, stream)
-                : launch_typed<false, GR_PLANES>(g, tw, tx, p, plan, stream);
-  return w_mn ? launch_typed<true, GR_BF16>(g, tw, tx, p, plan, stream)
-              : launch_typed<false, GR_BF16>(g, tw, tx, p, plan, stream);
+    return x_mn   ? launch_typed<true, true, GR_PLANES>(g, tw, tx, p, plan, stream)
+           : w_mn ? launch_typed<true, false, GR_PLANES>(g, tw, tx, p, plan, stream)
+                  : launch_typed<false, false, GR_PLANES>(g, tw, tx, p, plan, stream);
+  return x_mn   ? launch_typed<true, true, GR_BF16>(g, tw, tx, p, plan, stream)
+         : w_mn ? launch_typed<true, false, GR_BF16>(g, tw, tx, p, plan, stream)
+                : launch_typed<false, false, GR_BF16>(g, tw, tx, p, plan, stream);
 }
 
 }  // namespace tps

@@ -320,8 +320,6 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
     if ((rc = expect_vector(dbias, "dbias", dbias->dtype, c.N))) return rc;
   }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
-  int64_t dw_in = 0, dw_out = 0;
-  if (dW != nullptr) weight_strides(dw, weight_layout, &dw_in, &dw_out);
   if (c.T == 0) {  // sums of nothing
     if (dW != nullptr && (rc = launch_fill(dw.data, dw.dtype, dw.rows, dw.cols, dw.sr, dw.sc, s))) return rc;
     return dbias != nullptr ? launch_fill(dbias->data, dbias->dtype, 1, c.N, c.N, 1, s) : TPS_OK;
@@ -378,12 +376,14 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
   if (dW != nullptr) {
     Operand x;
     if ((rc = operand_of(c.dt, c.x.data, c.T, c.K, c.x.sr, c.x.sc, x_ok, &room, s, &x))) return rc;
-    GemmDesc g = linear_gemm("linear_dW", c.dt, c.K, c.N, c.T);
-    set_a(&g, x, true);
-    set_b(&g, dz, false);
+    // rows of dW as it is stored: those of X's columns, or of dz's
+    const bool io = weight_layout == TPS_W_IN_OUT;
+    GemmDesc g = linear_gemm("linear_dW", c.dt, dw.rows, dw.cols, c.T);
+    set_a(&g, io ? x : dz, true);
+    set_b(&g, io ? dz : x, false);
     g.epi.d = dw.data;
     g.epi.d_dtype = dw.dtype;
-    if ((rc = run_gemm(g, dw_in, dw_out, s))) return rc;
+    if ((rc = run_linear(g, dw.sr, dw.sc, s))) return rc;
   }
   return TPS_OK;
 }
