@@ -75,7 +75,7 @@ def _compile_binding() -> None:
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(at, "include"), "-isystem", sysconfig.get_paths()["include"],
            "-isystem", os.path.join(cuda, "include"), os.path.join(CSRC, "binding.cpp"), "-o", tmp,
-           "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python",
+           "-L", os.path.join(at, "lib"), "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_cuda", "-ltorch_python",
            f"-Wl,-rpath,{os.path.join(at, 'lib')}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
