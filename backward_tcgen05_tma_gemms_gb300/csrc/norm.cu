@@ -11,13 +11,13 @@
 //
 // All of it is bound by memory.  A row passes through the registers of a group
 // of threads once, and the group joins its sums by shuffles and one round
-// through shared memory.  Many rows: blocks walk them, and bulk copies keep a
-// ring of the next rows in shared memory full, whatever the threads wait for
-// (loads into registers, also those of the next row ahead of the sums, left the
-// memory idle during the joins: 8192 x 4096 with residual in 52 us).  Few rows:
-// a block a row, loads into registers.  The e4m3 output needs the largest |h w|
-// of the row, which is reduced together with the sum of squares: the codes do
-// not depend on r.
+// through shared memory; blocks walk the rows, and bulk copies keep a ring of
+// the next rows in shared memory full, whatever the threads wait for.  8192 x
+// 4096 in bf16 with residual take 46 us (5.8 TB/s) where loads into registers,
+// with those of the next row ahead of the sums, took 52, 64 rows 3.4 us and 5.9,
+// and the backward pass of 9728 rows 55 us and 81.  The e4m3 output needs the
+// largest |h w| of the row, which is reduced together with the sum of squares:
+// the codes do not depend on r.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -82,145 +82,6 @@ __device__ __forceinline__ Joined join_group(Joined v, int G, float2 (&buf)[kMax
   return all;
 }
 
-// ---- rows that fit into a group's registers --------------------------------
-// R runs of N elements a thread, lane + k G in the row; blockDim.x / G rows at a
-// time.  TX: x; TR: the residual and h (x's type without a residual).
-template <class TX, class TR, class TY, int N, int R>
-__global__ void __launch_bounds__(kMaxGroup, 2) norm_fwd_kernel(const NormParams p, const int G) {
-  constexpr bool CODES = sizeof(TY) == 1;
-  __shared__ float2 buf[2][kMaxWarps];
-  extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any
-  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
-  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, weighted = p.w != nullptr, joined = p.res.p != nullptr;
-  // This thread's first column of the group's row, which moves on by `step` rows.
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
-  const TX* xp = reinterpret_cast<const TX*>(p.x.p) + row * p.x.ld + lane * N;
-  const TR* rp = reinterpret_cast<const TR*>(p.res.p) + row * p.res.ld + lane * N;
-  TR* hp = reinterpret_cast<TR*>(p.h.p) + row * p.h.ld + lane * N;
-  TY* yp = reinterpret_cast<TY*>(p.y.p) + row * p.y.ld + lane * N;
-  bool mine[R];  // the row has these columns
-#pragma unroll
-  for (int k = 0; k < R; ++k) mine[k] = (lane + k * G) * N < d;
-  Typed<TX, N> x[R];
-  Typed<TR, N> r[R];
-  auto fetch = [&] {
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (mine[k]) {
-        x[k].load(xp + k * G * N);
-        if (joined) r[k].load(rp + k * G * N);
-      }
-    xp += step * p.x.ld;
-    rp += step * p.res.ld;
-  };
-  if (row < p.rows) fetch();
-  if (weighted) {
-    if (p.w_dtype == TPS_F32)
-      for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = reinterpret_cast<const float*>(p.w)[i];
-    else
-      for (int i = threadIdx.x; i < d; i += blockDim.x)
-        ws[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
-    __syncthreads();
-  }
-  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
-  int turn = 0;
-  for (; row0 < p.rows; row0 += step, row += step) {
-    const bool live = row < p.rows;
-    Typed<TR, N> h[R];  // the row, as it is stored
-    Joined own = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      if (!live || !mine[k]) continue;
-      bool have = false;
-      if constexpr (sizeof(TX) == sizeof(TR)) {
-        if (p.drop.step == 0u && !joined) {
-          h[k] = x[k];
-          have = true;
-        }
-        if constexpr (N == 8 && sizeof(TX) == 2) {
-          if (p.drop.step == 0u && joined) {  // one rounding, two values an instruction
-            h[k] = x[k];
-            add_bf16(h[k], r[k]);
-            have = true;
-          }
-        }
-      }
-      if (!have) {
-        float v[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = x[k].at(i);
-        if (p.drop.step != 0u) drop(p.drop, key, row * d + (lane + k * G) * N, v);
-        if (joined) {
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[i] += r[k].at(i);
-        }
-        h[k].set(v);
-      }
-      if (summed) h[k].store(hp + k * G * N);
-    }
-    hp += step * p.h.ld;
-    if (row + step < p.rows) fetch();
-    // the row's values times their weights
-    auto weigh = [&](int k, float(&v)[N]) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = h[k].at(i);
-      if (weighted) {
-        const int c = (lane + k * G) * N;
-        if constexpr (N == 8) {
-          const float4 a = *reinterpret_cast<const float4*>(ws + c), b = *reinterpret_cast<const float4*>(ws + c + 4);
-          v[0] *= a.x; v[1] *= a.y; v[2] *= a.z; v[3] *= a.w;
-          v[4] *= b.x; v[5] *= b.y; v[6] *= b.z; v[7] *= b.w;
-        } else {
-          v[0] *= ws[c];
-        }
-      }
-    };
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      if (!live || !mine[k]) continue;
-#pragma unroll
-      for (int i = 0; i < N; ++i) own.sum = fmaf(h[k].at(i), h[k].at(i), own.sum);
-      if (CODES) {
-        float v[N];
-        weigh(k, v);
-        if constexpr (N == 8) {
-#pragma unroll
-          for (int i = 0; i < N; i += 2) own.top = max_nan(own.top, fabsf(v[i]), fabsf(v[i + 1]));
-        } else {
-          own.top = max_nan(own.top, fabsf(v[0]), 0.0f);
-        }
-      }
-    }
-    own = join_group<CODES>(own, G, buf[turn]);
-    turn ^= 1;
-    const float rstd = normed ? rsqrtf(fmaf(own.sum, p.inv_d, p.eps)) : 1.0f;
-    if (live) {
-      const RowCodes codes(own.top);
-      if (lane == 0) {
-        if (normed) p.rstd[row] = rstd;
-        if (CODES) p.scale[row] = codes.scale() * rstd;
-      }
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (!mine[k]) continue;
-        float v[N];
-        weigh(k, v);
-        if constexpr (CODES) {
-          codes_store(reinterpret_cast<char*>(yp + k * G * N), codes, v);
-        } else {
-#pragma unroll
-          for (int i = 0; i < N; ++i) v[i] *= rstd;
-          Typed<TY, N> y;
-          y.set(v);
-          y.store(yp + k * G * N);
-        }
-      }
-    }
-    yp += step * p.y.ld;
-  }
-}
-
 struct NormBwdParams {
   Rows dy, h, dh, dsum, dx;  // p of dh, dsum, dx: nullptr when absent
   const char* w;
@@ -234,125 +95,7 @@ struct NormBwdParams {
   uint32_t* err;
 };
 
-// TD: dy; TH: h, dh and dsum; TX: dx.  The sums of dw stay in registers.
-template <class TD, class TH, class TX, int N, int R>
-__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(const NormBwdParams p, const int G) {
-  __shared__ float2 buf[2][kMaxWarps];
-  extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any; at last [row group][d] sums of dw
-  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
-  const bool past = p.dh.p != nullptr, weighted = p.w != nullptr;
-  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
-  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
-  const TD* dyp = reinterpret_cast<const TD*>(p.dy.p) + row * p.dy.ld + lane * N;
-  const TH* hp = reinterpret_cast<const TH*>(p.h.p) + row * p.h.ld + lane * N;
-  const TH* dhp = reinterpret_cast<const TH*>(p.dh.p) + row * p.dh.ld + lane * N;
-  TH* dsp = reinterpret_cast<TH*>(p.dsum.p) + row * p.dsum.ld + lane * N;
-  TX* dxp = reinterpret_cast<TX*>(p.dx.p) + row * p.dx.ld + lane * N;
-  bool mine[R];
-#pragma unroll
-  for (int k = 0; k < R; ++k) mine[k] = (lane + k * G) * N < d;
-  if (weighted) {
-    if (p.w_dtype == TPS_F32)
-      for (int i = threadIdx.x; i < d; i += blockDim.x) ws[i] = reinterpret_cast<const float*>(p.w)[i];
-    else
-      for (int i = threadIdx.x; i < d; i += blockDim.x)
-        ws[i] = __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
-    __syncthreads();
-  }
-  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
-  float dw[R][N];
-#pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int i = 0; i < N; ++i) dw[k][i] = 0.0f;
-  int turn = 0;
-  for (; row0 < p.rows; row0 += step, row += step) {
-    const bool live = row < p.rows;
-    const float r = live ? __ldg(p.rstd + row) : 0.0f;
-    Typed<TD, N> a[R];
-    Typed<TH, N> b[R], in[R];
-#pragma unroll
-    for (int k = 0; k < R; ++k)
-      if (live && mine[k]) {
-        a[k].load(dyp + k * G * N);
-        b[k].load(hp + k * G * N);
-        if (past) in[k].load(dhp + k * G * N);
-      }
-    dyp += step * p.dy.ld;
-    hp += step * p.h.ld;
-    dhp += step * p.dh.ld;
-    // dy times the weights
-    auto weigh = [&](int k, float(&g)[N]) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) g[i] = a[k].at(i);
-      if (weighted) {
-        const int c = (lane + k * G) * N;
-        if constexpr (N == 8) {
-          const float4 x = *reinterpret_cast<const float4*>(ws + c), y = *reinterpret_cast<const float4*>(ws + c + 4);
-          g[0] *= x.x; g[1] *= x.y; g[2] *= x.z; g[3] *= x.w;
-          g[4] *= y.x; g[5] *= y.y; g[6] *= y.z; g[7] *= y.w;
-        } else {
-          g[0] *= ws[c];
-        }
-      }
-    };
-    Joined own = {0.0f, 0.0f};
-#pragma unroll
-    for (int k = 0; k < R; ++k) {
-      if (!live || !mine[k]) continue;
-      float g[N];
-      weigh(k, g);
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        const float n = b[k].at(i) * r;
-        dw[k][i] = fmaf(a[k].at(i), n, dw[k][i]);
-        own.sum = fmaf(g[i], n, own.sum);
-      }
-    }
-    own = join_group<false>(own, G, buf[turn]);
-    turn ^= 1;
-    const float pull = -own.sum * p.inv_d * r;  // what h r is multiplied by
-    if (live) {
-#pragma unroll
-      for (int k = 0; k < R; ++k) {
-        if (!mine[k]) continue;
-        float v[N];
-        weigh(k, v);
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] = fmaf(v[i], r, fmaf(b[k].at(i) * r, pull, past ? in[k].at(i) : 0.0f));
-        if (p.dsum.p != nullptr) {
-          Typed<TH, N> o;
-          o.set(v);
-          o.store(dsp + k * G * N);
-        }
-        if (p.dx.p != nullptr) {
-          if (p.drop.step != 0u) drop(p.drop, key, row * d + (lane + k * G) * N, v);
-          Typed<TX, N> o;
-          o.set(v);
-          o.store(dxp + k * G * N);
-        }
-      }
-    }
-    dsp += step * p.dsum.ld;
-    dxp += step * p.dx.ld;
-  }
-  if (p.part == nullptr) return;
-  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
-  __syncthreads();  // the weights are done with
-#pragma unroll
-  for (int k = 0; k < R; ++k)
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (mine[k]) ws[group * d + (lane + k * G) * N + i] = dw[k][i];
-  __syncthreads();
-  for (int c = threadIdx.x; c < d; c += blockDim.x) {
-    float s = 0.0f;
-    for (int q = 0; q < groups; ++q) s += ws[q * d + c];
-    out[c] = s;
-  }
-}
-
-// ---- many rows, through a ring ---------------------------------------------
+// ---- rows through a ring ----------------------------------------------------
 // The next rows of up to three tensors in shared memory: a stage holds one row
 // of each for every group of the block.  A stage is filled again once the whole
 // block has taken its rows into registers.
@@ -654,6 +397,196 @@ __global__ void __launch_bounds__(kRingThreads, ring_bwd_blocks(R)) norm_bwd_rin
   }
 }
 
+// ---- rows of single elements -------------------------------------------------
+// Rows that do not start on 16 bytes or do not hold whole runs of eight, up to
+// kSingleRuns kMaxGroup columns: kSingleRuns elements a thread, lane + k G in the
+// row, loaded into registers, the next row's ahead of the present one's sums;
+// blockDim.x / G rows at a time.  TX: x; TR: the residual and h (x's type without
+// a residual).
+constexpr int kSingleRuns = 8;
+template <class TX, class TR, class TY>
+__global__ void __launch_bounds__(kMaxGroup, 2) norm_fwd_kernel(const NormParams p, const int G) {
+  constexpr bool CODES = sizeof(TY) == 1;
+  constexpr int R = kSingleRuns;
+  __shared__ float2 buf[2][kMaxWarps];
+  extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any
+  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
+  const bool normed = p.rstd != nullptr, summed = p.h.p != nullptr, weighted = p.w != nullptr, joined = p.res.p != nullptr;
+  // This thread's first column of the group's row, which moves on by `step` rows.
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
+  const TX* xp = reinterpret_cast<const TX*>(p.x.p) + row * p.x.ld + lane;
+  const TR* rp = reinterpret_cast<const TR*>(p.res.p) + row * p.res.ld + lane;
+  TR* hp = reinterpret_cast<TR*>(p.h.p) + row * p.h.ld + lane;
+  TY* yp = reinterpret_cast<TY*>(p.y.p) + row * p.y.ld + lane;
+  Typed<TX, 1> x[R];
+  Typed<TR, 1> r[R];
+  auto fetch = [&] {
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (lane + k * G < d) {
+        x[k].load(xp + k * G);
+        if (joined) r[k].load(rp + k * G);
+      }
+    xp += step * p.x.ld;
+    rp += step * p.res.ld;
+  };
+  if (row < p.rows) fetch();
+  if (weighted) {
+    for (int i = threadIdx.x; i < d; i += blockDim.x)
+      ws[i] = p.w_dtype == TPS_F32 ? reinterpret_cast<const float*>(p.w)[i]
+                                   : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
+    __syncthreads();
+  }
+  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  int turn = 0;
+  for (; row0 < p.rows; row0 += step, row += step) {
+    const bool live = row < p.rows;
+    float v[R];  // h, then w h
+    Joined own = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      v[k] = 0.0f;
+      if (!live || lane + k * G >= d) continue;
+      float q[1] = {x[k].at(0)};
+      if (p.drop.step != 0u) drop(p.drop, key, row * d + lane + k * G, q);
+      if (joined) q[0] += r[k].at(0);
+      if (summed) {
+        Typed<TR, 1> h;
+        h.set(q);
+        h.store(hp + k * G);
+        q[0] = h.at(0);
+      }
+      v[k] = q[0];
+      own.sum = fmaf(v[k], v[k], own.sum);
+    }
+    hp += step * p.h.ld;
+    if (row + step < p.rows) fetch();
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      if (weighted && lane + k * G < d) v[k] *= ws[lane + k * G];
+      if (CODES) own.top = max_nan(own.top, fabsf(v[k]), 0.0f);
+    }
+    own = join_group<CODES>(own, G, buf[turn]);
+    turn ^= 1;
+    const float rstd = normed ? rsqrtf(fmaf(own.sum, p.inv_d, p.eps)) : 1.0f;
+    if (live) {
+      const RowCodes codes(own.top);
+      if (lane == 0) {
+        if (normed) p.rstd[row] = rstd;
+        if (CODES) p.scale[row] = codes.scale() * rstd;
+      }
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (lane + k * G >= d) continue;
+        if constexpr (CODES) {
+          const float q[1] = {v[k]};
+          codes_store(reinterpret_cast<char*>(yp + k * G), codes, q);
+        } else {
+          const float q[1] = {v[k] * rstd};
+          Typed<TY, 1> y;
+          y.set(q);
+          y.store(yp + k * G);
+        }
+      }
+    }
+    yp += step * p.y.ld;
+  }
+}
+
+// TD: dy; TH: h, dh and dsum; TX: dx.  The sums of dw stay in registers.
+template <class TD, class TH, class TX>
+__global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(const NormBwdParams p, const int G) {
+  constexpr int R = kSingleRuns;
+  __shared__ float2 buf[2][kMaxWarps];
+  extern __shared__ __align__(16) float ws[];  // [d] weights, if there are any; at last [row group][d] sums of dw
+  const int groups = blockDim.x / G, group = threadIdx.x / G, lane = threadIdx.x & (G - 1), d = static_cast<int>(p.d);
+  const bool past = p.dh.p != nullptr, weighted = p.w != nullptr;
+  const int64_t step = static_cast<int64_t>(gridDim.x) * groups;
+  int64_t row = static_cast<int64_t>(blockIdx.x) * groups + group, row0 = row - group;
+  if (weighted) {
+    for (int i = threadIdx.x; i < d; i += blockDim.x)
+      ws[i] = p.w_dtype == TPS_F32 ? reinterpret_cast<const float*>(p.w)[i]
+                                   : __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.w)[i]);
+    __syncthreads();
+  }
+  const uint64_t key = p.drop.step != 0u ? p.drop.key() : 0;
+  float w[R], dw[R];
+#pragma unroll
+  for (int k = 0; k < R; ++k) {
+    w[k] = weighted && lane + k * G < d ? ws[lane + k * G] : 1.0f;
+    dw[k] = 0.0f;
+  }
+  Typed<TD, 1> a[R];
+  Typed<TH, 1> b[R], in[R];
+  auto fetch = [&](int64_t at) {
+    const TD* dyp = reinterpret_cast<const TD*>(p.dy.p) + at * p.dy.ld + lane;
+    const TH* hp = reinterpret_cast<const TH*>(p.h.p) + at * p.h.ld + lane;
+    const TH* dhp = reinterpret_cast<const TH*>(p.dh.p) + at * p.dh.ld + lane;
+#pragma unroll
+    for (int k = 0; k < R; ++k)
+      if (lane + k * G < d) {
+        a[k].load(dyp + k * G);
+        b[k].load(hp + k * G);
+        if (past) in[k].load(dhp + k * G);
+      }
+  };
+  if (row < p.rows) fetch(row);
+  int turn = 0;
+  for (; row0 < p.rows; row0 += step, row += step) {
+    const bool live = row < p.rows;
+    const float r = live ? __ldg(p.rstd + row) : 0.0f;
+    float g[R], n[R], up[R];  // dy w, h r and dh
+    Joined own = {0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < R; ++k) {
+      g[k] = n[k] = up[k] = 0.0f;
+      if (!live || lane + k * G >= d) continue;
+      g[k] = a[k].at(0) * w[k];
+      n[k] = b[k].at(0) * r;
+      if (past) up[k] = in[k].at(0);
+      dw[k] = fmaf(a[k].at(0), n[k], dw[k]);
+      own.sum = fmaf(g[k], n[k], own.sum);
+    }
+    if (row + step < p.rows) fetch(row + step);
+    own = join_group<false>(own, G, buf[turn]);
+    turn ^= 1;
+    const float pull = -own.sum * p.inv_d * r;  // what h r is multiplied by
+    if (live) {
+      TH* dsp = reinterpret_cast<TH*>(p.dsum.p) + row * p.dsum.ld + lane;
+      TX* dxp = reinterpret_cast<TX*>(p.dx.p) + row * p.dx.ld + lane;
+#pragma unroll
+      for (int k = 0; k < R; ++k) {
+        if (lane + k * G >= d) continue;
+        float v[1] = {fmaf(g[k], r, fmaf(n[k], pull, up[k]))};
+        if (p.dsum.p != nullptr) {
+          Typed<TH, 1> o;
+          o.set(v);
+          o.store(dsp + k * G);
+        }
+        if (p.dx.p != nullptr) {
+          if (p.drop.step != 0u) drop(p.drop, key, row * d + lane + k * G, v);
+          Typed<TX, 1> o;
+          o.set(v);
+          o.store(dxp + k * G);
+        }
+      }
+    }
+  }
+  if (p.part == nullptr) return;
+  float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
+  __syncthreads();  // the weights are done with
+#pragma unroll
+  for (int k = 0; k < R; ++k)
+    if (lane + k * G < d) ws[group * d + lane + k * G] = dw[k];
+  __syncthreads();
+  for (int c = threadIdx.x; c < d; c += blockDim.x) {
+    float s = 0.0f;
+    for (int q = 0; q < groups; ++q) s += ws[q * d + c];
+    out[c] = s;
+  }
+}
+
 // ---- other rows -------------------------------------------------------------
 // Rows wider than the registers hold, and rows of single elements whose types
 // differ: a block a row, which is read a second time (out of L2) after its sums.
@@ -801,16 +734,12 @@ int round_pow2(int64_t x) {
   return r;
 }
 // How a call is run: runs of N elements, R of them a thread, G threads a row,
-// blocks of `threads`.  N = 0: the kernels of long rows.
-// ring > 0: through a ring of so many stages, `per_sm` blocks an SM walking the
-// rows; where every row of every tensor starts on 16 bytes and holds whole runs of
-// eight, and where there are more rows than two for each group of the
-// blocks that the device holds, or more columns than the other form's registers
-// do.  Four runs a thread in bf16, two where fp32 is among the types (as many
-// bytes), more for more than 256 threads' worth.
-// Otherwise loads into registers, two runs a thread (one) and up to kMaxGroup
-// threads a row; single elements, eight a thread, where runs do not fit and the
-// types agree.
+// blocks of `threads`, `per_sm` of them an SM walking the rows.
+// N = 8: through a ring of `ring` stages, where every row of every tensor starts
+// on 16 bytes and holds whole runs of eight, up to 16384 columns.  Four runs a
+// thread in bf16, two where fp32 is among the types (as many bytes), more for more
+// than kRingThreads threads' worth.
+// N = 1: single elements, where the types agree.  N = 0: the kernels of long rows.
 constexpr int64_t kSms = 152, kMostBlocks = kSms * 16;
 constexpr int kRingShared = 216 << 10;  // of an SM
 struct Spread {
@@ -839,16 +768,13 @@ Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int6
           r.per_sm = per;
         }
       }
-      const int64_t groups = kSms * r.per_sm * (r.threads / r.G);
-      if (r.ring > 0 && (rows > 2 * groups || runs > int64_t(fp32 ? 1 : 2) * kMaxGroup)) return r;
+      if (r.ring > 0) return r;
     }
   }
-  if (!wide && (mixed || d > 8 * kMaxGroup)) return s;
-  s.N = wide ? 8 : 1;
-  s.R = wide ? (fp32 ? 1 : 2) : 8;
-  const int64_t runs = (d + s.N - 1) / s.N;
-  if (runs > int64_t(s.R) * kMaxGroup) return Spread{0, 0, 0, 0, 0, 0};
-  const int64_t need = (runs + s.R - 1) / s.R;
+  if (mixed || d > kSingleRuns * kMaxGroup) return s;
+  s.N = 1;
+  s.R = kSingleRuns;
+  const int64_t need = (d + s.R - 1) / s.R;
   s.G = need <= 32 ? 32 : round_pow2(need);
   s.threads = s.G < 256 ? 256 : s.G;
   while (s.threads > s.G && (rows * s.G + s.threads - 1) / s.threads < 2 * kSms) s.threads /= 2;  // few rows: a block each
@@ -874,7 +800,7 @@ int ring_ready(const Spread& sp, int* stages, uint32_t** err) {
   return *err != nullptr ? TPS_OK : fail(TPS_ERR_CUDA, "cannot resolve the device error word");
 }
 
-template <class TX, class TR, class TY, int N, int R, bool RING>
+template <class TX, class TR, class TY, int R, bool RING>
 int launch_fwd(NormParams p, const Spread& sp, cudaStream_t s) {
   int64_t blocks = 0;
   int rc;
@@ -892,8 +818,8 @@ int launch_fwd(NormParams p, const Spread& sp, cudaStream_t s) {
     norm_fwd_ring_kernel<TX, TR, TY, R, false><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
   } else {
     const size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
-    if ((rc = prepare_launch(norm_fwd_kernel<TX, TR, TY, N, R>, sp, p.rows, shared, &blocks))) return rc;
-    norm_fwd_kernel<TX, TR, TY, N, R><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
+    if ((rc = prepare_launch(norm_fwd_kernel<TX, TR, TY>, sp, p.rows, shared, &blocks))) return rc;
+    norm_fwd_kernel<TX, TR, TY><<<static_cast<unsigned>(blocks), sp.threads, shared, s>>>(p, sp.G);
   }
   return launched("norm");
 }
@@ -901,14 +827,13 @@ template <class TX, class TR, class TY>
 int launch_fwd_typed(const NormParams& p, const Spread& sp, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(TX) == 2 && sizeof(TR) == 2;
   if (sp.N == 1) {
-    if constexpr (sizeof(TX) == sizeof(TR)) return launch_fwd<TX, TR, TY, 1, 8, false>(p, sp, s);
+    if constexpr (sizeof(TX) == sizeof(TR)) return launch_fwd<TX, TR, TY, 1, false>(p, sp, s);
     return fail(TPS_ERR_DTYPE, "norm: single elements of two types");
   }
-  if (sp.ring == 0) return launch_fwd<TX, TR, TY, 8, kBf16 ? 2 : 1, false>(p, sp, s);
   if constexpr (!kBf16)
-    if (sp.R == 2) return launch_fwd<TX, TR, TY, 8, 2, true>(p, sp, s);
-  if (sp.R == 4) return launch_fwd<TX, TR, TY, 8, 4, true>(p, sp, s);
-  return launch_fwd<TX, TR, TY, 8, 8, true>(p, sp, s);
+    if (sp.R == 2) return launch_fwd<TX, TR, TY, 2, true>(p, sp, s);
+  if (sp.R == 4) return launch_fwd<TX, TR, TY, 4, true>(p, sp, s);
+  return launch_fwd<TX, TR, TY, 8, true>(p, sp, s);
 }
 template <class TX, class TR>
 int launch_fwd_out(const NormParams& p, const Spread& sp, cudaStream_t s) {
@@ -938,7 +863,7 @@ int launch_norm_fwd(const NormParams& p, const char* label, cudaStream_t s) {
   return launched("norm_long");
 }
 
-template <class TD, class TH, class TX, int N, int R, bool RING>
+template <class TD, class TH, class TX, int R, bool RING>
 int launch_bwd(NormBwdParams p, const Spread& sp, int64_t* parts, cudaStream_t s) {
   const int64_t per = sp.threads / sp.G;
   const size_t sums = p.part != nullptr ? sizeof(float) * p.d * per : 0;
@@ -953,8 +878,8 @@ int launch_bwd(NormBwdParams p, const Spread& sp, int64_t* parts, cudaStream_t s
   } else {
     size_t shared = p.w != nullptr ? sizeof(float) * p.d : 0;
     if (shared < sums) shared = sums;
-    if ((rc = prepare_launch(norm_bwd_kernel<TD, TH, TX, N, R>, sp, p.rows, shared, parts))) return rc;
-    norm_bwd_kernel<TD, TH, TX, N, R><<<static_cast<unsigned>(*parts), sp.threads, shared, s>>>(p, sp.G);
+    if ((rc = prepare_launch(norm_bwd_kernel<TD, TH, TX>, sp, p.rows, shared, parts))) return rc;
+    norm_bwd_kernel<TD, TH, TX><<<static_cast<unsigned>(*parts), sp.threads, shared, s>>>(p, sp.G);
   }
   return launched("norm_bwd");
 }
@@ -962,14 +887,13 @@ template <class TD, class TH, class TX>
 int launch_bwd_typed(const NormBwdParams& p, const Spread& sp, int64_t* parts, cudaStream_t s) {
   constexpr bool kBf16 = sizeof(TD) == 2 && sizeof(TH) == 2;
   if (sp.N == 1) {
-    if constexpr (sizeof(TD) == sizeof(TH)) return launch_bwd<TD, TH, TX, 1, 8, false>(p, sp, parts, s);
+    if constexpr (sizeof(TD) == sizeof(TH)) return launch_bwd<TD, TH, TX, 1, false>(p, sp, parts, s);
     return fail(TPS_ERR_DTYPE, "norm: single elements of two types");
   }
-  if (sp.ring == 0) return launch_bwd<TD, TH, TX, 8, kBf16 ? 2 : 1, false>(p, sp, parts, s);
   if constexpr (!kBf16)
-    if (sp.R == 2) return launch_bwd<TD, TH, TX, 8, 2, true>(p, sp, parts, s);
-  if (sp.R == 4) return launch_bwd<TD, TH, TX, 8, 4, true>(p, sp, parts, s);
-  return launch_bwd<TD, TH, TX, 8, 8, true>(p, sp, parts, s);
+    if (sp.R == 2) return launch_bwd<TD, TH, TX, 2, true>(p, sp, parts, s);
+  if (sp.R == 4) return launch_bwd<TD, TH, TX, 4, true>(p, sp, parts, s);
+  return launch_bwd<TD, TH, TX, 8, true>(p, sp, parts, s);
 }
 template <class TD, class TH>
 int launch_bwd_out(const NormBwdParams& p, const Spread& sp, int64_t* parts, cudaStream_t s) {
