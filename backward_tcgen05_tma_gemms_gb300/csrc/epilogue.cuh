@@ -182,20 +182,28 @@ __device__ __forceinline__ float any_elem(const void* base, int dtype, int64_t i
 }
 // The activation and its slope, also far from 0: act_fwd holds the sigmoid of
 // SiLU and of the tanh GELU at e^-80 and multiplies it by z, which shows from |z| = 1e33
-// on, and act_grad squares z.  Below -100 both are under 1e-40, above 100 the
-// slope is 1 in fp32.
+// on, and act_grad squares z.  At -100 both are 0 to 1e-33, and at 100 the slope
+// is 1: z is held there (a NaN stays one).
 constexpr float kActFar = 100.0f;
+__device__ __forceinline__ float at_least(float z, float low) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(low));
+  return r;
+}
+__device__ __forceinline__ float at_most(float z, float high) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(z), "f"(high));
+  return r;
+}
 template <int ACT>
 __device__ __forceinline__ float linear_act_c(float z) {
-  const float y = act_fwd_c<ACT>(z);
-  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) return z < -kActFar ? 0.0f : y;
-  return y;
+  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) z = at_least(z, -kActFar);
+  return act_fwd_c<ACT>(z);
 }
 template <int ACT>
 __device__ __forceinline__ float linear_slope_c(float z) {
-  const float y = act_grad_c<ACT>(z);
-  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) return z < -kActFar ? 0.0f : z > kActFar ? 1.0f : y;
-  return y;
+  if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) z = at_most(at_least(z, -kActFar), kActFar);
+  return act_grad_c<ACT>(z);
 }
 __device__ __forceinline__ float linear_act(int act, float z) {
   if (act != kActNone) act_dispatch(act, [&](auto A) { z = linear_act_c<decltype(A)::value>(z); });

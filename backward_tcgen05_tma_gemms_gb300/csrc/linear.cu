@@ -19,6 +19,7 @@
 #include <cuda_runtime.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "api_common.cuh"
 #include "epilogue.cuh"
@@ -40,12 +41,31 @@ struct DzParams {
   int act;
 };
 
+// A run of N elements in flight, of type T or (void) of the type that the tensor
+// has at run time.
+template <class T, int N>
+struct DzRun {
+  Typed<T, N> t;
+  __device__ __forceinline__ void load(const Rows& m, int64_t r, int64_t c) { t.load(reinterpret_cast<const T*>(m.p) + r * m.ld + c); }
+  __device__ __forceinline__ void value(const Rows&, float (&v)[N]) const {
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = t.at(i);
+  }
+};
+template <int N>
+struct DzRun<void, N> {
+  Raw<N> t;
+  __device__ __forceinline__ void load(const Rows& m, int64_t r, int64_t c) { raw_load(m.at(r, c), m.dtype, t); }
+  __device__ __forceinline__ void value(const Rows& m, float (&v)[N]) const { raw_value(t, m.dtype, v); }
+};
+
 // A warp takes 32 runs of N elements of a row, a block eight rows at a time, every
 // gridDim.y-th group of eight; the columns' sums stay in registers.  Some 25
 // instructions an element with an activation (two of them on the special function
-// unit), nearly the time that memory takes: the activation is a type, and four blocks an SM
-// leave loads in flight.
-template <int N, int ACT>
+// unit), nearly the time that memory takes: the activation is a type, and so is
+// that of the tensors where they share one; four blocks an SM leave loads in
+// flight.
+template <class T, int N, int ACT>
 __global__ void __launch_bounds__(32 * kDzRows, 4) linear_dz_kernel(const DzParams p) {
   __shared__ float sums[kDzRows][32 * N + 1];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -57,13 +77,13 @@ __global__ void __launch_bounds__(32 * kDzRows, 4) linear_dz_kernel(const DzPara
   const int64_t step = static_cast<int64_t>(gridDim.y) * kDzRows;
   if (c < p.N) {
     for (int64_t r0 = static_cast<int64_t>(blockIdx.y) * kDzRows + w; r0 < p.T; r0 += U * step) {
-      Raw<N> a[U], b[U];
+      DzRun<T, N> a[U], b[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
         const int64_t r = r0 + u * step;
         if (r < p.T) {
-          raw_load(p.dy.at(r, c), p.dy.dtype, a[u]);
-          if (ACT != kActNone) raw_load(p.z.at(r, c), p.z.dtype, b[u]);
+          a[u].load(p.dy, r, c);
+          if (ACT != kActNone) b[u].load(p.z, r, c);
         }
       }
 #pragma unroll
@@ -71,14 +91,22 @@ __global__ void __launch_bounds__(32 * kDzRows, 4) linear_dz_kernel(const DzPara
         const int64_t r = r0 + u * step;
         if (r >= p.T) continue;
         float v[N];
-        raw_value(a[u], p.dy.dtype, v);
+        a[u].value(p.dy, v);
         if constexpr (ACT != kActNone) {
           float z[N];
-          raw_value(b[u], p.z.dtype, z);
+          b[u].value(p.z, z);
 #pragma unroll
           for (int i = 0; i < N; ++i) v[i] *= linear_slope_c<ACT>(z[i]);
         }
-        if (p.dz.p != nullptr) run_store(p.dz.at(r, c), p.dz.dtype, v);
+        if (p.dz.p != nullptr) {
+          if constexpr (std::is_void_v<T>) {
+            run_store(p.dz.at(r, c), p.dz.dtype, v);
+          } else {
+            Typed<T, N> o;
+            o.set(v);
+            o.store(reinterpret_cast<T*>(p.dz.p) + r * p.dz.ld + c);
+          }
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i) s[i] += v[i];
       }
@@ -96,15 +124,26 @@ __global__ void __launch_bounds__(32 * kDzRows, 4) linear_dz_kernel(const DzPara
     p.part[static_cast<int64_t>(blockIdx.y) * p.N + c0 + i] = t;
   }
 }
+template <class T, int N>
+void launch_dz_act(const DzParams& p, dim3 grid, cudaStream_t s) {
+  switch (p.act) {
+    case TPS_ACT_GELU_ERF: linear_dz_kernel<T, N, TPS_ACT_GELU_ERF><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_GELU_TANH: linear_dz_kernel<T, N, TPS_ACT_GELU_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_TANH: linear_dz_kernel<T, N, TPS_ACT_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    case TPS_ACT_SILU: linear_dz_kernel<T, N, TPS_ACT_SILU><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+    default: linear_dz_kernel<T, N, kActNone><<<grid, 32 * kDzRows, 0, s>>>(p); break;
+  }
+}
 template <int N>
 void launch_dz(const DzParams& p, dim3 grid, cudaStream_t s) {
-  switch (p.act) {
-    case TPS_ACT_GELU_ERF: linear_dz_kernel<N, TPS_ACT_GELU_ERF><<<grid, 32 * kDzRows, 0, s>>>(p); break;
-    case TPS_ACT_GELU_TANH: linear_dz_kernel<N, TPS_ACT_GELU_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
-    case TPS_ACT_TANH: linear_dz_kernel<N, TPS_ACT_TANH><<<grid, 32 * kDzRows, 0, s>>>(p); break;
-    case TPS_ACT_SILU: linear_dz_kernel<N, TPS_ACT_SILU><<<grid, 32 * kDzRows, 0, s>>>(p); break;
-    default: linear_dz_kernel<N, kActNone><<<grid, 32 * kDzRows, 0, s>>>(p); break;
-  }
+  const int t = p.dy.dtype;
+  const bool one = (p.z.p == nullptr || p.z.dtype == t) && (p.dz.p == nullptr || p.dz.dtype == t);
+  if (one && t == TPS_BF16)
+    launch_dz_act<__nv_bfloat16, N>(p, grid, s);
+  else if (one)
+    launch_dz_act<float, N>(p, grid, s);
+  else
+    launch_dz_act<void, N>(p, grid, s);
 }
 
 // ------------------------------------------------------------------ host
