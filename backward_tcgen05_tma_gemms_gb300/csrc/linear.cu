@@ -276,7 +276,7 @@ extern "C" int tps_linear_fwd(const tps_tensor* X, const tps_tensor* W, const tp
   if (codes && weight_layout != TPS_W_OUT_IN) return fail(TPS_ERR_LAYOUT, "e4m3 weights are (out, in)");
   if (codes != (x_scale != nullptr) || codes != (w_scale != nullptr))
     return fail(TPS_ERR_ARG, "x_scale and w_scale go with e4m3 operands");
-  if (codes && ((rc = expect_vector(x_scale, "x_scale", TPS_F32, c.T)) || (rc = expect_vector(w_scale, "w_scale", TPS_F32, c.N))))
+  if (codes && ((rc = aligned_vector(x_scale, "x_scale", TPS_F32, c.T)) || (rc = aligned_vector(w_scale, "w_scale", TPS_F32, c.N))))
     return rc;
   GemmDesc g = linear_gemm("linear", c.dt, c.T, c.N, c.K);
   g.epi.mode = EPI_LINEAR;
@@ -356,7 +356,7 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
   }
   if (dbias != nullptr) {
     if (dbias->dtype != TPS_F32 && dbias->dtype != TPS_BF16) return fail(TPS_ERR_DTYPE, "dbias must be f32 or bf16");
-    if ((rc = expect_vector(dbias, "dbias", dbias->dtype, c.N))) return rc;
+    if ((rc = aligned_vector(dbias, "dbias", dbias->dtype, c.N))) return rc;
   }
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (c.T == 0) {  // sums of nothing

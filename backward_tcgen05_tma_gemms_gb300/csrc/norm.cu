@@ -967,8 +967,8 @@ extern "C" int tps_rmsnorm_fwd(const tps_tensor* X, const tps_tensor* residual, 
   if (n != rows || c != d) return fail(TPS_ERR_SHAPE, "Y: another shape than X");
   if ((rc = weight_vector(weight, d, &p.w, &p.w_dtype))) return rc;
   if ((p.y.dtype == TPS_E4M3) != (scale != nullptr)) return fail(TPS_ERR_ARG, "scale goes with an e4m3 output");
-  if (scale != nullptr && (rc = expect_vector(scale, "scale", TPS_F32, rows))) return rc;
-  if ((rc = expect_vector(rstd, "rstd", TPS_F32, rows))) return rc;
+  if (scale != nullptr && (rc = aligned_vector(scale, "scale", TPS_F32, rows))) return rc;
+  if ((rc = aligned_vector(rstd, "rstd", TPS_F32, rows))) return rc;
   if (rows == 0) return TPS_OK;
   if (d == 0) return fail(TPS_ERR_SHAPE, "rows without elements");
   p.rstd = static_cast<float*>(rstd->data);
@@ -991,7 +991,7 @@ extern "C" int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const
   if ((rc = rows_view(Q, "Q", true, &p.y, &n, &c))) return rc;
   if (n != rows || c != d) return fail(TPS_ERR_SHAPE, "Q: another shape than X");
   if (p.y.dtype != TPS_E4M3) return fail(TPS_ERR_DTYPE, "Q must be e4m3");
-  if ((rc = expect_vector(scale, "scale", TPS_F32, rows))) return rc;
+  if ((rc = aligned_vector(scale, "scale", TPS_F32, rows))) return rc;
   if (rows == 0) return TPS_OK;
   p.scale = static_cast<float*>(scale->data);
   p.rows = rows;
@@ -1017,14 +1017,14 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
   if ((rc = too_large(rows, d))) return rc;
   if ((rc = float_rows(H, "H", false, rows, d, &p.h))) return rc;
   if ((rc = weight_vector(weight, d, &p.w, &p.w_dtype))) return rc;
-  if ((rc = expect_vector(rstd, "rstd", TPS_F32, rows))) return rc;
+  if ((rc = aligned_vector(rstd, "rstd", TPS_F32, rows))) return rc;
   if (dH != nullptr && (rc = float_rows(dH, "dH", false, rows, d, &p.dh))) return rc;
   if ((rc = dropout_of(dropout, &p.drop))) return rc;
   if (dSum != nullptr && (rc = float_rows(dSum, "dSum", true, rows, d, &p.dsum))) return rc;
   for (const Rows* g : {&p.dh, &p.dsum})
     if (g->p != nullptr && g->dtype != p.h.dtype) return fail(TPS_ERR_DTYPE, "dH and dSum must have H's type");
   if (dX != nullptr && (rc = float_rows(dX, "dX", true, rows, d, &p.dx))) return rc;
-  if (dweight != nullptr && (rc = expect_vector(dweight, "dweight", TPS_F32, d))) return rc;
+  if (dweight != nullptr && (rc = aligned_vector(dweight, "dweight", TPS_F32, d))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (d == 0) return rows == 0 ? TPS_OK : fail(TPS_ERR_SHAPE, "rows without elements");
   if (rows == 0) return dweight != nullptr ? launch_fill(dweight->data, TPS_F32, 1, d, d, 1, s) : TPS_OK;

@@ -42,14 +42,19 @@ inline int float_rows(const tps_tensor* t, const char* name, bool out, int64_t r
   if (r->dtype == TPS_E4M3) return fail(TPS_ERR_DTYPE, "%s must be f32 or bf16", name);
   return TPS_OK;
 }
+// n contiguous entries, each at a multiple of its size.
+inline int aligned_vector(const tps_tensor* t, const char* name, int dtype, int64_t n) {
+  const int rc = expect_vector(t, name, dtype, n);
+  if (rc) return rc;
+  return reinterpret_cast<uintptr_t>(t->data) % es_of(dtype) == 0 ? TPS_OK : fail(TPS_ERR_LAYOUT, "%s: misaligned data", name);
+}
 inline int weight_vector(const tps_tensor* w, int64_t d, const char** p, int* dtype) {
   *p = nullptr;
   *dtype = TPS_F32;
   if (w == nullptr) return TPS_OK;
   if (w->dtype != TPS_F32 && w->dtype != TPS_BF16) return fail(TPS_ERR_DTYPE, "weight must be f32 or bf16");
   int rc;
-  if ((rc = expect_vector(w, "weight", w->dtype, d))) return rc;
-  if (reinterpret_cast<uintptr_t>(w->data) % es_of(w->dtype) != 0) return fail(TPS_ERR_LAYOUT, "weight: misaligned data");
+  if ((rc = aligned_vector(w, "weight", w->dtype, d))) return rc;
   *p = static_cast<const char*>(w->data);
   *dtype = w->dtype;
   return TPS_OK;

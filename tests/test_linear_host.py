@@ -116,3 +116,18 @@ def test_binding_refusals(lib):  # noqa: F811
         api.linear_fwd(x, W, act="relu")
     with pytest.raises(ValueError, match="shape"):
         api.linear_fwd(x, W[0])
+
+
+def test_vectors_off_their_elements(lib):  # noqa: F811
+    """A vector that does not start at a multiple of its element's size is refused."""
+    def off(n, dtype=F32, by=2):
+        t = _fake([n], dtype)
+        t.data += by
+        return t
+    assert fwd(lib, bias=off(40)) == LAYOUT and fwd(lib, bias=off(40, BF16, 1)) == LAYOUT
+    codes = dict(x=_fake([6, 64], E4M3), w=_fake([40, 64], E4M3), layout=OUT_IN)
+    assert fwd(lib, **codes, xs=off(6), ws=_fake([40])) == LAYOUT
+    assert fwd(lib, **codes, xs=_fake([6]), ws=off(40)) == LAYOUT
+    for db in (off(40), off(40, BF16, 1)):
+        assert lib.tps_linear_bwd(_r(_fake([6, 64], BF16)), _r(_fake([64, 40], BF16)), _r(_fake([6, 40], BF16)), None, NONE,
+                                  IN_OUT, None, None, _r(db), 0x1000, 1 << 20, None) == LAYOUT

@@ -144,3 +144,18 @@ def test_binding_refusals(lib):  # noqa: F811
                  lambda: api.quantize_e4m3([1.0]), lambda: api.rmsnorm_fwd(x, out_dtype="f32")):
         with pytest.raises((TypeError, ValueError)):
             call()
+
+
+def test_vectors_off_their_elements(lib):  # noqa: F811
+    """A vector that does not start at a multiple of its element's size is refused."""
+    def off(n, dtype=F32, by=2):
+        t = _fake([n], dtype)
+        t.data += by
+        return t
+    x = _fake([6, 64], BF16)
+    assert fwd(lib, rstd=off(6)) == LAYOUT
+    assert fwd(lib, w=off(64)) == LAYOUT and fwd(lib, w=off(64, BF16, 1)) == LAYOUT
+    assert fwd(lib, y=_fake([6, 64], E4M3), scale=off(6)) == LAYOUT
+    assert lib.tps_quantize_e4m3(_r(x), _r(_fake([6, 64], E4M3)), _r(off(6)), None) == LAYOUT
+    for rstd, dw in ((off(6), None), (_fake([6]), off(64))):
+        assert lib.tps_rmsnorm_bwd(_r(x), _r(x), None, _r(rstd), None, None, None, None, _r(dw), 0x1000, 1 << 20, None) == LAYOUT
