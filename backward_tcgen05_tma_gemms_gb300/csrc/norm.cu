@@ -782,11 +782,12 @@ Spread spread_of(int64_t rows, int64_t d, bool wide, bool fp32, bool mixed, int6
   return s;
 }
 
-// Blocks of `f`, and its shared memory.
+// Blocks of `f`, and its shared memory: the most that any call of it may have,
+// for another host thread may be launching it with more than this call needs.
 template <class F>
 int prepare_launch(F f, const Spread& sp, int64_t rows, size_t shared, int64_t* blocks) {
   if (shared > (40u << 10) &&  // with the static part, beyond 48 KB
-      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(shared)) != cudaSuccess)
+      cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingShared) != cudaSuccess)
     return fail(TPS_ERR_CUDA, "norm: %s", cudaGetErrorString(cudaGetLastError()));
   int64_t per = sp.per_sm;
   if (sp.ring == 0 && per * (int64_t(shared) + 2048) > kRingShared) per = kRingShared / (int64_t(shared) + 2048);

@@ -370,3 +370,30 @@ def test_rows_around_are_untouched():
     api.quantize_e4m3(x, out=(q8[2:6, 16:80], torch.empty(4, device="cuda")))
     f = q8.float()
     assert (f[:2] == 1).all() and (f[6:] == 1).all() and (f[:, :16] == 1).all() and (f[:, 80:] == 1).all()
+
+
+def test_two_threads():
+    """Calls of two widths from two host threads at once, each on its own stream: as one after the other."""
+    import threading
+    xs = [torch.randn(40, d, device="cuda", generator=torch.Generator(device="cuda").manual_seed(d)) for d in (512, 4096)]
+    want = [(api.rmsnorm_fwd(x)[0], api.rmsnorm_bwd(x, x, None, api.rmsnorm_fwd(x)[3])[0]) for x in xs]
+    torch.cuda.synchronize()
+    wrong = []
+
+    def work(x, want):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(300):
+                    y, _, _, rstd = api.rmsnorm_fwd(x)
+                    dx, _, _ = api.rmsnorm_bwd(x, x, None, rstd)
+                torch.cuda.current_stream().synchronize()
+                if not (torch.equal(y, want[0]) and torch.equal(dx, want[1])):
+                    wrong.append("another result")
+        except Exception as e:  # noqa: BLE001
+            wrong.append(repr(e))
+    threads = [threading.Thread(target=work, args=a) for a in zip(xs, want)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong, wrong
