@@ -314,6 +314,15 @@ struct ProfScope {
   cudaStream_t stream;
 };
 void note_launch();
+// A launch with this attribute starts before the kernel in front has ended, once
+// all blocks of that have allowed it; it waits for it itself (wait_for_prior_kernel
+// in ptx.cuh).
+inline cudaLaunchAttribute early_attribute() {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  return a;
+}
 // Device address of the current device's error word (nullptr on failure).
 uint32_t* device_error_word();
 // Sets the text tps_last_error_detail returns on this host thread.

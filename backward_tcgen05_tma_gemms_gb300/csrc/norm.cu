@@ -173,6 +173,7 @@ constexpr int ring_bwd_blocks(int R) { return ring_blocks(2 * R * 8); }
 template <class TX, class TR, class TY, int R, bool BARE>
 __global__ void __launch_bounds__(kRingThreads, BARE ? ring_blocks(R * (sizeof(TR) == 4 ? 8 : 4)) : ring_fwd_blocks(R, sizeof(TR) == 4))
     norm_fwd_ring_kernel(const NormParams p, const int G) {
+  let_next_kernel_start();  // a product that reads the rows
   constexpr bool CODES = sizeof(TY) == 1;
   __shared__ float2 buf[2][kMaxWarps];
   __shared__ RowRing ring;
@@ -381,6 +382,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_bwd_blocks(R)) norm_bwd_rin
     dxp += step * p.dx.ld;
   }
   if (p.part == nullptr) return;
+  let_next_kernel_start();
   float* sums = reinterpret_cast<float*>(stages_at);
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
   __syncthreads();  // the rows are done with
@@ -406,6 +408,7 @@ __global__ void __launch_bounds__(kRingThreads, ring_bwd_blocks(R)) norm_bwd_rin
 constexpr int kSingleRuns = 8;
 template <class TX, class TR, class TY>
 __global__ void __launch_bounds__(kMaxGroup, 2) norm_fwd_kernel(const NormParams p, const int G) {
+  let_next_kernel_start();
   constexpr bool CODES = sizeof(TY) == 1;
   constexpr int R = kSingleRuns;
   __shared__ float2 buf[2][kMaxWarps];
@@ -574,6 +577,7 @@ __global__ void __launch_bounds__(kMaxGroup, 1) norm_bwd_kernel(const NormBwdPar
     }
   }
   if (p.part == nullptr) return;
+  let_next_kernel_start();
   float* out = p.part + static_cast<int64_t>(blockIdx.x) * d;
   __syncthreads();  // the weights are done with
 #pragma unroll
@@ -907,6 +911,7 @@ int launch_bwd_out(const NormBwdParams& p, const Spread& sp, int64_t* parts, cud
 // Sum of `n` rows of d floats to out (f32 or bf16), in row order.
 __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64_t n, int64_t d, void* out, int dtype) {
   __shared__ float s[32][33];
+  wait_for_prior_kernel();
   const int w = threadIdx.x >> 5, lane = threadIdx.x & 31, warps = blockDim.x >> 5;
   const int64_t c = static_cast<int64_t>(blockIdx.x) * 32 + lane;
   float acc = 0.0f;
@@ -931,11 +936,19 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64
     static_cast<__nv_bfloat16*>(out)[c] = __float2bfloat16_rn(acc);
 }
 
-int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, cudaStream_t s) {
+int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, bool early, cudaStream_t s) {
   ProfScope prof("sum_rows", "dw", 0.0, 4.0 * double(n) * double(d), s);
   const int64_t warps = (n + 7) / 8 < 32 ? (n + 7) / 8 : 32;  // eight rows a warp at a time
-  sum_rows_kernel<<<static_cast<unsigned>((d + 31) / 32), static_cast<unsigned>(32 * warps), 0, s>>>(part, n, d, out, dtype);
-  return launched("sum_rows");
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr = early_attribute();
+  cfg.gridDim = dim3(static_cast<unsigned>((d + 31) / 32), 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(32 * warps), 1, 1);
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = early ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, sum_rows_kernel, part, n, d, out, dtype);
+  note_launch();
+  return e == cudaSuccess ? TPS_OK : fail(TPS_ERR_CUDA, "sum_rows: launch failed: %s", cudaGetErrorString(cudaGetLastError()));
 }
 
 }  // namespace tps
@@ -1067,5 +1080,8 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
     }
     if (rc) return rc;
   }
-  return p.part != nullptr ? launch_sum_rows(p.part, parts, d, dweight->data, TPS_F32, s) : TPS_OK;
+  // Launched early behind a short pass: backward norms of 64 x 4096, 600 x 2048 and
+  // 8192 x 4096 in bf16 take 9.1, 9.2 and 47.8 us so, else 9.7, 9.8 and 47.1.
+  const bool early = rows < (1ll << 24) / d;
+  return p.part != nullptr ? launch_sum_rows(p.part, parts, d, dweight->data, TPS_F32, early, s) : TPS_OK;
 }

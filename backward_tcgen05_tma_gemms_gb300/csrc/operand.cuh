@@ -26,6 +26,15 @@ inline int64_t laid_bytes(int64_t ni, int64_t nj, int planes) {
 // tiles with zeros behind, three planes side by side for f32 (operand.cu).
 int lay_operand(int dtype, const char* src, int64_t ni, int64_t nj, int64_t si, int64_t sj, char* dst, const char* label,
                 cudaStream_t s, Operand* o);
+// The same of up to kLayJobs operands of one type in one launch.
+constexpr int kLayJobs = 3;
+struct LayJob {
+  const void* src;
+  void* dst;
+  int64_t rows, cols, ld, plane;
+};
+void lay_job(int dtype, const char* src, int64_t ni, int64_t nj, int64_t si, int64_t sj, char* dst, LayJob* job, Operand* o);
+int launch_lay(int dtype, const LayJob* jobs, int n, const char* label, cudaStream_t s);
 
 // A(m, k) = X(i, j) or, transposed, X(j, i); B(k, n) alike.
 inline void set_a(GemmDesc* g, const Operand& x, bool t) {

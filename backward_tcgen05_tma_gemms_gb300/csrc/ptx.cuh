@@ -134,6 +134,13 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Programmatic dependent launches (early_attribute in internal.cuh).  Every thread of
+// such a kernel waits here, before it reads or writes global memory, until the
+// kernel in front has ended and what that wrote is visible.
+__device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Once every block of a kernel has come here, the next one may start if it is launched so.
+__device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // 2-D tiled load of one box into shared memory; completion is counted in
 // bytes on `bar`.  Coordinates are in elements, innermost first.
 __device__ __forceinline__ void tma_load_2d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int32_t c0,

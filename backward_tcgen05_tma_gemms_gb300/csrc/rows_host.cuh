@@ -72,6 +72,7 @@ inline int launched(const char* what) {
 // Checks and fills a dropout (defined in dropout.cu; nullptr: none).
 int dropout_of(const tps_dropout* o, Dropout* d);
 // Sum of `n` rows of d floats to `out` (f32 or bf16), in a fixed order (norm.cu).
-int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, cudaStream_t s);
+// early: see early_attribute.
+int launch_sum_rows(const float* part, int64_t n, int64_t d, void* out, int dtype, bool early, cudaStream_t s);
 
 }  // namespace tps

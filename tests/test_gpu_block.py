@@ -108,3 +108,48 @@ def test_one_token_on_e4m3():
         want = torch.nn.functional.silu(want @ W1.double() + b1.double()) @ W2.double() + b2.double()
         assert ((h.double() - total) - want).norm() <= 0.11 * want.norm() + 2 * 2.0 ** -8 * total.norm()
         assert torch.equal(stream, before)
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T", [1, 8, 64, 300])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3", "f32"])
+def test_products_right_behind_what_they_read(kind, T, captured):
+    """A few-row product is started before the kernel in front of it ends: in a chain through the same
+    buffers, every call sees the rows and weights of the call before, as with a wait after each."""
+    g = torch.Generator(device="cuda").manual_seed(T)
+    t = torch.float32 if kind == "f32" else torch.bfloat16
+    xs = [torch.randn(T, 512, device="cuda", generator=g).to(t) for _ in range(6)]
+    ws = [(torch.randn(512, 512, device="cuda", generator=g) / 20).to(t) for _ in range(6)]
+    h, r, y, W = torch.empty_like(xs[0]), torch.empty(T, device="cuda"), torch.empty_like(xs[0]), torch.empty_like(ws[0])
+    q = (torch.empty(T, 512, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(T, device="cuda"))
+    qw = (torch.empty(512, 512, dtype=torch.float8_e4m3fn, device="cuda"), torch.empty(512, device="cuda"))
+
+    def chain(wait):
+        out = []
+        for x, w in zip(xs, ws):
+            for weights_last in (False, True):
+                if kind == "e4m3":
+                    pair = [lambda: api.quantize_e4m3(y if weights_last else x, out=q), lambda: api.quantize_e4m3(w, out=qw)]
+                else:
+                    pair = [lambda: api.rmsnorm_fwd(y if weights_last else x, out=(h, None, None, r)),
+                            lambda: api.rmsnorm_fwd(w, out=(W, None, None, torch.empty(512, device="cuda")))]
+                for f in pair if weights_last else pair[::-1]:
+                    f()
+                    wait()
+                if kind == "e4m3":
+                    api.linear_fwd(q[0], qw[0], x_scale=q[1], w_scale=qw[1], weight_layout="out_in", out=(y, None))
+                else:
+                    api.linear_fwd(h, W, weight_layout="out_in", out=(y, None))
+                wait()
+                out.append(y.clone())
+        return out
+    want = chain(torch.cuda.synchronize)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(lambda: None)
+        graph.replay()
+    else:
+        got = chain(lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
