@@ -29,8 +29,8 @@
 // 19.1 us in e4m3.  Fetching W into L2 before the wait as well gave these 27.7 and
 // 17.8 us, but cost a product that follows none of them up to 1 us: left out.
 //
-// Warp roles (192 threads): warp 0 loads (TMA), warp 1 issues the MMAs, warps
-// 2..5 drain tensor memory; all of them add and store.
+// Warp roles (192 to 576 threads): warp 0 loads (TMA), warp 1 issues the MMAs, the
+// others drain tensor memory, four at a time; all of them add and store.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -45,7 +45,7 @@ namespace tps {
 
 namespace {
 
-constexpr int GR_THREADS = 192;
+constexpr int GR_THREADS = 192, GR_MOST_THREADS = 576;  // see threads_of
 constexpr int GR_FEATURES = 128;
 constexpr int GR_W_BYTES = GR_FEATURES * 128;  // 128 bytes of K for each feature
 constexpr int GR_MAX_STAGES = 8, GR_MAX_SPLIT = 8;
@@ -183,7 +183,7 @@ __device__ __forceinline__ int gr_w_plane(int i) { return (0x124 >> (2 * i)) & 3
 
 // W_MN: W's unit stride is along the features.  X_MN: X's along the rows.
 template <bool W_MN, bool X_MN, int KIND>
-__global__ void __launch_bounds__(GR_THREADS)
+__global__ void __launch_bounds__(GR_MOST_THREADS)
     gemm_rows_kernel(const __grid_constant__ CUtensorMap tw, const __grid_constant__ CUtensorMap tx, const GrParams p) {
   extern __shared__ uint8_t smem_raw[];
   const uint32_t raw_addr = smem_u32(smem_raw);
@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(GR_THREADS)
     const int q = warp & 3;
     float* part = reinterpret_cast<float*>(smem) + q * 32 + lane;
     const uint32_t t_row = tmem + (static_cast<uint32_t>(q * 32) << 16);
-    for (int c = 0; c < tokens; c += 16) {
+    for (int c = (warp - 2) / 4 * 16; c < tokens; c += (blockDim.x / 32 - 2) / 4 * 16) {
       uint32_t r[16];
       tmem_ld_32x32b_x16(t_row + c, r);
       tmem_ld_wait();
@@ -492,11 +492,16 @@ constexpr int GR_SHARED_TWO = 106 << 10, GR_SHARED_ONE = 212 << 10;  // of a CTA
 //   start and join of a CTA, its K tiles in turn or the reading of W at the
 //   copy's rate, whichever is longer, and what further waves of clusters add.
 // Fitted to calls of 1 to 512 tokens with K and N from 1024 to 14336, which it
-// gives within about 10 %.  With (K, N) = (14336, 4096), (4096, 14336) and
+// gives within about 20 %.  With (K, N) = (14336, 4096), (4096, 14336) and
 // (4096, 1024), 1 token takes 78, 27, 25 us with one run, 42, 23, 15 with 2, 25, 26, 10 with 4 and
 // 23, 32, 7.5 with 8, where reading W takes 17.3, 17.3 and 1.2 us.
 double tile_us(int bn) { return 0.32 + 0.0003 * bn; }
-double start_us(int bn, int s) { return 5.5 + 0.01 * bn + 0.04 * bn / s; }
+double start_us(int bn, int s) { return 5.5 + 0.005 * bn + 0.012 * bn / s; }
+// More warps drain and add up a wider tile: with 192, 320 and 576 threads 256
+// tokens through 4096 x 4096 take 18.6, 17.4 and 16.8 us in bf16 and 16.1, 14.8 and 13.6 in
+// e4m3; 64 tokens through 4096 x 14336 26.0 and 25.4, one token 22.9 and 23.1 (two
+// CTAs an SM have registers for 320 each).
+int threads_of(int bn) { return bn > 64 ? GR_MOST_THREADS : bn > 32 ? 320 : GR_THREADS; }
 constexpr double kWaveUs = 3.0;        // a further wave where memory bounds the call
 constexpr double kBytesPerUs = 6.776e6;
 // K tiles of one accumulator of planes: the tensor cores cut each partial sum
@@ -582,7 +587,7 @@ int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx
   if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.t_tiles * plan.n_tiles * plan.splits), 1, 1);
-  cfg.blockDim = dim3(GR_THREADS, 1, 1);
+  cfg.blockDim = dim3(static_cast<unsigned>(threads_of(plan.bn)), 1, 1);
   cfg.dynamicSmemBytes = plan.shared;
   cfg.stream = stream;
   cudaLaunchAttribute attr[2];
@@ -682,9 +687,10 @@ bool gemm_rows_supported(const GemmDesc& g) {
 }
 
 // By what either kernel takes: a pair tile's K tile costs 0.31 us, whatever
-// fills its 256 x 256.  Measured (us, this kernel / pairs, bf16): K = 14336, N =
-// 4096: 256 tokens 35 / 72, 512 55 / 72, 1024 96 / 72; K = 4096, N = 4096: 19 / 26, 26 / 26,
-// 41 / 26; K = 4096, N = 14336: 47 / 31, 77 / 48; K = 1024, N = 4096: 13.5 / 11.9, 17.6 / 12.0.
+// fills its 256 x 256.  Measured (us, this kernel / pairs, bf16, 256, 512 and 1024
+// tokens): K = 14336, N = 4096: 33 / 72, 51 / 72, 88 / 74; K = 4096, N = 4096: 17 / 26, 22 / 26,
+// 33 / 27; K = 4096, N = 14336: 37 / 31, 65 / 48, 99 / 70; K = 1024, N = 4096: 11.4 / 11.9, 13.4 /
+// 12.1, 16.9 / 12.6.
 // TPS_LINEAR_ROWS=n takes this kernel for up to n rows and no others.
 bool gemm_rows_preferred(const GemmDesc& g) {
   const char* most = getenv("TPS_LINEAR_ROWS");

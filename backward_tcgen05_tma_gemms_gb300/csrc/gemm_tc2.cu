@@ -529,16 +529,19 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
               if (e.d2 != nullptr) {
                 if (p.tma_store) {
                   tc_store_box(&m.d[1], e.d2_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
-                } else if (live && dbg_store_ok(e, row, col0, n)) {
-                  store_run32(e.d2, e.d2_dtype, row * e.ldd2 + col0, n, v);
+                } else {
+                  tc_store_rows32(e, e.d2, e.d2_dtype, e.ldd2, stg, lane, row0, p.M, col0, n, v);
                 }
               }
               linear_acted(e, v);
-              res.add(e, row, col0, n, live, v);
+              if (e.res != nullptr && !p.tma_store && !__all_sync(0xffffffffu, res.have || !live))
+                tc_add_rows32(e, stg, lane, row0, p.M, col0, n, v);
+              else
+                res.add(e, row, col0, n, live, v);
               if (p.tma_store) {
                 tc_store_box(&m.d[0], e.d_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
-              } else if (live && dbg_store_ok(e, row, col0, n)) {
-                store_run32(e.d, e.d_dtype, row * e.ldd + col0, n, v);
+              } else {
+                tc_store_rows32(e, e.d, e.d_dtype, e.ldd, stg, lane, row0, p.M, col0, n, v);
               }
               continue;
             }
@@ -631,17 +634,20 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
           if (e.d2 != nullptr) {
             if (p.tma_store) {
               tc_store_box(&m.d[1], e.d2_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
-            } else if (live && dbg_store_ok(e, row, col0, n)) {
-              store_run32(e.d2, e.d2_dtype, row * e.ldd2 + col0, n, v);
+            } else {
+              tc_store_rows32(e, e.d2, e.d2_dtype, e.ldd2, stg, lane, row0, p.M, col0, n, v);
             }
           }
           linear_acted(e, v);
-          res.add(e, row, col0, n, live, v);
+          if (e.res != nullptr && !p.tma_store && !__all_sync(0xffffffffu, res.have || !live))
+            tc_add_rows32(e, stg, lane, row0, p.M, col0, n, v);
+          else
+            res.add(e, row, col0, n, live, v);
           if (c + 1 < warp_cols / 32) res.load(e, row, col0 + 32, min(32, p.N - col0 - 32), live);
           if (p.tma_store) {
             tc_store_box(&m.d[0], e.d_dtype, stg + (chunk++ & 1u) * L::kBufBytes, lane, row0, col0, v);
-          } else if (live && dbg_store_ok(e, row, col0, n)) {
-            store_run32(e.d, e.d_dtype, row * e.ldd + col0, n, v);
+          } else {
+            tc_store_rows32(e, e.d, e.d_dtype, e.ldd, stg, lane, row0, p.M, col0, n, v);
           }
         }
         ce_done = true;
@@ -714,7 +720,10 @@ __global__ void __launch_bounds__(T2_THREADS, 1)
           }
         }
         if (FAM != T2_CE && !p.tma_store) {
-          if (row < p.M) epilogue_run32(e, row, col0, n, v);
+          if (FAM == T2_PLAIN && e.mode == EPI_STORE)
+            tc_store_rows32(e, e.d, e.d_dtype, e.ldd, stg, lane, row0, p.M, col0, n, v);
+          else if (row < p.M)
+            epilogue_run32(e, row, col0, n, v);
           continue;
         }
         // the fp32 and bf16 slots (store-only: one shared box), single- or double-buffered

@@ -117,7 +117,7 @@ struct Epilogue {
   // float that multiplies the product, nullptr: 1.
   const float* alpha = nullptr;
   // EPI_LINEAR: each may be null; act may be kActNone.  The residual may be D
-  // itself: every element is read by the thread that stores it, before.
+  // itself: every element is read by the warp that stores it, before.
   const float* row_scale = nullptr;
   const float* col_scale = nullptr;
   const void* bias = nullptr;

@@ -553,6 +553,45 @@ __device__ __forceinline__ void tma_load_maybe_hint(void* dst, const CUtensorMap
 // box_cols x box_rows box, 128-byte swizzle, zero fill out of bounds.
 bool tc_make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                  int box_rows);
+// A 32 x n box of v (lane = row) to rows that TMA cannot store to, through a
+// staging of 33 words a row: row by row, a lane a column.  (Each lane its own row
+// touches 32 sectors a store: 1024 rows by 1024 x 4100 in bf16 33 us so, 16.5 here.)
+__device__ __forceinline__ void tc_store_rows32(const Epilogue& e, void* base, int dtype, int64_t ld, uint8_t* buf, int lane,
+                                                int row0, int M, int col0, int n, const float (&v)[32]) {
+  float* s = reinterpret_cast<float*>(buf);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) s[lane * 33 + i] = v[i];
+  __syncwarp();
+  if (lane < n) {
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) {
+      if (row0 + r >= M) break;
+      if (!dbg_store_ok(e, row0 + r, col0 + lane, 1)) continue;
+      const int64_t at = static_cast<int64_t>(row0 + r) * ld + col0 + lane;
+      const float x = s[r * 33 + lane];
+      if (dtype == TPS_F32)
+        static_cast<float*>(base)[at] = x;
+      else
+        static_cast<__nv_bfloat16*>(base)[at] = __float2bfloat16_rn(x);
+    }
+  }
+  __syncwarp();
+}
+// The residual's box added to v, alike.
+__device__ __forceinline__ void tc_add_rows32(const Epilogue& e, uint8_t* buf, int lane, int row0, int M, int col0, int n,
+                                              float (&v)[32]) {
+  float* s = reinterpret_cast<float*>(buf);
+#pragma unroll 4
+  for (int r = 0; r < 32; ++r) {
+    const bool there = lane < n && row0 + r < M;
+    s[r * 33 + lane] = there ? any_elem(e.res, e.res_dtype, static_cast<int64_t>(row0 + r) * e.ld_res + col0 + lane) : 0.0f;
+  }
+  __syncwarp();
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] += s[lane * 33 + i];
+  __syncwarp();
+}
+
 // The same of e4m3 operands (box_cols: 128, one swizzle row).
 bool tc_make_map8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                   int box_rows);
