@@ -509,7 +509,7 @@ constexpr double kBytesPerUs = 6.776e6;
 // gemm_tc2.cu (T2_SUB).
 constexpr int64_t kPlaneRun = 8;
 // Clusters of s CTAs that the device holds at once with one CTA on an SM, by
-// what the driver says of the kernel: an SM group holds whole clusters only (on
+// what CUDA says of the kernel: an SM group holds whole clusters only (on
 // a GB300 76, 36 and 15 of 2, 4 and 8).
 int64_t clusters_at_once(int s) {
   static std::mutex mu;
