@@ -1007,6 +1007,7 @@ extern "C" int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const
   if (p.y.dtype != TPS_E4M3) return fail(TPS_ERR_DTYPE, "Q must be e4m3");
   if ((rc = aligned_vector(scale, "scale", TPS_F32, rows))) return rc;
   if (rows == 0) return TPS_OK;
+  if (d == 0) return fail(TPS_ERR_SHAPE, "rows without elements");
   p.scale = static_cast<float*>(scale->data);
   p.rows = rows;
   p.d = d;

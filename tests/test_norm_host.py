@@ -159,3 +159,12 @@ def test_vectors_off_their_elements(lib):  # noqa: F811
     assert lib.tps_quantize_e4m3(_r(x), _r(_fake([6, 64], E4M3)), _r(off(6)), None) == LAYOUT
     for rstd, dw in ((off(6), None), (_fake([6]), off(64))):
         assert lib.tps_rmsnorm_bwd(_r(x), _r(x), None, _r(rstd), None, None, None, None, _r(dw), 0x1000, 1 << 20, None) == LAYOUT
+
+
+def test_quantize_rows_without_elements(lib):  # noqa: F811
+    """Rows of nothing have no largest magnitude."""
+    def quant(T, d, dtype=BF16):
+        return lib.tps_quantize_e4m3(_r(_fake([T, d], dtype)), _r(_fake([T, d], E4M3)), _r(_fake([T])), None)
+    for dtype in (BF16, F32):
+        assert quant(6, 0, dtype) == SHAPE and quant(1, 0, dtype) == SHAPE
+        assert quant(0, 0, dtype) == OK
