@@ -209,16 +209,18 @@ __device__ __forceinline__ float linear_act(int act, float z) {
   if (act != kActNone) act_dispatch(act, [&](auto A) { z = linear_act_c<decltype(A)::value>(z); });
   return z;
 }
-// z of one row's columns [col0, col0 + n), n <= C, from the accumulators.
+// z of one row's columns [col0, col0 + n), n <= C, from the accumulators.  Plain
+// loads, and not those of the read-only path: the few-row kernels are resident
+// while the kernel in front may still write the scales and the bias.
 template <int C>
 __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64_t col0, int n, float (&v)[C]) {
   if (e.row_scale != nullptr) {
-    const float rs = __ldg(e.row_scale + row);
+    const float rs = e.row_scale[row];
     const float* p = e.col_scale + col0;
     if (n == C && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
 #pragma unroll
       for (int i = 0; i < C / 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+        const float4 q = reinterpret_cast<const float4*>(p)[i];
         v[4 * i] *= rs * q.x;
         v[4 * i + 1] *= rs * q.y;
         v[4 * i + 2] *= rs * q.z;
@@ -227,7 +229,7 @@ __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64
     } else {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (i < n) v[i] *= rs * __ldg(p + i);
+        if (i < n) v[i] *= rs * p[i];
     }
   }
   if (e.bias == nullptr) return;
@@ -236,7 +238,7 @@ __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64
     if (n == C && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
 #pragma unroll
       for (int i = 0; i < C / 4; ++i) {
-        const float4 q = __ldg(reinterpret_cast<const float4*>(p) + i);
+        const float4 q = reinterpret_cast<const float4*>(p)[i];
         v[4 * i] += q.x;
         v[4 * i + 1] += q.y;
         v[4 * i + 2] += q.z;
@@ -245,14 +247,14 @@ __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64
     } else {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (i < n) v[i] += __ldg(p + i);
+        if (i < n) v[i] += p[i];
     }
   } else {
     const uint16_t* p = static_cast<const uint16_t*>(e.bias) + col0;
     if (n == C && (reinterpret_cast<uintptr_t>(p) & 7u) == 0) {
 #pragma unroll
       for (int i = 0; i < C / 4; ++i) {
-        const uint2 q = __ldg(reinterpret_cast<const uint2*>(p) + i);
+        const uint2 q = reinterpret_cast<const uint2*>(p)[i];
         v[4 * i] += __uint_as_float(q.x << 16);
         v[4 * i + 1] += __uint_as_float(q.x & 0xffff0000u);
         v[4 * i + 2] += __uint_as_float(q.y << 16);
@@ -261,7 +263,7 @@ __device__ __forceinline__ void linear_pre(const Epilogue& e, int64_t row, int64
     } else {
 #pragma unroll
       for (int i = 0; i < C; ++i)
-        if (i < n) v[i] += __uint_as_float(static_cast<uint32_t>(__ldg(p + i)) << 16);
+        if (i < n) v[i] += __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
     }
   }
 }

@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
 #pragma unroll
         for (int u = 0; u < 2; ++u)
 #pragma unroll
-          for (int f = 0; f < F; ++f) q[u][f] = __ldg(reinterpret_cast<const float4*>(src[f] + k + u * 128));
+          for (int f = 0; f < F; ++f) q[u][f] = *reinterpret_cast<const float4*>(src[f] + k + u * 128);
         add(q[0], k);
         add(q[1], k + 128);
       }
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
 #pragma unroll
         for (int f = 0; f < F; ++f) {
           if (k + 4 <= kn) {
-            q[f] = __ldg(reinterpret_cast<const float4*>(src[f] + k));
+            q[f] = *reinterpret_cast<const float4*>(src[f] + k);
           } else {  // the end of K
             q[f].x = src[f][k];
             q[f].y = k + 1 < kn ? src[f][k + 1] : 0.0f;
@@ -433,7 +433,7 @@ __global__ void __launch_bounds__(32 * GF_WARPS) gemm_few_kernel(const GfParams 
         const float* a = src + kk * p.ldw;
         if (kk < kn) {
           if (col + 4 <= p.N) {
-            q[u] = __ldg(reinterpret_cast<const float4*>(a));
+            q[u] = *reinterpret_cast<const float4*>(a);
           } else {
             q[u].x = a[0];
             q[u].y = col + 1 < p.N ? a[1] : 0.0f;

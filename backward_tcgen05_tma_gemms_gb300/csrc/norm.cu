@@ -920,7 +920,7 @@ __global__ void __launch_bounds__(1024) sum_rows_kernel(const float* part, int64
     for (int64_t i = w; i < n; i += U * warps) {
       float x[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) x[u] = i + u * warps < n ? __ldg(part + (i + u * warps) * d + c) : 0.0f;
+      for (int u = 0; u < U; ++u) x[u] = i + u * warps < n ? part[(i + u * warps) * d + c] : 0.0f;
 #pragma unroll
       for (int u = 0; u < U; ++u) acc += x[u];
     }

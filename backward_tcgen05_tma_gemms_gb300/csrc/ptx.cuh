@@ -137,6 +137,9 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
 // Programmatic dependent launches (early_attribute in internal.cuh).  Every thread of
 // such a kernel waits here, before it reads or writes global memory, until the
 // kernel in front has ended and what that wrote is visible.
+// It was resident while the kernel in front wrote, so it has no read-only data: nothing
+// that such a kernel reads goes through __ldg, whose loads the compiler may also move
+// ahead of the wait.
 __device__ __forceinline__ void wait_for_prior_kernel() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Once every block of a kernel has come here, the next one may start if it is launched so.
 __device__ __forceinline__ void let_next_kernel_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
