@@ -28,7 +28,6 @@
 
 #include <cmath>
 #include <cstdlib>
-#include <mutex>
 
 #include "internal.cuh"
 #include "ptx.cuh"
@@ -1285,20 +1284,18 @@ int launch_ce_from_tile_stats(const CeDesc& c, const float* tile_stats, int64_t 
       note_launch();
       if (cudaPeekAtLastError() != cudaSuccess) return TPS_ERR_CUDA;
     }
-    static int occ_f = 0, occ_b = 0;
-    static cudaError_t attr_err = cudaSuccess;
-    static std::once_flag once;
-    std::call_once(once, [] {
-      const int smem = static_cast<int>(sizeof(CfsShared));
-      attr_err = cudaFuncSetAttribute(ce_fused_stream_kernel<float>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      if (attr_err == cudaSuccess)
-        attr_err = cudaFuncSetAttribute(ce_fused_stream_kernel<__nv_bfloat16>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_f, ce_fused_stream_kernel<float>, CFS_THREADS, smem);
-      cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_b, ce_fused_stream_kernel<__nv_bfloat16>, CFS_THREADS, smem);
+    static PerDevice<bool> ready_f, ready_b;
+    static PerDevice<int> blocks_f, blocks_b;
+    const bool f32 = c.dlogits_dtype == TPS_F32;
+    if (!(f32 ? allow_shared(ready_f, ce_fused_stream_kernel<float>, sizeof(CfsShared))
+              : allow_shared(ready_b, ce_fused_stream_kernel<__nv_bfloat16>, sizeof(CfsShared))))
+      return TPS_ERR_CUDA;
+    int occ = 0;
+    on_this_device(f32 ? blocks_f : blocks_b, &occ, [f32](int* n) {
+      return (f32 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, ce_fused_stream_kernel<float>, CFS_THREADS, sizeof(CfsShared))
+                  : cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, ce_fused_stream_kernel<__nv_bfloat16>, CFS_THREADS,
+                                                                  sizeof(CfsShared))) == cudaSuccess;
     });
-    if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
-    const int occ = c.dlogits_dtype == TPS_F32 ? occ_f : occ_b;
     const int64_t items = c.T * ((c.V + CFS_CHUNK - 1) / CFS_CHUNK);
     const int64_t want = static_cast<int64_t>(sms) * (occ > 0 ? occ : 1);
     const unsigned grid = static_cast<unsigned>(items < want ? items : want);
@@ -1324,13 +1321,14 @@ int launch_ce_from_tile_stats(const CeDesc& c, const float* tile_stats, int64_t 
   }
   // exactly the blocks that fit at once: a larger grid would run as a
   // second, partial wave
-  static int occ_f = 0, occ_b = 0;
-  static std::once_flag occ_once;
-  std::call_once(occ_once, [] {
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_f, ce_grad_stream_kernel<float>, CEF_THREADS, 0);
-    cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ_b, ce_grad_stream_kernel<__nv_bfloat16>, CEF_THREADS, 0);
+  static PerDevice<int> blocks_f, blocks_b;
+  const bool f32 = c.dlogits_dtype == TPS_F32;
+  int occ = 0;
+  on_this_device(f32 ? blocks_f : blocks_b, &occ, [f32](int* n) {
+    return (f32 ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, ce_grad_stream_kernel<float>, CEF_THREADS, 0)
+                : cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, ce_grad_stream_kernel<__nv_bfloat16>, CEF_THREADS, 0)) ==
+           cudaSuccess;
   });
-  const int occ = (c.dlogits_dtype == TPS_F32 ? occ_f : occ_b);
   const unsigned grid = static_cast<unsigned>(sms * (occ > 0 ? occ : 1));
   if (c.dlogits_dtype == TPS_F32)
     ce_grad_stream_kernel<float><<<grid, CEF_THREADS, 0, stream>>>(p, ms);
@@ -1393,13 +1391,8 @@ static int launch_cluster(const CeParams& p, cudaStream_t stream) {
   if (z_aligned && max_len + 3 <= CEP_BUF_FLOATS) {
     // persistent clusters, as many as can be resident at once
     const size_t smem = size_t(CEP_NBUF) * CEP_BUF_FLOATS * sizeof(float);
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [smem] {
-      attr_err = cudaFuncSetAttribute(ce_persistent_kernel<TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>(smem));
-    });
-    if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!allow_shared(ready, ce_persistent_kernel<TOut>, smem)) return TPS_ERR_CUDA;
     cfg.blockDim = dim3(CEP_THREADS, 1, 1);
     cfg.dynamicSmemBytes = smem;
     int clusters = 0;
@@ -1416,13 +1409,8 @@ static int launch_cluster(const CeParams& p, cudaStream_t stream) {
   } else if (max_len <= CE_THREADS * 4 * 8) {
     e = launch_cluster_reg<TOut, 8>(p, cfg);
   } else {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-      attr_err = cudaFuncSetAttribute(ce_cluster_kernel<TOut>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                      static_cast<int>((CE_MAX_SHARD + 4) * sizeof(float)));
-    });
-    if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+    static PerDevice<bool> ready;
+    if (!allow_shared(ready, ce_cluster_kernel<TOut>, (CE_MAX_SHARD + 4) * sizeof(float))) return TPS_ERR_CUDA;
     cfg.dynamicSmemBytes = static_cast<size_t>(max_len + 4) * sizeof(float);
     e = cudaLaunchKernelEx(&cfg, ce_cluster_kernel<TOut>, p);
   }

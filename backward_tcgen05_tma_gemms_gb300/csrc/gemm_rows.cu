@@ -36,7 +36,6 @@
 
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 
 #include "api_common.cuh"
 #include "tc_common.cuh"
@@ -485,6 +484,7 @@ struct GrPlan {
 };
 constexpr int64_t kSms = 152;
 constexpr int GR_SHARED_TWO = 106 << 10, GR_SHARED_ONE = 212 << 10;  // of a CTA, two or one on an SM
+constexpr int GR_SHARED_MOST = 227 << 10;
 
 // The tile's tokens, the split of K and the stages.  Tiles of up to 64 tokens
 // leave room for two CTAs on an SM.  The split (powers of two, up to a portable
@@ -510,33 +510,30 @@ constexpr double kBytesPerUs = 6.776e6;
 constexpr int64_t kPlaneRun = 8;
 // Clusters of s CTAs that the device holds at once with one CTA on an SM, by
 // what CUDA says of the kernel: an SM group holds whole clusters only (on
-// a GB300 76, 36 and 15 of 2, 4 and 8).
+// a GB300 76, 36 and 15 of 2, 4 and 8).  Where CUDA does not say it, the SMs
+// divided by s, for this call.
 int64_t clusters_at_once(int s) {
-  static std::mutex mu;
-  static int64_t known[GR_MAX_SPLIT + 1] = {};
-  std::lock_guard<std::mutex> lock(mu);
-  int64_t& n = known[s];
-  if (n == 0) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
-    cfg.blockDim = dim3(GR_THREADS, 1, 1);
-    cfg.dynamicSmemBytes = GR_SHARED_ONE;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = static_cast<unsigned>(s);
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    int m = 0;
-    if (cudaFuncSetAttribute(gemm_rows_kernel<false, false, GR_BF16>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448) != cudaSuccess ||
-        cudaOccupancyMaxActiveClusters(&m, gemm_rows_kernel<false, false, GR_BF16>, &cfg) != cudaSuccess || m < 1) {
-      cudaGetLastError();
-      m = static_cast<int>(kSms / s);
-    }
-    n = m;
-  }
-  return n;
+  static PerDevice<bool> ready;
+  static PerDevice<int> known[GR_MAX_SPLIT + 1];
+  int n = 0;
+  if (on_this_device(known[s], &n, [s](int* m) {
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(s), 1, 1);
+        cfg.blockDim = dim3(GR_THREADS, 1, 1);
+        cfg.dynamicSmemBytes = GR_SHARED_ONE;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeClusterDimension;
+        attr[0].val.clusterDim.x = static_cast<unsigned>(s);
+        attr[0].val.clusterDim.y = 1;
+        attr[0].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return allow_shared(ready, gemm_rows_kernel<false, false, GR_BF16>, GR_SHARED_MOST) &&
+               cudaOccupancyMaxActiveClusters(m, gemm_rows_kernel<false, false, GR_BF16>, &cfg) == cudaSuccess && *m > 0;
+      }))
+    return n;
+  cudaGetLastError();
+  return kSms / s;
 }
 GrPlan plan_of(const GemmDesc& g) {
   GrPlan r;
@@ -579,12 +576,8 @@ GrPlan plan_of(const GemmDesc& g) {
 template <bool W_MN, bool X_MN, int KIND>
 int launch_typed(const GemmDesc& g, const CUtensorMap& tw, const CUtensorMap& tx, const GrParams& p, const GrPlan& plan,
                  cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_rows_kernel<W_MN, X_MN, KIND>, cudaFuncAttributeMaxDynamicSharedMemorySize, 232448);
-  });
-  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  static PerDevice<bool> ready;
+  if (!allow_shared(ready, gemm_rows_kernel<W_MN, X_MN, KIND>, GR_SHARED_MOST)) return TPS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(plan.t_tiles * plan.n_tiles * plan.splits), 1, 1);
   cfg.blockDim = dim3(static_cast<unsigned>(threads_of(plan.bn)), 1, 1);
@@ -621,13 +614,8 @@ bool gemm_few_supported(const GemmDesc& g) {
 
 template <int TT, bool OUT_IN>
 static int launch_few(const GemmDesc& g, const GfParams& p, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_few_kernel<TT, OUT_IN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    GF_SHARED + 4 * GF_WARPS * GF_ROWS * GR_FEATURES);
-  });
-  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  static PerDevice<bool> ready;
+  if (!allow_shared(ready, gemm_few_kernel<TT, OUT_IN>, GF_SHARED + 4 * GF_WARPS * GF_ROWS * GR_FEATURES)) return TPS_ERR_CUDA;
   const int64_t run = ((p.K + 3) / 4 + p.splits - 1) / p.splits * 4;
   const int64_t floats = TT * run + (OUT_IN ? 1 : GF_WARPS) * TT * GR_FEATURES;
   cudaLaunchConfig_t cfg = {};

@@ -489,13 +489,8 @@ bool tc_make_output_maps(const GemmDesc& g, CUtensorMap* td, CUtensorMap* td2, C
 template <bool A_MN, bool B_MN>
 static int launch_typed(const GemmDesc& g, const CUtensorMap& ta, const CUtensorMap& tb, const CUtensorMap& td,
                         const CUtensorMap& td2, const TcParams& p, int grid, cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_tc_kernel<A_MN, B_MN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(TC_SMEM_BYTES));
-  });
-  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  static PerDevice<bool> ready;
+  if (!allow_shared(ready, gemm_tc_kernel<A_MN, B_MN>, TC_SMEM_BYTES)) return TPS_ERR_CUDA;
   ProfScope prof("gemm_tc", g.name, 2.0 * double(g.M) * double(g.N) * double(g.K), 0.0, stream);
   gemm_tc_kernel<A_MN, B_MN><<<grid, TC_THREADS, TC_SMEM_BYTES, stream>>>(ta, tb, td, td2, p);
   note_launch();

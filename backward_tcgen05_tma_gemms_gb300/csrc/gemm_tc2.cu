@@ -42,7 +42,6 @@
 #include <cuda_runtime.h>
 
 #include <cstring>
-#include <mutex>
 
 #include "tc_common.cuh"
 
@@ -771,13 +770,8 @@ bool tc_make_output_maps(const GemmDesc& g, CUtensorMap* td, CUtensorMap* td2, C
 template <bool A_MN, bool B_MN, int FAM>
 static int launch_pair_typed(const GemmDesc& g, const T2Maps& m, const T2Params& p, int pairs,
                              cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(gemm_tc2_kernel<A_MN, B_MN, FAM>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(T2Layout<FAM>::kSmem));
-  });
-  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  static PerDevice<bool> ready;
+  if (!allow_shared(ready, gemm_tc2_kernel<A_MN, B_MN, FAM>, T2Layout<FAM>::kSmem)) return TPS_ERR_CUDA;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   cfg.blockDim = dim3(T2_THREADS, 1, 1);
@@ -794,13 +788,12 @@ static int launch_pair_typed(const GemmDesc& g, const T2Maps& m, const T2Params&
     // Under a K split an epilogue waits for a run that another pair holds:
     // launch only as many pairs as can be resident at once, so that every
     // run it waits for belongs to a running pair.
-    static std::once_flag cl_once;
-    static int max_clusters = 0;
-    std::call_once(cl_once, [&cfg] {
-      if (cudaOccupancyMaxActiveClusters(&max_clusters, gemm_tc2_kernel<A_MN, B_MN, FAM>, &cfg) != cudaSuccess)
-        max_clusters = 0;
-    });
-    if (max_clusters < 1) return TPS_ERR_CUDA;
+    static PerDevice<int> clusters;
+    int max_clusters = 0;
+    if (!on_this_device(clusters, &max_clusters, [&cfg](int* n) {
+          return cudaOccupancyMaxActiveClusters(n, gemm_tc2_kernel<A_MN, B_MN, FAM>, &cfg) == cudaSuccess && *n > 0;
+        }))
+      return TPS_ERR_CUDA;
     if (pairs > max_clusters) cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
   }
   const double flops = 2.0 * double(g.M) * double(g.N) * double(g.K + g.K2 + g.K3) * (p.glu ? 2.0 : 1.0) *

@@ -43,7 +43,6 @@
 
 #include <cstdlib>
 #include <cstring>
-#include <mutex>
 
 #include "tc_common.cuh"
 
@@ -475,9 +474,8 @@ bool gemm_wide_supported(const GemmDesc& g) {
 template <bool B_MN, bool XF>
 static int launch_wide_typed(const WMaps& m, const WParams& p, int pairs, double flops, const char* name,
                              cudaStream_t stream) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;
+  static PerDevice<bool> ready;
+  static PerDevice<int> clusters;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs), 1, 1);
   cfg.blockDim = dim3(W_THREADS, 1, 1);
@@ -490,18 +488,15 @@ static int launch_wide_typed(const WMaps& m, const WParams& p, int pairs, double
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  std::call_once(once, [&cfg] {
-    attr_err = cudaFuncSetAttribute(gemm_wide_kernel<B_MN, XF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    static_cast<int>(W_SMEM));
-    if (attr_err == cudaSuccess &&
-        cudaOccupancyMaxActiveClusters(&max_clusters, gemm_wide_kernel<B_MN, XF>, &cfg) != cudaSuccess)
-      max_clusters = 0;
-  });
-  if (attr_err != cudaSuccess) return TPS_ERR_CUDA;
+  if (!allow_shared(ready, gemm_wide_kernel<B_MN, XF>, W_SMEM)) return TPS_ERR_CUDA;
   // Under a K split an epilogue waits for a run that another pair holds:
   // launch only as many pairs as can be resident at once.
   if (p.ksplit > 1) {
-    if (max_clusters < 1) return TPS_ERR_CUDA;
+    int max_clusters = 0;
+    if (!on_this_device(clusters, &max_clusters, [&cfg](int* n) {
+          return cudaOccupancyMaxActiveClusters(n, gemm_wide_kernel<B_MN, XF>, &cfg) == cudaSuccess && *n > 0;
+        }))
+      return TPS_ERR_CUDA;
     if (pairs > max_clusters) cfg.gridDim = dim3(static_cast<unsigned>(2 * max_clusters), 1, 1);
   }
   ProfScope prof("gemm_tc", name, flops, 0.0, stream);

@@ -5,6 +5,7 @@
 #include <cstdint>
 #include <type_traits>
 
+#include "per_device.h"
 #include "tps.h"
 
 namespace tps {
@@ -314,6 +315,22 @@ struct ProfScope {
   cudaStream_t stream;
 };
 void note_launch();
+// The current device's value of `known`, from `set_up` on the first call there.
+template <class T, class F>
+bool on_this_device(PerDevice<T>& known, T* value, F&& set_up) {
+  int device = -1;
+  return cudaGetDevice(&device) == cudaSuccess && known.get(device, value, set_up);
+}
+// Lets `kernel` have up to `bytes` of dynamic shared memory on the current device.
+// `known` belongs to the kernel.
+template <class K>
+bool allow_shared(PerDevice<bool>& known, K kernel, size_t bytes) {
+  bool done = false;
+  return on_this_device(known, &done, [&](bool* made) {
+    *made = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes)) == cudaSuccess;
+    return *made;
+  });
+}
 // A launch with this attribute starts before the kernel in front has ended, once
 // all blocks of that have allowed it; it waits for it itself (wait_for_prior_kernel
 // in ptx.cuh).

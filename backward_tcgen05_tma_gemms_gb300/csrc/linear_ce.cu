@@ -44,7 +44,6 @@
 
 #include <cmath>
 #include <cstdlib>
-#include <mutex>
 
 #include "api_common.cuh"
 #include "operand.cuh"
@@ -584,12 +583,9 @@ int launch_few(const Call& c, const FewParams& p, cudaStream_t s) {
   if (c.w_out == 1) {
     ce_few_in_out_kernel<E, TT><<<blocks, 32 * kFewWarps, 0, s>>>(p);
   } else {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-      attr = cudaFuncSetAttribute(ce_few_out_in_kernel<E, TT>, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewShared);
-    });
-    if (attr != cudaSuccess) return fail(TPS_ERR_CUDA, "ce_few: %s", cudaGetErrorString(attr));
+    static PerDevice<bool> ready;
+    if (!allow_shared(ready, ce_few_out_in_kernel<E, TT>, kFewShared))
+      return fail(TPS_ERR_CUDA, "ce_few: %s", cudaGetErrorString(cudaGetLastError()));
     const size_t n = 16 / sizeof(E);
     ce_few_out_in_kernel<E, TT><<<blocks, 32 * kFewWarps, TT * ((c.d + n - 1) / n * n) * sizeof(E), s>>>(p);
   }
