@@ -371,9 +371,11 @@ PyObject* quantize_e4m3(PyObject* const* a) {
   return rc != TPS_OK ? PyLong_FromLong(rc) : tuple_of(q, scale);
 }
 
-// Runs body(workspace, bytes) with the caller's workspace, or with one for
-// aligned operands; others are refused before any launch and run again with the
-// size that holds them laid out.
+// Runs body(workspace, bytes) with the caller's workspace, or with the least that
+// may do: a call that needs more is refused before any launch and run again.  A few
+// fp32 rows mostly need none; then comes the size for aligned operands, and at last
+// the one that holds all of them laid out.
+constexpr int64_t kFewRows = 8;
 template <class F>
 int with_room(const Tensor* ws, const Tensor& x, int64_t T, int64_t K, int64_t N, int backward, F&& body) {
   if (ws != nullptr) {
@@ -382,15 +384,20 @@ int with_room(const Tensor* ws, const Tensor& x, int64_t T, int64_t K, int64_t N
     const size_t n = ws->nbytes();
     return run([&] { return body(p, n); });
   }
-  int rc = TPS_OK;
   const int own = dtype_of(x.scalar_type(), true);
-  for (const int dtype : {own, static_cast<int>(TPS_F32)}) {
-    const size_t n = f.linear_workspace_bytes(T, K, N, dtype, backward);
+  const size_t aligned = f.linear_workspace_bytes(T, K, N, own, backward);
+  const size_t laid = own == TPS_BF16 ? f.linear_workspace_bytes(T, K, N, TPS_F32, backward) : aligned;
+  const bool few = own == TPS_F32 && !backward && T <= kFewRows;
+  int rc = TPS_ERR_WORKSPACE;
+  std::optional<size_t> had;
+  for (const size_t n : {few ? size_t(0) : aligned, aligned, laid}) {
+    if (rc != TPS_ERR_WORKSPACE) break;
+    if (had.has_value() && n <= *had) continue;
     std::optional<Tensor> room;
     if (n > 0) room = make({static_cast<int64_t>(n)}, at::kByte, x);
     void* p = n > 0 ? room->data_ptr() : nullptr;
     rc = run([&] { return body(p, n); });
-    if (rc != TPS_ERR_WORKSPACE || own == TPS_F32) break;
+    had = n;
   }
   return rc;
 }
