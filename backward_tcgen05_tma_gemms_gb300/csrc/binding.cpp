@@ -159,6 +159,16 @@ struct Given {
   }
 };
 const Tensor* ptr(const std::optional<Tensor>& t) { return t.has_value() ? &*t : nullptr; }
+// The caller's tensors hold something else now: what an eager graph saved of them is
+// not what it computed with, and its backward pass raises instead of using it.
+// (Inference tensors have no such count, and no graph saves them.)
+template <class... T>
+void written(const T&... given) {
+  auto one = [](const Tensor* t) {
+    if (t != nullptr && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+  };
+  (one(ptr(given)), ...);
+}
 PyObject* wrap(const std::optional<Tensor>& t) { return t.has_value() ? THPVariable_Wrap(*t) : Py_NewRef(Py_None); }
 template <class... T>
 PyObject* tuple_of(const T&... t) {
@@ -267,7 +277,9 @@ PyObject* rmsnorm_fwd(PyObject* const* a) {
   const int rc = run([&] {
     return f.rmsnorm_fwd(vx.p(), vr.p(), vw.p(), eps, dropped ? &d : nullptr, vh.p(), vy.p(), vs.p(), vd.p(), stream);
   });
-  return rc != TPS_OK ? PyLong_FromLong(rc) : tuple_of(y, scale, h, rstd);
+  if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (a[8] != Py_None) written(y, scale, h, rstd);
+  return tuple_of(y, scale, h, rstd);
 }
 
 // (dy, h, weight, rstd, dh, dropout, seed, site, x_dtype, want_dweight, workspace, out)
@@ -318,6 +330,7 @@ PyObject* rmsnorm_bwd(PyObject* const* a) {
                          bytes, stream);
   });
   if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (a[11] != Py_None) written(dx, dres, dw);
   if (!one) return tuple_of(dx, dres, dw);
   PyObject* t = wrap(dres);  // one object for both
   PyObject* u = t == nullptr ? nullptr : wrap(dw);
@@ -336,14 +349,15 @@ PyObject* dropout(PyObject* const* a) {
   const tps_dropout d = dropout_of(a[1], a[2], a[3], &call);
   for (const Tensor* t : {x, res, given}) call.on(t);
   call.check();
-  const Tensor y = given != nullptr ? *given : make(x->sizes(), x->scalar_type(), *x);
-  const View vx = view(x, ROWS), vr = view(res, ROWS), vy = view(&y, ROWS);
+  const std::optional<Tensor> y = given != nullptr ? *given : make(x->sizes(), x->scalar_type(), *x);
+  const View vx = view(x, ROWS), vr = view(res, ROWS), vy = view(ptr(y), ROWS);
   const bool back = truth(a[6]);
   void* stream = call.stream();
   const int rc = run([&] {
     return back ? f.dropout_bwd(vx.p(), &d, vy.p(), stream) : f.dropout_fwd(vx.p(), vr.p(), &d, vy.p(), stream);
   });
   if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (given != nullptr) written(y);
   return wrap(y);
 }
 
@@ -368,7 +382,9 @@ PyObject* quantize_e4m3(PyObject* const* a) {
   const View vx = view(x, ROWS), vq = view(ptr(q), ROWS, true), vs = view(ptr(scale), FLAT);
   void* stream = call.stream();
   const int rc = run([&] { return f.quantize_e4m3(vx.p(), vq.p(), vs.p(), stream); });
-  return rc != TPS_OK ? PyLong_FromLong(rc) : tuple_of(q, scale);
+  if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (a[1] != Py_None) written(q, scale);
+  return tuple_of(q, scale);
 }
 
 // Runs body(workspace, bytes) with the caller's workspace, or with the least that
@@ -442,7 +458,9 @@ PyObject* linear_fwd(PyObject* const* a) {
   const int rc = with_room(ws, *x, s.T, s.K, s.N, 0, [&](void* p, size_t n) {
     return f.linear_fwd(vx.p(), vw.p(), vb.p(), vr.p(), act, layout, v1.p(), v2.p(), vz.p(), vy.p(), p, n, stream);
   });
-  return rc != TPS_OK ? PyLong_FromLong(rc) : tuple_of(y, z);
+  if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (a[11] != Py_None) written(y, z);
+  return tuple_of(y, z);
 }
 
 // (x, W, dy, pre, act, layout, want_dx, want_dw, want_dbias, grad_dtype, workspace, out)
@@ -472,7 +490,9 @@ PyObject* linear_bwd(PyObject* const* a) {
   const int rc = with_room(ws, *x, s.T, s.K, s.N, 1, [&](void* p, size_t n) {
     return f.linear_bwd(vx.p(), vw.p(), vy.p(), vz.p(), act, layout, v1.p(), v2.p(), v3.p(), p, n, stream);
   });
-  return rc != TPS_OK ? PyLong_FromLong(rc) : tuple_of(dx, dw, db);
+  if (rc != TPS_OK) return PyLong_FromLong(rc);
+  if (a[11] != Py_None) written(dx, dw, db);
+  return tuple_of(dx, dw, db);
 }
 
 // Addresses of the library's entry points, in the order of Entries.

@@ -32,3 +32,81 @@ def test_few_fp32_rows_take_no_workspace(T, layout):
     want, S = x.double() @ w64, x.double().abs() @ w64.abs()
     for got in (y, z):  # sums of K products, each rounding at most 2^-24 of what is summed, and the output's
         assert ((got.double() - want).abs() <= (K + 2) * 2.0 ** -24 * S).all()
+
+
+def calls():
+    """name -> (call, outputs it is given)."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+
+    def r(*s):
+        return torch.randn(*s, device="cuda", generator=g).to(BF)
+    x, res, dy, W, z = r(16, 64), r(16, 64), r(16, 64), r(64, 64), r(16, 64)
+    rstd, dw, vec = torch.ones(16, device="cuda"), torch.empty(64, device="cuda"), torch.empty(16, device="cuda")
+    q8, y8 = (torch.empty(16, 64, device="cuda", dtype=torch.float8_e4m3fn) for _ in range(2))
+    out = {}
+    y, h = r(16, 64), r(16, 64)
+    out["norm"] = (lambda: api.rmsnorm_fwd(x, residual=res, out=(y, None, h, rstd)), [y, h, rstd])
+    over, r2 = r(16, 64), torch.ones(16, device="cuda")
+    out["norm over its input"] = (lambda: api.rmsnorm_fwd(over, out=(over, None, None, r2)), [over, r2])
+    joined, y2, r3 = r(16, 64), r(16, 64), torch.ones(16, device="cuda")
+    out["norm over the residual"] = (lambda: api.rmsnorm_fwd(x, residual=joined, out=(y2, None, joined, r3)), [joined, y2, r3])
+    r4, s4 = torch.ones(16, device="cuda"), torch.ones(16, device="cuda")
+    out["norm to e4m3"] = (lambda: api.rmsnorm_fwd(x, out_dtype=y8.dtype, out=(y8, s4, None, r4)), [y8, s4, r4])
+    dx, ds = r(16, 64), r(16, 64)
+    out["norm backward"] = (lambda: api.rmsnorm_bwd(dy, x, None, vec.fill_(1.0), out=(dx, ds, dw)), [dx, ds, dw])
+    d1, d2 = r(16, 64), r(16, 64)
+    out["dropout"] = (lambda: api.dropout_fwd(d1, 0.5, 3, out=d1), [d1])
+    out["dropout backward"] = (lambda: api.dropout_bwd(dy, 0.5, 3, out=d2), [d2])
+    sq = torch.empty(16, device="cuda")
+    out["e4m3 rows"] = (lambda: api.quantize_e4m3(x, out=(q8, sq)), [q8, sq])
+    l1, l2 = r(16, 64), r(16, 64)
+    out["linear"] = (lambda: api.linear_fwd(x, W, act="silu", out=(l1, l2)), [l1, l2])
+    l3 = r(16, 64)
+    out["linear over the residual"] = (lambda: api.linear_fwd(x, W, residual=l3, out=(l3, None)), [l3])
+    g1, g2, g3 = r(16, 64), r(64, 64), torch.empty(64, device="cuda")
+    out["linear backward"] = (lambda: api.linear_bwd(x, W, dy, pre=z, act="silu", out=(g1, g2, g3)), [g1, g2, g3])
+    return out
+
+
+def test_writes_are_counted():
+    """Each tensor that a call was given as an output has another version afterwards, the inputs the same."""
+    for name, (call, given) in calls().items():
+        before = [t._version for t in given]
+        call()
+        assert all(t._version > v for t, v in zip(given, before)), name
+    x = torch.randn(16, 64, device="cuda")
+    y, _, _, rstd = api.rmsnorm_fwd(x)
+    api.linear_fwd(x, torch.randn(64, 64, device="cuda"))
+    assert x._version == 0 and y._version == 0 and rstd._version == 0
+
+
+def test_a_refused_call_counts_nothing():
+    x, y = torch.randn(4, 64, device="cuda"), torch.randn(4, 63, device="cuda")
+    before = y._version
+    with pytest.raises(ValueError, match="shape"):
+        api.dropout_fwd(x, 0.5, 1, out=y)
+    assert y._version == before
+
+
+def test_an_eager_graph_notices():
+    """exp saves its result for its backward pass, which raises once a call has written over it."""
+    for call in (lambda s: api.rmsnorm_fwd(s, out=(s, None, None, torch.empty(8, device="cuda"))),
+                 lambda s: api.dropout_fwd(s, 0.5, 1, out=s),
+                 lambda s: api.linear_fwd(torch.randn(8, 64, device="cuda"), torch.randn(64, 64, device="cuda"), residual=s,
+                                          out=(s, None)),
+                 lambda s: api.rmsnorm_bwd(s, s.clone(), None, torch.ones(8, device="cuda"), out=(s, None, None))):
+        leaf = torch.randn(8, 64, device="cuda", requires_grad=True)
+        saved = leaf.exp()
+        call(saved.detach())
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            saved.sum().backward()
+
+
+def test_inference_tensors():
+    with torch.inference_mode():
+        x = torch.randn(8, 64, device="cuda")
+        want = api.dropout_fwd(x, 0.5, 1)
+        api.dropout_fwd(x, 0.5, 1, out=x)
+    assert torch.equal(x, want)
+    api.dropout_fwd(torch.zeros(8, 64, device="cuda"), 0.5, 1, out=x)
+    assert not x.any()
