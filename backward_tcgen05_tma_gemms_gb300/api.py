@@ -10,6 +10,8 @@ built library or a GPU these functions raise.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 import struct
 from array import array
@@ -259,6 +261,22 @@ def _raw_stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _counts_writes(fn):
+    """The tensors that a call is given by `out` hold something else afterwards:
+    what autograd saved of them is not what it computed with."""
+    at = list(inspect.signature(fn).parameters).index("out")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        r = fn(*args, **kw)
+        out = kw.get("out") if len(args) <= at else args[at]
+        if out is not None:
+            given = (out,) if isinstance(out, torch.Tensor) else out
+            torch.autograd.graph.increment_version([t for t in given if t is not None and not t.is_inference()])
+        return r
+    return call
+
+
 def _parts(v, name="parts") -> int:
     if type(v) is not int or v < 1:
         raise ValueError("partition")
@@ -275,6 +293,7 @@ def plan_shards(dim: int, parts: int) -> list:
     return list(off)
 
 
+@_counts_writes
 def matmul_fwd_bwd(A: torch.Tensor, B: torch.Tensor, G: torch.Tensor, parts: int, axis: str,
                    out: Optional[Sequence[torch.Tensor]] = None):
     """(Y, dA, dB) of L = <G, AB> split over `parts` ranks along `axis`.
@@ -300,6 +319,7 @@ def mlp_workspace_bytes(T: int, d: int, F: int, tp: int, dtype: torch.dtype) -> 
     return int(library().tps_mlp_workspace_bytes(T, d, F, tp, _DTYPES[dtype]))
 
 
+@_counts_writes
 def mlp_fwd_bwd(X: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, GY: torch.Tensor, tp: int,
                 act: str = "gelu_tanh", weight_layout: str = "in_out", workspace: Optional[torch.Tensor] = None,
                 out: Optional[Sequence[torch.Tensor]] = None):
@@ -330,6 +350,7 @@ def mlp_fwd_bwd(X: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, GY: torch.T
 MLP_NOALLOC_SCRATCH_BYTES = 32 * 1024 * 1024
 
 
+@_counts_writes
 def mlp_fwd_bwd_noalloc(X: torch.Tensor, W1: torch.Tensor, W2: torch.Tensor, GY: torch.Tensor, tp: int,
                         act: str = "gelu_tanh", weight_layout: str = "in_out",
                         out: Optional[Sequence[torch.Tensor]] = None):
@@ -383,6 +404,7 @@ def glu_mlp_workspace_bytes(T: int, d: int, F: int, tp: int, dtype: torch.dtype)
     return int(library().tps_glu_mlp_workspace_bytes(T, d, F, tp, _DTYPES[dtype]))
 
 
+@_counts_writes
 def glu_mlp_fwd_bwd(X: torch.Tensor, Wg: torch.Tensor, Wu: torch.Tensor, W2: torch.Tensor, GY: torch.Tensor,
                     tp: int, act: str = "silu", weight_layout: str = "in_out",
                     workspace: Optional[torch.Tensor] = None, out: Optional[Sequence[torch.Tensor]] = None):
@@ -421,6 +443,7 @@ def plan_heads(n_heads: int, n_kv_heads: int, tp: int):
     return list(q_off), list(kv_first), int(cnt.value), int(rep.value)
 
 
+@_counts_writes
 def attn_qkv_fwd(X, Wq, Wk, Wv, n_heads: int, n_kv_heads: int, tp: int, weight_layout: str = "in_out",
                  out_dtype: Optional[torch.dtype] = None, out: Optional[Sequence[torch.Tensor]] = None):
     """(Q, K, V) of the head-split column-parallel projections."""
@@ -440,6 +463,7 @@ def attn_qkv_fwd(X, Wq, Wk, Wv, n_heads: int, n_kv_heads: int, tp: int, weight_l
     return tuple(out)
 
 
+@_counts_writes
 def attn_qkv_bwd(X, Wq, Wk, Wv, dQ, dK, dV, n_heads: int, n_kv_heads: int, tp: int, weight_layout: str = "in_out",
                  out: Optional[Sequence[torch.Tensor]] = None):
     """fp32 (dX, dWq, dWk, dWv)."""
@@ -456,6 +480,7 @@ def attn_qkv_bwd(X, Wq, Wk, Wv, dQ, dK, dV, n_heads: int, n_kv_heads: int, tp: i
     return tuple(out)
 
 
+@_counts_writes
 def attn_out_fwd_bwd(C, Wo, GY, n_heads: int, tp: int, weight_layout: str = "in_out",
                      dC_dtype: Optional[torch.dtype] = None, out: Optional[Sequence[torch.Tensor]] = None):
     """(Y fp32, dC, dWo fp32) of the row-parallel output projection."""
@@ -473,6 +498,7 @@ def attn_out_fwd_bwd(C, Wo, GY, n_heads: int, tp: int, weight_layout: str = "in_
     return tuple(out)
 
 
+@_counts_writes
 def vocab_ce_fwd_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, tp: int,
                      weight_layout: str = "in_out", workspace: Optional[torch.Tensor] = None,
                      out: Optional[Sequence[torch.Tensor]] = None):
@@ -499,6 +525,7 @@ def vocab_ce_fwd_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor,
     return loss, dlog, dh, owner
 
 
+@_counts_writes
 def vocab_ce_fwd_bwd_ex(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, tp: int,
                         weight_layout: str = "in_out", ignore_index: Optional[int] = None, vocab_size: int = 0,
                         reduction: str = "none", denominator: float = 0.0, want_dwhead: bool = False,
@@ -583,6 +610,7 @@ def _linear_ce_args(h, Whead, weight_layout, ignore_index, vocab_size, reduction
     return (h.numel() // d if d else 0), d, V, opts
 
 
+@_counts_writes
 def linear_ce_fwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, weight_layout: str = "in_out",
                   ignore_index: Optional[int] = None, vocab_size: int = 0, reduction: str = "none",
                   denominator: float = 0.0, workspace: Optional[torch.Tensor] = None,
@@ -605,6 +633,7 @@ def linear_ce_fwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, we
     return loss, red, lse
 
 
+@_counts_writes
 def linear_ce_bwd(h: torch.Tensor, Whead: torch.Tensor, labels: torch.Tensor, lse: torch.Tensor,
                   grad_loss: Optional[torch.Tensor] = None, weight_layout: str = "in_out",
                   ignore_index: Optional[int] = None, vocab_size: int = 0, reduction: str = "none",
@@ -663,6 +692,7 @@ def _rope(fn, plan, q, k, positions, head_dim, out):
     return tuple(out)
 
 
+@_counts_writes
 def rope_fwd(plan: RopePlan, q: torch.Tensor, k: Optional[torch.Tensor], positions: torch.Tensor,
              head_dim: Optional[int] = None, out: Optional[Sequence[torch.Tensor]] = None):
     """(q', k'): the heads turned by their positions.  q and k are (T, H, D)
@@ -671,6 +701,7 @@ def rope_fwd(plan: RopePlan, q: torch.Tensor, k: Optional[torch.Tensor], positio
     return _rope(library().tps_rope_fwd, plan, q, k, positions, head_dim, out)
 
 
+@_counts_writes
 def rope_bwd(plan: RopePlan, dq: torch.Tensor, dk: Optional[torch.Tensor], positions: torch.Tensor,
              head_dim: Optional[int] = None, out: Optional[Sequence[torch.Tensor]] = None):
     """Gradients of q and k from those of rope_fwd's results."""
@@ -918,6 +949,7 @@ def _grad_list(grads):
     return grads, array("Q", list(map(cls.data_ptr, grads))), array("q", list(map(cls.numel, grads))), codes, devices
 
 
+@_counts_writes
 def grad_norm(grads: Sequence[torch.Tensor], max_norm: float = 0.0, workspace: Optional[torch.Tensor] = None,
               out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """fp32 tensor (norm, coefficient): the 2-norm of all gradients together

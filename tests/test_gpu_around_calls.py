@@ -110,3 +110,34 @@ def test_inference_tensors():
     assert torch.equal(x, want)
     api.dropout_fwd(torch.zeros(8, 64, device="cuda"), 0.5, 1, out=x)
     assert not x.any()
+
+
+def test_writes_of_the_other_calls_are_counted():
+    g = torch.Generator(device="cuda").manual_seed(2)
+
+    def r(*s, t=FP):
+        return torch.randn(*s, device="cuda", generator=g).to(t)
+    T, d, F, V = 32, 64, 128, 256
+    X, W1, W2, GY, h = r(T, d, t=BF), r(d, F, t=BF), r(F, d, t=BF), r(T, d, t=BF), r(T, d, t=BF)
+    Wh, labels = r(d, V, t=BF), torch.randint(0, V, (T,), device="cuda", generator=g)
+    q, k, pos = r(T, 2, 32, t=BF), r(T, 1, 32, t=BF), torch.arange(T, device="cuda")
+    plan = api.rope_plan(32)
+    lse = api.linear_ce_fwd(h, Wh, labels)[2]
+    cases = {
+        "matmul": (lambda out: api.matmul_fwd_bwd(X, W1, r(T, F, t=BF), 2, "rows", out=out), [r(T, F), r(T, d), r(d, F)]),
+        "mlp": (lambda out: api.mlp_fwd_bwd(X, W1, W2, GY, 2, out=out), [r(T, d), r(T, d), r(d, F), r(F, d)]),
+        "mlp without workspace": (lambda out: api.mlp_fwd_bwd_noalloc(X, W1, W2, GY, 2, out=out), [r(T, d), r(T, d), r(d, F), r(F, d)]),
+        "gated mlp": (lambda out: api.glu_mlp_fwd_bwd(X, W1, W1, W2, GY, 2, out=out), [r(T, d), r(T, d), r(d, F), r(d, F), r(F, d)]),
+        "cross entropy": (lambda out: api.vocab_ce_fwd_bwd(h, Wh, labels, 2, out=out),
+                          [r(T), r(T, V, t=BF), r(T, d), torch.zeros(T, device="cuda", dtype=torch.int32)]),
+        "head cross entropy": (lambda out: api.linear_ce_fwd(h, Wh, labels, out=out), [r(T), None, r(T)]),
+        "its backward": (lambda out: api.linear_ce_bwd(h, Wh, labels, lse, out=out), [r(T, d), r(d, V)]),
+        "rope": (lambda out: api.rope_fwd(plan, *out, pos, out=out), [q, k]),
+        "rope backward": (lambda out: api.rope_bwd(plan, *out, pos, out=out), [q, k]),
+        "norm of gradients": (lambda out: api.grad_norm([X], 1.0, out=out[0]), [r(2)]),
+    }
+    for name, (call, out) in cases.items():
+        given = [t for t in out if t is not None]
+        before = [t._version for t in given]
+        call(out)
+        assert all(t._version > v for t, v in zip(given, before)), name
