@@ -137,11 +137,19 @@ int as_mat(const tps_tensor* t, const char* name, bool flatten, Mat* m) {
   int64_t rows = 1;
   for (int i = 0; i < last; ++i) rows *= t->shape[i];
   m->rows = rows;
-  // row stride: the stride of the innermost leading dim; the others must nest
+  // row stride: the stride of the innermost leading dimension; the others must
+  // nest (extents of one have no say: nothing is reached over their strides)
   m->sr = t->stride[last - 1];
-  for (int i = 0; i < last - 1; ++i) {
-    if (t->shape[i] > 1 && t->stride[i] != t->stride[i + 1] * t->shape[i + 1])
+  bool first = true;
+  int64_t nested = 0;
+  for (int i = last - 1; i >= 0; --i) {
+    if (t->shape[i] <= 1) continue;
+    if (first)
+      m->sr = t->stride[i];
+    else if (t->stride[i] != nested)
       return fail(TPS_ERR_LAYOUT, "%s: leading dimensions are not contiguous", name);
+    first = false;
+    nested = t->stride[i] * t->shape[i];
   }
   if (m->rows <= 1) m->sr = (m->sc == 1) ? (m->cols > 0 ? m->cols : 1) : 1;
   if (m->cols <= 1) m->sc = (m->sr == 1) ? (m->rows > 0 ? m->rows : 1) : 1;

@@ -141,3 +141,22 @@ def test_writes_of_the_other_calls_are_counted():
         before = [t._version for t in given]
         call(out)
         assert all(t._version > v for t, v in zip(given, before)), name
+
+
+def test_last_tokens_of_a_batch():
+    """Views [:, -1:] of (batch, tokens, d), in and out: as their contiguous copies."""
+    big, bres, bout = (torch.randn(5, 3, 64, device="cuda").to(BF) for _ in range(3))
+    x, res = big[:, -1:], bres[:, -1:]
+    W = torch.randn(64, 72, device="cuda").to(BF)
+    want = api.rmsnorm_fwd(x.contiguous(), residual=res.contiguous())
+    got = api.rmsnorm_fwd(x, residual=res)
+    assert all(a is b is None or torch.equal(a, b) for a, b in zip(got, want))
+    rest = bout[:, :2].clone()
+    api.rmsnorm_fwd(x, residual=res, out=(bout[:, -1:], None, got[2], got[3]))
+    assert torch.equal(bout[:, -1:], want[0]) and torch.equal(bout[:, :2], rest)
+    assert torch.equal(api.linear_fwd(x, W)[0], api.linear_fwd(x.contiguous(), W)[0])
+    assert torch.equal(api.dropout_fwd(x, 0.5, 3), api.dropout_fwd(x.contiguous(), 0.5, 3))
+    assert all(torch.equal(a, b) for a, b in zip(api.quantize_e4m3(x), api.quantize_e4m3(x.contiguous())))
+    a = api.rmsnorm_bwd(x, got[2], None, got[3], dh=res)
+    b = api.rmsnorm_bwd(x.contiguous(), got[2], None, got[3], dh=res.contiguous())
+    assert all(torch.equal(p, q) for p, q in zip(a, b))

@@ -168,3 +168,21 @@ def test_quantize_rows_without_elements(lib):  # noqa: F811
     for dtype in (BF16, F32):
         assert quant(6, 0, dtype) == SHAPE and quant(1, 0, dtype) == SHAPE
         assert quant(0, 0, dtype) == OK
+
+
+def test_leading_extents_of_one(lib):  # noqa: F811
+    """Rows with one pitch are rows with one pitch whatever the strides of extents of one are: the last tokens of
+    a batch, [:, -1:].  What passes the views is refused for its eps, before any launch."""
+    def view(shape, strides):
+        return fwd(lib, x=_fake(shape, BF16, strides), eps=-1.0)
+    assert view([6, 1, 64], [128, 64, 1]) == ARG
+    assert view([1, 6, 64], [999, 128, 1]) == ARG
+    assert view([6, 1, 64], [128, 999, 1]) == ARG
+    assert view([2, 1, 3, 64], [384, 7, 128, 1]) == ARG
+    assert view([2, 3, 1, 64], [384, 128, 7, 1]) == ARG
+    assert view([3, 0, 64], [64, 64, 1]) == ARG
+    assert view([2, 3, 64], [0, 0, 1]) == ARG
+    assert view([2, 3, 64], [192, 0, 1]) == LAYOUT
+    assert view([2, 3, 64], [0, 64, 1]) == LAYOUT
+    assert view([2, 1, 3, 64], [999, 192, 64, 1]) == LAYOUT
+    assert view([2, 3, 1, 64], [999, 64, 64, 1]) == LAYOUT
