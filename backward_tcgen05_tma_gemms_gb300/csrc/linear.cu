@@ -356,8 +356,9 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
   if (dW != nullptr) {
     if ((rc = as_mat(dW, "dW", false, &dw)) || (rc = expect(dw, "dW", c.w.rows, c.w.cols))) return rc;
     if (dw.dtype != TPS_F32 && dw.dtype != TPS_BF16) return fail(TPS_ERR_DTYPE, "dW must be f32 or bf16");
-    const int64_t outer = dw.sc == 1 ? dw.sr : dw.sc, inner = dw.sc == 1 ? dw.cols : dw.rows;
-    if (dw.rows > 1 && dw.cols > 1 && outer < inner) return fail(TPS_ERR_LAYOUT, "dW: rows overlap");
+    const bool by_rows = dw.sc == 1;
+    if ((by_rows ? dw.rows : dw.cols) > 1 && (by_rows ? dw.sr < dw.cols : dw.sc < dw.rows))
+      return fail(TPS_ERR_LAYOUT, "dW: rows overlap");
     if (reinterpret_cast<uintptr_t>(dw.data) % es_of(dw.dtype) != 0) return fail(TPS_ERR_LAYOUT, "dW: misaligned data");
   }
   if (dbias != nullptr) {

@@ -131,3 +131,21 @@ def test_vectors_off_their_elements(lib):  # noqa: F811
     for db in (off(40), off(40, BF16, 1)):
         assert lib.tps_linear_bwd(_r(_fake([6, 64], BF16)), _r(_fake([64, 40], BF16)), _r(_fake([6, 40], BF16)), None, NONE,
                                   IN_OUT, None, None, _r(db), 0x1000, 1 << 20, None) == LAYOUT
+
+
+def test_weight_gradient_that_overlaps(lib):  # noqa: F811
+    """Every element of dW has a place of its own, also where W is a vector."""
+    def bwd(w, dw):
+        K, N = w
+        return lib.tps_linear_bwd(_r(_fake([6, K], BF16)), _r(_fake(list(w), BF16)), _r(_fake([6, N], BF16)), None, NONE,
+                                  IN_OUT, None, _r(_fake(list(w), F32, dw)), None, None, 0, None)
+    for w, dw in (((64, 40), [0, 1]), ((64, 40), [39, 1]), ((64, 40), [1, 63]), ((64, 1), [0, 1]), ((64, 1), [-1, 1]),
+                  ((1, 40), [40, 0]), ((1, 40), [40, -1])):
+        assert bwd(w, dw) == LAYOUT, (w, dw)
+    # fine: refused at last for want of a workspace for x and W, which start off 16 bytes
+    for w, dw in (((64, 1), [1, 1]), ((64, 1), [5, 1]), ((1, 40), [40, 1]), ((1, 40), [0, 1]), ((64, 1), [1, 0])):
+        K, N = w
+        x, W = _fake([6, K], BF16), _fake(list(w), BF16)
+        x.data = W.data = 0x1002
+        assert lib.tps_linear_bwd(_r(x), _r(W), _r(_fake([6, N], BF16)), None, NONE, IN_OUT, None, _r(_fake(list(w), F32, dw)),
+                                  None, None, 0, None) == WORKSPACE, (w, dw)
