@@ -737,7 +737,8 @@ def rmsnorm_bwd(dy: torch.Tensor, h: torch.Tensor, weight: Optional[torch.Tensor
     (dx, dresidual, dweight).  dh: the gradient that reaches h past the norm.
     dx has x_dtype (h's by default), dresidual h's type; without dropout and
     with one type the two are one tensor.  dweight is fp32.  dropout, seed and
-    site as in the forward call.  `out` may supply the three."""
+    site as in the forward call.  `out` may supply the three; one tensor for
+    the first two only without dropout."""
     r = (_fast or _native()).rmsnorm_bwd(dy, h, weight, rstd, dh, dropout, seed, site, x_dtype, want_dweight, workspace,
                                          out)
     return r if type(r) is tuple else _check(r)

@@ -1039,6 +1039,10 @@ extern "C" int tps_rmsnorm_bwd(const tps_tensor* dY, const tps_tensor* H, const 
   for (const Rows* g : {&p.dh, &p.dsum})
     if (g->p != nullptr && g->dtype != p.h.dtype) return fail(TPS_ERR_DTYPE, "dH and dSum must have H's type");
   if (dX != nullptr && (rc = float_rows(dX, "dX", true, rows, d, &p.dx))) return rc;
+  // One tensor for both holds both where they are one number.
+  if (rows > 0 && d > 0 && p.dsum.p != nullptr && p.dsum.p == p.dx.p &&
+      (p.drop.step != 0u || p.dx.dtype != p.dsum.dtype || (rows > 1 && p.dx.ld != p.dsum.ld)))
+    return fail(TPS_ERR_ARG, "dSum and dX are one tensor, but differ by the dropout, their types or pitches");
   if (dweight != nullptr && (rc = aligned_vector(dweight, "dweight", TPS_F32, d))) return rc;
   cudaStream_t s = static_cast<cudaStream_t>(cuda_stream);
   if (d == 0) return rows == 0 ? TPS_OK : fail(TPS_ERR_SHAPE, "rows without elements");

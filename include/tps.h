@@ -449,9 +449,10 @@ size_t tps_linear_ce_workspace_bytes(int64_t T, int64_t d, int64_t V, int32_t dt
  * H: the h of the forward pass.  dH (NULL: none): the gradient that reaches h
  * on the residual's own way.  dY, dX: F32 or BF16, each of its own; dH, dSum:
  * H's type; dweight (d): F32.  dSum, dX and dweight may each be NULL.  dSum may
- * be dH, dX may be dY.  dweight needs a workspace
- * of tps_rmsnorm_workspace_bytes, 256-byte aligned; its sums are taken in a
- * fixed order.
+ * be dH, dX may be dY, and without dropout dSum and dX of one type may be one
+ * tensor (TPS_ERR_ARG with it); otherwise outputs overlap nothing.  dweight needs
+ * a workspace of tps_rmsnorm_workspace_bytes, 256-byte aligned; its sums are
+ * taken in a fixed order.
  * tps_dropout_fwd: Y = dropout(X) + residual (NULL: none); tps_dropout_bwd:
  * dX = dropout(dY).  (..., d), F32 or BF16, each of its own; Y may be X or the
  * residual.
@@ -497,7 +498,7 @@ int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor
  * once.  Backward: dY and Z F32 or BF16 (Z NULL without an activation); dX,
  * dW, dbias F32 or BF16, each of its own, each may be NULL.  dz is rounded to
  * the operands' type where it enters the products; dbias sums it unrounded, in
- * a fixed order.  The residual's gradient is dY itself.
+ * a fixed order.  The residual's gradient is dY itself.  Outputs overlap nothing.
  * `workspace`: 256-byte aligned.  tps_linear_workspace_bytes gives what a call
  * of F32 or BF16 operands needs at most (0: none, as for E4M3); BF16 operands
  * that TMA cannot describe (a base or a row pitch that is not a multiple of 16

@@ -186,3 +186,19 @@ def test_leading_extents_of_one(lib):  # noqa: F811
     assert view([2, 3, 64], [0, 64, 1]) == LAYOUT
     assert view([2, 1, 3, 64], [999, 192, 64, 1]) == LAYOUT
     assert view([2, 3, 1, 64], [999, 64, 64, 1]) == LAYOUT
+
+
+def test_one_tensor_for_both_gradients(lib):  # noqa: F811
+    """dSum and dX differ by the dropout: they cannot be one tensor then.  What passes is refused for its
+    workspace, before any launch."""
+    def bwd(drop, dsum, dx, h=BF16):
+        return lib.tps_rmsnorm_bwd(_r(_fake([6, 64], BF16)), _r(_fake([6, 64], h)), None, _r(_fake([6])), None, drop, _r(dsum),
+                                   _r(dx), _r(_fake([64])), None, 0, None)
+    t, other = _fake([6, 64], BF16), _fake([6, 64], BF16)
+    other.data = 0x9000
+    assert bwd(_drop(0.25), t, t) == ARG
+    assert bwd(_drop(0.25), t, other) == WORKSPACE
+    assert bwd(None, t, t) == WORKSPACE and bwd(_drop(0.0), t, t) == WORKSPACE
+    assert bwd(None, _fake([6, 64]), t, h=F32) == ARG                               # fp32 and bf16 in one place
+    assert bwd(None, t, _fake([6, 64], BF16, [128, 1])) == ARG
+    assert bwd(_drop(0.25), t, None) == WORKSPACE and bwd(_drop(0.25), None, t) == WORKSPACE
