@@ -247,6 +247,10 @@ int run_few(GemmDesc g, int64_t d_sm, cudaStream_t s) {
   return rc == TPS_ERR_CUDA ? fail(rc, "%s: launch failed: %s", g.name, cudaGetErrorString(cudaGetLastError())) : rc;
 }
 
+// The six products of fp32 planes go through one count of K tiles.
+int contraction(int dt, int64_t K) {
+  return dt == TPS_F32 && 6 * K >= (1ll << 31) ? fail(TPS_ERR_SHAPE, "a contraction over 2^31 / 6 or more in fp32") : TPS_OK;
+}
 int need_room(const void* workspace, size_t bytes, size_t need) {
   if (need > 0 && (workspace == nullptr || bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255)))
     return fail(TPS_ERR_WORKSPACE, "workspace needs %zu bytes, 256-byte aligned", need);
@@ -324,6 +328,7 @@ extern "C" int tps_linear_fwd(const tps_tensor* X, const tps_tensor* W, const tp
     f.planes = 1;
     if (gemm_few_supported(f)) return run_few(f, y.ld, s);
   }
+  if ((rc = contraction(c.dt, c.K))) return rc;
   const bool bf16 = c.dt == TPS_BF16;
   const bool x_ok = bf16 && direct_of(g.a, c.T, c.K, c.x.sr, c.x.sc), w_ok = bf16 && direct_of(g.b, c.K, c.N, c.w_in, c.w_out);
   const int planes = bf16 ? 1 : 3;
@@ -370,6 +375,8 @@ extern "C" int tps_linear_bwd(const tps_tensor* X, const tps_tensor* W, const tp
     if (dW != nullptr && (rc = launch_fill(dw.data, dw.dtype, dw.rows, dw.cols, dw.sr, dw.sc, s))) return rc;
     return dbias != nullptr ? launch_fill(dbias->data, dbias->dtype, 1, c.N, c.N, 1, s) : TPS_OK;
   }
+  if (dX != nullptr && (rc = contraction(c.dt, c.N))) return rc;
+  if (dW != nullptr && (rc = contraction(c.dt, c.T))) return rc;
   // dz: dy itself where nothing multiplies it and the products can read it
   const bool as_is = !acted && p.dy.dtype == c.dt && (!bf16 || direct_of(p.dy.p, c.T, c.N, p.dy.ld, 1));
   const bool products = dX != nullptr || dW != nullptr;

@@ -504,8 +504,9 @@ int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor
  * that TMA cannot describe (a base or a row pitch that is not a multiple of 16
  * bytes) are laid out there and need the bytes given for TPS_F32; a call that
  * needs more than it was given is refused with TPS_ERR_WORKSPACE before
- * anything is launched.  K, N >= 1; extents below 2^31, 2^29 for F32.  Both may
- * be captured into a CUDA graph.
+ * anything is launched.  K, N >= 1; extents below 2^31, 2^29 for F32, and of an
+ * F32 product's contraction (K; N for dX, T for dW) below 2^31 / 6.  Both may be
+ * captured into a CUDA graph.
  * ---------------------------------------------------------------------- */
 int tps_linear_fwd(const tps_tensor* X, const tps_tensor* W, const tps_tensor* bias, const tps_tensor* residual,
                    int32_t act, int32_t weight_layout, const tps_tensor* x_scale, const tps_tensor* w_scale,

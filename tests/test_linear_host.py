@@ -149,3 +149,22 @@ def test_weight_gradient_that_overlaps(lib):  # noqa: F811
         x.data = W.data = 0x1002
         assert lib.tps_linear_bwd(_r(x), _r(W), _r(_fake([6, N], BF16)), None, NONE, IN_OUT, None, _r(_fake(list(w), F32, dw)),
                                   None, None, 0, None) == WORKSPACE, (w, dw)
+
+
+def test_long_fp32_contractions(lib):  # noqa: F811
+    """Six products over K must count below 2^31: what does not is refused before a workspace is asked for."""
+    most = ((1 << 31) - 1) // 6
+    for K, want in ((most + 1, SHAPE), (most, WORKSPACE)):
+        assert fwd(lib, x=_fake([9, K]), w=_fake([K, 1]), y=_fake([9, 1])) == want
+
+    def bwd(T, K, N, dx, dw):
+        return lib.tps_linear_bwd(_r(_fake([T, K])), _r(_fake([K, N])), _r(_fake([T, N])), None, NONE, IN_OUT,
+                                  _r(_fake([T, K])) if dx else None, _r(_fake([K, N])) if dw else None, None, None, 0, None)
+    for n, want in ((most + 1, SHAPE), (most, WORKSPACE)):
+        assert bwd(2, 1, n, True, False) == want and bwd(n, 1, 2, False, True) == want
+        assert bwd(2, n, 1, True, True) == WORKSPACE  # K is no contraction backwards
+    assert bwd(most + 1, 1, 2, True, False) == WORKSPACE
+    # bf16 runs one product
+    x, w = _fake([9, most + 1], BF16, [1 << 29, 1]), _fake([most + 1, 1], BF16)
+    x.data = 0x1002
+    assert fwd(lib, x=x, w=w, y=_fake([9, 1], BF16)) == WORKSPACE
