@@ -205,10 +205,6 @@ __device__ __forceinline__ float linear_slope_c(float z) {
   if constexpr (ACT == TPS_ACT_SILU || ACT == TPS_ACT_GELU_TANH) z = at_most(at_least(z, -kActFar), kActFar);
   return act_grad_c<ACT>(z);
 }
-__device__ __forceinline__ float linear_act(int act, float z) {
-  if (act != kActNone) act_dispatch(act, [&](auto A) { z = linear_act_c<decltype(A)::value>(z); });
-  return z;
-}
 // z of one row's columns [col0, col0 + n), n <= C, from the accumulators.  Plain
 // loads, and not those of the read-only path: the few-row kernels are resident
 // while the kernel in front may still write the scales and the bias.
@@ -340,12 +336,6 @@ __device__ __forceinline__ void epilogue_elem(const Epilogue& e, int64_t row, in
     act_fwd_grad(e.act, e.aux[row * e.ld_aux + col], f, g);
     store_elem(e.d, e.d_dtype, row * e.ldd + col, v * e.aux2[row * e.ld_aux2 + col] * g);
     store_elem(e.d2, e.d2_dtype, row * e.ldd2 + col, v * f);
-  } else if (e.mode == EPI_LINEAR) {
-    if (e.bias != nullptr) v += any_elem(e.bias, e.bias_dtype, col);
-    if (e.d2 != nullptr) store_elem(e.d2, e.d2_dtype, row * e.ldd2 + col, v);
-    v = linear_act(e.act, v);
-    if (e.res != nullptr) v += any_elem(e.res, e.res_dtype, row * e.ld_res + col);
-    store_elem(e.d, e.d_dtype, row * e.ldd + col, v);
   } else {
     const int64_t i = row * e.ld_aux + col;
     const float pre = e.aux_bf16 != nullptr ? __uint_as_float(static_cast<uint32_t>(e.aux_bf16[i]) << 16) : e.aux[i];

@@ -169,10 +169,10 @@ int launch_gemm_simt(const GemmDesc& g, uint32_t* /*dev_err*/, cudaStream_t stre
   p.b3_sk = g.b3_sk;
   p.b3_sn = g.b3_sn;
   p.kparts = g.kparts < 1 ? 1 : g.kparts;
-  // the fused gate/up form, the CE statistics form and column segments are
-  // tensor-core only
+  // the fused gate/up form, the CE statistics form, the linear product's
+  // epilogue and column segments are tensor-core only
   if (g.epi.mode == EPI_GLU_FWD || g.epi.mode == EPI_CE_STATS || g.epi.mode == EPI_CE_LSE ||
-      g.epi.mode == EPI_CE_GRAD || g.n_segs > 1 || (g.epi.accumulate && g.epi.d_dtype != TPS_F32) ||
+      g.epi.mode == EPI_CE_GRAD || g.epi.mode == EPI_LINEAR || g.n_segs > 1 || (g.epi.accumulate && g.epi.d_dtype != TPS_F32) ||
       g.epi.alpha != nullptr)
     return TPS_ERR_ARG;
   p.epi = g.epi;

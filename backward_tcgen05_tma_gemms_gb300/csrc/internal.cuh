@@ -45,8 +45,7 @@ constexpr uint32_t TPS_DEVERR_BOUNDS = 4u;  // debug builds: a store outside its
 // EPI_CE_LSE   per (row, 128-column tile) the max and the sum of
 //              e^{acc - max}, and per row the logit at its label column
 // EPI_CE_GRAD  D = bf16(g_row (e^{acc - lse_row} - [column = label_row]))
-// Product with bias, activation and residual (CTA-pair, few-row and SIMT
-// kernels):
+// Product with bias, activation and residual (CTA-pair and few-row kernels):
 // EPI_LINEAR   z = acc row_scale[row] col_scale[column] + bias[column], D2 = z
 //              (may be null), D = act(z) + residual
 enum EpiMode : int {
