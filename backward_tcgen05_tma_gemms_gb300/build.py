@@ -33,6 +33,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libtps.so")
 BINDING = os.path.join(PKG, "_binding.so")
+BINDING_STAMP = os.path.join(PKG, "_build", "binding.txt")  # the torch that it was compiled against
 BUILD_DEBUG = os.path.join(PKG, "_build_debug")
 LIB_DEBUG = os.path.join(PKG, "libtps_debug.so")
 
@@ -67,10 +68,26 @@ def _compile(src: str, extra, build_dir: str = BUILD) -> str:
     return obj
 
 
+def _torch_stamp() -> str:
+    """What the extension is compiled against: it fits no other torch or Python."""
+    import torch
+    return f"{torch.__version__} {torch.version.git_version} {os.path.dirname(torch.__file__)} {sys.version}"
+
+
+def _binding_current() -> bool:
+    """Whether the extension is newer than the sources and was compiled against the installed torch."""
+    try:
+        with open(BINDING_STAMP) as f:
+            return os.path.getmtime(BINDING) >= _deps_mtime() and f.read() == _torch_stamp()
+    except OSError:
+        return False
+
+
 def _compile_binding() -> None:
     import torch
     at = os.path.dirname(torch.__file__)
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    os.makedirs(BUILD, exist_ok=True)
     tmp = BINDING + ".tmp"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
            "-I", INCLUDE, "-isystem", os.path.join(at, "include"), "-isystem", sysconfig.get_paths()["include"],
@@ -80,18 +97,20 @@ def _compile_binding() -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed on binding.cpp:\n{r.stderr}")
+    if os.path.exists(BINDING_STAMP):
+        os.remove(BINDING_STAMP)
     os.replace(tmp, BINDING)
+    with open(BINDING_STAMP, "w") as f:
+        f.write(_torch_stamp())
 
 
 def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False) -> str:
     """Compile and link libtps.so (libtps_debug.so with debug=True) and the
-    extension if any source is newer than they; return the library's path."""
+    extension if any source is newer than they, the extension also if it was
+    compiled against another torch; return the library's path."""
     lib, build_dir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
-
-    def current(path):
-        return not force and os.path.exists(path) and os.path.getmtime(path) >= _deps_mtime()
-    if current(lib):
-        if not current(BINDING):
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= _deps_mtime():
+        if not _binding_current():
             _compile_binding()
         return lib
     os.makedirs(build_dir, exist_ok=True)
@@ -100,7 +119,7 @@ def build(force: bool = False, verbose_ptxas: bool = False, debug: bool = False)
         extra += ["-DTPS_DEBUG=1"]
     srcs = sources()
     with ThreadPoolExecutor(max_workers=max(1, min(len(srcs) + 1, os.cpu_count() or 1))) as ex:
-        binding = None if current(BINDING) else ex.submit(_compile_binding)
+        binding = None if not force and _binding_current() else ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, extra, build_dir), srcs))
         if binding is not None:
             binding.result()
