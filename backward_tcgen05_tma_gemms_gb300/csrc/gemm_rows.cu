@@ -329,6 +329,7 @@ __global__ void __launch_bounds__(GR_MOST_THREADS)
 // ---- fp32, up to eight rows ---------------------------------------------------
 // The fp32 pipes do it: 2 T operations a weight of four bytes.  A block takes
 // 128 features of the cluster's run of K, with that run of X in shared memory.
+// One token through 14336 x 4096, (N, K), takes 39.5 us, 0.88 of the copy's rate.
 constexpr int GF_ROWS = 8, GF_WARPS = 8;
 constexpr int GF_SHARED = 96 << 10;  // of X
 

@@ -13,8 +13,12 @@
 // Backward.  One pass over dy and z forms dz in the operands' type and the
 // sums of its columns (fp32, of dz before its rounding); the two products then
 // read dz.  Without an activation dz is dy itself, where it has the operands'
-// type, and only the sums are formed.  bf16's rounding of dz costs 2^-9 of
-// random sign a term, as much as that of dx itself.
+// type, and only the sums are formed.  For bf16 operands dz is bf16, whatever
+// the types of dy and of the gradients, for the tensor cores take both operands
+// of one type and a second plane of dz would double the products.  Each term is
+// off by up to 2^-8 of itself, with either sign: 8192 x 4096 x 14336 gives bf16
+// gradients 2.3e-3 off where an fp32 dz gives 1.7e-3, which is their own
+// rounding.  fp32 operands have an fp32 dz.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -193,7 +197,7 @@ struct Room {  // of a workspace
   }
 };
 // Operands that are laid out, all in one launch (fp32, 500 x 1024 by 1024 x 4100: the
-// call takes 42 us, 47 with a launch for each).
+// call takes 41.0 us, 44.7 with a launch for each; in a CUDA graph 38.6 and 40.7).
 struct Lay {
   int dt;
   Room* room;

@@ -553,6 +553,9 @@ __device__ __forceinline__ void tma_load_maybe_hint(void* dst, const CUtensorMap
 // box_cols x box_rows box, 128-byte swizzle, zero fill out of bounds.
 bool tc_make_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
                  int box_rows);
+// The same of e4m3 operands (box_cols: 128, one swizzle row).
+bool tc_make_map8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
+                  int box_rows);
 // A 32 x n box of v (lane = row) to rows that TMA cannot store to, through a
 // staging of 33 words a row: row by row, a lane a column.  (Each lane its own row
 // touches 32 sectors a store: 1024 rows by 1024 x 4100 in bf16 33 us so, 16.5 here.)
@@ -592,9 +595,6 @@ __device__ __forceinline__ void tc_add_rows32(const Epilogue& e, uint8_t* buf, i
   __syncwarp();
 }
 
-// The same of e4m3 operands (box_cols: 128, one swizzle row).
-bool tc_make_map8(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int box_cols,
-                  int box_rows);
 // Row-major output view (fp32 or bf16) with a 32 x 32 box whose swizzle
 // matches the staging layout.
 bool tc_make_out_map(CUtensorMap* map, const void* base, int64_t rows, int64_t cols, int64_t ld, int dtype);

@@ -497,7 +497,8 @@ int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor
  * they pass the tensor cores as three bf16 values each); Y and Z are rounded
  * once.  Backward: dY and Z F32 or BF16 (Z NULL without an activation); dX,
  * dW, dbias F32 or BF16, each of its own, each may be NULL.  dz is rounded to
- * the operands' type where it enters the products; dbias sums it unrounded, in
+ * the operands' type where it enters the products, to BF16 also where dY and
+ * the gradients are F32 (F32 operands keep it); dbias sums it unrounded, in
  * a fixed order.  The residual's gradient is dY itself.  Outputs overlap nothing.
  * `workspace`: 256-byte aligned.  tps_linear_workspace_bytes gives what a call
  * of F32 or BF16 operands needs at most (0: none, as for E4M3); BF16 operands
