@@ -5,7 +5,8 @@ Argument marshalling only: every step of the computation runs in the
 library's CUDA kernels.  Tensors must be CUDA tensors on the current device;
 outputs and workspace are allocated with torch on that device and the work
 is enqueued on torch's current stream.  There is no CPU path: without the
-built library or a GPU these functions raise.
+built library or a GPU these functions raise.  Tensors given by `out` are
+written in place, and autograd is told so (their version counters move on).
 """
 from __future__ import annotations
 

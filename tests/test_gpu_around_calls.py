@@ -160,3 +160,38 @@ def test_last_tokens_of_a_batch():
     a = api.rmsnorm_bwd(x, got[2], None, got[3], dh=res)
     b = api.rmsnorm_bwd(x.contiguous(), got[2], None, got[3], dh=res.contiguous())
     assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("captured", [False, True])
+@pytest.mark.parametrize("T,d", [(40, 512), (700, 2048), (33, 77), (9, 20000)])
+def test_sums_right_behind_their_parts(T, d, captured):
+    """The kernel that adds up a gradient's parts is started before the one that writes them ends: through one
+    workspace, call after call, each sum is that of its own parts, as with a wait after each call."""
+    g = torch.Generator(device="cuda").manual_seed(d)
+    xs = [torch.randn(T, d, device="cuda", generator=g).to(BF) for _ in range(8)]
+    rstd, W = torch.ones(T, device="cuda"), torch.randn(d, 64, device="cuda", generator=g).to(BF)
+    N = 64
+    dys = [x[:, :N] if d % 8 == 0 else x[:, :N].contiguous() for x in xs]
+    ws = torch.empty(max(api.rmsnorm_workspace_bytes(T, d), api.linear_workspace_bytes(T, d, N, FP, True)), dtype=torch.uint8,
+                     device="cuda")
+
+    def chain(wait):
+        out = []
+        for i, (x, dy) in enumerate(zip(xs, dys)):
+            out.append(api.rmsnorm_bwd(x, xs[i - 1], None, rstd, workspace=ws)[2])
+            wait()
+            out.append(api.linear_bwd(x, W, dy, want_dx=False, want_dw=False, workspace=ws)[2])
+            wait()
+        return out
+    want = chain(torch.cuda.synchronize)
+    if captured:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            got = chain(lambda: None)
+        graph.replay()
+    else:
+        got = chain(lambda: None)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    terms = xs[0].double() * xs[-1].double()  # exact in fp32: T - 1 additions, each off by at most 2^-24 of all of them
+    assert ((want[0].double() - terms.sum(0)).abs() <= T * 2.0 ** -24 * terms.abs().sum(0)).all()
