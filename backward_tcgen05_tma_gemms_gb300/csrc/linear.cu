@@ -323,7 +323,10 @@ extern "C" int tps_linear_fwd(const tps_tensor* X, const tps_tensor* W, const tp
   g.b = c.w.data; g.b_sk = c.w_in; g.b_sn = c.w_out;
   if (codes) {
     g.epi.ldd = y.ld;
-    if (!gemm_tc_supported(g)) return fail(TPS_ERR_LAYOUT, "e4m3 operands need rows that start on 16 bytes");
+    // a single row has no pitch: any that TMA can describe
+    if (c.T == 1 && c.x.sc == 1) g.a_sm = round_up(c.K, 16);
+    if (c.N == 1 && c.w.sc == 1) g.b_sn = round_up(c.K, 16);
+    if (!gemm_tc_supported(g)) return fail(TPS_ERR_LAYOUT, "e4m3 operands need rows that start on 16 bytes and do not overlap");
     return run_linear(g, y.ld, 1, s);
   }
   if (c.dt == TPS_F32) {

@@ -487,8 +487,8 @@ int tps_quantize_e4m3(const tps_tensor* X, const tps_tensor* Q, const tps_tensor
  * BF16, or (forward) both E4M3 with x_scale (T floats) and w_scale (N floats),
  * one for each row as tps_quantize_e4m3 gives them:
  *   z = x_scale_t w_scale_n (X W) + bias;
- * E4M3 weights are TPS_W_OUT_IN, and rows of both start on 16 bytes
- * (TPS_ERR_LAYOUT otherwise).  bias (N) and residual (..., N) may be NULL.
+ * E4M3 weights are TPS_W_OUT_IN, and rows of both start on 16 bytes and do not
+ * overlap (TPS_ERR_LAYOUT otherwise).  bias (N) and residual (..., N) may be NULL.
  * act: TPS_ACT_*, TPS_ACT_NONE for none.  Y (..., N); Z (..., N) or NULL: the
  * pre-activation, which the backward pass needs when there is an activation.
  * bias, residual, Y, Z: F32 or BF16, each of its own; rows of unit stride, any

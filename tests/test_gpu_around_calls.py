@@ -195,3 +195,23 @@ def test_sums_right_behind_their_parts(T, d, captured):
     assert all(torch.equal(a, b) for a, b in zip(want, got))
     terms = xs[0].double() * xs[-1].double()  # exact in fp32: T - 1 additions, each off by at most 2^-24 of all of them
     assert ((want[0].double() - terms.sum(0)).abs() <= T * 2.0 ** -24 * terms.abs().sum(0)).all()
+
+
+@pytest.mark.parametrize("T", [1, 5, 64, 300])
+@pytest.mark.parametrize("K,N", [(1, 1), (50, 1), (50, 40), (130, 129)])
+def test_e4m3_rows_of_any_length(T, K, N):
+    """Rows that start on 16 bytes, whatever their length: what lies behind them (NaN here) is not read, and a
+    single row starts where it starts.  Sums in fp32 of K products, exact ones: K 2^-24 of their magnitudes, three
+    roundings of the scales and one of the output beside it."""
+    E8 = torch.float8_e4m3fn
+
+    def rows(n):
+        big = torch.full((n, -(-K // 16) * 16 + 16), float("nan"), device="cuda").to(E8)
+        v, scale = big[:, :K], torch.empty(n, device="cuda")
+        api.quantize_e4m3(torch.randn(n, K, device="cuda"), out=(v, scale))
+        return v, scale
+    (x, xs), (W, ws) = rows(T), rows(N)
+    y, _ = api.linear_fwd(x, W, x_scale=xs, w_scale=ws, weight_layout="out_in", out_dtype=FP)
+    a, b = x.double() * xs.double()[:, None], W.double() * ws.double()[:, None]
+    assert ((y.double() - a @ b.t()).abs() <= (K + 4) * 2.0 ** -24 * (a.abs() @ b.abs().t())).all()
+    assert api.last_device_error() == 0
